@@ -31,6 +31,17 @@ Ready-distribution cache (C ABI in ``include/specverify_cache.h``), through
 - :meth:`ReadyCacheTable.serve`      — the confidence-gated fast path for a batch of requests.
 - :meth:`ReadyCacheTable.invalidate` — a mutation of the listed sessions' state.
 
+Logits ahead of a verify (C ABI in ``include/specverify_logits.h``):
+
+- :func:`logit_adjust` — repetition, presence and frequency penalties, per-token biases and an
+  allowed-token mask over the rows of all k+1 positions.
+
+The paged key-value cache around a verify (C ABI in ``include/specverify_kv.h``):
+
+- :func:`paged_attention`      — attention of the new positions over the cache.
+- :func:`attention_weight_sum` — the weight the accepted positions gave each cached key.
+- :func:`kv_cache_evict`       — keeps the most recent and the heaviest keys.
+
 Workspaces: pass ``workspace=`` (a uint8 CUDA tensor of at least the size the matching
 ``*_workspace`` query returns, 256-byte aligned, not shared by calls in flight at the same
 time; it needs no initialisation), or let the binding keep one cached per (device, stream,
@@ -55,11 +66,13 @@ __all__ = [
     "gate_risk_coverage", "conformal_residual", "conformal_quantile_workspace",
     "conformal_quantile", "conformal_admit_workspace", "conformal_admit", "gate_points_dict",
     "ReadyCacheTable", "ready_cache_record_workspace", "SV_CACHE_VALID", "SV_CACHE_DECODED",
-    "SV_CACHE_CONSUMED", "CACHE_STATS",
+    "SV_CACHE_CONSUMED", "CACHE_STATS", "SV_F16", "logit_adjust", "paged_attention_workspace",
+    "paged_attention", "attention_weight_sum", "kv_cache_evict",
 ]
 
 SV_F32 = 0
 SV_BF16 = 1
+SV_F16 = 2
 SV_MAX_K = 16
 SV_CONF_TOP_PROB = 0
 SV_CONF_INV_ENTROPY = 1
@@ -558,3 +571,195 @@ def ngram_propose(history, hist_len, n_max: int, n_min: int, k: int, *, out_draf
     _ok(library().ngram_propose(_ptr(history), _ptr(hist_len), B, L_max, n_max, n_min, k,
                                 _ptr(out_draft), _ptr(out_num_draft), h), "ngram_propose")
     return out_draft, out_num_draft
+
+
+# ------------------------------------------------------------------------------ logits
+def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_tokens=None,
+                 num_draft=None, repetition=None, presence=None, frequency=None,
+                 bias_tokens=None, bias_values=None, allowed=None, out=None, stream=None):
+    """Penalties, biases and the allowed-token mask over logits [B, P, V], whose rows may lie
+    apart (last dimension contiguous). ``allowed`` holds bits, [B, P, ceil(V/32)] int32.
+    Returns the adjusted logits [B, P, V] (``out``, which may be ``logits`` itself; rows past a
+    request's num_draft are left as they are in it)."""
+    B, P, V = logits.shape
+    dev = logits.device
+    code = _dtype_code(logits)
+    _check_strided("logits", logits)
+    L_max = 0
+    if history is not None:
+        L_max = history.shape[-1]
+        _check_cuda("history", history, torch.int32, (B, L_max), dev)
+    _check_cuda("hist_len", hist_len, torch.int32, (B,), dev)
+    _check_cuda("prompt_len", prompt_len, torch.int32, (B,), dev)
+    _check_cuda("draft_tokens", draft_tokens, torch.int32, (B, P - 1), dev)
+    _check_cuda("num_draft", num_draft, torch.int32, (B,), dev)
+    _check_cuda("repetition", repetition, torch.float32, (B,), dev)
+    _check_cuda("presence", presence, torch.float32, (B,), dev)
+    _check_cuda("frequency", frequency, torch.float32, (B,), dev)
+    n_bias = 0
+    if bias_tokens is not None:
+        n_bias = bias_tokens.shape[-1]
+        _check_cuda("bias_tokens", bias_tokens, torch.int32, (B, n_bias), dev)
+    _check_cuda("bias_values", bias_values, torch.float32, (B, n_bias), dev)
+    if n_bias == 0:
+        bias_tokens = bias_values = None
+    _check_cuda("allowed", allowed, torch.int32, (B, P, (V + 31) // 32), dev)
+    if out is None:
+        out = torch.empty((B, P, V), dtype=logits.dtype, device=dev)
+    _check_strided("out", out, logits.dtype, (B, P, V), dev)
+    h, _ = _stream_handle(stream)
+    _ok(library().logit_adjust(
+        _ptr(logits), logits.stride(0), logits.stride(1), code, _ptr(history), _ptr(hist_len),
+        _ptr(prompt_len), L_max, _ptr(draft_tokens), _ptr(num_draft), _ptr(repetition),
+        _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), n_bias,
+        _ptr(allowed), B, P, V, _ptr(out), out.stride(0), out.stride(1), h), "logit_adjust")
+    return out
+
+
+# ------------------------------------------------------------------------------ paged cache
+def _check_strided(name, t, dtype=None, shape=None, device=None, last=True):
+    """As _check_cuda, for a tensor of which at most the last dimension must be contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if last and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _kv_dtype(t):
+    if t.dtype == torch.bfloat16:
+        return SV_BF16
+    if t.dtype == torch.float16:
+        return SV_F16
+    raise TypeError(f"keys and values must be bfloat16 or float16, got {t.dtype}")
+
+
+def _kv_pool(t):
+    return _native.KvPool(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _kv_shape(B, P, Hq, k_cache, page_table):
+    pages, page_size, Hkv, D = k_cache.shape
+    return _native.KvShape(_kv_dtype(k_cache), B, P, Hq, Hkv, D, page_size, pages,
+                           page_table.shape[-1])
+
+
+def _score_rule(scale, softcap, window, slopes, D):
+    return _native.ScoreRule(float(D ** -0.5 if scale is None else scale), float(softcap),
+                             int(window), None if slopes is None else slopes.data_ptr())
+
+
+def _check_kv(q, k_cache, v_cache, page_table, seq_len, num_draft, slopes):
+    B, P, Hq, D = q.shape
+    dev = q.device
+    pages, page_size, Hkv, _ = k_cache.shape
+    _check_strided("q", q, k_cache.dtype)
+    _check_strided("k_cache", k_cache, None, (pages, page_size, Hkv, D), dev)
+    if v_cache is not None:
+        _check_strided("v_cache", v_cache, k_cache.dtype, (pages, page_size, Hkv, D), dev)
+    _check_cuda("page_table", page_table, torch.int32, (B, page_table.shape[-1]), dev)
+    _check_cuda("seq_len", seq_len, torch.int32, (B,), dev)
+    _check_cuda("num_draft", num_draft, torch.int32, (B,), dev)
+    _check_cuda("slopes", slopes, torch.float32, (Hq,), dev)
+    return B, P, Hq, D, dev
+
+
+def paged_attention_workspace(B: int, P: int, Hq: int, k_cache, page_table) -> int:
+    return int(library().paged_attention_workspace(_kv_shape(B, P, Hq, k_cache, page_table)))
+
+
+def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None, scale=None,
+                    softcap: float = 0.0, window: int = 0, slopes=None, out=None, out_lse=None,
+                    want_lse: bool = True, workspace=None, stream=None):
+    """Attention of q [B, P, Hq, D] over a paged cache: k_cache and v_cache are views [pages,
+    page_size, Hkv, D] of any page, token and head stride, page_table [B, max_pages] int32,
+    seq_len [B] int32 (the new positions included). ``scale`` defaults to D ** -0.5. Returns
+    (out [B, P, Hq, D], lse [B, P, Hq] fp32 or None)."""
+    B, P, Hq, D, dev = _check_kv(q, k_cache, v_cache, page_table, seq_len, num_draft, slopes)
+    if out is None:
+        out = torch.empty((B, P, Hq, D), dtype=q.dtype, device=dev)
+    if out_lse is None and want_lse:
+        out_lse = torch.empty((B, P, Hq), dtype=torch.float32, device=dev)
+    _check_cuda("out", out, q.dtype, (B, P, Hq, D), dev)
+    _check_cuda("out_lse", out_lse, torch.float32, (B, P, Hq), dev)
+    shape = _kv_shape(B, P, Hq, k_cache, page_table)
+    h, st = _stream_handle(stream)
+    L = library()
+    ws = workspace
+    if ws is None:
+        ws = _workspace("attention", int(L.paged_attention_workspace(shape)), dev, st)
+    _ok(L.paged_attention(
+        shape, _score_rule(scale, softcap, window, slopes, D), _ptr(q), q.stride(0), q.stride(1),
+        q.stride(2), _kv_pool(k_cache), _kv_pool(v_cache), _ptr(page_table), _ptr(seq_len),
+        _ptr(num_draft), _ptr(out), _ptr(out_lse), _ptr(ws), ws.numel(), h), "paged_attention")
+    return out, out_lse
+
+
+def attention_weight_sum(q, k_cache, page_table, seq_len, lse, *, num_draft=None,
+                         accept_len=None, scale=None, softcap: float = 0.0, window: int = 0,
+                         slopes=None, prior=None, out=None, stream=None):
+    """Adds to ``prior`` [B, Hkv, N] fp32 (zeros if None) the softmax weight that the rows up to
+    accept_len gave each cached key, with ``lse`` [B, P, Hq] as paged_attention returned it.
+    Returns the sums [B, Hkv, N] (``out``, which may be ``prior``)."""
+    B, P, Hq, D, dev = _check_kv(q, k_cache, None, page_table, seq_len, num_draft, slopes)
+    Hkv = k_cache.shape[2]
+    if out is None:
+        N = page_table.shape[-1] * k_cache.shape[1] if prior is None else prior.shape[-1]
+        out = torch.zeros((B, Hkv, N), dtype=torch.float32, device=dev)
+    N = out.shape[-1]
+    _check_strided("lse", lse, torch.float32, (B, P, Hq), dev, last=False)
+    _check_cuda("accept_len", accept_len, torch.int32, (B,), dev)
+    _check_cuda("prior", prior, torch.float32, (B, Hkv, N), dev)
+    _check_cuda("out", out, torch.float32, (B, Hkv, N), dev)
+    h, _ = _stream_handle(stream)
+    _ok(library().attention_weight_sum(
+        _kv_shape(B, P, Hq, k_cache, page_table),
+        _score_rule(scale, softcap, window, slopes, D), _ptr(q), q.stride(0), q.stride(1),
+        q.stride(2), _kv_pool(k_cache), _ptr(page_table), _ptr(seq_len), _ptr(num_draft),
+        _ptr(lse), *lse.stride(), _ptr(accept_len), _ptr(prior), _ptr(out), N, h),
+        "attention_weight_sum")
+    return out
+
+
+def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, recent: int,
+                   new_k, new_v, new_page_table, *, out_len=None, out_index=None,
+                   out_weights=None, stream=None):
+    """Keeps min(seq_len, budget) keys of every request and kv head, the last ``recent`` and the
+    heaviest others by ``weights`` [B, Hkv, N] fp32, and copies them in order to the pages of
+    new_page_table in new_k and new_v (which may be the same pools). Returns (out_len [B],
+    out_index [B, Hkv, budget] int32, out_weights [B, Hkv, budget] fp32)."""
+    B, max_pages = page_table.shape
+    dev = k_cache.device
+    pages, page_size, Hkv, D = k_cache.shape
+    N = weights.shape[-1]
+    new_pages = new_k.shape[0]
+    _check_strided("k_cache", k_cache)
+    _check_strided("v_cache", v_cache, k_cache.dtype, (pages, page_size, Hkv, D), dev)
+    _check_strided("new_k", new_k, k_cache.dtype, (new_pages, page_size, Hkv, D), dev)
+    _check_strided("new_v", new_v, k_cache.dtype, (new_pages, page_size, Hkv, D), dev)
+    _check_cuda("page_table", page_table, torch.int32, (B, max_pages), dev)
+    _check_cuda("seq_len", seq_len, torch.int32, (B,), dev)
+    _check_cuda("weights", weights, torch.float32, (B, Hkv, N), dev)
+    _check_cuda("new_page_table", new_page_table, torch.int32, (B, new_page_table.shape[-1]), dev)
+    if out_len is None:
+        out_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    if out_index is None:
+        out_index = torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev)
+    if out_weights is None:
+        out_weights = torch.empty((B, Hkv, budget), dtype=torch.float32, device=dev)
+    _check_cuda("out_len", out_len, torch.int32, (B,), dev)
+    _check_cuda("out_index", out_index, torch.int32, (B, Hkv, budget), dev)
+    _check_cuda("out_weights", out_weights, torch.float32, (B, Hkv, budget), dev)
+    h, _ = _stream_handle(stream)
+    _ok(library().kv_cache_evict(
+        _kv_shape(B, 1, Hkv, k_cache, page_table), _kv_pool(k_cache), _kv_pool(v_cache),
+        _ptr(page_table), _ptr(seq_len), _ptr(weights), N, int(budget), int(recent),
+        _kv_pool(new_k), _kv_pool(new_v), new_pages, _ptr(new_page_table),
+        new_page_table.shape[-1], _ptr(out_len), _ptr(out_index), _ptr(out_weights), h),
+        "kv_cache_evict")
+    return out_len, out_index, out_weights

@@ -97,6 +97,27 @@ def lib():
     return _lib
 
 
+class KvPool(ctypes.Structure):
+    """sv_kv_pool"""
+
+    _fields_ = [("data", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class KvShape(ctypes.Structure):
+    """sv_kv_shape"""
+
+    _fields_ = [(n, ctypes.c_int) for n in ("dtype", "B", "P", "Hq", "Hkv", "D", "page_size",
+                                            "num_pages", "max_pages")]
+
+
+class ScoreRule(ctypes.Structure):
+    """sv_score_rule"""
+
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int),
+                ("slopes", ctypes.c_void_p)]
+
+
 def _declare(L):
     P, I, F, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
     L.sv_version.restype = I
@@ -152,3 +173,18 @@ def _declare(L):
     L.ready_cache_serve.argtypes = [P, P, I, I, P, P, P, P, P, I, F, P, I, I, P, P, P]
     L.ready_cache_invalidate.restype = I
     L.ready_cache_invalidate.argtypes = [P, I, P, P, I, P]
+    q = ctypes.c_int64
+    L.logit_adjust.restype = I
+    L.logit_adjust.argtypes = [P, q, q, I, P, P, P, I, P, P, P, P, P, P, P, I, P, I, I, I, P, q,
+                               q, P]
+    shape, rule, pool = (ctypes.POINTER(t) for t in (KvShape, ScoreRule, KvPool))
+    L.paged_attention_workspace.restype = Z
+    L.paged_attention_workspace.argtypes = [shape]
+    L.paged_attention.restype = I
+    L.paged_attention.argtypes = [shape, rule, P, q, q, q, pool, pool, P, P, P, P, P, P, Z, P]
+    L.attention_weight_sum.restype = I
+    L.attention_weight_sum.argtypes = [shape, rule, P, q, q, q, pool, P, P, P, P, q, q, q, P, P,
+                                       P, q, P]
+    L.kv_cache_evict.restype = I
+    L.kv_cache_evict.argtypes = [shape, pool, pool, P, P, P, q, I, I, pool, pool, I, P, I, P, P,
+                                 P, P]
