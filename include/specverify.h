@@ -70,8 +70,7 @@ typedef enum {
 
 typedef enum {
   SV_F32 = 0,  /* IEEE binary32 logits */
-  SV_BF16 = 1, /* bfloat16 logits (upper 16 bits of a binary32) */
-  SV_F16 = 2   /* IEEE binary16, for the key-value calls of specverify_kv.h only */
+  SV_BF16 = 1  /* bfloat16 logits (upper 16 bits of a binary32) */
 } sv_dtype;
 
 /* Largest draft length k the verify calls accept. */

@@ -22,6 +22,12 @@
 extern "C" {
 #endif
 
+/* Types of queries, keys, values and outputs. */
+typedef enum {
+  SV_KV_BF16 = 1, /* bfloat16 (the value of SV_BF16) */
+  SV_KV_F16 = 2   /* IEEE binary16 */
+} sv_kv_dtype;
+
 /* A pool of pages holding keys or values: element d of kv head h of the token in slot s of
  * page p is at data[p * page_stride + s * token_stride + h * head_stride + d] (strides in
  * elements, so both [pages, page_size, heads, D] and [pages, heads, page_size, D] fit).
@@ -33,7 +39,7 @@ typedef struct {
 } sv_kv_pool;
 
 /* Sizes shared by the calls below. HOST memory, read during the call.
- *   dtype       SV_BF16 or SV_F16, of queries, keys, values and outputs.
+ *   dtype       of queries, keys, values and outputs.
  *   B           requests, B >= 0 (0 is a no-op).
  *   P           query positions per request, 1 <= P <= SV_MAX_K + 1.
  *   Hq, Hkv     query and key-value heads, Hq a multiple of Hkv; query heads h*G .. h*G+G-1
@@ -43,7 +49,7 @@ typedef struct {
  *   num_pages   pages in the pool.
  *   max_pages   columns of the page table; max_pages * page_size < 2^30.  */
 typedef struct {
-  sv_dtype dtype;
+  sv_kv_dtype dtype;
   int B, P, Hq, Hkv, D, page_size, num_pages, max_pages;
 } sv_kv_shape;
 

@@ -216,7 +216,7 @@ extern "C" sv_status paged_attention(const sv_kv_shape* shape, const sv_score_ru
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const int64_t rows = (int64_t)A.B * A.P * A.Hq;
   const unsigned grid = (unsigned)((rows + kWarpsPerCta - 1) / kWarpsPerCta);
-  if (shape->dtype == SV_BF16)
+  if (shape->dtype == SV_KV_BF16)
     attend_rows<__nv_bfloat16><<<grid, 32 * kWarpsPerCta, 0, st>>>(A);
   else
     attend_rows<__half><<<grid, 32 * kWarpsPerCta, 0, st>>>(A);
@@ -251,7 +251,7 @@ extern "C" sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_sco
   A.stride = stride;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const dim3 grid(64, (unsigned)(shape->B * shape->Hkv));
-  if (shape->dtype == SV_BF16)
+  if (shape->dtype == SV_KV_BF16)
     weigh_keys<__nv_bfloat16><<<grid, 32 * kWarpsPerCta, 0, st>>>(A);
   else
     weigh_keys<__half><<<grid, 32 * kWarpsPerCta, 0, st>>>(A);

@@ -16,7 +16,7 @@ constexpr int kMaxPageSize = 1024;
 
 inline sv_status check_kv_shape(const sv_kv_shape* s, bool queries) {
   if (!s) return SV_ERR_INVALID_ARG;
-  if (s->dtype != SV_BF16 && s->dtype != SV_F16) return SV_ERR_INVALID_ARG;
+  if (s->dtype != SV_KV_BF16 && s->dtype != SV_KV_F16) return SV_ERR_INVALID_ARG;
   if (s->B < 0 || s->Hkv < 1 || s->D < 1 || s->page_size < 1 || s->num_pages < 0 ||
       s->max_pages < 1)
     return SV_ERR_INVALID_ARG;
