@@ -54,11 +54,11 @@ inline int log2_of(int x) {
 // The rule as the kernels take it.
 struct ScoreRule {
   float scale, softcap;
-  int window;  // INT32_MAX for none
+  int window;  // 2^30 (past every position) for none
   const float* slopes;
 };
 inline ScoreRule score_rule(const sv_score_rule* r) {
-  return {r->scale, r->softcap, r->window > 0 ? r->window : 0x7fffffff, r->slopes};
+  return {r->scale, r->softcap, r->window > 0 && r->window < (1 << 30) ? r->window : 1 << 30, r->slopes};
 }
 
 }  // namespace sv
