@@ -113,25 +113,24 @@ sv_status fill_tile_args(TileArgs& A, CUtensorMap* mq, CUtensorMap* mk, const sv
 
 namespace {
 
-// Workspace: the join counters (cleared at the start of a call), then two pieces per CTA.
+// Workspace: what each CTA leaves to join, then two pieces per CTA.
 struct AttnLayout {
-  size_t counters, counter_bytes, part, total;
+  size_t part, total;
 };
 AttnLayout attn_layout(const sv_kv_shape* s) {
   int pos_block, blocks, columns;
   row_blocks(s, false, &pos_block, &blocks, &columns);
   const size_t ctas = (size_t)device_sm_count();
   AttnLayout L{};
-  L.counter_bytes = round_up(ctas * sizeof(unsigned int), 16);
-  L.part = round_up(L.counter_bytes, 256);
+  L.part = round_up(ctas * sizeof(JoinItem), 256);
   L.total = round_up(L.part + 2 * ctas * columns * (s->D + 2) * sizeof(float), 256);
   return L;
 }
 
-template <int D, int N>
+template <int D, int N, bool kBf16>
 sv_status launch_attention(const TileArgs& A, const CUtensorMap& mq, const CUtensorMap& mk,
                            const CUtensorMap& mv, const ValuePool& v, cudaStream_t st) {
-  using S = TileShape<D, N, false>;
+  using S = TileShape<D, N, false, kBf16>;
   auto kernel = tile_kernel<S>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;
@@ -143,30 +142,46 @@ sv_status launch_attention(const TileArgs& A, const CUtensorMap& mq, const CUten
     if (e != cudaSuccess) return cuda_fail(e);
     ready.fetch_or(bit);
   }
+  const unsigned ctas = (unsigned)device_sm_count();
+  kernel<<<ctas, S::Threads, S::Smem, st>>>(mq, mk, mv, A, v);
+  const sv_status s = launch_status();
+  if (s != SV_OK) return s;
+  // the join takes its place while the tiles are still walked, and waits for their end
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)device_sm_count());
-  cfg.blockDim = dim3(S::Threads);
-  cfg.dynamicSmemBytes = S::Smem;
+  cfg.gridDim = dim3(ctas, kJoinShares);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, A, v);
+  e = cudaLaunchKernelEx(&cfg, join_kernel<D, N, kBf16>, (const JoinItem*)A.joins,
+                         (const float*)A.part, A.G, A.Hq, A.out, A.out_lse);
   return e == cudaSuccess ? launch_status() : cuda_fail(e);
 }
 
-template <int D>
+template <int D, bool kBf16>
 sv_status launch_columns(int columns, const TileArgs& A, const CUtensorMap& mq,
                          const CUtensorMap& mk, const CUtensorMap& mv, const ValuePool& v,
                          cudaStream_t st) {
   switch (columns) {
-    case 16: return launch_attention<D, 16>(A, mq, mk, mv, v, st);
-    case 32: return launch_attention<D, 32>(A, mq, mk, mv, v, st);
-    case 64: return launch_attention<D, 64>(A, mq, mk, mv, v, st);
+    case 16: return launch_attention<D, 16, kBf16>(A, mq, mk, mv, v, st);
+    case 32: return launch_attention<D, 32, kBf16>(A, mq, mk, mv, v, st);
+    case 64: return launch_attention<D, 64, kBf16>(A, mq, mk, mv, v, st);
   }
-  return launch_attention<D, D == 256 ? 64 : 128>(A, mq, mk, mv, v, st);
+  return launch_attention<D, D == 256 ? 64 : 128, kBf16>(A, mq, mk, mv, v, st);
+}
+
+template <bool kBf16>
+sv_status launch_width(int D, int columns, const TileArgs& A, const CUtensorMap& mq,
+                       const CUtensorMap& mk, const CUtensorMap& mv, const ValuePool& v,
+                       cudaStream_t st) {
+  switch (D) {
+    case 64: return launch_columns<64, kBf16>(columns, A, mq, mk, mv, v, st);
+    case 128: return launch_columns<128, kBf16>(columns, A, mq, mk, mv, v, st);
+  }
+  return launch_columns<256, kBf16>(columns, A, mq, mk, mv, v, st);
 }
 
 }  // namespace
@@ -202,19 +217,14 @@ extern "C" sv_status paged_attention(const sv_kv_shape* shape, const sv_score_ru
   if (s == SV_OK) s = encode_pool(&mv, shape, v);
   if (s != SV_OK) return s;
   char* ws = static_cast<char*>(workspace);
-  A.counters = reinterpret_cast<unsigned int*>(ws);
+  A.joins = reinterpret_cast<JoinItem*>(ws);
   A.part = reinterpret_cast<float*>(ws + L.part);
   A.out = out;
   A.out_lse = out_lse;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  s = launch_clear(ws, L.counter_bytes, st);
-  if (s != SV_OK) return s;
   const ValuePool vp{v->data, v->page_stride, v->token_stride, v->head_stride};
   int pos_block, blocks, columns;
   row_blocks(shape, false, &pos_block, &blocks, &columns);
-  switch (shape->D) {
-    case 64: return launch_columns<64>(columns, A, mq, mk, mv, vp, st);
-    case 128: return launch_columns<128>(columns, A, mq, mk, mv, vp, st);
-    default: return launch_columns<256>(columns, A, mq, mk, mv, vp, st);
-  }
+  return A.bf16 ? launch_width<true>(shape->D, columns, A, mq, mk, mv, vp, st)
+                : launch_width<false>(shape->D, columns, A, mq, mk, mv, vp, st);
 }

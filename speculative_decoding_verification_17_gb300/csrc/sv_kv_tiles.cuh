@@ -52,6 +52,8 @@ constexpr int kUnitSmemMax = 232448 - 8192;  // dynamic shared memory for operan
 constexpr float kNoMax = -3.402823466e38f;   // a maximum below every finite score
 constexpr float kLog2e = 1.4426950408889634f;
 
+struct JoinItem;
+
 struct TileArgs {
   const int32_t *table, *seq_len, *num_draft, *accept_len;
   int B, P, Hq, Hkv, G, log_page, num_pages, max_pages;
@@ -62,35 +64,58 @@ struct TileArgs {
   // attention
   void* out;
   float *out_lse, *part;
-  unsigned int* counters;
+  struct JoinItem* joins;
   // key weights
   const float *lse, *prior;
   float* weights;
   int64_t stride, lse_req, lse_row, lse_head;
 };
 
-template <int kD, int kN, bool kWeigh>
+// An item split over several CTAs, as its first CTA leaves it for the joining kernel.
+struct JoinItem {
+  int rows, pieces;  // rows = 0: none
+  int64_t row0;      // output row of its first column
+};
+
+template <int kD, int kN, bool kWeigh, bool kBf16 = false>
 struct TileShape {
   static constexpr int D = kD, N = kN;
+  static constexpr bool Bf16 = kBf16;  // (attention) the type is bf16, else fp16
   static constexpr bool Weigh = kWeigh;
   static constexpr int U = D / 64;  // units of a key or value tile
-  // softmax warps: groups of four (one per quarter of the tile's keys). In the attention two
-  // groups share the columns of a wide tile; in the key weights each takes every other tile.
-  static constexpr int Groups = kWeigh ? 2 : (N >= 64 ? 2 : 1);
-  static constexpr int SoftWarps = 4 * Groups;
+  // Softmax warps: two groups of four (one warp per quarter of the tile's keys). In the
+  // attention of up to 32 columns the groups are two teams that take the pieces in turn, each
+  // with its own score, weight and output buffers, so one team's end of a piece (its last
+  // product, its output, the next piece's tables) passes under the other's tiles; of wider
+  // tiles each group takes half of the columns and there is one team. In the key weights each
+  // group takes every other tile.
+  static constexpr int Teams = !kWeigh && N <= 32 ? 2 : 1;
+  static constexpr int SoftWarps = 8;
   static constexpr int SoftThreads = 32 * SoftWarps;
   static constexpr int Threads = SoftThreads + 64;
-  static constexpr int NC = kWeigh ? N : N / Groups;  // columns per softmax thread
+  static constexpr int TeamThreads = SoftThreads / Teams;
+  static constexpr int NC = kWeigh || Teams == 2 ? N : N / 2;  // columns per softmax thread
+  static constexpr int CH = NC < 32 ? NC : 32;                 // of which at a time
   static constexpr int QBytes = N * D * 2;
   static constexpr int NQ = N * D <= 64 * 128 ? 2 : 1;  // query buffers
   static constexpr int PBytes = kWeigh ? 0 : 2 * kTileKeys * N * 2;
-  static constexpr int Room = (kUnitSmemMax - 1024 - NQ * QBytes - PBytes) / kUnitBytes;
+  // two buffers of weights per team where the ring keeps three tensors (two tiles of D = 256)
+  static constexpr int kLeft = kUnitSmemMax - 1024 - NQ * QBytes;
+  static constexpr int NP =
+      kWeigh ? 1 : (kLeft - 2 * Teams * PBytes) / kUnitBytes >= (U == 4 ? 8 : 6) ? 2 : 1;
+  static constexpr int Room = (kLeft - Teams * NP * PBytes) / kUnitBytes;
   static constexpr int NU = (Room > 12 ? 12 : Room) / 2 * 2;  // ring units, an even number
-  static constexpr int Smem = 1024 + NQ * QBytes + PBytes + NU * kUnitBytes;
+  static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * kUnitBytes;
   static constexpr int MBlocks = kWeigh ? 0 : (D + 127) / 128;  // accumulators of 128 of D
-  static constexpr int TmemNeed = (2 + MBlocks) * N;
+  // two score buffers per team, two outputs
+  static constexpr int TmemNeed = 2 * (Teams + MBlocks) * N;
   static constexpr int TmemCols = TmemNeed <= 32 ? 32 : TmemNeed <= 64 ? 64 : TmemNeed <= 128 ? 128
                                   : TmemNeed <= 256 ? 256 : 512;
+  // The cost of a tile and of starting a piece, in the units the work is divided by: a quarter
+  // of the time a tile's bytes take (about 350 clocks per 64 columns; half that for the keys
+  // alone).
+  static constexpr int TileCost = 4;
+  static constexpr int PieceCost = (kWeigh ? 12 : Teams == 2 ? 4 : 10) / U + 1;
   // the last value tile lies one (unused) key tile past the last key tile: its place must not
   // have been that key tile's
   static_assert(kWeigh || NU >= 2 * U, "ring");
@@ -106,6 +131,10 @@ struct Item {
   int pos0;         // cache position of row i0
   int first, last;  // the keys any live row sees; last < first: none
   int t0, tiles;    // tiles to walk (0: nothing to write)
+  template <class S>
+  __device__ __forceinline__ int64_t cost() const {
+    return tiles == 0 ? 0 : S::PieceCost + (int64_t)tiles * S::TileCost;
+  }
 };
 
 template <bool kWeigh>
@@ -150,21 +179,22 @@ __device__ __forceinline__ int load_acc(const TileArgs& A, int b, int nd) {
   return A.accept_len ? __ldg(A.accept_len + b) : nd;
 }
 
-// Tiles of a request per kv head, over its row blocks (in the key weights a tile is walked once
+// Cost of a request per kv head, over its row blocks (in the key weights a tile is walked once
 // per block, so all blocks count as one item).
-template <bool kWeigh>
-__device__ __forceinline__ int request_tiles(const TileArgs& A, int b) {
-  const int n = load_n(A, b), nd = load_nd(A, b), acc = kWeigh ? load_acc(A, b, nd) : 0;
-  if (kWeigh) return item_of<true>(A, n, nd, acc, 0).tiles;
-  int t = 0;
-  for (int rb = 0; rb < A.blocks; ++rb) t += item_of<false>(A, n, nd, acc, rb).tiles;
-  return t;
+template <class S>
+__device__ __forceinline__ int64_t request_cost(const TileArgs& A, int b) {
+  const int n = load_n(A, b), nd = load_nd(A, b), acc = S::Weigh ? load_acc(A, b, nd) : 0;
+  int64_t c = 0;
+  for (int rb = 0; rb < (S::Weigh ? 1 : A.blocks); ++rb)
+    c += item_of<S::Weigh>(A, n, nd, acc, rb).template cost<S>();
+  return c;
 }
 
 // Where a CTA's range starts (shared memory).
 struct Start {
   int64_t flat, left, per;
-  int b, h, rb, off;
+  int64_t off;  // the start's offset into its item
+  int b, h, rb;
 };
 
 // A CTA's part of one item: tiles [ta, tb) of the item, of which [ma, mb) go through the tensor
@@ -174,7 +204,7 @@ struct Piece {
   Item it;
   int ta, tb, ma, mb;
   bool starts, ends;  // whether it holds the item's first and last tile
-  int64_t item0;      // flat index of the item's first tile
+  int64_t item0;      // flat position of the item
 };
 
 // The tiles of a piece that some key of [first, last] falls into.
@@ -197,11 +227,13 @@ __device__ __forceinline__ bool weigh_pass(const TileArgs& A, Piece& p, int rb) 
   return p.it.live > 0;
 }
 
-template <bool kWeigh>
+// Walks a range of the flat work list, in which an item takes PieceCost + tiles * TileCost
+// units; tile k belongs to the range that holds the item's unit PieceCost + k * TileCost.
+template <class S>
 struct Walk {
   const TileArgs& A;
-  int b, h, rb, off, n, nd, acc;
-  int64_t flat, left;
+  int b, h, rb, n, nd, acc;
+  int64_t off, flat, left;
   Item it;
   __device__ __forceinline__ Walk(const TileArgs& a, const Start& s)
       : A(a), b(s.b), h(s.h), rb(s.rb), off(s.off), flat(s.flat), left(s.left) {
@@ -210,33 +242,42 @@ struct Walk {
   __device__ __forceinline__ void load() {
     n = load_n(A, b);
     nd = load_nd(A, b);
-    acc = kWeigh ? load_acc(A, b, nd) : 0;
-    it = item_of<kWeigh>(A, n, nd, acc, rb);
+    acc = S::Weigh ? load_acc(A, b, nd) : 0;
+    it = item_of<S::Weigh>(A, n, nd, acc, rb);
+  }
+  // The first tile at or past unit u of the item.
+  __device__ __forceinline__ int tile_from(int64_t u) const {
+    return u <= S::PieceCost ? 0 : (int)((u - S::PieceCost + S::TileCost - 1) / S::TileCost);
   }
   __device__ __forceinline__ bool next(Piece& p) {
-    if (left <= 0) return false;
-    while (it.tiles == 0) advance();
-    const int64_t rest = it.tiles - off, take = rest < left ? rest : left;
-    p.b = b;
-    p.h = h;
-    p.rb = rb;
-    p.it = it;
-    p.ta = it.t0 + off;
-    p.tb = p.ta + (int)take;
-    p.starts = off == 0;
-    p.ends = take == rest;
-    p.item0 = flat - off;
-    mma_range(p);
-    flat += take;
-    left -= take;
-    off += (int)take;
-    if (off == it.tiles && left > 0) advance();
-    return true;
+    while (left > 0) {
+      while (it.tiles == 0) advance();
+      const int64_t rest = it.template cost<S>() - off, take = rest < left ? rest : left;
+      const int ka = tile_from(off), kb = tile_from(off + take);
+      p.b = b;
+      p.h = h;
+      p.rb = rb;
+      p.it = it;
+      p.ta = it.t0 + ka;
+      p.tb = it.t0 + kb;
+      p.starts = ka == 0;
+      p.ends = kb == it.tiles;
+      p.item0 = flat - off;
+      flat += take;
+      left -= take;
+      off += take;
+      if (take == rest && left > 0) advance();
+      if (kb > ka) {
+        mma_range(p);
+        return true;
+      }
+    }
+    return false;
   }
   __device__ __forceinline__ void advance() {
     off = 0;
-    if (!kWeigh && ++rb < A.blocks) {
-      it = item_of<kWeigh>(A, n, nd, acc, rb);
+    if (!S::Weigh && ++rb < A.blocks) {
+      it = item_of<S::Weigh>(A, n, nd, acc, rb);
       return;
     }
     rb = 0;
@@ -244,8 +285,8 @@ struct Walk {
       h = 0;
       ++b;
       load();
-    } else if (!kWeigh) {
-      it = item_of<kWeigh>(A, n, nd, acc, rb);
+    } else if (!S::Weigh) {
+      it = item_of<S::Weigh>(A, n, nd, acc, rb);
     }
   }
 };
@@ -258,7 +299,7 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
   const int each = (A.B + S::Threads - 1) / S::Threads;
   const int b0 = tid * each, b1 = b0 + each < A.B ? b0 + each : A.B;
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (int64_t)request_tiles<S::Weigh>(A, b) * A.Hkv;
+  for (int b = b0; b < b1; ++b) mine += request_cost<S>(A, b) * A.Hkv;
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -273,7 +314,9 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
     total += scratch[q];
   }
   incl += before;
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  // (a range of TileCost units or more holds a tile of any item that spans it)
+  int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  if (per < S::TileCost) per = S::TileCost;
   const int64_t from = per * blockIdx.x;
   if (tid == 0) {
     s->flat = from;
@@ -283,23 +326,23 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
   if (from < total && incl - mine <= from && from < incl) {
     int64_t at = incl - mine;
     int b = b0;
-    int64_t t = (int64_t)request_tiles<S::Weigh>(A, b) * A.Hkv;
+    int64_t t = request_cost<S>(A, b) * A.Hkv;
     while (at + t <= from) {
       at += t;
       ++b;
-      t = (int64_t)request_tiles<S::Weigh>(A, b) * A.Hkv;
+      t = request_cost<S>(A, b) * A.Hkv;
     }
     const int64_t per_head = t / A.Hkv;
     s->b = b;
     s->h = (int)((from - at) / per_head);
-    int off = (int)((from - at) % per_head);
+    int64_t off = (from - at) % per_head;
     int rb = 0;
     if (!S::Weigh) {
       const int n = load_n(A, b), nd = load_nd(A, b);
-      int tiles = item_of<false>(A, n, nd, 0, 0).tiles;
-      while (off >= tiles) {
-        off -= tiles;
-        tiles = item_of<false>(A, n, nd, 0, ++rb).tiles;
+      int64_t cost = item_of<false>(A, n, nd, 0, 0).template cost<S>();
+      while (off >= cost) {
+        off -= cost;
+        cost = item_of<false>(A, n, nd, 0, ++rb).template cost<S>();
       }
     }
     s->rb = rb;
@@ -313,26 +356,28 @@ template <class S>
 struct TileShared {
   uint64_t full[S::NU], empty[S::NU];
   uint64_t q_full[S::NQ], q_empty[S::NQ];
-  uint64_t s_full[2], s_empty[2];
-  uint64_t p_full, pv_done;
+  uint64_t s_full[S::Teams][2], s_empty[S::Teams][2];
+  uint64_t p_full[S::Teams][S::NP], pv_done[S::Teams][S::NP];
+  uint64_t o_done[2];  // a piece has its last product, by ordinal % 2
   uint32_t tmem;
   int dead;
-  int bad_piece[4];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 4
+  int bad_piece[8];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 8
   int issued[S::NU]; // passes whose copies into the unit were started
   int q_issued[S::NQ];
   uint64_t drain;
-  int last_arrival;
   int64_t scratch[16];
   Start start;
-  alignas(16) float m[S::N];       // running maximum; in the key weights the row's lse (log2)
-  alignas(16) float slope[S::N];   // log2(e) * slope
-  alignas(16) float ahead[S::N];   // the column's position less the block's first
-  alignas(16) float alpha[S::N];
-  alignas(16) float red[4][S::N];  // per-warp maxima or sums
-  int hi[S::N], lo[S::N];          // the column sees keys j with lo < j <= hi
-  int row[S::N];                   // output row of the column, from the item's first
-  unsigned int odd_keys;           // partly visible keys whose values are not finite
-  int odd_first;
+  struct Table {
+    alignas(16) float m[S::N];       // running maximum; in the key weights the row's lse (log2)
+    alignas(16) float slope[S::N];   // log2(e) * slope
+    alignas(16) float ahead[S::N];   // the column's position less the block's first
+    alignas(16) float alpha[S::N];
+    alignas(16) float red[4][S::N];  // per-warp maxima or sums
+    int hi[S::N], lo[S::N];          // the column sees keys j with lo < j <= hi
+    int row[S::N];                   // output row of the column, from the item's first
+    unsigned int odd_keys;           // partly visible keys whose values are not finite
+  } table[2];                        // by ordinal % 2 (with two teams: one each)
+  JoinItem join;
 };
 
 // Position of tensor `idx` (in ring order) in the ring.
@@ -352,6 +397,13 @@ __device__ __forceinline__ int k_unit(int x) {
 template <class S>
 __device__ __forceinline__ int v_unit(int x) {
   return (2 * x + 2) * S::U;
+}
+
+// The i-th tile a piece walks: the attention goes from the newest keys to the oldest, so that
+// a bias by distance (or plain recency) puts the maximum into the first tile.
+template <class S>
+__device__ __forceinline__ int tile_at(const Piece& p, int i) {
+  return S::Weigh ? p.ma + i : p.mb - 1 - i;
 }
 
 // ---- the copying warp -----------------------------------------------------------------------
@@ -403,7 +455,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
                                           const CUtensorMap* mv) {
   const int lane = threadIdx.x & 31;
   Loader<S> L{A, sh, ring, lane};
-  Walk<S::Weigh> w(A, sh.start);
+  Walk<S> w(A, sh.start);
   Piece p, prev{};
   int x = 0, ordinal = 0, prev_tile = 0, prev_page = 0;
   while (w.next(p)) {
@@ -420,11 +472,12 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
                    p.it.i0, p.b);
       }
       __syncwarp();
-      int page = L.page_of(p, p.ma);
-      for (int t = p.ma; t < p.mb; ++t) {
-        const int next_page = t + 1 < p.mb ? L.page_of(p, t + 1) : -1;
+      int page = L.page_of(p, tile_at<S>(p, 0));
+      for (int i = 0; i < p.mb - p.ma; ++i) {
+        const int t = tile_at<S>(p, i);
+        const int next_page = i + 1 < p.mb - p.ma ? L.page_of(p, tile_at<S>(p, i + 1)) : -1;
         if (__any_sync(0xffffffffu, page == -2) && lane == 0)
-          *(volatile int*)&sh.bad_piece[ordinal & 3] = ordinal + 1;
+          *(volatile int*)&sh.bad_piece[ordinal & 7] = ordinal + 1;
         __syncwarp();
         L.load(mk, p, t, page, k_unit<S>(x));
         if (!S::Weigh) {
@@ -461,8 +514,8 @@ struct Issuer {
 
   __device__ __forceinline__ bool dead() const { return *(volatile int*)&sh.dead != 0; }
 
-  // S^T of the tile whose keys start at ring unit `unit`, into S buffer `buf`.
-  __device__ __forceinline__ void scores(int unit, int qs, int buf) const {
+  // S^T of the tile whose keys start at ring unit `unit`, into a team's score buffer `buf`.
+  __device__ __forceinline__ void scores(int unit, int qs, int team, int buf) const {
 #pragma unroll
     for (int c = 0; c < S::U; ++c) {
       const int s = unit_slot<S>(unit + c);
@@ -473,20 +526,23 @@ struct Issuer {
       const uint32_t b0 = q_addr + qs * S::QBytes + c * S::N * 128;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        mma_f16(tmem + buf * S::N, smem_desc(a0 + 32 * k, 16, 1024, kSwizzle128),
+        mma_f16(tmem + (2 * team + buf) * S::N, smem_desc(a0 + 32 * k, 16, 1024, kSwizzle128),
                 smem_desc(b0 + 32 * k, 16, 1024, kSwizzle128), qk_desc, c > 0 || k > 0);
       mma_commit(&sh.empty[s]);
     }
-    if (!dead()) mma_commit(&sh.s_full[buf]);
+    if (!dead()) mma_commit(&sh.s_full[team][buf]);
   }
-  // O^T (+)= V^T P^T of the y-th tile.
-  __device__ __forceinline__ void values(int y, bool first) const {
-    wait_phase(&sh.p_full, (uint32_t)y & 1u, &sh.dead);
+  // O^T (+)= V^T P^T of the x-th tile, the y-th of its team.
+  __device__ __forceinline__ void values(int x, int y, bool first, bool last, int ordinal) const {
+    const int team = ordinal % S::Teams, ob = ordinal & 1;
+    const int pb = y % S::NP;
+    const uint32_t p_at = p_addr + (team * S::NP + pb) * S::PBytes;
+    wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.dead);
     tc_fence_after();
     constexpr int kPer = S::U >= 2 ? 2 : 1;  // units per accumulator
 #pragma unroll
     for (int m = 0; m < S::MBlocks; ++m) {
-      const int unit = v_unit<S>(y) + m * kPer;
+      const int unit = v_unit<S>(x) + m * kPer;
       const int s = unit_slot<S>(unit);
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
@@ -501,15 +557,18 @@ struct Issuer {
         for (int k = 0; k < kTileKeys / 16; ++k)
           // values of 64 columns lie 128 bytes per key; with D = 64 both halves of the
           // instruction's rows read the same columns, and the upper half is not used
-          mma_f16(tmem + (2 + m) * S::N,
+          mma_f16(tmem + (2 * S::Teams + ob * S::MBlocks + m) * S::N,
                   smem_desc(a0 + k * 2048, kPer == 2 ? kUnitBytes : 0, 1024, kSwizzle128),
-                  smem_desc(p_addr + part * (kTileKeys * S::N * 2) + k * 512, kTileKeys * 32, 256,
+                  smem_desc(p_at + part * (kTileKeys * S::N * 2) + k * 512, kTileKeys * 32, 256,
                             kSwizzle32),
                   pv_desc, !(first && part == 0 && k == 0));
 #pragma unroll
       for (int c = 0; c < kPer; ++c) mma_commit(&sh.empty[unit_slot<S>(unit + c)]);
     }
-    if (!dead()) mma_commit(&sh.pv_done);
+    if (!dead()) {
+      mma_commit(&sh.pv_done[team][pb]);
+      if (last) mma_commit(&sh.o_done[ob]);
+    }
   }
 };
 
@@ -519,32 +578,38 @@ __device__ __forceinline__ void issue_role(const TileArgs& A, TileShared<S>& sh,
                                            unsigned char* ring) {
   Issuer<S> I{A, sh, smem_u32(qbuf), smem_u32(pbuf), smem_u32(ring), sh.tmem,
               mma_desc(A.bf16, false, false, 128, S::N), mma_desc(A.bf16, true, true, 128, S::N)};
-  Walk<S::Weigh> w(A, sh.start);
+  Walk<S> w(A, sh.start);
   Piece p;
+  // used: tiles so far per team (attention) or per score buffer (key weights)
   int x = 0, ordinal = 0, used[2] = {0, 0};
-  bool prev_first = false;
+  bool prev_first = false, prev_last = false;
+  int prev_ordinal = 0, prev_y = 0;
   while (w.next(p)) {
     for (int rb = 0; S::Weigh ? weigh_pass(A, p, rb) : rb == 0; ++rb) {
       if (p.mb <= p.ma) continue;
-      const int qs = ordinal % S::NQ;
+      const int qs = ordinal % S::NQ, team = ordinal % S::Teams;
       wait_phase(&sh.q_full[qs], (uint32_t)(ordinal / S::NQ) & 1u, &sh.dead);
-      for (int t = p.ma; t < p.mb; ++t) {
-        const int buf = (S::Weigh ? t : x) & 1;
-        const int c = buf ? used[1]++ : used[0]++;
-        if (c > 0) wait_phase(&sh.s_empty[buf], (uint32_t)(c - 1) & 1u, &sh.dead);
+      for (int i = 0; i < p.mb - p.ma; ++i) {
+        const int of = S::Weigh ? tile_at<S>(p, i) & 1 : team;
+        const int y = of ? used[1]++ : used[0]++;
+        const int buf = S::Weigh ? of : y & 1, turn = S::Weigh ? y : y >> 1;
+        if (turn > 0) wait_phase(&sh.s_empty[team][buf], (uint32_t)(turn - 1) & 1u, &sh.dead);
         tc_fence_after();
-        I.scores(k_unit<S>(x), qs, buf);
-        if (t + 1 == p.mb && !I.dead()) mma_commit(&sh.q_empty[qs]);
+        I.scores(k_unit<S>(x), qs, team, buf);
+        if (i + 1 == p.mb - p.ma && !I.dead()) mma_commit(&sh.q_empty[qs]);
         if (!S::Weigh) {
-          if (x > 0) I.values(x - 1, prev_first);
-          prev_first = t == p.ma;
+          if (x > 0) I.values(x - 1, prev_y, prev_first, prev_last, prev_ordinal);
+          prev_first = i == 0;
+          prev_last = i + 1 == p.mb - p.ma;
+          prev_ordinal = ordinal;
+          prev_y = y;
         }
         ++x;
       }
       ++ordinal;
     }
   }
-  if (!S::Weigh && x > 0) I.values(x - 1, prev_first);
+  if (!S::Weigh && x > 0) I.values(x - 1, prev_y, prev_first, prev_last, prev_ordinal);
   if (I.dead()) {  // given up: no instruction may outlive the tensor memory
     mma_commit(&sh.drain);
     mbar_wait(&sh.drain, 0, kTileWaitNs);
@@ -619,18 +684,19 @@ __device__ __forceinline__ void apply_rule(float (&s)[kC], const ScoreRule& r, f
   }
 }
 
-// The tables of a piece's columns (all softmax threads; barriers around it are the caller's).
+// The tables of a piece's columns, by thread `me` of `all` (barriers around it are the caller's).
 template <class S>
-__device__ __forceinline__ void set_columns(const TileArgs& A, TileShared<S>& sh, const Piece& p) {
-  for (int c = threadIdx.x; c < S::N; c += S::SoftThreads) {
+__device__ __forceinline__ void set_columns(const TileArgs& A, typename TileShared<S>::Table& T,
+                                            const Piece& p, int me, int all) {
+  for (int c = me; c < S::N; c += all) {
     const int i = c / A.G, g = c - i * A.G;
     const bool live = i < p.it.live;
     const int pos = p.it.pos0 + i;
-    sh.slope[c] = live && A.rule.slopes ? __ldg(A.rule.slopes + p.h * A.G + g) * kLog2e : 0.0f;
-    sh.ahead[c] = (float)i;
-    sh.hi[c] = live ? pos : -1;
-    sh.lo[c] = pos - A.rule.window;
-    sh.row[c] = i * A.Hq + g;
+    T.slope[c] = live && A.rule.slopes ? __ldg(A.rule.slopes + p.h * A.G + g) * kLog2e : 0.0f;
+    T.ahead[c] = (float)i;
+    T.hi[c] = live ? pos : -1;
+    T.lo[c] = pos - A.rule.window;
+    T.row[c] = i * A.Hq + g;
     if (S::Weigh) {
       // a row that does not count, or one of no weight, gets none from any key
       float l = INFINITY;
@@ -639,79 +705,104 @@ __device__ __forceinline__ void set_columns(const TileArgs& A, TileShared<S>& sh
                               (p.h * A.G + g) * A.lse_head);
         if (v != -INFINITY) l = v * kLog2e;
       }
-      sh.m[c] = l;
+      T.m[c] = l;
     } else {
-      sh.m[c] = kNoMax;
+      T.m[c] = kNoMax;
     }
   }
 }
 
-__device__ __forceinline__ uint32_t pack16(bool bf16, float a, float b) {
-  if (bf16) {
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+  if (kBf16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ float2 unpack16(bool bf16, uint32_t w) {
-  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack16(uint32_t w) {
+  if (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
-__device__ __forceinline__ void store16(void* base, int64_t at, bool bf16, float x) {
-  if (bf16)
-    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(x);
-  else
-    static_cast<__half*>(base)[at] = __float2half_rn(x);
+template <bool kBf16>
+__device__ __forceinline__ void store16(void* base, int64_t at, float x) {
+  static_cast<uint16_t*>(base)[at] = (uint16_t)pack16<kBf16>(x, 0.0f);
 }
-__device__ __forceinline__ bool not_finite16(bool bf16, uint32_t x) {
-  const uint32_t m = bf16 ? 0x7f80u : 0x7c00u;
-  return (x & m) == m;
+// Nonzero where one of two 16-bit values is infinite or NaN: its exponent field carries into
+// the sign's place.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+  return kBf16 ? ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u
+               : ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
-constexpr int kAllBar = 3;  // named barriers: 1 and 2 for the groups, 3 for all softmax threads
+// Named barriers: 1 and 2 for the two groups of softmax warps, 3 for all of them.
+constexpr int kAllBar = 3;
+
+struct ValuePool {
+  const void* data;
+  int64_t page, token, head;
+};
 
 // ---- attention --------------------------------------------------------------------------------
 // What one softmax thread does for the attention: its key of every tile, its share of O.
 template <class S>
 struct Attend {
+  using Table = typename TileShared<S>::Table;
   const TileArgs& A;
+  const ValuePool& vpool;
   TileShared<S>& sh;
   unsigned char *pbuf, *ring;
   int lane, quarter, group, key;
   uint32_t lane_base;  // tensor-memory address of the thread's lanes
+  int team, me;        // the team, the thread's index in it
   int col0;            // the group's first column
 
+  // Wait until the products of the team's tile y have read P and are in O.
+  __device__ __forceinline__ void wait_values(int y) const {
+    wait_phase(&sh.pv_done[team][y % S::NP], (uint32_t)(y / S::NP) & 1u, &sh.dead);
+  }
   __device__ __forceinline__ void group_sync() const { bar_sync(1 + group, 128); }
+  __device__ __forceinline__ void team_sync() const {
+    bar_sync(S::Teams == 2 ? 1 + group : kAllBar, S::TeamThreads);
+  }
+  // The accumulator of a piece, the group's first column.
+  __device__ __forceinline__ uint32_t output(int ordinal) const {
+    return lane_base + (2 * S::Teams + (ordinal & 1) * S::MBlocks) * S::N + col0;
+  }
 
-  // Raise the columns' maxima to those of this tile's scores s, and scale what they hold.
-  __device__ __forceinline__ void raise(const float (&s)[S::NC], float (&l)[S::NC], bool first) {
-    column_reduce<S::NC, true>(s, &sh.red[quarter][col0], lane);
+  // Raise the maxima of the CH columns from c0 to those of this tile's scores s, and scale what
+  // those columns hold.
+  __device__ __forceinline__ void raise(Table& T, const float (&s)[S::CH], float (&l)[S::NC], int k,
+                                        bool first, uint32_t o_base) {
+    const int c0 = col0 + k;
+    column_reduce<S::CH, true>(s, &T.red[quarter][c0], lane);
     group_sync();
-    if (quarter == 0) {
-      for (int c = col0 + lane; c < col0 + S::NC; c += 32) {
-        const float was = sh.m[c];
-        const float m = fmaxf(fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]),
-                                    fmaxf(sh.red[2][c], sh.red[3][c])), was);
-        sh.alpha[c] = ex2(was - m);
-        sh.m[c] = m;
-      }
+    if (quarter == 0 && lane < S::CH) {
+      const int c = c0 + lane;
+      const float was = T.m[c];
+      const float m =
+          fmaxf(fmaxf(fmaxf(T.red[0][c], T.red[1][c]), fmaxf(T.red[2][c], T.red[3][c])), was);
+      T.alpha[c] = ex2(was - m);
+      T.m[c] = m;
     }
     group_sync();
-#pragma unroll
-    for (int c = 0; c < S::NC; ++c) l[c] *= sh.alpha[col0 + c];
     if (first) return;
+#pragma unroll
+    for (int c = 0; c < S::CH; ++c) l[k + c] *= T.alpha[c0 + c];
     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
     for (int m = 0; m < S::MBlocks; ++m)
-#pragma unroll
-      for (int q = 0; q < S::NC; q += 16) {
+#pragma unroll 1
+      for (int q = 0; q < S::CH; q += 16) {
         float o[16];
-        const uint32_t at = lane_base + (2 + m) * S::N + col0 + q;
+        const uint32_t at = o_base + m * S::N + k + q;
         tmem_ld16(at, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] *= sh.alpha[col0 + q + c];
+        for (int c = 0; c < 16; ++c) o[c] *= T.alpha[c0 + q + c];
         tmem_st16(at, o);
       }
     tmem_wait_st();
@@ -720,276 +811,286 @@ struct Attend {
   // Values of keys that some row of a tile does not see: what no row sees becomes 0; of a key
   // that only some rows see, the values that are not finite become 0 and are added to the rows
   // that see it at the end (0 times infinity would reach the others).
-  __device__ __forceinline__ void clean_values(const Piece& p, int x, int j, int first_full) {
-    const int unit = v_unit<S>(x);
-#pragma unroll
-    for (int c = 0; c < S::U; ++c)
-      wait_phase(&sh.full[unit_slot<S>(unit + c)], unit_pass<S>(unit + c) & 1u, &sh.dead);
+  __device__ __forceinline__ void clean_values(Table& T, const Piece& p, int x, int j,
+                                               int first_full) {
     const bool none = j > p.it.last || j < p.it.first;
     const bool some = !none && (j > p.it.pos0 || j < first_full);
-    if (!none && !some) return;
-    bool odd = false;
+    if (!__any_sync(0xffffffffu, none || some)) return;
+    const int unit = v_unit<S>(x);
+    uint32_t odd = 0;
 #pragma unroll
     for (int c = 0; c < S::U; ++c) {
+      wait_phase(&sh.full[unit_slot<S>(unit + c)], unit_pass<S>(unit + c) & 1u, &sh.dead);
       uint4* row = reinterpret_cast<uint4*>(ring + unit_slot<S>(unit + c) * kUnitBytes + key * 128);
+      // (each lane starts with another 16 bytes of its row: no bank conflicts)
+      if (none) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (none) {
-          row[q] = make_uint4(0u, 0u, 0u, 0u);
-          continue;
-        }
-        uint4 v = row[q];
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-        bool hit = false;
+        for (int q = 0; q < 8; ++q) row[(q + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
+      } else if (some) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (not_finite16(A.bf16, w[e] & 0xffffu)) {
-            w[e] &= 0xffff0000u;
-            hit = true;
-          }
-          if (not_finite16(A.bf16, w[e] >> 16)) {
-            w[e] &= 0xffffu;
-            hit = true;
-          }
+        for (int q = 0; q < 8; ++q) {
+          const uint4 v = row[(q + lane) & 7];
+          odd |= not_finite2<S::Bf16>(v.x) | not_finite2<S::Bf16>(v.y) |
+                 not_finite2<S::Bf16>(v.z) | not_finite2<S::Bf16>(v.w);
         }
-        if (hit) row[q] = v;
-        odd |= hit;
       }
     }
-    if (odd) atomicOr(&sh.odd_keys, 1u << (j > p.it.pos0 ? j - p.it.pos0 - 1 : 16 + j - p.it.first));
+    if (odd) {
+      atomicOr(&T.odd_keys,
+               1u << (j > p.it.pos0 ? j - p.it.pos0 - 1 : 16 + j - p.it.first));
+#pragma unroll 1
+      for (int c = 0; c < S::U; ++c) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(ring + unit_slot<S>(unit + c) * kUnitBytes +
+                                                  key * 128);
+#pragma unroll 1
+        for (int e = 0; e < 32; ++e) {
+          const uint32_t bad = not_finite2<S::Bf16>(w[e]);
+          if (bad) w[e] &= ~((bad >> 15) * 0xffffu);
+        }
+      }
+    }
   }
 
-  // One tile: the scores of x, their weights into shared memory.
-  __device__ __forceinline__ void tile(const Piece& p, int t, int x, int first_full,
-                                       float (&l)[S::NC]) {
-    const int buf = x & 1, j = t * kTileKeys + key;
-    const bool first = t == p.ma;
-    float s[S::NC];
-    wait_phase(&sh.s_full[buf], (uint32_t)(x >> 1) & 1u, &sh.dead);
+  // One tile, the CTA's x-th and the team's y-th: its scores, their weights into shared memory.
+  __device__ __forceinline__ void tile(Table& T, const Piece& p, int t, bool first, int x, int y,
+                                       int ordinal, float (&l)[S::NC]) {
+    const int buf = y & 1, j = t * kTileKeys + key;
+    // keys from here on are inside every row's window
+    const int first_full = p.it.last - A.rule.window + 1;
+    const bool edge = t * kTileKeys < first_full || t * kTileKeys + kTileKeys - 1 > p.it.pos0;
+    wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.dead);
     tc_fence_after();
 #pragma unroll
-    for (int q = 0; q < S::NC; q += 16)
-      tmem_ld16(lane_base + buf * S::N + col0 + q, reinterpret_cast<float(&)[16]>(s[q]));
-    tmem_wait_ld();
-    tc_fence_before();
-    mbar_arrive(&sh.s_empty[buf]);
-    apply_rule<S::NC>(s, A.rule, (float)(p.it.pos0 - j), &sh.slope[col0], &sh.ahead[col0]);
-    const bool edge = t * kTileKeys < first_full || t * kTileKeys + kTileKeys - 1 > p.it.pos0;
-    if (edge) {
+    for (int k = 0; k < S::NC; k += S::CH) {
+      const int c0 = col0 + k;
+      float s[S::CH];
 #pragma unroll
-      for (int c = 0; c < S::NC; ++c)
-        if (j > sh.hi[col0 + c] || j <= sh.lo[col0 + c]) s[c] = -INFINITY;
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < S::NC; ++c) top = fmaxf(top, s[c] - sh.m[col0 + c]);
-    bool waited = first;  // the previous product of this piece has read P and written O
-    if (bar_or(1 + group, 128, top > 8.0f)) {
-      if (!waited) wait_phase(&sh.pv_done, (uint32_t)(x - 1) & 1u, &sh.dead);
-      waited = true;
-      raise(s, l, first);
-    }
-    if (!waited) wait_phase(&sh.pv_done, (uint32_t)(x - 1) & 1u, &sh.dead);
-#pragma unroll
-    for (int q = 0; q < S::NC; q += 16) {
-      uint32_t hi[8], lo[8];
-#pragma unroll
-      for (int c = 0; c < 16; c += 2) {
-        const float a = ex2(s[q + c] - sh.m[col0 + q + c]);
-        const float b = ex2(s[q + c + 1] - sh.m[col0 + q + c + 1]);
-        l[q + c] += a;
-        l[q + c + 1] += b;
-        hi[c / 2] = pack16(A.bf16, a, b);
-        const float2 h = unpack16(A.bf16, hi[c / 2]);
-        lo[c / 2] = pack16(A.bf16, a - h.x, b - h.y);
+      for (int q = 0; q < S::CH; q += 16)
+        tmem_ld16(lane_base + (2 * team + buf) * S::N + c0 + q,
+                  reinterpret_cast<float(&)[16]>(s[q]));
+      tmem_wait_ld();
+      if (k + S::CH == S::NC) {
+        tc_fence_before();
+        mbar_arrive(&sh.s_empty[team][buf]);
       }
-      // 16 columns of a key: 32 bytes, their 16-byte halves swapped in every other 4 keys
-      unsigned char* at = pbuf + (col0 + q) / 16 * (kTileKeys * 32) + key * 32;
-      const int sw = ((key >> 2) & 1) * 16;
-      *reinterpret_cast<uint4*>(at + sw) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(at + (16 - sw)) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-      at += kTileKeys * S::N * 2;
-      *reinterpret_cast<uint4*>(at + sw) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      *reinterpret_cast<uint4*>(at + (16 - sw)) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+      apply_rule<S::CH>(s, A.rule, (float)(p.it.pos0 - j), &T.slope[c0], &T.ahead[c0]);
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c)
+          if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[c] = -INFINITY;
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < S::CH; ++c) top = fmaxf(top, s[c] - T.m[c0 + c]);
+      if (bar_or(1 + group, 128, top > 8.0f)) {
+        if (!first) wait_values(y - 1);
+        raise(T, s, l, k, first, output(ordinal));
+      }
+      uint32_t hi[S::CH / 2], lo[S::CH / 2];
+#pragma unroll
+      for (int c = 0; c < S::CH; c += 2) {
+        const float a = ex2(s[c] - T.m[c0 + c]), b = ex2(s[c + 1] - T.m[c0 + c + 1]);
+        l[k + c] += a;
+        l[k + c + 1] += b;
+        hi[c / 2] = pack16<S::Bf16>(a, b);
+        const float2 h = unpack16<S::Bf16>(hi[c / 2]);
+        lo[c / 2] = pack16<S::Bf16>(a - h.x, b - h.y);
+      }
+      // the product that last read this buffer
+      if (k == 0 && y >= S::NP) wait_values(y - S::NP);
+#pragma unroll
+      for (int q = 0; q < S::CH; q += 16) {
+        // 16 columns of a key: 32 bytes, their 16-byte halves swapped in every other 4 keys
+        unsigned char* at = pbuf + (team * S::NP + y % S::NP) * S::PBytes +
+                            (c0 + q) / 16 * (kTileKeys * 32) + key * 32;
+        const int sw = ((key >> 2) & 1) * 16, w = q / 2;
+        *reinterpret_cast<uint4*>(at + sw) = make_uint4(hi[w], hi[w + 1], hi[w + 2], hi[w + 3]);
+        *reinterpret_cast<uint4*>(at + (16 - sw)) =
+            make_uint4(hi[w + 4], hi[w + 5], hi[w + 6], hi[w + 7]);
+        at += kTileKeys * S::N * 2;
+        *reinterpret_cast<uint4*>(at + sw) = make_uint4(lo[w], lo[w + 1], lo[w + 2], lo[w + 3]);
+        *reinterpret_cast<uint4*>(at + (16 - sw)) =
+            make_uint4(lo[w + 4], lo[w + 5], lo[w + 6], lo[w + 7]);
+      }
     }
-    if (edge && group == 0) clean_values(p, x, j, first_full);
+    if (edge && (S::Teams == 2 || group == 0)) clean_values(T, p, x, j, first_full);
     fence_proxy_async();
     tc_fence_before();
-    mbar_arrive(&sh.p_full);
+    mbar_arrive(&sh.p_full[team][y % S::NP]);
+  }
+
+  // Output row of a piece's first column.
+  __device__ __forceinline__ int64_t first_row(const Piece& p) const {
+    return ((int64_t)p.b * A.P + p.it.i0) * A.Hq + p.h * A.G;
   }
 
   // Rows without a visible key, or of a request with bad counts.
-  __device__ __forceinline__ void fill(const Piece& p) const {
-    const int64_t row0 = ((int64_t)p.b * A.P + p.it.i0) * A.Hq + p.h * A.G;
+  __device__ __forceinline__ void fill(const Table& T, const Piece& p) const {
+    const int64_t row0 = first_row(p);
     const float v = p.it.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
     const int rows = p.it.live * A.G;
-    for (int e = threadIdx.x; e < rows * S::D; e += S::SoftThreads)
-      store16(A.out, (row0 + sh.row[e / S::D]) * S::D + e % S::D, A.bf16, v);
+    for (int e = me; e < rows * S::D; e += S::TeamThreads)
+      store16<S::Bf16>(A.out, (row0 + T.row[e / S::D]) * S::D + e % S::D, v);
     if (A.out_lse)
-      for (int c = threadIdx.x; c < rows; c += S::SoftThreads)
-        A.out_lse[row0 + sh.row[c]] = p.it.bad ? v : -INFINITY;
+      for (int c = me; c < rows; c += S::TeamThreads)
+        A.out_lse[row0 + T.row[c]] = p.it.bad ? v : -INFINITY;
   }
 
-  __device__ __forceinline__ float* slot(int64_t i) const {
-    return A.part + i * (S::N * (S::D + 2));
-  }
-
-  // The end of a piece: O and the sums leave for the output or for the workspace.
-  __device__ __forceinline__ void finish(const Piece& p, int x, int ordinal, float (&l)[S::NC]) {
-    wait_phase(&sh.pv_done, (uint32_t)x & 1u, &sh.dead);
-    tc_fence_after();
-    column_reduce<S::NC, false>(l, &sh.red[quarter][col0], lane);
+  // The end of a piece (its sums' warp parts are in T.red): O and the sums leave for the output
+  // or for the workspace.
+  __device__ __forceinline__ void finish(Table& T, const Piece& p, int ordinal) {
     group_sync();
     const bool poison = *(volatile int*)&sh.dead ||
-                        *(volatile int*)&sh.bad_piece[ordinal & 3] == ordinal + 1;
+                        *(volatile int*)&sh.bad_piece[ordinal & 7] == ordinal + 1;
     const bool whole = p.starts && p.ends;
     const int rows = p.it.live * A.G;
-    const int64_t row0 = ((int64_t)p.b * A.P + p.it.i0) * A.Hq + p.h * A.G;
-    float* part = slot(2 * (int64_t)blockIdx.x + (p.starts ? 1 : 0));
+    const int64_t row0 = first_row(p);
+    float* part =
+        A.part + (2 * (int64_t)blockIdx.x + (p.starts ? 1 : 0)) * (S::N * (S::D + 2));
     if (quarter == 0) {
       for (int c = col0 + lane; c < col0 + S::NC; c += 32) {
-        float sum = (sh.red[0][c] + sh.red[1][c]) + (sh.red[2][c] + sh.red[3][c]);
+        float sum = (T.red[0][c] + T.red[1][c]) + (T.red[2][c] + T.red[3][c]);
         if (poison) sum = __uint_as_float(0x7fc00000u);
-        const float m = sh.m[c];
+        const float m = T.m[c];
         if (c < rows) {
-          if (whole) {
-            if (A.out_lse)
-              A.out_lse[row0 + sh.row[c]] =
-                  sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
-          } else {
+          if (!whole)
             *reinterpret_cast<float2*>(part + S::N * S::D + 2 * c) = make_float2(m, sum);
-          }
+          else if (A.out_lse)
+            A.out_lse[row0 + T.row[c]] =
+                sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
         }
-        sh.alpha[c] = sum == 0.0f ? 0.0f : 1.0f / sum;
+        T.alpha[c] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
       }
+    }
+    if (me == 0 && p.starts && !whole) {
+      const int64_t at = p.item0 + S::PieceCost, per = sh.start.per;
+      sh.join.pieces =
+          (int)((at + (int64_t)(p.it.tiles - 1) * S::TileCost) / per - at / per) + 1;
+      sh.join.row0 = row0;
+      sh.join.rows = rows;
     }
     group_sync();
-    const unsigned int odd = *(volatile unsigned int*)&sh.odd_keys;
+    wait_phase(&sh.o_done[ordinal & 1], (uint32_t)(ordinal >> 1) & 1u, &sh.dead);
+    tc_fence_after();
     if (S::D >= 128 || quarter < 2) {
-#pragma unroll
-      for (int m = 0; m < S::MBlocks; ++m) {
-        const int d = m * 128 + quarter * 32 + lane;
-#pragma unroll
-        for (int q = 0; q < S::NC; q += 16) {
+      int d = quarter * 32 + lane;
+#pragma unroll 1
+      for (int m = 0; m < S::MBlocks; ++m, d += 128)
+#pragma unroll 1
+        for (int q = 0; q < S::NC && col0 + q < rows; q += 16) {
           float o[16];
-          tmem_ld16(lane_base + (2 + m) * S::N + col0 + q, o);
+          tmem_ld16(output(ordinal) + m * S::N + q, o);
           tmem_wait_ld();
-          if (odd) add_odd(p, odd, d, col0 + q, o);
+          const int n0 = col0 + q;
+          if (whole) {
+            uint16_t* out = static_cast<uint16_t*>(A.out) + row0 * S::D + d;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int n = col0 + q + c;
-            if (n < rows) {
-              if (whole)
-                store16(A.out, (row0 + sh.row[n]) * S::D + d, A.bf16, o[c] * sh.alpha[n]);
-              else
-                part[n * S::D + d] = o[c];
+            for (int c = 0; c < 16; c += 2) {
+              const uint32_t w =
+                  pack16<S::Bf16>(o[c] * T.alpha[n0 + c], o[c + 1] * T.alpha[n0 + c + 1]);
+              if (n0 + c < rows) out[T.row[n0 + c] * S::D] = (uint16_t)w;
+              if (n0 + c + 1 < rows) out[T.row[n0 + c + 1] * S::D] = (uint16_t)(w >> 16);
             }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              if (n0 + c < rows) part[(n0 + c) * S::D + d] = o[c];
           }
         }
-      }
+      const unsigned int odd = *(volatile unsigned int*)&T.odd_keys;
+      if (odd && !poison) add_odd(T, p, odd, whole ? nullptr : part, row0, rows);
     }
     tc_fence_before();
-    if (!whole) join(p, rows, row0);
   }
 
-  __device__ __forceinline__ void add_odd(const Piece& p, unsigned int odd, int d, int n0,
-                                          float (&o)[16]) const {
-    while (odd) {
-      const int bit = __ffs(odd) - 1;
-      odd &= odd - 1;
-      const int j = bit < 16 ? p.it.pos0 + 1 + bit : p.it.first + bit - 16;
-      const float v = odd_value(p, j, d);
-      if (isfinite(v)) continue;
-#pragma unroll
-      for (int c = 0; c < 16; ++c)
-        if (j <= sh.hi[n0 + c] && j > sh.lo[n0 + c]) o[c] += v;
-    }
-  }
-  const void* v_data;
-  int64_t vp, vt, vh;
-  __device__ __forceinline__ float odd_value(const Piece& p, int j, int d) const {
-    const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
-    if (page < 0 || page >= A.num_pages) return 0.0f;
-    const int64_t at = page * vp + (j & ((1 << A.log_page) - 1)) * vt + p.h * vh + d;
-    return A.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(v_data)[at])
-                  : __half2float(static_cast<const __half*>(v_data)[at]);
-  }
-
-  // Count this piece in; the CTA that brings an item's last piece joins them, in order.
-  __device__ __forceinline__ void join(const Piece& p, int rows, int64_t row0) {
-    const int64_t per = sh.start.per;
-    const int64_t c0 = p.item0 / per, c1 = (p.item0 + p.it.tiles - 1) / per;
-    __threadfence();
-    bar_sync(kAllBar, S::SoftThreads);
-    if (threadIdx.x == 0) {
-      // the counters are cleared by the launch ahead of this one
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      sh.last_arrival = arrive_last(A.counters + c0, (unsigned int)(c1 - c0 + 1));
-    }
-    bar_sync(kAllBar, S::SoftThreads);
-    if (!sh.last_arrival) return;
-    __threadfence();
-    const int np = (int)(c1 - c0 + 1);
-    auto slot_of = [&](int i) { return slot(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)); };
-    constexpr int kV = S::D / 32;  // of D per lane
-    for (int n = threadIdx.x >> 5; n < rows; n += S::SoftWarps) {
-      float m = kNoMax;
-      for (int i = lane; i < np; i += 32)
-        m = fmaxf(m, __ldcg(slot_of(i) + S::N * S::D + 2 * n));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float sum = 0.0f;
-      for (int i = lane; i < np; i += 32) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(slot_of(i) + S::N * S::D + 2 * n));
-        sum += ex2(ml.x - m) * ml.y;
+  // The values that are not finite of keys only some rows see: what such a row's sum is then.
+  __device__ __forceinline__ void add_odd(const Table& T, const Piece& p, unsigned int odd,
+                                          float* part, int64_t row0, int rows) const {
+#pragma unroll 1
+    for (int d = quarter * 32 + lane; d < S::D; d += 128)
+#pragma unroll 1
+      for (int n = col0; n < col0 + S::NC && n < rows; ++n) {
+        float sum = 0.0f;
+#pragma unroll 1
+        for (unsigned int left = odd; left; left &= left - 1) {
+          const int bit = __ffs(left) - 1;
+          const int j = bit < 16 ? p.it.pos0 + 1 + bit : p.it.first + bit - 16;
+          if (j > T.hi[n] || j <= T.lo[n]) continue;
+          const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
+          if (page < 0 || page >= A.num_pages) continue;
+          const int64_t at = page * vpool.page + (j & ((1 << A.log_page) - 1)) * vpool.token +
+                             p.h * vpool.head + d;
+          const float v = unpack16<S::Bf16>(static_cast<const uint16_t*>(vpool.data)[at]).x;
+          if (!isfinite(v)) sum += v;
+        }
+        if (isfinite(sum)) continue;
+        if (part)
+          part[n * S::D + d] = sum;
+        else
+          store16<S::Bf16>(A.out, (row0 + T.row[n]) * S::D + d, sum);
       }
+  }
+
+  // The pieces in turn. With one team the end of a piece waits until the first tile of the next
+  // one is in the tensor cores' hands, so that its last product, and its output, pass under that
+  // tile; with two the other team's tiles cover it.
+  __device__ __forceinline__ void run() {
+    Walk<S> w(A, sh.start);
+    Piece p, ended;
+    int x = 0, y = 0, ordinal = -1, next = 0, fills = 0, ended_ordinal = 0;
+    int i = 0, tiles = 0;
+    bool pending = false;
+    float l[S::NC];
+    for (;;) {
+      const bool flush = S::Teams == 2 && pending;  // the end first
+      bool more = true;
+      if (!flush) {
+        if (i == tiles) {
+          for (;;) {
+            more = w.next(p);
+            if (!more) break;
+            i = 0;
+            tiles = p.mb - p.ma;
+            const int turn = tiles > 0 ? next++ : fills++;
+            if (turn % S::Teams != team) {
+              x += tiles;
+              continue;
+            }
+            // (a piece without tiles borrows the table of the next one with tiles)
+            Table& T = sh.table[S::Teams == 2 ? team : ((tiles > 0 ? turn : next) + 1) & 1];
+            team_sync();  // the last piece with this table is out of it
+            set_columns<S>(A, T, p, me, S::TeamThreads);
+            if (me == 0) T.odd_keys = 0;
+            team_sync();
+            if (tiles > 0) {
+              ordinal = turn;
+              break;
+            }
+            fill(T, p);
+          }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      float acc[kV];
-#pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-      for (int i = 0; i < np; ++i) {
-        const float* s = slot_of(i);
-        const float w = ex2(__ldcg(s + S::N * S::D + 2 * n) - m);
-#pragma unroll
-        for (int e = 0; e < kV; e += 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(s + n * S::D + e * 32 + 2 * lane));
-          acc[e] = fmaf(w, v.x, acc[e]);
-          acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+          for (int c = 0; c < S::NC; ++c) l[c] = 0.0f;
+        }
+        if (more) {
+          tile(sh.table[S::Teams == 2 ? team : (ordinal + 1) & 1], p, tile_at<S>(p, i), i == 0, x,
+               y, ordinal, l);
+          ++i;
+          ++x;
+          ++y;
         }
       }
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int64_t at = (row0 + sh.row[n]) * S::D;
-#pragma unroll
-      for (int e = 0; e < kV; e += 2)
-        *reinterpret_cast<uint32_t*>(static_cast<char*>(A.out) + 2 * (at + e * 32 + 2 * lane)) =
-            pack16(A.bf16, acc[e] * inv, acc[e + 1] * inv);
-      if (A.out_lse && lane == 0)
-        A.out_lse[row0 + sh.row[n]] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
-    }
-  }
-
-  __device__ __forceinline__ void run() {
-    Walk<false> w(A, sh.start);
-    Piece p;
-    int x = 0, ordinal = 0;
-    while (w.next(p)) {
-      bar_sync(kAllBar, S::SoftThreads);  // the last piece's tables have been read
-      set_columns<S>(A, sh, p);
-      if (threadIdx.x == 0) sh.odd_keys = 0;
-      bar_sync(kAllBar, S::SoftThreads);
-      if (p.mb <= p.ma) {
-        fill(p);
-        continue;
+      if (pending) {
+        finish(sh.table[S::Teams == 2 ? team : (ended_ordinal + 1) & 1], ended, ended_ordinal);
+        pending = false;
       }
-      float l[S::NC];
-#pragma unroll
-      for (int c = 0; c < S::NC; ++c) l[c] = 0.0f;
-      // keys from here on are inside every row's window
-      const int first_full = p.it.last - A.rule.window + 1;
-      for (int t = p.ma; t < p.mb; ++t) tile(p, t, x++, first_full, l);
-      finish(p, x - 1, ordinal++, l);
+      if (!more) break;
+      if (!flush && i == tiles) {
+        Table& T = sh.table[S::Teams == 2 ? team : (ordinal + 1) & 1];
+        column_reduce<S::NC, false>(l, &T.red[quarter][col0], lane);
+        ended = p;
+        ended_ordinal = ordinal;
+        pending = true;
+      }
     }
   }
 };
@@ -1001,7 +1102,8 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
   const int key = quarter * 32 + lane;
   const uint32_t lane_base = sh.tmem + ((uint32_t)(quarter * 32) << 16);
   const float nan = __uint_as_float(0x7fc00000u);
-  Walk<true> w(A, sh.start);
+  auto& T = sh.table[0];
+  Walk<S> w(A, sh.start);
   Piece p;
   int used = 0;  // tiles this group has taken from its S buffer
   while (w.next(p)) {
@@ -1014,7 +1116,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
     }
     for (int rb = 0; weigh_pass(A, p, rb); ++rb) {
       bar_sync(kAllBar, S::SoftThreads);
-      set_columns<S>(A, sh, p);
+      set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
       bar_sync(kAllBar, S::SoftThreads);
       const int first_full = p.it.last - A.rule.window + 1;
       const int ta = rb == 0 ? p.ta : p.ma, tb = rb == 0 ? p.tb : p.mb;
@@ -1032,7 +1134,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
           }
           const bool edge =
               t * kTileKeys < first_full || t * kTileKeys + kTileKeys - 1 > p.it.pos0;
-          wait_phase(&sh.s_full[group], (uint32_t)used & 1u, &sh.dead);
+          wait_phase(&sh.s_full[0][group], (uint32_t)used & 1u, &sh.dead);
           ++used;
           tc_fence_after();
 #pragma unroll
@@ -1040,18 +1142,18 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
             float s[16];
             tmem_ld16(lane_base + group * S::N + q, s);
             tmem_wait_ld();
-            apply_rule<16>(s, A.rule, (float)(p.it.pos0 - j), &sh.slope[q], &sh.ahead[q]);
+            apply_rule<16>(s, A.rule, (float)(p.it.pos0 - j), &T.slope[q], &T.ahead[q]);
             float part = 0.0f;
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              float e = ex2(s[c] - sh.m[q + c]);
-              if (edge && (j > sh.hi[q + c] || j <= sh.lo[q + c])) e = 0.0f;
+              float e = ex2(s[c] - T.m[q + c]);
+              if (edge && (j > T.hi[q + c] || j <= T.lo[q + c])) e = 0.0f;
               part += e;
             }
             total += part;
           }
           tc_fence_before();
-          mbar_arrive(&sh.s_empty[group]);
+          mbar_arrive(&sh.s_empty[0][group]);
           if (bad || *(volatile int*)&sh.dead) total = nan;
         }
         if (inside) out[j] = before + total;
@@ -1061,11 +1163,6 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
 }
 
 // ---- the kernel ---------------------------------------------------------------------------------
-struct ValuePool {
-  const void* data;
-  int64_t page, token, head;
-};
-
 template <class S>
 __global__ void __launch_bounds__(S::Threads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -1073,15 +1170,14 @@ __global__ void __launch_bounds__(S::Threads, 1)
                 const __grid_constant__ ValuePool vpool) {
   extern __shared__ unsigned char tile_smem[];
   __shared__ TileShared<S> sh;
+  static_assert(S::Smem + sizeof(TileShared<S>) <= 232448, "shared memory");
   // operand tiles start on 1024-byte boundaries (the swizzle pattern's period)
   unsigned char* base = tile_smem + ((1024u - (smem_u32(tile_smem) & 1023u)) & 1023u);
   unsigned char* qbuf = base;
   unsigned char* pbuf = qbuf + S::NQ * S::QBytes;
-  unsigned char* ring = pbuf + S::PBytes;
+  unsigned char* ring = pbuf + S::Teams * S::NP * S::PBytes;
   const int tid = threadIdx.x, warp = tid >> 5;
 
-  find_start<S>(A, &sh.start, sh.scratch);
-  if (sh.start.left <= 0) return;
   if (tid == 0) {
     for (int s = 0; s < S::NU; ++s) {
       mbar_init(&sh.full[s], 1);
@@ -1093,18 +1189,30 @@ __global__ void __launch_bounds__(S::Threads, 1)
       mbar_init(&sh.q_empty[s], 1);
       sh.q_issued[s] = 0;
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&sh.s_full[s], 1);
-      mbar_init(&sh.s_empty[s], S::Weigh ? 128 : S::SoftThreads);
+    for (int t = 0; t < S::Teams; ++t) {
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&sh.s_full[t][s], 1);
+        mbar_init(&sh.s_empty[t][s], S::Weigh ? 128 : S::TeamThreads);
+      }
+      for (int s = 0; s < S::NP; ++s) {
+        mbar_init(&sh.p_full[t][s], S::TeamThreads);
+        mbar_init(&sh.pv_done[t][s], 1);
+      }
     }
-    mbar_init(&sh.p_full, S::SoftThreads);
-    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.o_done[0], 1);
+    mbar_init(&sh.o_done[1], 1);
     mbar_init(&sh.drain, 1);
     sh.dead = 0;
-    for (int i = 0; i < 4; ++i) sh.bad_piece[i] = 0;
+    sh.join.rows = 0;
+    for (int i = 0; i < 8; ++i) sh.bad_piece[i] = 0;
     fence_barrier_init();
   }
-  if (warp == 0) tmem_alloc(&sh.tmem, S::TmemCols);
+  if (tid == 32) {
+    prefetch_map(&mq);
+    prefetch_map(&mk);
+    if (!S::Weigh) prefetch_map(&mv);
+  }
+  if (warp == S::SoftWarps + 1) tmem_alloc(&sh.tmem, S::TmemCols);
   // columns past the query rows multiply zeros: the copies never write them
   {
     const int rows = A.G * A.pos_block;
@@ -1117,8 +1225,17 @@ __global__ void __launch_bounds__(S::Threads, 1)
     fence_proxy_async();
   }
   tc_fence_before();
-  __syncthreads();
+  find_start<S>(A, &sh.start, sh.scratch);
   tc_fence_after();
+  if (!S::Weigh) {
+    // the joining kernel may take its place beside this one; it waits for this one's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  }
+  if (sh.start.left <= 0) {
+    if (!S::Weigh && tid == 0) A.joins[blockIdx.x] = JoinItem{};
+    if (warp == S::SoftWarps + 1) tmem_free(sh.tmem, S::TmemCols);
+    return;
+  }
 
   if (warp == S::SoftWarps) {
     copy_role<S>(A, sh, qbuf, ring, &mq, &mk, &mv);
@@ -1129,15 +1246,82 @@ __global__ void __launch_bounds__(S::Threads, 1)
     weigh_role<S>(A, sh);
   } else {
     const int lane = tid & 31, quarter = warp & 3, group = warp >> 2;
-    Attend<S> R{A, sh, pbuf, ring, lane, quarter, group, quarter * 32 + lane,
-                sh.tmem + ((uint32_t)(quarter * 32) << 16), group * S::NC,
-                vpool.data, vpool.page, vpool.token, vpool.head};
+    const int team = S::Teams == 2 ? group : 0;
+    Attend<S> R{A, vpool, sh, pbuf, ring, lane, quarter, group, quarter * 32 + lane,
+                sh.tmem + ((uint32_t)(quarter * 32) << 16), team,
+                S::Teams == 2 ? tid & 127 : tid, S::Teams == 2 ? 0 : group * S::NC};
     R.run();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_free(sh.tmem, S::TmemCols);
+  if (!S::Weigh && tid == 0) A.joins[blockIdx.x] = sh.join;
+  if (warp == S::SoftWarps + 1) tmem_free(sh.tmem, S::TmemCols);
+}
+
+// ---- joining the pieces of split items --------------------------------------------------------
+// Block (c, q): the q-th share of the item that CTA c began and left to others. Its pieces are
+// the second slot of CTA c and the first slots of the CTAs after it, joined in that order.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinShares = 4;
+
+template <int kD, int kN, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_kernel(const JoinItem* joins, const float* part, int G, int Hq, void* out, float* out_lse) {
+  __shared__ float s_m[kN], s_inv[kN];
+  constexpr int64_t kSlot = kN * (kD + 2);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x;
+  const JoinItem J = joins[c];
+  if (J.rows == 0) return;
+  const float* s0 = part + (2 * c + 1) * kSlot;  // the first piece; the i-th is at s1 + 2 i slots
+  const float* s1 = part + 2 * c * kSlot;
+  auto at = [&](int i) { return i == 0 ? s0 : s1 + 2 * i * kSlot; };
+  for (int n = threadIdx.x; n < J.rows; n += kJoinThreads) {
+    float m = kNoMax, sum = 0.0f;
+    constexpr int kBatch = 8;
+#pragma unroll 1
+    for (int i0 = 0; i0 < J.pieces; i0 += kBatch) {
+      float2 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        v[i] = i0 + i < J.pieces
+                   ? *reinterpret_cast<const float2*>(at(i0 + i) + kN * kD + 2 * n)
+                   : make_float2(kNoMax, 0.0f);
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, v[i].x);
+      sum *= ex2(m - top);
+      m = top;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) sum += ex2(v[i].x - m) * v[i].y;
+    }
+    s_m[n] = m;
+    s_inv[n] = sum == 0.0f ? 0.0f : 1.0f / sum;
+    if (out_lse && blockIdx.y == 0)
+      out_lse[J.row0 + n / G * Hq + n % G] =
+          sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
+  }
+  __syncthreads();
+  for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < J.rows * (kD / 4);
+       e += kJoinShares * kJoinThreads) {
+    const int n = e / (kD / 4), d = e % (kD / 4) * 4;
+    const float m = s_m[n], inv = s_inv[n];
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int i = 0; i < J.pieces; ++i) {
+      const float* s = at(i);
+      const float4 v = *reinterpret_cast<const float4*>(s + n * kD + d);
+      const float w = ex2(s[kN * kD + 2 * n] - m);
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+    const int64_t row = J.row0 + n / G * Hq + n % G;
+    *reinterpret_cast<uint2*>(static_cast<char*>(out) + 2 * (row * kD + d)) =
+        make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
+  }
 }
 
 // ---- the host side ------------------------------------------------------------------------------
