@@ -148,7 +148,7 @@ sv_status launch_attention(const TileArgs& A, const CUtensorMap& mq, const CUten
   if (s != SV_OK) return s;
   // the join takes its place while the tiles are still walked, and waits for their end
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, kJoinShares);
+  cfg.gridDim = dim3(ctas, kJoinShares<D, N>);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];

@@ -28,10 +28,10 @@
 // pieces in order, so the result does not depend on the order of arrival. No CTA waits for
 // another one.
 //
-// Roles. One warp looks up pages and starts the tiled copies (a ring of 16 KiB units, 64
-// columns of 128 keys each, in the order K0 K1 V0 K2 V1 ...), one thread issues the matrix
-// instructions in the same order, 4 or 8 warps do the softmax and the outputs. S is double
-// buffered: the scores of tile t+1 are computed while tile t is in the softmax.
+// Roles. One warp looks up pages and starts the tiled copies (rings of 16 KiB units, 64
+// columns of 128 keys each, in the order K0 K1 V0 K2 V1 ...), one thread each issues the matrix
+// instructions of the scores and of the values, 8 warps do the softmax and the outputs. S is
+// double buffered: the scores of tile t+1 are computed while tile t is in the softmax.
 #pragma once
 
 #include <cstdint>
@@ -48,7 +48,7 @@ namespace sv {
 
 constexpr int kTileKeys = 128;
 constexpr int kUnitBytes = kTileKeys * 128;  // 64 columns of a tile
-constexpr int kUnitSmemMax = 232448 - 8192;  // dynamic shared memory for operands
+constexpr int kSmemMax = 232448;             // shared memory of a CTA
 constexpr float kNoMax = -3.402823466e38f;   // a maximum below every finite score
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -92,7 +92,7 @@ struct TileShape {
   static constexpr int Teams = !kWeigh && N <= 32 ? 2 : 1;
   static constexpr int SoftWarps = 8;
   static constexpr int SoftThreads = 32 * SoftWarps;
-  static constexpr int Threads = SoftThreads + 64;
+  static constexpr int Threads = SoftThreads + (kWeigh ? 64 : 96);
   static constexpr int TeamThreads = SoftThreads / Teams;
   static constexpr int NC = kWeigh || Teams == 2 ? N : N / 2;  // columns per softmax thread
   static constexpr int CH = NC < 32 ? NC : 32;                 // of which at a time
@@ -100,15 +100,25 @@ struct TileShape {
   static constexpr int NQ = N * D <= 64 * 128 ? 2 : 1;  // query buffers
   static constexpr int PBytes = kWeigh ? 0 : 2 * kTileKeys * N * 2;
   // two buffers of weights per team where the ring keeps three tensors (two tiles of D = 256)
-  static constexpr int kLeft = kUnitSmemMax - 1024 - NQ * QBytes;
+  static constexpr int kTables = 96 * N + 768;  // (the size of TileShared, at most)
+  static constexpr int kLeft = kSmemMax - kTables - 1024 - NQ * QBytes;
   static constexpr int NP =
       kWeigh ? 1 : (kLeft - 2 * Teams * PBytes) / kUnitBytes >= (U == 4 ? 8 : 6) ? 2 : 1;
   static constexpr int Room = (kLeft - Teams * NP * PBytes) / kUnitBytes;
-  static constexpr int NU = (Room > 12 ? 12 : Room) / 2 * 2;  // ring units, an even number
+  // Ring units: one ring for keys, one for values, as each has its own consumer. (A consumer
+  // that skipped some phases of a unit's barrier could not tell a phase from the one after next.)
+  static constexpr int NU = Room > 12 ? 12 : Room;
+  static constexpr int NV = kWeigh ? 0 : U == 1 ? NU / 2 : (NU + 2) / 4 * 2;  // (pairs)
+  static constexpr int NK = NU - NV;
   static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * kUnitBytes;
   static constexpr int MBlocks = kWeigh ? 0 : (D + 127) / 128;  // accumulators of 128 of D
-  // two score buffers per team, two outputs
-  static constexpr int TmemNeed = 2 * (Teams + MBlocks) * N;
+  // Two score buffers per team, two outputs. Where tensor memory has room, the products with the
+  // high and the low halves of the weights are one instruction of twice the columns (the values,
+  // whose read from shared memory bounds a narrow instruction, are read once) and are added at
+  // the end; else the second accumulates onto the first.
+  static constexpr bool Wide = !kWeigh && 2 * (Teams + 2 * MBlocks) * N <= 512;
+  static constexpr int ON = Wide ? 2 * N : N;  // columns of an accumulator
+  static constexpr int TmemNeed = 2 * (Teams * N + MBlocks * ON);
   static constexpr int TmemCols = TmemNeed <= 32 ? 32 : TmemNeed <= 64 ? 64 : TmemNeed <= 128 ? 128
                                   : TmemNeed <= 256 ? 256 : 512;
   // The cost of a tile and of starting a piece, in the units the work is divided by: a quarter
@@ -116,10 +126,7 @@ struct TileShape {
   // alone).
   static constexpr int TileCost = 4;
   static constexpr int PieceCost = (kWeigh ? 12 : Teams == 2 ? 4 : 10) / U + 1;
-  // the last value tile lies one (unused) key tile past the last key tile: its place must not
-  // have been that key tile's
-  static_assert(kWeigh || NU >= 2 * U, "ring");
-  static_assert(TmemNeed <= 512 && NU >= U && Smem <= kUnitSmemMax, "tile shape");
+  static_assert(TmemNeed <= 512 && NK >= 2 && Smem + kTables <= kSmemMax, "tile shape");
 };
 
 // ---- the work list ----------------------------------------------------------------------------
@@ -358,13 +365,14 @@ struct TileShared {
   uint64_t q_full[S::NQ], q_empty[S::NQ];
   uint64_t s_full[S::Teams][2], s_empty[S::Teams][2];
   uint64_t p_full[S::Teams][S::NP], pv_done[S::Teams][S::NP];
+  uint64_t v_ready[S::Teams];  // the values of a tile that some rows see in part have landed
   uint64_t o_done[2];  // a piece has its last product, by ordinal % 2
   uint32_t tmem;
   int dead;
   int bad_piece[8];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 8
   int issued[S::NU]; // passes whose copies into the unit were started
   int q_issued[S::NQ];
-  uint64_t drain;
+  uint64_t drain[2];
   int64_t scratch[16];
   Start start;
   struct Table {
@@ -380,23 +388,15 @@ struct TileShared {
   JoinItem join;
 };
 
-// Position of tensor `idx` (in ring order) in the ring.
+// Where the c-th unit of the key or value tile of the CTA's x-th tile lies in its ring, and the
+// how-manieth use of that place it is.
 template <class S>
-__device__ __forceinline__ int unit_slot(int unit) {
-  return unit % S::NU;
+__device__ __forceinline__ int unit_slot(bool value, int x, int c) {
+  return value && !S::Weigh ? S::NK + (x * S::U + c) % (S::NV + S::Weigh) : (x * S::U + c) % S::NK;
 }
 template <class S>
-__device__ __forceinline__ uint32_t unit_pass(int unit) {
-  return (uint32_t)(unit / S::NU);
-}
-// First unit of the key tile and of the value tile of the x-th tile the CTA walks.
-template <class S>
-__device__ __forceinline__ int k_unit(int x) {
-  return S::Weigh ? x * S::U : (x == 0 ? 0 : (2 * x - 1) * S::U);
-}
-template <class S>
-__device__ __forceinline__ int v_unit(int x) {
-  return (2 * x + 2) * S::U;
+__device__ __forceinline__ uint32_t unit_pass(bool value, int x, int c) {
+  return (uint32_t)((x * S::U + c) / (value && !S::Weigh ? S::NV + S::Weigh : S::NK));
 }
 
 // The i-th tile a piece walks: the attention goes from the newest keys to the oldest, so that
@@ -404,6 +404,15 @@ __device__ __forceinline__ int v_unit(int x) {
 template <class S>
 __device__ __forceinline__ int tile_at(const Piece& p, int i) {
   return S::Weigh ? p.ma + i : p.mb - 1 - i;
+}
+
+// Keys from here on are inside the window of every row of an item.
+__device__ __forceinline__ int first_full(const Item& it, int window) {
+  return it.last - window + 1;
+}
+// Whether some row of the item does not see some key of tile t.
+__device__ __forceinline__ bool edge_tile(const Item& it, int window, int t) {
+  return t * kTileKeys < first_full(it, window) || t * kTileKeys + kTileKeys - 1 > it.pos0;
 }
 
 // ---- the copying warp -----------------------------------------------------------------------
@@ -423,15 +432,15 @@ struct Loader {
     return id < 0 || id >= A.num_pages ? -2 : id;
   }
   __device__ __forceinline__ void load(const CUtensorMap* map, const Piece& p, int tile, int page,
-                                       int unit0) const {
+                                       bool value, int x) const {
     const bool mine = page >= 0;
     const uint32_t bytes =
         (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
     const int slot_in_page = (tile * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
 #pragma unroll
     for (int c = 0; c < S::U; ++c) {
-      const int s = unit_slot<S>(unit0 + c);
-      const uint32_t pass = unit_pass<S>(unit0 + c);
+      const int s = unit_slot<S>(value, x, c);
+      const uint32_t pass = unit_pass<S>(value, x, c);
       if (pass > 0) wait_phase(&sh.empty[s], (pass - 1) & 1u, &sh.dead);
       __syncwarp();
       const bool dead = __any_sync(0xffffffffu, *(volatile int*)&sh.dead);
@@ -479,9 +488,9 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
         if (__any_sync(0xffffffffu, page == -2) && lane == 0)
           *(volatile int*)&sh.bad_piece[ordinal & 7] = ordinal + 1;
         __syncwarp();
-        L.load(mk, p, t, page, k_unit<S>(x));
+        L.load(mk, p, t, page, false, x);
         if (!S::Weigh) {
-          if (x > 0) L.load(mv, prev, prev_tile, prev_page, v_unit<S>(x - 1));
+          if (x > 0) L.load(mv, prev, prev_tile, prev_page, true, x - 1);
           prev = p;
           prev_tile = t;
           prev_page = page;
@@ -492,7 +501,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
       ++ordinal;
     }
   }
-  if (!S::Weigh && x > 0) L.load(mv, prev, prev_tile, prev_page, v_unit<S>(x - 1));
+  if (!S::Weigh && x > 0) L.load(mv, prev, prev_tile, prev_page, true, x - 1);
   if (*(volatile int*)&sh.dead && lane == 0) {
     // given up: no copy may outlive the CTA
     for (int s = 0; s < S::NU; ++s)
@@ -504,7 +513,8 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
   __syncwarp();
 }
 
-// ---- the thread that issues the matrix instructions -----------------------------------------
+// ---- the threads that issue the matrix instructions -------------------------------------------
+// One issues the scores, as far ahead as their buffers allow, one the products with the values.
 template <class S>
 struct Issuer {
   const TileArgs& A;
@@ -514,12 +524,12 @@ struct Issuer {
 
   __device__ __forceinline__ bool dead() const { return *(volatile int*)&sh.dead != 0; }
 
-  // S^T of the tile whose keys start at ring unit `unit`, into a team's score buffer `buf`.
-  __device__ __forceinline__ void scores(int unit, int qs, int team, int buf) const {
+  // S^T of the x-th tile into a team's score buffer `buf`.
+  __device__ __forceinline__ void scores(int x, int qs, int team, int buf) const {
 #pragma unroll
     for (int c = 0; c < S::U; ++c) {
-      const int s = unit_slot<S>(unit + c);
-      wait_phase(&sh.full[s], unit_pass<S>(unit + c) & 1u, &sh.dead);
+      const int s = unit_slot<S>(false, x, c);
+      wait_phase(&sh.full[s], unit_pass<S>(false, x, c) & 1u, &sh.dead);
       tc_fence_after();
       if (dead()) continue;
       const uint32_t a0 = ring_addr + s * kUnitBytes;
@@ -532,38 +542,45 @@ struct Issuer {
     }
     if (!dead()) mma_commit(&sh.s_full[team][buf]);
   }
-  // O^T (+)= V^T P^T of the x-th tile, the y-th of its team.
-  __device__ __forceinline__ void values(int x, int y, bool first, bool last, int ordinal) const {
+  // O^T (+)= V^T P^T of the x-th tile, the y-th of its team. Of an edge tile the softmax threads
+  // clean the values once they have landed, before they pass on the weights.
+  __device__ __forceinline__ void values(int x, int y, bool first, bool last, bool edge,
+                                         int ordinal) const {
     const int team = ordinal % S::Teams, ob = ordinal & 1;
     const int pb = y % S::NP;
     const uint32_t p_at = p_addr + (team * S::NP + pb) * S::PBytes;
+    if (edge) {
+#pragma unroll
+      for (int c = 0; c < S::U; ++c)
+        wait_phase(&sh.full[unit_slot<S>(true, x, c)], unit_pass<S>(true, x, c) & 1u, &sh.dead);
+      if (!dead()) mbar_arrive(&sh.v_ready[team]);
+    }
     wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.dead);
     tc_fence_after();
     constexpr int kPer = S::U >= 2 ? 2 : 1;  // units per accumulator
 #pragma unroll
     for (int m = 0; m < S::MBlocks; ++m) {
-      const int unit = v_unit<S>(x) + m * kPer;
-      const int s = unit_slot<S>(unit);
+      const int s = unit_slot<S>(true, x, m * kPer);
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) {
-        wait_phase(&sh.full[unit_slot<S>(unit + c)], unit_pass<S>(unit + c) & 1u, &sh.dead);
-      }
+      for (int c = m * kPer; c < (m + 1) * kPer; ++c)
+        wait_phase(&sh.full[unit_slot<S>(true, x, c)], unit_pass<S>(true, x, c) & 1u, &sh.dead);
       tc_fence_after();
       if (dead()) continue;
       const uint32_t a0 = ring_addr + s * kUnitBytes;
 #pragma unroll
-      for (int part = 0; part < 2; ++part)  // the weights' high and low halves
+      for (int part = 0; part < (S::Wide ? 1 : 2); ++part)  // the weights' high and low halves
 #pragma unroll
         for (int k = 0; k < kTileKeys / 16; ++k)
           // values of 64 columns lie 128 bytes per key; with D = 64 both halves of the
           // instruction's rows read the same columns, and the upper half is not used
-          mma_f16(tmem + (2 * S::Teams + ob * S::MBlocks + m) * S::N,
+          mma_f16(tmem + 2 * S::Teams * S::N + (ob * S::MBlocks + m) * S::ON,
                   smem_desc(a0 + k * 2048, kPer == 2 ? kUnitBytes : 0, 1024, kSwizzle128),
                   smem_desc(p_at + part * (kTileKeys * S::N * 2) + k * 512, kTileKeys * 32, 256,
                             kSwizzle32),
                   pv_desc, !(first && part == 0 && k == 0));
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) mma_commit(&sh.empty[unit_slot<S>(unit + c)]);
+      for (int c = m * kPer; c < (m + 1) * kPer; ++c)
+        mma_commit(&sh.empty[unit_slot<S>(true, x, c)]);
     }
     if (!dead()) {
       mma_commit(&sh.pv_done[team][pb]);
@@ -573,17 +590,29 @@ struct Issuer {
 };
 
 template <class S>
-__device__ __forceinline__ void issue_role(const TileArgs& A, TileShared<S>& sh,
-                                           unsigned char* qbuf, unsigned char* pbuf,
-                                           unsigned char* ring) {
-  Issuer<S> I{A, sh, smem_u32(qbuf), smem_u32(pbuf), smem_u32(ring), sh.tmem,
-              mma_desc(A.bf16, false, false, 128, S::N), mma_desc(A.bf16, true, true, 128, S::N)};
+__device__ __forceinline__ Issuer<S> issuer(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* qbuf, unsigned char* pbuf,
+                                            unsigned char* ring) {
+  return Issuer<S>{A, sh, smem_u32(qbuf), smem_u32(pbuf), smem_u32(ring), sh.tmem,
+                   mma_desc(A.bf16, false, false, 128, S::N),
+                   mma_desc(A.bf16, true, true, 128, S::ON)};
+}
+
+// Given up: no instruction may outlive the tensor memory.
+template <class S>
+__device__ __forceinline__ void drain(TileShared<S>& sh, int which) {
+  if (!*(volatile int*)&sh.dead) return;
+  mma_commit(&sh.drain[which]);
+  mbar_wait(&sh.drain[which], 0, kTileWaitNs);
+}
+
+template <class S>
+__device__ __forceinline__ void score_role(const TileArgs& A, const Issuer<S>& I,
+                                           TileShared<S>& sh) {
   Walk<S> w(A, sh.start);
   Piece p;
   // used: tiles so far per team (attention) or per score buffer (key weights)
   int x = 0, ordinal = 0, used[2] = {0, 0};
-  bool prev_first = false, prev_last = false;
-  int prev_ordinal = 0, prev_y = 0;
   while (w.next(p)) {
     for (int rb = 0; S::Weigh ? weigh_pass(A, p, rb) : rb == 0; ++rb) {
       if (p.mb <= p.ma) continue;
@@ -595,25 +624,33 @@ __device__ __forceinline__ void issue_role(const TileArgs& A, TileShared<S>& sh,
         const int buf = S::Weigh ? of : y & 1, turn = S::Weigh ? y : y >> 1;
         if (turn > 0) wait_phase(&sh.s_empty[team][buf], (uint32_t)(turn - 1) & 1u, &sh.dead);
         tc_fence_after();
-        I.scores(k_unit<S>(x), qs, team, buf);
+        I.scores(x, qs, team, buf);
         if (i + 1 == p.mb - p.ma && !I.dead()) mma_commit(&sh.q_empty[qs]);
-        if (!S::Weigh) {
-          if (x > 0) I.values(x - 1, prev_y, prev_first, prev_last, prev_ordinal);
-          prev_first = i == 0;
-          prev_last = i + 1 == p.mb - p.ma;
-          prev_ordinal = ordinal;
-          prev_y = y;
-        }
         ++x;
       }
       ++ordinal;
     }
   }
-  if (!S::Weigh && x > 0) I.values(x - 1, prev_y, prev_first, prev_last, prev_ordinal);
-  if (I.dead()) {  // given up: no instruction may outlive the tensor memory
-    mma_commit(&sh.drain);
-    mbar_wait(&sh.drain, 0, kTileWaitNs);
+  drain<S>(sh, 0);
+}
+
+template <class S>
+__device__ __forceinline__ void value_role(const TileArgs& A, const Issuer<S>& I,
+                                           TileShared<S>& sh) {
+  Walk<S> w(A, sh.start);
+  Piece p;
+  int x = 0, ordinal = 0, used[2] = {0, 0};
+  while (w.next(p)) {
+    const int tiles = p.mb - p.ma;
+    if (tiles == 0) continue;
+    for (int i = 0; i < tiles; ++i, ++x) {
+      const int y = ordinal % S::Teams ? used[1]++ : used[0]++;
+      I.values(x, y, i == 0, i + 1 == tiles, edge_tile(p.it, A.rule.window, tile_at<S>(p, i)),
+               ordinal);
+    }
+    ++ordinal;
   }
+  drain<S>(sh, 1);
 }
 
 // ---- the softmax threads ------------------------------------------------------------------------
@@ -759,6 +796,7 @@ struct Attend {
   uint32_t lane_base;  // tensor-memory address of the thread's lanes
   int team, me;        // the team, the thread's index in it
   int col0;            // the group's first column
+  int edges = 0;       // edge tiles so far
 
   // Wait until the products of the team's tile y have read P and are in O.
   __device__ __forceinline__ void wait_values(int y) const {
@@ -770,7 +808,7 @@ struct Attend {
   }
   // The accumulator of a piece, the group's first column.
   __device__ __forceinline__ uint32_t output(int ordinal) const {
-    return lane_base + (2 * S::Teams + (ordinal & 1) * S::MBlocks) * S::N + col0;
+    return lane_base + 2 * S::Teams * S::N + (ordinal & 1) * S::MBlocks * S::ON + col0;
   }
 
   // Raise the maxima of the CH columns from c0 to those of this tile's scores s, and scale what
@@ -794,7 +832,7 @@ struct Attend {
     for (int c = 0; c < S::CH; ++c) l[k + c] *= T.alpha[c0 + c];
     tc_fence_after();
 #pragma unroll 1
-    for (int m = 0; m < S::MBlocks; ++m)
+    for (int m = 0; m < S::MBlocks * (S::Wide ? 2 : 1); ++m)  // (wide: high and low products)
 #pragma unroll 1
       for (int q = 0; q < S::CH; q += 16) {
         float o[16];
@@ -811,17 +849,14 @@ struct Attend {
   // Values of keys that some row of a tile does not see: what no row sees becomes 0; of a key
   // that only some rows see, the values that are not finite become 0 and are added to the rows
   // that see it at the end (0 times infinity would reach the others).
-  __device__ __forceinline__ void clean_values(Table& T, const Piece& p, int x, int j,
-                                               int first_full) {
+  __device__ __forceinline__ void clean_values(Table& T, const Piece& p, int x, int j) {
     const bool none = j > p.it.last || j < p.it.first;
-    const bool some = !none && (j > p.it.pos0 || j < first_full);
+    const bool some = !none && (j > p.it.pos0 || j < first_full(p.it, A.rule.window));
     if (!__any_sync(0xffffffffu, none || some)) return;
-    const int unit = v_unit<S>(x);
     uint32_t odd = 0;
 #pragma unroll
     for (int c = 0; c < S::U; ++c) {
-      wait_phase(&sh.full[unit_slot<S>(unit + c)], unit_pass<S>(unit + c) & 1u, &sh.dead);
-      uint4* row = reinterpret_cast<uint4*>(ring + unit_slot<S>(unit + c) * kUnitBytes + key * 128);
+      uint4* row = reinterpret_cast<uint4*>(ring + unit_slot<S>(true, x, c) * kUnitBytes + key * 128);
       // (each lane starts with another 16 bytes of its row: no bank conflicts)
       if (none) {
 #pragma unroll
@@ -840,7 +875,7 @@ struct Attend {
                1u << (j > p.it.pos0 ? j - p.it.pos0 - 1 : 16 + j - p.it.first));
 #pragma unroll 1
       for (int c = 0; c < S::U; ++c) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(ring + unit_slot<S>(unit + c) * kUnitBytes +
+        uint32_t* w = reinterpret_cast<uint32_t*>(ring + unit_slot<S>(true, x, c) * kUnitBytes +
                                                   key * 128);
 #pragma unroll 1
         for (int e = 0; e < 32; ++e) {
@@ -855,9 +890,7 @@ struct Attend {
   __device__ __forceinline__ void tile(Table& T, const Piece& p, int t, bool first, int x, int y,
                                        int ordinal, float (&l)[S::NC]) {
     const int buf = y & 1, j = t * kTileKeys + key;
-    // keys from here on are inside every row's window
-    const int first_full = p.it.last - A.rule.window + 1;
-    const bool edge = t * kTileKeys < first_full || t * kTileKeys + kTileKeys - 1 > p.it.pos0;
+    const bool edge = edge_tile(p.it, A.rule.window, t);
     wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.dead);
     tc_fence_after();
 #pragma unroll
@@ -913,7 +946,10 @@ struct Attend {
             make_uint4(lo[w + 4], lo[w + 5], lo[w + 6], lo[w + 7]);
       }
     }
-    if (edge && (S::Teams == 2 || group == 0)) clean_values(T, p, x, j, first_full);
+    if (edge) {
+      wait_phase(&sh.v_ready[team], (uint32_t)(edges++) & 1u, &sh.dead);
+      if (S::Teams == 2 || group == 0) clean_values(T, p, x, j);
+    }
     fence_proxy_async();
     tc_fence_before();
     mbar_arrive(&sh.p_full[team][y % S::NP]);
@@ -979,8 +1015,16 @@ struct Attend {
 #pragma unroll 1
         for (int q = 0; q < S::NC && col0 + q < rows; q += 16) {
           float o[16];
-          tmem_ld16(output(ordinal) + m * S::N + q, o);
-          tmem_wait_ld();
+          tmem_ld16(output(ordinal) + m * S::ON + q, o);
+          if (S::Wide) {
+            float low[16];
+            tmem_ld16(output(ordinal) + m * S::ON + S::N + q, low);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) o[c] += low[c];
+          } else {
+            tmem_wait_ld();
+          }
           const int n0 = col0 + q;
           if (whole) {
             uint16_t* out = static_cast<uint16_t*>(A.out) + row0 * S::D + d;
@@ -1118,7 +1162,6 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
       bar_sync(kAllBar, S::SoftThreads);
       set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
       bar_sync(kAllBar, S::SoftThreads);
-      const int first_full = p.it.last - A.rule.window + 1;
       const int ta = rb == 0 ? p.ta : p.ma, tb = rb == 0 ? p.tb : p.mb;
       for (int t = ta; t < tb; ++t) {
         if ((t & 1) != group) continue;
@@ -1132,8 +1175,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
             const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
             bad = page < 0 || page >= A.num_pages;
           }
-          const bool edge =
-              t * kTileKeys < first_full || t * kTileKeys + kTileKeys - 1 > p.it.pos0;
+          const bool edge = edge_tile(p.it, A.rule.window, t);
           wait_phase(&sh.s_full[0][group], (uint32_t)used & 1u, &sh.dead);
           ++used;
           tc_fence_after();
@@ -1170,7 +1212,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
                 const __grid_constant__ ValuePool vpool) {
   extern __shared__ unsigned char tile_smem[];
   __shared__ TileShared<S> sh;
-  static_assert(S::Smem + sizeof(TileShared<S>) <= 232448, "shared memory");
+  static_assert(sizeof(TileShared<S>) <= S::kTables, "shared memory");
   // operand tiles start on 1024-byte boundaries (the swizzle pattern's period)
   unsigned char* base = tile_smem + ((1024u - (smem_u32(tile_smem) & 1023u)) & 1023u);
   unsigned char* qbuf = base;
@@ -1199,9 +1241,11 @@ __global__ void __launch_bounds__(S::Threads, 1)
         mbar_init(&sh.pv_done[t][s], 1);
       }
     }
+    for (int t = 0; t < S::Teams; ++t) mbar_init(&sh.v_ready[t], 1);
     mbar_init(&sh.o_done[0], 1);
     mbar_init(&sh.o_done[1], 1);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     sh.dead = 0;
     sh.join.rows = 0;
     for (int i = 0; i < 8; ++i) sh.bad_piece[i] = 0;
@@ -1240,7 +1284,10 @@ __global__ void __launch_bounds__(S::Threads, 1)
   if (warp == S::SoftWarps) {
     copy_role<S>(A, sh, qbuf, ring, &mq, &mk, &mv);
   } else if (warp == S::SoftWarps + 1) {
-    if ((tid & 31) == 0) issue_role<S>(A, sh, qbuf, pbuf, ring);
+    if ((tid & 31) == 0) score_role<S>(A, issuer<S>(A, sh, qbuf, pbuf, ring), sh);
+    __syncwarp();
+  } else if (!S::Weigh && warp == S::SoftWarps + 2) {
+    if ((tid & 31) == 0) value_role<S>(A, issuer<S>(A, sh, qbuf, pbuf, ring), sh);
     __syncwarp();
   } else if constexpr (S::Weigh) {
     weigh_role<S>(A, sh);
@@ -1260,68 +1307,67 @@ __global__ void __launch_bounds__(S::Threads, 1)
 }
 
 // ---- joining the pieces of split items --------------------------------------------------------
-// Block (c, q): the q-th share of the item that CTA c began and left to others. Its pieces are
-// the second slot of CTA c and the first slots of the CTAs after it, joined in that order.
+// Thread: four of D of one row, over all its pieces: those of an item are the second slot of the
+// CTA that began it and the first slots of the CTAs after it, joined in that order, eight in
+// flight.
 constexpr int kJoinThreads = 128;
-constexpr int kJoinShares = 4;
+template <int kD, int kN>
+constexpr int kJoinShares = kN * (kD / 4) / kJoinThreads;
 
 template <int kD, int kN, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const JoinItem* joins, const float* part, int G, int Hq, void* out, float* out_lse) {
-  __shared__ float s_m[kN], s_inv[kN];
   constexpr int64_t kSlot = kN * (kD + 2);
+  constexpr int kBatch = 8;
+  const int c = blockIdx.x, e = blockIdx.y * kJoinThreads + threadIdx.x;
+  const int n = e / (kD / 4), d = e % (kD / 4) * 4;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x;
   const JoinItem J = joins[c];
-  if (J.rows == 0) return;
+  if (n >= J.rows) return;
   const float* s0 = part + (2 * c + 1) * kSlot;  // the first piece; the i-th is at s1 + 2 i slots
   const float* s1 = part + 2 * c * kSlot;
-  auto at = [&](int i) { return i == 0 ? s0 : s1 + 2 * i * kSlot; };
-  for (int n = threadIdx.x; n < J.rows; n += kJoinThreads) {
-    float m = kNoMax, sum = 0.0f;
-    constexpr int kBatch = 8;
+  float m = kNoMax, sum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-    for (int i0 = 0; i0 < J.pieces; i0 += kBatch) {
-      float2 v[kBatch];
+  for (int i0 = 0; i0 < J.pieces; i0 += kBatch) {
+    float2 ml[kBatch];
+    float4 v[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        v[i] = i0 + i < J.pieces
-                   ? *reinterpret_cast<const float2*>(at(i0 + i) + kN * kD + 2 * n)
-                   : make_float2(kNoMax, 0.0f);
-      float top = m;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, v[i].x);
-      sum *= ex2(m - top);
-      m = top;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) sum += ex2(v[i].x - m) * v[i].y;
+    for (int i = 0; i < kBatch; ++i) {
+      ml[i] = make_float2(kNoMax, 0.0f);
+      v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (i0 + i < J.pieces) {
+        const float* s = i0 + i == 0 ? s0 : s1 + 2 * (i0 + i) * kSlot;
+        ml[i] = *reinterpret_cast<const float2*>(s + kN * kD + 2 * n);
+        v[i] = *reinterpret_cast<const float4*>(s + n * kD + d);
+      }
     }
-    s_m[n] = m;
-    s_inv[n] = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (out_lse && blockIdx.y == 0)
-      out_lse[J.row0 + n / G * Hq + n % G] =
-          sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
-  }
-  __syncthreads();
-  for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < J.rows * (kD / 4);
-       e += kJoinShares * kJoinThreads) {
-    const int n = e / (kD / 4), d = e % (kD / 4) * 4;
-    const float m = s_m[n], inv = s_inv[n];
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-    for (int i = 0; i < J.pieces; ++i) {
-      const float* s = at(i);
-      const float4 v = *reinterpret_cast<const float4*>(s + n * kD + d);
-      const float w = ex2(s[kN * kD + 2 * n] - m);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, ml[i].x);
+    const float a = ex2(m - top);
+    m = top;
+    sum *= a;
+    acc.x *= a;
+    acc.y *= a;
+    acc.z *= a;
+    acc.w *= a;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float w = ex2(ml[i].x - m);
+      sum += w * ml[i].y;
+      acc.x = fmaf(w, v[i].x, acc.x);
+      acc.y = fmaf(w, v[i].y, acc.y);
+      acc.z = fmaf(w, v[i].z, acc.z);
+      acc.w = fmaf(w, v[i].w, acc.w);
     }
-    const int64_t row = J.row0 + n / G * Hq + n % G;
-    *reinterpret_cast<uint2*>(static_cast<char*>(out) + 2 * (row * kD + d)) =
-        make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
   }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t row = J.row0 + n / G * Hq + n % G;
+  *reinterpret_cast<uint2*>(static_cast<char*>(out) + 2 * (row * kD + d)) =
+      make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
+  if (out_lse && d == 0)
+    out_lse[row] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
 }
 
 // ---- the host side ------------------------------------------------------------------------------
