@@ -28,10 +28,10 @@
 // pieces in order, so the result does not depend on the order of arrival. No CTA waits for
 // another one.
 //
-// Roles. One warp looks up pages and starts the tiled copies (rings of 16 KiB units, 64
-// columns of 128 keys each, in the order K0 K1 V0 K2 V1 ...), one thread each issues the matrix
-// instructions of the scores and of the values, 8 warps do the softmax and the outputs. S is
-// double buffered: the scores of tile t+1 are computed while tile t is in the softmax.
+// Roles. Keys and values have a ring each of 16 KiB units (64 columns of 128 keys), a warp each
+// that looks up the pages and starts the tiled copies, and a thread each that issues the matrix
+// instructions; 8 warps do the softmax and the outputs. S is double buffered: the scores of tile
+// t+1 are computed while tile t is in the softmax.
 #pragma once
 
 #include <cstdint>
@@ -92,7 +92,10 @@ struct TileShape {
   static constexpr int Teams = !kWeigh && N <= 32 ? 2 : 1;
   static constexpr int SoftWarps = 8;
   static constexpr int SoftThreads = 32 * SoftWarps;
-  static constexpr int Threads = SoftThreads + (kWeigh ? 64 : 96);
+  static constexpr int Threads = SoftThreads + (kWeigh ? 64 : 128);
+  // the warps after the softmax: key (and query) copies, scores, value copies, values
+  static constexpr int KeyWarp = SoftWarps, ScoreWarp = KeyWarp + 1, CopyVWarp = KeyWarp + 2,
+                       ValueWarp = KeyWarp + 3;
   static constexpr int TeamThreads = SoftThreads / Teams;
   static constexpr int NC = kWeigh || Teams == 2 ? N : N / 2;  // columns per softmax thread
   static constexpr int CH = NC < 32 ? NC : 32;                 // of which at a time
@@ -100,7 +103,7 @@ struct TileShape {
   static constexpr int NQ = N * D <= 64 * 128 ? 2 : 1;  // query buffers
   static constexpr int PBytes = kWeigh ? 0 : 2 * kTileKeys * N * 2;
   // two buffers of weights per team where the ring keeps three tensors (two tiles of D = 256)
-  static constexpr int kTables = 96 * N + 768;  // (the size of TileShared, at most)
+  static constexpr int kTables = 96 * N + 1664;  // (the size of TileShared, at most)
   static constexpr int kLeft = kSmemMax - kTables - 1024 - NQ * QBytes;
   static constexpr int NP =
       kWeigh ? 1 : (kLeft - 2 * Teams * PBytes) / kUnitBytes >= (U == 4 ? 8 : 6) ? 2 : 1;
@@ -139,8 +142,8 @@ struct Item {
   int first, last;  // the keys any live row sees; last < first: none
   int t0, tiles;    // tiles to walk (0: nothing to write)
   template <class S>
-  __device__ __forceinline__ int64_t cost() const {
-    return tiles == 0 ? 0 : S::PieceCost + (int64_t)tiles * S::TileCost;
+  __device__ __forceinline__ int cost() const {
+    return tiles == 0 ? 0 : S::PieceCost + tiles * S::TileCost;
   }
 };
 
@@ -189,112 +192,125 @@ __device__ __forceinline__ int load_acc(const TileArgs& A, int b, int nd) {
 // Cost of a request per kv head, over its row blocks (in the key weights a tile is walked once
 // per block, so all blocks count as one item).
 template <class S>
-__device__ __forceinline__ int64_t request_cost(const TileArgs& A, int b) {
+__device__ __noinline__ int64_t request_cost(const TileArgs& A, int b) {
   const int n = load_n(A, b), nd = load_nd(A, b), acc = S::Weigh ? load_acc(A, b, nd) : 0;
   int64_t c = 0;
+#pragma unroll 1
   for (int rb = 0; rb < (S::Weigh ? 1 : A.blocks); ++rb)
     c += item_of<S::Weigh>(A, n, nd, acc, rb).template cost<S>();
   return c;
 }
 
-// Where a CTA's range starts (shared memory).
+// A CTA's range (shared memory): `left` units of `per`, which the other CTAs have too, from unit
+// `off` of item (b, h, rb) on.
 struct Start {
-  int64_t flat, left, per;
-  int64_t off;  // the start's offset into its item
+  int left, per, off;
   int b, h, rb;
 };
 
-// A CTA's part of one item: tiles [ta, tb) of the item, of which [ma, mb) go through the tensor
-// cores (none: filled or copied without them).
+// A CTA's part of one item (in the key weights: one pass over it, for one row block), as the warp
+// that walks the work list hands it to the other roles.
 struct Piece {
-  int b, h, rb;
-  Item it;
-  int ta, tb, ma, mb;
-  bool starts, ends;  // whether it holds the item's first and last tile
-  int64_t item0;      // flat position of the item
+  int b, h, i0, live, pos0, first, last;  // of the item
+  int n;                                  // tokens of the request
+  int ta, tb;                             // its tiles
+  int ma, mb;                             // those that go through the tensor cores
+  int pass;    // (key weights) the row block
+  int turn;    // pieces before it with (or, of one without, without) such tiles
+  int x0;      // such tiles before it
+  int pieces;  // CTAs that hold a part of the item
+  int flags;
 };
-
-// The tiles of a piece that some key of [first, last] falls into.
-__device__ __forceinline__ void mma_range(Piece& p) {
-  p.ma = p.mb = 0;
-  if (p.it.bad || p.it.last < p.it.first || p.it.last < 0) return;
-  const int lo = p.it.first / kTileKeys, hi = p.it.last / kTileKeys + 1;
-  p.ma = p.ta > lo ? p.ta : lo;
-  p.mb = p.tb < hi ? p.tb : hi;
-  if (p.mb < p.ma) p.mb = p.ma;
-}
-
-// The key weights walk a piece once per row block: turns p into its pass rb; false past the last.
-__device__ __forceinline__ bool weigh_pass(const TileArgs& A, Piece& p, int rb) {
-  if (rb == 0) return true;
-  if (rb >= A.blocks || p.it.bad) return false;
-  p.it = item_of<true>(A, p.it.n, p.it.nd, p.it.acc, rb);
-  p.rb = rb;
-  mma_range(p);
-  return p.it.live > 0;
-}
+enum { kStarts = 1, kEnds = 2, kBad = 4, kEndOfList = 8 };
 
 // Walks a range of the flat work list, in which an item takes PieceCost + tiles * TileCost
 // units; tile k belongs to the range that holds the item's unit PieceCost + k * TileCost.
 template <class S>
 struct Walk {
   const TileArgs& A;
-  int b, h, rb, n, nd, acc;
-  int64_t off, flat, left;
+  int b, h, rb, n = 0, nd = 0, acc = 0;
+  int off, left, per;
   Item it;
+  int turns = 0, fills = 0, x = 0;
+  int pass = 0;  // (key weights) the pass last given out
+  bool more_passes = false;
+  enum { kLoad, kStay, kAdvance } step = kLoad;
   __device__ __forceinline__ Walk(const TileArgs& a, const Start& s)
-      : A(a), b(s.b), h(s.h), rb(s.rb), off(s.off), flat(s.flat), left(s.left) {
-    load();
-  }
-  __device__ __forceinline__ void load() {
-    n = load_n(A, b);
-    nd = load_nd(A, b);
-    acc = S::Weigh ? load_acc(A, b, nd) : 0;
-    it = item_of<S::Weigh>(A, n, nd, acc, rb);
-  }
+      : A(a), b(s.b), h(s.h), rb(s.rb), off(s.off), left(s.left), per(s.per) {}
   // The first tile at or past unit u of the item.
-  __device__ __forceinline__ int tile_from(int64_t u) const {
-    return u <= S::PieceCost ? 0 : (int)((u - S::PieceCost + S::TileCost - 1) / S::TileCost);
+  __device__ __forceinline__ int tile_from(int u) const {
+    return u <= S::PieceCost ? 0 : (u - S::PieceCost + S::TileCost - 1) / S::TileCost;
+  }
+  __device__ __forceinline__ bool has_pass(int k) const {
+    return k < A.blocks && k * A.pos_block < acc + 1;
   }
   __device__ __forceinline__ bool next(Piece& p) {
-    while (left > 0) {
-      while (it.tiles == 0) advance();
-      const int64_t rest = it.template cost<S>() - off, take = rest < left ? rest : left;
-      const int ka = tile_from(off), kb = tile_from(off + take);
-      p.b = b;
-      p.h = h;
-      p.rb = rb;
-      p.it = it;
-      p.ta = it.t0 + ka;
-      p.tb = it.t0 + kb;
-      p.starts = ka == 0;
-      p.ends = kb == it.tiles;
-      p.item0 = flat - off;
-      flat += take;
-      left -= take;
-      off += take;
-      if (take == rest && left > 0) advance();
-      if (kb > ka) {
-        mma_range(p);
-        return true;
+    bool found = S::Weigh && more_passes;  // the same tiles for the next row block
+    if (found) it = item_of<S::Weigh>(A, n, nd, acc, ++pass);
+#pragma unroll 1
+    while (!found) {
+      if (left <= 0) return false;
+      if (step != kStay) {
+        bool load = step == kLoad;
+        if (step == kAdvance) {
+          off = 0;
+          if (S::Weigh || ++rb == A.blocks) {
+            rb = 0;
+            if (++h == A.Hkv) {
+              h = 0;
+              ++b;
+              load = true;
+            }
+          }
+        }
+        if (load) {
+          n = load_n(A, b);
+          nd = load_nd(A, b);
+          acc = S::Weigh ? load_acc(A, b, nd) : 0;
+        }
+        it = item_of<S::Weigh>(A, n, nd, acc, rb);
       }
+      const int rest = it.template cost<S>() - off, take = rest < left ? rest : left;
+      const int ka = tile_from(off), kb = tile_from(off + take);
+      step = take == rest ? kAdvance : kStay;
+      if (kb > ka) {
+        found = true;
+        p.b = b;
+        p.h = h;
+        p.n = n;
+        p.ta = it.t0 + ka;
+        p.tb = it.t0 + kb;
+        pass = 0;
+        p.flags = (ka == 0 ? kStarts : 0) | (kb == it.tiles ? kEnds : 0) | (it.bad ? kBad : 0);
+        // of an item that goes on in other CTAs: how many of the ranges, from this one on, hold
+        // its tiles (the first lies at unit PieceCost of it)
+        p.pieces = 1 + (per - left + S::PieceCost - off + (it.tiles - 1) * S::TileCost) / per;
+      }
+      off += take;
+      left -= take;
     }
-    return false;
-  }
-  __device__ __forceinline__ void advance() {
-    off = 0;
-    if (!S::Weigh && ++rb < A.blocks) {
-      it = item_of<S::Weigh>(A, n, nd, acc, rb);
-      return;
+    p.pass = pass;
+    p.i0 = it.i0;
+    p.live = it.live;
+    p.pos0 = it.pos0;
+    p.first = it.first;
+    p.last = it.last;
+    p.ma = p.mb = 0;
+    if (!it.bad && it.last >= it.first && it.last >= 0) {
+      const int lo = it.first / kTileKeys, hi = it.last / kTileKeys + 1;
+      p.ma = p.ta > lo ? p.ta : lo;
+      p.mb = p.tb < hi ? p.tb : hi;
+      if (p.mb < p.ma) p.mb = p.ma;
     }
-    rb = 0;
-    if (++h == A.Hkv) {
-      h = 0;
-      ++b;
-      load();
-    } else if (!S::Weigh) {
-      it = item_of<S::Weigh>(A, n, nd, acc, rb);
+    p.turn = p.mb > p.ma ? turns++ : fills++;
+    p.x0 = x;
+    x += p.mb - p.ma;
+    if (S::Weigh) {
+      more_passes = !it.bad && has_pass(pass + 1);
+      // (the next piece starts from the item of the first pass)
+      if (!more_passes && pass > 0 && step == kStay) step = kLoad;
     }
+    return true;
   }
 };
 
@@ -306,6 +322,7 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
   const int each = (A.B + S::Threads - 1) / S::Threads;
   const int b0 = tid * each, b1 = b0 + each < A.B ? b0 + each : A.B;
   int64_t mine = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) mine += request_cost<S>(A, b) * A.Hkv;
   int64_t incl = mine;
 #pragma unroll
@@ -316,47 +333,49 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
   if (lane == 31) scratch[warp] = incl;
   __syncthreads();
   int64_t before = 0, total = 0;
+#pragma unroll 1
   for (int q = 0; q < kW; ++q) {
     if (q < warp) before += scratch[q];
     total += scratch[q];
   }
   incl += before;
   // (a range of TileCost units or more holds a tile of any item that spans it)
-  int64_t per = (total + gridDim.x - 1) / gridDim.x;
-  if (per < S::TileCost) per = S::TileCost;
-  const int64_t from = per * blockIdx.x;
+  const int wanted = (int)((total + gridDim.x - 1) / gridDim.x);
+  const int per = wanted < S::TileCost ? S::TileCost : wanted;
+  const int64_t from = (int64_t)per * blockIdx.x;
   if (tid == 0) {
-    s->flat = from;
     s->per = per;
-    s->left = from >= total ? 0 : (total - from < per ? total - from : per);
+    s->left = from >= total ? 0 : (int)(total - from < per ? total - from : per);
   }
   if (from < total && incl - mine <= from && from < incl) {
-    int64_t at = incl - mine;
+    int64_t at = from - (incl - mine);
     int b = b0;
-    int64_t t = request_cost<S>(A, b) * A.Hkv;
-    while (at + t <= from) {
-      at += t;
-      ++b;
+    int64_t t = 0;
+#pragma unroll 1
+    for (;; ++b, at -= t) {
       t = request_cost<S>(A, b) * A.Hkv;
+      if (at < t) break;
     }
-    const int64_t per_head = t / A.Hkv;
+    const int n = load_n(A, b), nd = load_nd(A, b), acc = S::Weigh ? load_acc(A, b, nd) : 0;
+    // the head, then the row block
+    const int per_head = (int)(t / A.Hkv);
     s->b = b;
-    s->h = (int)((from - at) / per_head);
-    int64_t off = (from - at) % per_head;
-    int rb = 0;
-    if (!S::Weigh) {
-      const int n = load_n(A, b), nd = load_nd(A, b);
-      int64_t cost = item_of<false>(A, n, nd, 0, 0).template cost<S>();
-      while (off >= cost) {
-        off -= cost;
-        cost = item_of<false>(A, n, nd, 0, ++rb).template cost<S>();
-      }
+    s->h = (int)(at / per_head);
+    int off = (int)(at - (int64_t)s->h * per_head), rb = 0;
+#pragma unroll 1
+    for (; !S::Weigh; ++rb) {
+      const int cost = item_of<S::Weigh>(A, n, nd, acc, rb).template cost<S>();
+      if (off < cost) break;
+      off -= cost;
     }
     s->rb = rb;
     s->off = off;
   }
   __syncthreads();
 }
+
+// Pieces handed out and not yet taken by every role.
+constexpr int kPieceQueue = 8;
 
 // ---- shared memory ------------------------------------------------------------------------------
 template <class S>
@@ -370,13 +389,14 @@ struct TileShared {
   uint32_t tmem;
   int dead;
   int bad_piece[8];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 8
-  int issued[S::NU]; // passes whose copies into the unit were started
-  int q_issued[S::NQ];
   uint64_t drain[2];
+  // the pieces, from the warp that walks the work list to the other roles
+  Piece piece[kPieceQueue];
+  uint64_t piece_full[kPieceQueue], piece_empty[kPieceQueue];
   int64_t scratch[16];
   Start start;
   struct Table {
-    alignas(16) float m[S::N];       // running maximum; in the key weights the row's lse (log2)
+    alignas(16) float m[S::N];       // minus the running maximum, or the row's lse (log2)
     alignas(16) float slope[S::N];   // log2(e) * slope
     alignas(16) float ahead[S::N];   // the column's position less the block's first
     alignas(16) float alpha[S::N];
@@ -388,15 +408,21 @@ struct TileShared {
   JoinItem join;
 };
 
-// Where the c-th unit of the key or value tile of the CTA's x-th tile lies in its ring, and the
-// how-manieth use of that place it is.
+// A place in a ring of n units whose barriers start at full[base], and the parity of its use.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+// Where the c-th unit of the values of the CTA's x-th tile lies.
 template <class S>
-__device__ __forceinline__ int unit_slot(bool value, int x, int c) {
-  return value && !S::Weigh ? S::NK + (x * S::U + c) % (S::NV + S::Weigh) : (x * S::U + c) % S::NK;
-}
-template <class S>
-__device__ __forceinline__ uint32_t unit_pass(bool value, int x, int c) {
-  return (uint32_t)((x * S::U + c) / (value && !S::Weigh ? S::NV + S::Weigh : S::NK));
+__device__ __forceinline__ int value_slot(int x, int c) {
+  return S::NK + (x * S::U + c) % S::NV;
 }
 
 // The i-th tile a piece walks: the attention goes from the newest keys to the oldest, so that
@@ -406,198 +432,161 @@ __device__ __forceinline__ int tile_at(const Piece& p, int i) {
   return S::Weigh ? p.ma + i : p.mb - 1 - i;
 }
 
-// Keys from here on are inside the window of every row of an item.
-__device__ __forceinline__ int first_full(const Item& it, int window) {
-  return it.last - window + 1;
+// Keys from here on are inside the window of every row of a piece.
+__device__ __forceinline__ int first_full(const Piece& p, int window) {
+  return p.last - window + 1;
 }
-// Whether some row of the item does not see some key of tile t.
-__device__ __forceinline__ bool edge_tile(const Item& it, int window, int t) {
-  return t * kTileKeys < first_full(it, window) || t * kTileKeys + kTileKeys - 1 > it.pos0;
+// Whether some row of the piece does not see some key of tile t.
+__device__ __forceinline__ bool edge_tile(const Piece& p, int window, int t) {
+  return t * kTileKeys < first_full(p, window) || t * kTileKeys + kTileKeys - 1 > p.pos0;
 }
 
-// ---- the copying warp -----------------------------------------------------------------------
+// How the other roles take the pieces: every one in turn, none left out (a reader that skipped
+// some could not tell a phase of a barrier from the one after next).
 template <class S>
-struct Loader {
-  const TileArgs& A;
+struct Reader {
   TileShared<S>& sh;
-  unsigned char* ring;
-  int lane;
-
-  // Page of the lane's group of `box` keys in a tile, or -1 where no key of it is seen, -2 for
-  // a page that does not exist.
-  __device__ __forceinline__ int page_of(const Piece& p, int tile) const {
-    const int j = tile * kTileKeys + lane * A.box;
-    if (lane * A.box >= kTileKeys || j > p.it.last || j + A.box - 1 < p.it.first) return -1;
-    const int id = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
-    return id < 0 || id >= A.num_pages ? -2 : id;
+  RingPos at;
+  __device__ __forceinline__ explicit Reader(TileShared<S>& s) : sh(s) {}
+  __device__ __forceinline__ const Piece& wait() {
+    wait_phase(&sh.piece_full[at.slot], at.phase, &sh.dead);
+    return sh.piece[at.slot];
   }
-  __device__ __forceinline__ void load(const CUtensorMap* map, const Piece& p, int tile, int page,
-                                       bool value, int x) const {
-    const bool mine = page >= 0;
-    const uint32_t bytes =
-        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
-    const int slot_in_page = (tile * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
-#pragma unroll
-    for (int c = 0; c < S::U; ++c) {
-      const int s = unit_slot<S>(value, x, c);
-      const uint32_t pass = unit_pass<S>(value, x, c);
-      if (pass > 0) wait_phase(&sh.empty[s], (pass - 1) & 1u, &sh.dead);
-      __syncwarp();
-      const bool dead = __any_sync(0xffffffffu, *(volatile int*)&sh.dead);
-      if (dead) continue;
-      if (lane == 0) {
-        sh.issued[s] = (int)pass + 1;
-        mbar_arrive_expect_tx(&sh.full[s], bytes);
-      }
-      __syncwarp();
-      if (mine)
-        tile_g2s(ring + s * kUnitBytes + lane * A.box * 128, map, &sh.full[s], c * 64,
-                 slot_in_page, p.h, page);
+  // One thread of each role (of the softmax, of each warp) gives the place back.
+  __device__ __forceinline__ void release(bool mine) {
+    if (mine) mbar_arrive(&sh.piece_empty[at.slot]);
+    at.next(kPieceQueue);
+  }
+  // Takes the next piece with tiles, by one thread or (kWarp) by a whole warp; false at the end
+  // of the list or when the CTA has given up.
+  template <bool kWarp>
+  __device__ __forceinline__ bool next(Piece& p) {
+#pragma unroll 1
+    for (;;) {
+      p = wait();
+      bool end = *(volatile int*)&sh.dead || (p.flags & kEndOfList);
+      if (kWarp) end = __any_sync(0xffffffffu, end);  // (and every lane has read the piece)
+      if (end) return false;
+      release(!kWarp || (threadIdx.x & 31) == 0);
+      if (p.mb > p.ma) return true;
     }
   }
 };
 
-template <class S>
+// ---- the copying warps ------------------------------------------------------------------------
+// Whether some row sees a key of the lane's group of `box` keys in a tile, and that group's page
+// (not looked at here: the load is a tile ahead of its use).
+__device__ __forceinline__ bool group_seen(const TileArgs& A, const Piece& p, int tile, int lane) {
+  const int j = tile * kTileKeys + lane * A.box;
+  return lane * A.box < kTileKeys && j <= p.last && j + A.box - 1 >= p.first;
+}
+__device__ __forceinline__ int group_page(const TileArgs& A, const Piece& p, int tile, int lane) {
+  const int j = tile * kTileKeys + lane * A.box;
+  return __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
+}
+
+// One warp walks the work list, hands out the pieces and copies the keys (and the queries) of
+// their tiles; another copies the values. Each lane starts the copies of its group of keys; the
+// pages of the next tile are looked up a tile ahead. (All roles' loops are kept short and rolled:
+// together they have to stay in the instruction cache, whose misses are latency of every tile.)
+template <class S, bool kValues>
 __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
                                           unsigned char* qbuf, unsigned char* ring,
-                                          const CUtensorMap* mq, const CUtensorMap* mk,
-                                          const CUtensorMap* mv) {
+                                          const CUtensorMap* mq, const CUtensorMap* map) {
+  constexpr int kBase = kValues ? S::NK : 0, kUnits = kValues ? S::NV + S::Weigh : S::NK;
   const int lane = threadIdx.x & 31;
-  Loader<S> L{A, sh, ring, lane};
-  Walk<S> w(A, sh.start);
-  Piece p, prev{};
-  int x = 0, ordinal = 0, prev_tile = 0, prev_page = 0;
-  while (w.next(p)) {
-    for (int rb = 0; S::Weigh ? weigh_pass(A, p, rb) : rb == 0; ++rb) {
-      if (p.mb <= p.ma) continue;
-      const int qs = ordinal % S::NQ, qp = ordinal / S::NQ;
-      if (qp > 0) wait_phase(&sh.q_empty[qs], (uint32_t)(qp - 1) & 1u, &sh.dead);
-      __syncwarp();
-      if (lane == 0 && !*(volatile int*)&sh.dead) {
-        sh.q_issued[qs] = qp + 1;
-        mbar_arrive_expect_tx(&sh.q_full[qs], (uint32_t)(A.G * A.pos_block * S::D * 2));
-        for (int c = 0; c < S::U; ++c)
-          tile_g2s(qbuf + qs * S::QBytes + c * S::N * 128, mq, &sh.q_full[qs], c * 64, p.h * A.G,
-                   p.it.i0, p.b);
+  unsigned char* dst = ring + kBase * kUnitBytes + lane * A.box * 128;
+  Walk<S> walk(A, sh.start);
+  Reader<S> reader(sh);
+  // the next piece with tiles; all lanes
+  auto take = [&](Piece& p) -> bool {
+#pragma unroll 1
+    for (;;) {
+      if (kValues) return reader.template next<true>(p);
+      const bool more = walk.next(p);
+      if (!more) p.flags = kEndOfList;
+      bool ok = wait_phase(&sh.piece_empty[reader.at.slot], reader.at.phase ^ 1u, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (lane == 0) {
+        sh.piece[reader.at.slot] = p;
+        mbar_arrive(&sh.piece_full[reader.at.slot]);
       }
-      __syncwarp();
-      int page = L.page_of(p, tile_at<S>(p, 0));
-      for (int i = 0; i < p.mb - p.ma; ++i) {
-        const int t = tile_at<S>(p, i);
-        const int next_page = i + 1 < p.mb - p.ma ? L.page_of(p, tile_at<S>(p, i + 1)) : -1;
-        if (__any_sync(0xffffffffu, page == -2) && lane == 0)
-          *(volatile int*)&sh.bad_piece[ordinal & 7] = ordinal + 1;
-        __syncwarp();
-        L.load(mk, p, t, page, false, x);
-        if (!S::Weigh) {
-          if (x > 0) L.load(mv, prev, prev_tile, prev_page, true, x - 1);
-          prev = p;
-          prev_tile = t;
-          prev_page = page;
-        }
-        page = next_page;
-        ++x;
-      }
-      ++ordinal;
+      reader.at.next(kPieceQueue);
+      if (!more || !ok) return false;
+      if (p.mb > p.ma) return true;
     }
+  };
+  Piece p;
+  bool more = take(p);
+  int i = 0;
+  bool seen = more && group_seen(A, p, tile_at<S>(p, 0), lane);
+  int page = seen ? group_page(A, p, tile_at<S>(p, 0), lane) : 0;
+  RingPos at;
+  int issued = 0, q_issued = 0;
+  bool ok = true;
+#pragma unroll 1
+  while (more) {
+    const int head = p.h, turn = p.turn;
+    const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
+    if (!kValues && i == 0) {
+      const int qs = turn % S::NQ;
+      ok = wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sh.q_full[qs], (uint32_t)(A.G * A.pos_block * S::D * 2));
+#pragma unroll 1
+          for (int c = 0; c < S::U; ++c)
+            tile_g2s(qbuf + qs * S::QBytes + c * S::N * 128, mq, &sh.q_full[qs], c * 64,
+                     head * A.G, p.i0, p.b);
+        }
+        ++q_issued;
+      }
+      __syncwarp();
+    }
+    if (__builtin_expect(++i == p.mb - p.ma, 0)) {
+      more = take(p);
+      i = 0;
+    }
+    const bool next_seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
+    const int next_page = next_seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
+    const bool mine = seen && page >= 0 && page < A.num_pages;
+    if (!kValues) {
+      if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
+        *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
+    }
+    const uint32_t bytes =
+        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
+#pragma unroll 1
+    for (int c = 0; c < S::U; ++c) {
+      uint64_t* full = &sh.full[kBase + at.slot];
+      ok = wait_phase(&sh.empty[kBase + at.slot], at.phase ^ 1u, &sh.dead);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+        ++issued;
+      }
+      __syncwarp();
+      if (ok && mine) tile_g2s(dst + at.slot * kUnitBytes, map, full, c * 64, slot, head, page);
+      at.next(kUnits);
+    }
+    page = next_page;
+    seen = next_seen;
   }
-  if (!S::Weigh && x > 0) L.load(mv, prev, prev_tile, prev_page, true, x - 1);
   if (*(volatile int*)&sh.dead && lane == 0) {
     // given up: no copy may outlive the CTA
-    for (int s = 0; s < S::NU; ++s)
-      if (sh.issued[s] > 0) mbar_wait(&sh.full[s], (uint32_t)(sh.issued[s] - 1) & 1u, kTileWaitNs);
-    for (int s = 0; s < S::NQ; ++s)
-      if (sh.q_issued[s] > 0)
-        mbar_wait(&sh.q_full[s], (uint32_t)(sh.q_issued[s] - 1) & 1u, kTileWaitNs);
+#pragma unroll 1
+    for (int u = issued > kUnits ? issued - kUnits : 0; u < issued; ++u)
+      mbar_wait(&sh.full[kBase + u % kUnits], (uint32_t)(u / kUnits) & 1u, kTileWaitNs);
+#pragma unroll 1
+    for (int u = q_issued > S::NQ ? q_issued - S::NQ : 0; u < q_issued; ++u)
+      mbar_wait(&sh.q_full[u % S::NQ], (uint32_t)(u / S::NQ) & 1u, kTileWaitNs);
   }
   __syncwarp();
 }
 
 // ---- the threads that issue the matrix instructions -------------------------------------------
 // One issues the scores, as far ahead as their buffers allow, one the products with the values.
-template <class S>
-struct Issuer {
-  const TileArgs& A;
-  TileShared<S>& sh;
-  uint32_t q_addr, p_addr, ring_addr, tmem;
-  uint32_t qk_desc, pv_desc;
-
-  __device__ __forceinline__ bool dead() const { return *(volatile int*)&sh.dead != 0; }
-
-  // S^T of the x-th tile into a team's score buffer `buf`.
-  __device__ __forceinline__ void scores(int x, int qs, int team, int buf) const {
-#pragma unroll
-    for (int c = 0; c < S::U; ++c) {
-      const int s = unit_slot<S>(false, x, c);
-      wait_phase(&sh.full[s], unit_pass<S>(false, x, c) & 1u, &sh.dead);
-      tc_fence_after();
-      if (dead()) continue;
-      const uint32_t a0 = ring_addr + s * kUnitBytes;
-      const uint32_t b0 = q_addr + qs * S::QBytes + c * S::N * 128;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        mma_f16(tmem + (2 * team + buf) * S::N, smem_desc(a0 + 32 * k, 16, 1024, kSwizzle128),
-                smem_desc(b0 + 32 * k, 16, 1024, kSwizzle128), qk_desc, c > 0 || k > 0);
-      mma_commit(&sh.empty[s]);
-    }
-    if (!dead()) mma_commit(&sh.s_full[team][buf]);
-  }
-  // O^T (+)= V^T P^T of the x-th tile, the y-th of its team. Of an edge tile the softmax threads
-  // clean the values once they have landed, before they pass on the weights.
-  __device__ __forceinline__ void values(int x, int y, bool first, bool last, bool edge,
-                                         int ordinal) const {
-    const int team = ordinal % S::Teams, ob = ordinal & 1;
-    const int pb = y % S::NP;
-    const uint32_t p_at = p_addr + (team * S::NP + pb) * S::PBytes;
-    if (edge) {
-#pragma unroll
-      for (int c = 0; c < S::U; ++c)
-        wait_phase(&sh.full[unit_slot<S>(true, x, c)], unit_pass<S>(true, x, c) & 1u, &sh.dead);
-      if (!dead()) mbar_arrive(&sh.v_ready[team]);
-    }
-    wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.dead);
-    tc_fence_after();
-    constexpr int kPer = S::U >= 2 ? 2 : 1;  // units per accumulator
-#pragma unroll
-    for (int m = 0; m < S::MBlocks; ++m) {
-      const int s = unit_slot<S>(true, x, m * kPer);
-#pragma unroll
-      for (int c = m * kPer; c < (m + 1) * kPer; ++c)
-        wait_phase(&sh.full[unit_slot<S>(true, x, c)], unit_pass<S>(true, x, c) & 1u, &sh.dead);
-      tc_fence_after();
-      if (dead()) continue;
-      const uint32_t a0 = ring_addr + s * kUnitBytes;
-#pragma unroll
-      for (int part = 0; part < (S::Wide ? 1 : 2); ++part)  // the weights' high and low halves
-#pragma unroll
-        for (int k = 0; k < kTileKeys / 16; ++k)
-          // values of 64 columns lie 128 bytes per key; with D = 64 both halves of the
-          // instruction's rows read the same columns, and the upper half is not used
-          mma_f16(tmem + 2 * S::Teams * S::N + (ob * S::MBlocks + m) * S::ON,
-                  smem_desc(a0 + k * 2048, kPer == 2 ? kUnitBytes : 0, 1024, kSwizzle128),
-                  smem_desc(p_at + part * (kTileKeys * S::N * 2) + k * 512, kTileKeys * 32, 256,
-                            kSwizzle32),
-                  pv_desc, !(first && part == 0 && k == 0));
-#pragma unroll
-      for (int c = m * kPer; c < (m + 1) * kPer; ++c)
-        mma_commit(&sh.empty[unit_slot<S>(true, x, c)]);
-    }
-    if (!dead()) {
-      mma_commit(&sh.pv_done[team][pb]);
-      if (last) mma_commit(&sh.o_done[ob]);
-    }
-  }
-};
-
-template <class S>
-__device__ __forceinline__ Issuer<S> issuer(const TileArgs& A, TileShared<S>& sh,
-                                            unsigned char* qbuf, unsigned char* pbuf,
-                                            unsigned char* ring) {
-  return Issuer<S>{A, sh, smem_u32(qbuf), smem_u32(pbuf), smem_u32(ring), sh.tmem,
-                   mma_desc(A.bf16, false, false, 128, S::N),
-                   mma_desc(A.bf16, true, true, 128, S::ON)};
-}
-
 // Given up: no instruction may outlive the tensor memory.
 template <class S>
 __device__ __forceinline__ void drain(TileShared<S>& sh, int which) {
@@ -606,49 +595,109 @@ __device__ __forceinline__ void drain(TileShared<S>& sh, int which) {
   mbar_wait(&sh.drain[which], 0, kTileWaitNs);
 }
 
+// S^T = K Q^T of every tile.
 template <class S>
-__device__ __forceinline__ void score_role(const TileArgs& A, const Issuer<S>& I,
-                                           TileShared<S>& sh) {
-  Walk<S> w(A, sh.start);
+__device__ __forceinline__ void score_role(const TileArgs& A, TileShared<S>& sh,
+                                           unsigned char* qbuf, unsigned char* ring) {
+  const uint32_t idesc = mma_desc(A.bf16, false, false, 128, S::N);
+  const uint64_t rows = smem_desc(0, 16, 1024, kSwizzle128);
+  const uint64_t a0 = rows + (smem_u32(ring) >> 4), b0 = rows + (smem_u32(qbuf) >> 4);
+  Reader<S> reader(sh);
+  RingPos at;
+  int used[2] = {0, 0};  // tiles so far per team (attention) or per score buffer (key weights)
+  bool ok = true;
   Piece p;
-  // used: tiles so far per team (attention) or per score buffer (key weights)
-  int x = 0, ordinal = 0, used[2] = {0, 0};
-  while (w.next(p)) {
-    for (int rb = 0; S::Weigh ? weigh_pass(A, p, rb) : rb == 0; ++rb) {
-      if (p.mb <= p.ma) continue;
-      const int qs = ordinal % S::NQ, team = ordinal % S::Teams;
-      wait_phase(&sh.q_full[qs], (uint32_t)(ordinal / S::NQ) & 1u, &sh.dead);
-      for (int i = 0; i < p.mb - p.ma; ++i) {
-        const int of = S::Weigh ? tile_at<S>(p, i) & 1 : team;
-        const int y = of ? used[1]++ : used[0]++;
-        const int buf = S::Weigh ? of : y & 1, turn = S::Weigh ? y : y >> 1;
-        if (turn > 0) wait_phase(&sh.s_empty[team][buf], (uint32_t)(turn - 1) & 1u, &sh.dead);
+#pragma unroll 1
+  while (reader.template next<false>(p)) {
+    const int qs = p.turn % S::NQ, team = p.turn % S::Teams, tiles = p.mb - p.ma;
+    wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.dead);
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int of = S::Weigh ? tile_at<S>(p, i) & 1 : team;
+      const int y = of ? used[1]++ : used[0]++;
+      const int buf = S::Weigh ? of : y & 1, turn = S::Weigh ? y : y >> 1;
+      wait_phase(&sh.s_empty[team][buf], ((uint32_t)turn & 1u) ^ 1u, &sh.dead);
+      tc_fence_after();
+      const uint32_t d = sh.tmem + (2 * team + buf) * S::N;
+      uint64_t b = b0 + qs * (S::QBytes >> 4);
+#pragma unroll 1
+      for (int c = 0; c < S::U; ++c, b += S::N * 8) {
+        ok = wait_phase(&sh.full[at.slot], at.phase, &sh.dead);
         tc_fence_after();
-        I.scores(x, qs, team, buf);
-        if (i + 1 == p.mb - p.ma && !I.dead()) mma_commit(&sh.q_empty[qs]);
-        ++x;
+        const uint64_t a = a0 + at.slot * (kUnitBytes >> 4);
+        if (ok) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_f16(d, a + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
+          mma_commit(&sh.empty[at.slot]);
+        }
+        at.next(S::NK);
       }
-      ++ordinal;
+      if (ok) mma_commit(&sh.s_full[team][buf]);
     }
+    if (ok) mma_commit(&sh.q_empty[qs]);
   }
   drain<S>(sh, 0);
 }
 
+// O^T (+)= V^T P^T of every tile. Of an edge tile the softmax threads clean the values once they
+// have landed, before they pass on the weights.
 template <class S>
-__device__ __forceinline__ void value_role(const TileArgs& A, const Issuer<S>& I,
-                                           TileShared<S>& sh) {
-  Walk<S> w(A, sh.start);
+__device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
+                                           unsigned char* pbuf, unsigned char* ring) {
+  constexpr int kPer = S::U >= 2 ? 2 : 1;  // units per accumulator
+  const uint32_t idesc = mma_desc(A.bf16, true, true, 128, S::ON);
+  // values of 64 columns lie 128 bytes per key; with D = 64 both halves of the instruction's rows
+  // read the same columns, and the upper half is not used
+  const uint64_t a0 = smem_desc(0, kPer == 2 ? kUnitBytes : 0, 1024, kSwizzle128) +
+                      ((smem_u32(ring) + S::NK * kUnitBytes) >> 4);
+  const uint64_t b0 = smem_desc(0, kTileKeys * 32, 256, kSwizzle32) + (smem_u32(pbuf) >> 4);
+  Reader<S> reader(sh);
+  RingPos at;
+  int used[2] = {0, 0};
   Piece p;
-  int x = 0, ordinal = 0, used[2] = {0, 0};
-  while (w.next(p)) {
-    const int tiles = p.mb - p.ma;
-    if (tiles == 0) continue;
-    for (int i = 0; i < tiles; ++i, ++x) {
-      const int y = ordinal % S::Teams ? used[1]++ : used[0]++;
-      I.values(x, y, i == 0, i + 1 == tiles, edge_tile(p.it, A.rule.window, tile_at<S>(p, i)),
-               ordinal);
+#pragma unroll 1
+  while (reader.template next<false>(p)) {
+    const int team = p.turn % S::Teams, tiles = p.mb - p.ma;
+    const uint32_t o = sh.tmem + 2 * S::Teams * S::N + (p.turn & 1) * S::MBlocks * S::ON;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int y = team ? used[1]++ : used[0]++, pb = y % S::NP;
+      bool ok = true;
+      if (__builtin_expect(edge_tile(p, A.rule.window, tile_at<S>(p, i)), 0)) {
+        RingPos look = at;
+#pragma unroll 1
+        for (int c = 0; c < S::U; ++c) {
+          ok = wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.dead);
+          look.next(S::NV);
+        }
+        if (ok) mbar_arrive(&sh.v_ready[team]);
+      }
+      ok = wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.dead);
+      const uint64_t b = b0 + (team * S::NP + pb) * (S::PBytes >> 4);
+      uint32_t d = o;
+#pragma unroll 1
+      for (int m = 0; m < S::MBlocks; ++m, d += S::ON) {
+        const uint64_t a = a0 + at.slot * (kUnitBytes >> 4);
+        uint64_t* empty = &sh.empty[S::NK + at.slot];
+#pragma unroll 1
+        for (int c = 0; c < kPer; ++c) {
+          ok = wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.dead);
+          at.next(S::NV);
+        }
+        tc_fence_after();
+        if (!ok) continue;
+#pragma unroll 1
+        for (int part = 0; part < (S::Wide ? 1 : 2); ++part)  // the weights' high and low halves
+#pragma unroll 4
+          for (int k = 0; k < kTileKeys / 16; ++k)
+            mma_f16(d, a + k * 128, b + part * (kTileKeys * S::N * 2 >> 4) + k * 32, idesc,
+                    !(i == 0 && part == 0 && k == 0));
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) mma_commit(empty + c);  // (a pair lies side by side)
+      }
+      if (ok) mma_commit(&sh.pv_done[team][pb]);
     }
-    ++ordinal;
+    if (!*(volatile int*)&sh.dead) mma_commit(&sh.o_done[p.turn & 1]);
   }
   drain<S>(sh, 1);
 }
@@ -668,6 +717,28 @@ __device__ __forceinline__ bool bar_or(int id, int threads, bool pred) {
       : "r"((uint32_t)pred), "r"(id), "r"(threads)
       : "memory");
   return r != 0;
+}
+// Two floats in one 64-bit register: one instruction for both.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  return v;
+}
+__device__ __forceinline__ float2 split(Two v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ Two two_fma(Two a, Two b, Two c) {
+  Two v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
+__device__ __forceinline__ Two two_add(Two a, Two b) {
+  Two v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
 }
 __device__ __forceinline__ float rcp_fast(float x) {
   float y;
@@ -706,7 +777,7 @@ template <int kC>
 __device__ __forceinline__ void apply_rule(float (&s)[kC], const ScoreRule& r, float away,
                                            const float* slope, const float* ahead) {
   const float scale2 = r.scale * kLog2e;
-  if (r.softcap > 0.0f) {
+  if (__builtin_expect(r.softcap > 0.0f, 0)) {
     // c tanh(y) = c - 2 c / (1 + 2^(2 log2(e) y))
     const float in = 2.0f * scale2 / r.softcap, c2 = r.softcap * kLog2e;
 #pragma unroll
@@ -715,7 +786,7 @@ __device__ __forceinline__ void apply_rule(float (&s)[kC], const ScoreRule& r, f
 #pragma unroll
     for (int c = 0; c < kC; ++c) s[c] *= scale2;
   }
-  if (r.slopes) {
+  if (__builtin_expect(r.slopes != nullptr, 0)) {
 #pragma unroll
     for (int c = 0; c < kC; ++c) s[c] = fmaf(-slope[c], away + ahead[c], s[c]);
   }
@@ -725,10 +796,11 @@ __device__ __forceinline__ void apply_rule(float (&s)[kC], const ScoreRule& r, f
 template <class S>
 __device__ __forceinline__ void set_columns(const TileArgs& A, typename TileShared<S>::Table& T,
                                             const Piece& p, int me, int all) {
+#pragma unroll 1
   for (int c = me; c < S::N; c += all) {
     const int i = c / A.G, g = c - i * A.G;
-    const bool live = i < p.it.live;
-    const int pos = p.it.pos0 + i;
+    const bool live = i < p.live;
+    const int pos = p.pos0 + i;
     T.slope[c] = live && A.rule.slopes ? __ldg(A.rule.slopes + p.h * A.G + g) * kLog2e : 0.0f;
     T.ahead[c] = (float)i;
     T.hi[c] = live ? pos : -1;
@@ -738,13 +810,13 @@ __device__ __forceinline__ void set_columns(const TileArgs& A, typename TileShar
       // a row that does not count, or one of no weight, gets none from any key
       float l = INFINITY;
       if (live) {
-        const float v = __ldg(A.lse + p.b * A.lse_req + (p.it.i0 + i) * A.lse_row +
+        const float v = __ldg(A.lse + p.b * A.lse_req + (p.i0 + i) * A.lse_row +
                               (p.h * A.G + g) * A.lse_head);
         if (v != -INFINITY) l = v * kLog2e;
       }
-      T.m[c] = l;
+      T.m[c] = -l;
     } else {
-      T.m[c] = kNoMax;
+      T.m[c] = live ? -kNoMax : kNoMax;  // (a column without a row never rises)
     }
   }
 }
@@ -807,29 +879,32 @@ struct Attend {
     bar_sync(S::Teams == 2 ? 1 + group : kAllBar, S::TeamThreads);
   }
   // The accumulator of a piece, the group's first column.
-  __device__ __forceinline__ uint32_t output(int ordinal) const {
-    return lane_base + 2 * S::Teams * S::N + (ordinal & 1) * S::MBlocks * S::ON + col0;
+  __device__ __forceinline__ uint32_t output(int turn) const {
+    return lane_base + 2 * S::Teams * S::N + (turn & 1) * S::MBlocks * S::ON + col0;
   }
 
   // Raise the maxima of the CH columns from c0 to those of this tile's scores s, and scale what
   // those columns hold.
-  __device__ __forceinline__ void raise(Table& T, const float (&s)[S::CH], float (&l)[S::NC], int k,
-                                        bool first, uint32_t o_base) {
+  __device__ __forceinline__ void raise(Table& T, const float (&s)[S::CH], Two (&l)[S::NC / 2],
+                                        int k, bool first, uint32_t o_base) {
     const int c0 = col0 + k;
     column_reduce<S::CH, true>(s, &T.red[quarter][c0], lane);
     group_sync();
     if (quarter == 0 && lane < S::CH) {
       const int c = c0 + lane;
-      const float was = T.m[c];
+      const float was = -T.m[c];
       const float m =
           fmaxf(fmaxf(fmaxf(T.red[0][c], T.red[1][c]), fmaxf(T.red[2][c], T.red[3][c])), was);
       T.alpha[c] = ex2(was - m);
-      T.m[c] = m;
+      T.m[c] = -m;
     }
     group_sync();
     if (first) return;
 #pragma unroll
-    for (int c = 0; c < S::CH; ++c) l[k + c] *= T.alpha[c0 + c];
+    for (int c = 0; c < S::CH; c += 2) {
+      const float2 v = split(l[(k + c) / 2]);
+      l[(k + c) / 2] = two(v.x * T.alpha[c0 + c], v.y * T.alpha[c0 + c + 1]);
+    }
     tc_fence_after();
 #pragma unroll 1
     for (int m = 0; m < S::MBlocks * (S::Wide ? 2 : 1); ++m)  // (wide: high and low products)
@@ -850,13 +925,13 @@ struct Attend {
   // that only some rows see, the values that are not finite become 0 and are added to the rows
   // that see it at the end (0 times infinity would reach the others).
   __device__ __forceinline__ void clean_values(Table& T, const Piece& p, int x, int j) {
-    const bool none = j > p.it.last || j < p.it.first;
-    const bool some = !none && (j > p.it.pos0 || j < first_full(p.it, A.rule.window));
+    const bool none = j > p.last || j < p.first;
+    const bool some = !none && (j > p.pos0 || j < first_full(p, A.rule.window));
     if (!__any_sync(0xffffffffu, none || some)) return;
     uint32_t odd = 0;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < S::U; ++c) {
-      uint4* row = reinterpret_cast<uint4*>(ring + unit_slot<S>(true, x, c) * kUnitBytes + key * 128);
+      uint4* row = reinterpret_cast<uint4*>(ring + value_slot<S>(x, c) * kUnitBytes + key * 128);
       // (each lane starts with another 16 bytes of its row: no bank conflicts)
       if (none) {
 #pragma unroll
@@ -872,10 +947,10 @@ struct Attend {
     }
     if (odd) {
       atomicOr(&T.odd_keys,
-               1u << (j > p.it.pos0 ? j - p.it.pos0 - 1 : 16 + j - p.it.first));
+               1u << (j > p.pos0 ? j - p.pos0 - 1 : 16 + j - p.first));
 #pragma unroll 1
       for (int c = 0; c < S::U; ++c) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(ring + unit_slot<S>(true, x, c) * kUnitBytes +
+        uint32_t* w = reinterpret_cast<uint32_t*>(ring + value_slot<S>(x, c) * kUnitBytes +
                                                   key * 128);
 #pragma unroll 1
         for (int e = 0; e < 32; ++e) {
@@ -887,16 +962,21 @@ struct Attend {
   }
 
   // One tile, the CTA's x-th and the team's y-th: its scores, their weights into shared memory.
+  // (What most tiles do is kept short: it has to stay in the instruction cache beside the other
+  // roles' loops.)
   __device__ __forceinline__ void tile(Table& T, const Piece& p, int t, bool first, int x, int y,
-                                       int ordinal, float (&l)[S::NC]) {
+                                       Two (&l)[S::NC / 2]) {
     const int buf = y & 1, j = t * kTileKeys + key;
-    const bool edge = edge_tile(p.it, A.rule.window, t);
+    const bool edge = edge_tile(p, A.rule.window, t);
+    unsigned char* const pb =
+        pbuf + (team * S::NP + y % S::NP) * S::PBytes + col0 / 16 * (kTileKeys * 32) + key * 32;
     wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.dead);
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < S::NC; k += S::CH) {
       const int c0 = col0 + k;
       float s[S::CH];
+      float scale = A.rule.scale * kLog2e;  // to what the thread holds in s
 #pragma unroll
       for (int q = 0; q < S::CH; q += 16)
         tmem_ld16(lane_base + (2 * team + buf) * S::N + c0 + q,
@@ -906,36 +986,58 @@ struct Attend {
         tc_fence_before();
         mbar_arrive(&sh.s_empty[team][buf]);
       }
-      apply_rule<S::CH>(s, A.rule, (float)(p.it.pos0 - j), &T.slope[c0], &T.ahead[c0]);
-      if (edge) {
+      if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
+        apply_rule<S::CH>(s, A.rule, (float)(p.pos0 - j), &T.slope[c0], &T.ahead[c0]);
+        scale = 1.0f;
+        if (edge) {
 #pragma unroll
-        for (int c = 0; c < S::CH; ++c)
-          if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[c] = -INFINITY;
+          for (int c = 0; c < S::CH; ++c)
+            if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[c] = -INFINITY;
+        }
       }
+      Two e[S::CH / 2];
+      auto exponents = [&]() {
+        const Two sc = two(scale, scale);
+#pragma unroll
+        for (int c = 0; c < S::CH; c += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&T.m[c0 + c]);
+          e[c / 2] = two_fma(two(s[c], s[c + 1]), sc, two(m.x, m.y));
+          e[c / 2 + 1] = two_fma(two(s[c + 2], s[c + 3]), sc, two(m.z, m.w));
+        }
+      };
+      exponents();
       float top = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < S::CH; ++c) top = fmaxf(top, s[c] - T.m[c0 + c]);
-      if (bar_or(1 + group, 128, top > 8.0f)) {
+      for (int c = 0; c < S::CH / 2; ++c) {
+        const float2 v = split(e[c]);
+        top = fmaxf(top, fmaxf(v.x, v.y));
+      }
+      if (__builtin_expect(bar_or(1 + group, 128, top > 8.0f), 0)) {
         if (!first) wait_values(y - 1);
-        raise(T, s, l, k, first, output(ordinal));
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) s[c] *= scale;
+        scale = 1.0f;
+        raise(T, s, l, k, first, output(p.turn));
+        exponents();
       }
       uint32_t hi[S::CH / 2], lo[S::CH / 2];
 #pragma unroll
-      for (int c = 0; c < S::CH; c += 2) {
-        const float a = ex2(s[c] - T.m[c0 + c]), b = ex2(s[c + 1] - T.m[c0 + c + 1]);
-        l[k + c] += a;
-        l[k + c + 1] += b;
-        hi[c / 2] = pack16<S::Bf16>(a, b);
-        const float2 h = unpack16<S::Bf16>(hi[c / 2]);
-        lo[c / 2] = pack16<S::Bf16>(a - h.x, b - h.y);
+      for (int c = 0; c < S::CH / 2; ++c) {
+        const float2 v = split(e[c]);
+        const float a = ex2(v.x), b = ex2(v.y);
+        const Two w = two(a, b);
+        l[k / 2 + c] = two_add(l[k / 2 + c], w);
+        hi[c] = pack16<S::Bf16>(a, b);
+        const float2 h = unpack16<S::Bf16>(hi[c]);
+        const float2 r = split(two_fma(two(h.x, h.y), two(-1.0f, -1.0f), w));
+        lo[c] = pack16<S::Bf16>(r.x, r.y);
       }
       // the product that last read this buffer
       if (k == 0 && y >= S::NP) wait_values(y - S::NP);
 #pragma unroll
       for (int q = 0; q < S::CH; q += 16) {
         // 16 columns of a key: 32 bytes, their 16-byte halves swapped in every other 4 keys
-        unsigned char* at = pbuf + (team * S::NP + y % S::NP) * S::PBytes +
-                            (c0 + q) / 16 * (kTileKeys * 32) + key * 32;
+        unsigned char* at = pb + (k + q) / 16 * (kTileKeys * 32);
         const int sw = ((key >> 2) & 1) * 16, w = q / 2;
         *reinterpret_cast<uint4*>(at + sw) = make_uint4(hi[w], hi[w + 1], hi[w + 2], hi[w + 3]);
         *reinterpret_cast<uint4*>(at + (16 - sw)) =
@@ -946,7 +1048,7 @@ struct Attend {
             make_uint4(lo[w + 4], lo[w + 5], lo[w + 6], lo[w + 7]);
       }
     }
-    if (edge) {
+    if (__builtin_expect(edge, 0)) {
       wait_phase(&sh.v_ready[team], (uint32_t)(edges++) & 1u, &sh.dead);
       if (S::Teams == 2 || group == 0) clean_values(T, p, x, j);
     }
@@ -957,37 +1059,41 @@ struct Attend {
 
   // Output row of a piece's first column.
   __device__ __forceinline__ int64_t first_row(const Piece& p) const {
-    return ((int64_t)p.b * A.P + p.it.i0) * A.Hq + p.h * A.G;
+    return ((int64_t)p.b * A.P + p.i0) * A.Hq + p.h * A.G;
   }
 
   // Rows without a visible key, or of a request with bad counts.
   __device__ __forceinline__ void fill(const Table& T, const Piece& p) const {
     const int64_t row0 = first_row(p);
-    const float v = p.it.bad ? __uint_as_float(0x7fc00000u) : 0.0f;
-    const int rows = p.it.live * A.G;
+    const bool bad = p.flags & kBad;
+    const float v = bad ? __uint_as_float(0x7fc00000u) : 0.0f;
+    const int rows = p.live * A.G;
+#pragma unroll 1
     for (int e = me; e < rows * S::D; e += S::TeamThreads)
       store16<S::Bf16>(A.out, (row0 + T.row[e / S::D]) * S::D + e % S::D, v);
     if (A.out_lse)
+#pragma unroll 1
       for (int c = me; c < rows; c += S::TeamThreads)
-        A.out_lse[row0 + T.row[c]] = p.it.bad ? v : -INFINITY;
+        A.out_lse[row0 + T.row[c]] = bad ? v : -INFINITY;
   }
 
   // The end of a piece (its sums' warp parts are in T.red): O and the sums leave for the output
   // or for the workspace.
-  __device__ __forceinline__ void finish(Table& T, const Piece& p, int ordinal) {
+  __device__ __forceinline__ void finish(Table& T, const Piece& p) {
     group_sync();
     const bool poison = *(volatile int*)&sh.dead ||
-                        *(volatile int*)&sh.bad_piece[ordinal & 7] == ordinal + 1;
-    const bool whole = p.starts && p.ends;
-    const int rows = p.it.live * A.G;
+                        *(volatile int*)&sh.bad_piece[p.turn & 7] == p.turn + 1;
+    const bool starts = p.flags & kStarts, whole = starts && (p.flags & kEnds);
+    const int rows = p.live * A.G;
     const int64_t row0 = first_row(p);
     float* part =
-        A.part + (2 * (int64_t)blockIdx.x + (p.starts ? 1 : 0)) * (S::N * (S::D + 2));
+        A.part + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * (S::N * (S::D + 2));
     if (quarter == 0) {
+#pragma unroll 1
       for (int c = col0 + lane; c < col0 + S::NC; c += 32) {
         float sum = (T.red[0][c] + T.red[1][c]) + (T.red[2][c] + T.red[3][c]);
         if (poison) sum = __uint_as_float(0x7fc00000u);
-        const float m = T.m[c];
+        const float m = -T.m[c];
         if (c < rows) {
           if (!whole)
             *reinterpret_cast<float2*>(part + S::N * S::D + 2 * c) = make_float2(m, sum);
@@ -995,18 +1101,16 @@ struct Attend {
             A.out_lse[row0 + T.row[c]] =
                 sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
         }
-        T.alpha[c] = !whole ? 1.0f : sum == 0.0f ? 0.0f : 1.0f / sum;
+        T.alpha[c] = !whole ? 1.0f : sum == 0.0f ? 0.0f : rcp_fast(sum);
       }
     }
-    if (me == 0 && p.starts && !whole) {
-      const int64_t at = p.item0 + S::PieceCost, per = sh.start.per;
-      sh.join.pieces =
-          (int)((at + (int64_t)(p.it.tiles - 1) * S::TileCost) / per - at / per) + 1;
+    if (me == 0 && starts && !whole) {
+      sh.join.pieces = p.pieces;
       sh.join.row0 = row0;
       sh.join.rows = rows;
     }
     group_sync();
-    wait_phase(&sh.o_done[ordinal & 1], (uint32_t)(ordinal >> 1) & 1u, &sh.dead);
+    wait_phase(&sh.o_done[p.turn & 1], (uint32_t)(p.turn >> 1) & 1u, &sh.dead);
     tc_fence_after();
     if (S::D >= 128 || quarter < 2) {
       int d = quarter * 32 + lane;
@@ -1015,10 +1119,10 @@ struct Attend {
 #pragma unroll 1
         for (int q = 0; q < S::NC && col0 + q < rows; q += 16) {
           float o[16];
-          tmem_ld16(output(ordinal) + m * S::ON + q, o);
+          tmem_ld16(output(p.turn) + m * S::ON + q, o);
           if (S::Wide) {
             float low[16];
-            tmem_ld16(output(ordinal) + m * S::ON + S::N + q, low);
+            tmem_ld16(output(p.turn) + m * S::ON + S::N + q, low);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 16; ++c) o[c] += low[c];
@@ -1058,7 +1162,7 @@ struct Attend {
 #pragma unroll 1
         for (unsigned int left = odd; left; left &= left - 1) {
           const int bit = __ffs(left) - 1;
-          const int j = bit < 16 ? p.it.pos0 + 1 + bit : p.it.first + bit - 16;
+          const int j = bit < 16 ? p.pos0 + 1 + bit : p.first + bit - 16;
           if (j > T.hi[n] || j <= T.lo[n]) continue;
           const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
           if (page < 0 || page >= A.num_pages) continue;
@@ -1079,60 +1183,62 @@ struct Attend {
   // one is in the tensor cores' hands, so that its last product, and its output, pass under that
   // tile; with two the other team's tiles cover it.
   __device__ __forceinline__ void run() {
-    Walk<S> w(A, sh.start);
-    Piece p, ended;
-    int x = 0, y = 0, ordinal = -1, next = 0, fills = 0, ended_ordinal = 0;
-    int i = 0, tiles = 0;
+    Reader<S> reader(sh);
+    Piece p{}, ended{};
+    int y = 0, i = 0;
     bool pending = false;
-    float l[S::NC];
+    Two l[S::NC / 2];
+    auto table = [&](int turn) -> Table& { return sh.table[S::Teams == 2 ? team : turn & 1]; };
+#pragma unroll 1
     for (;;) {
       const bool flush = S::Teams == 2 && pending;  // the end first
       bool more = true;
       if (!flush) {
-        if (i == tiles) {
+        if (__builtin_expect(i == p.mb - p.ma, 0)) {
+#pragma unroll 1
           for (;;) {
-            more = w.next(p);
+            p = reader.wait();
+            more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.dead;
+            more = !bar_or(1 + group, 128, !more);
+            if (S::Teams == 1) more = !bar_or(kAllBar, S::SoftThreads, !more);
             if (!more) break;
-            i = 0;
-            tiles = p.mb - p.ma;
-            const int turn = tiles > 0 ? next++ : fills++;
-            if (turn % S::Teams != team) {
-              x += tiles;
-              continue;
-            }
-            // (a piece without tiles borrows the table of the next one with tiles)
-            Table& T = sh.table[S::Teams == 2 ? team : ((tiles > 0 ? turn : next) + 1) & 1];
+            reader.release(lane == 0);
+            const int tiles = p.mb - p.ma;
+            if (p.turn % S::Teams != team) continue;
+            // (a piece without tiles borrows the table that is not the ended piece's)
+            Table& T = table(tiles > 0 ? p.turn : pending ? ended.turn + 1 : 0);
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
             if (me == 0) T.odd_keys = 0;
             team_sync();
-            if (tiles > 0) {
-              ordinal = turn;
-              break;
-            }
+            i = 0;
+            if (tiles > 0) break;
             fill(T, p);
           }
 #pragma unroll
-          for (int c = 0; c < S::NC; ++c) l[c] = 0.0f;
+          for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
         }
         if (more) {
-          tile(sh.table[S::Teams == 2 ? team : (ordinal + 1) & 1], p, tile_at<S>(p, i), i == 0, x,
-               y, ordinal, l);
+          tile(table(p.turn), p, tile_at<S>(p, i), i == 0, p.x0 + i, y, l);
           ++i;
-          ++x;
           ++y;
         }
       }
       if (pending) {
-        finish(sh.table[S::Teams == 2 ? team : (ended_ordinal + 1) & 1], ended, ended_ordinal);
+        finish(table(ended.turn), ended);
         pending = false;
       }
       if (!more) break;
-      if (!flush && i == tiles) {
-        Table& T = sh.table[S::Teams == 2 ? team : (ordinal + 1) & 1];
-        column_reduce<S::NC, false>(l, &T.red[quarter][col0], lane);
+      if (!flush && i == p.mb - p.ma) {
+        float sums[S::NC];
+#pragma unroll
+        for (int c = 0; c < S::NC; c += 2) {
+          const float2 v = split(l[c / 2]);
+          sums[c] = v.x;
+          sums[c + 1] = v.y;
+        }
+        column_reduce<S::NC, false>(sums, &table(p.turn).red[quarter][col0], lane);
         ended = p;
-        ended_ordinal = ordinal;
         pending = true;
       }
     }
@@ -1147,58 +1253,85 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
   const uint32_t lane_base = sh.tmem + ((uint32_t)(quarter * 32) << 16);
   const float nan = __uint_as_float(0x7fc00000u);
   auto& T = sh.table[0];
-  Walk<S> w(A, sh.start);
+  Reader<S> reader(sh);
   Piece p;
   int used = 0;  // tiles this group has taken from its S buffer
-  while (w.next(p)) {
+#pragma unroll 1
+  for (;;) {
+    p = reader.wait();
+    bool more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.dead;
+    more = !bar_or(kAllBar, S::SoftThreads, !more);  // (the last piece's tables have been read)
+    if (!more) return;
+    reader.release(lane == 0);
     const int64_t row = ((int64_t)p.b * A.Hkv + p.h) * A.stride;
     float* out = A.weights + row;
     const float* prior = A.prior ? A.prior + row : nullptr;
-    if (p.it.bad) {
-      if (threadIdx.x == 0) out[0] = nan;
-      continue;
-    }
-    for (int rb = 0; weigh_pass(A, p, rb); ++rb) {
-      bar_sync(kAllBar, S::SoftThreads);
+    const int pass = p.pass;
+    {
+      if (p.flags & kBad) {
+        if (threadIdx.x == 0) out[0] = nan;
+        continue;
+      }
       set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
       bar_sync(kAllBar, S::SoftThreads);
-      const int ta = rb == 0 ? p.ta : p.ma, tb = rb == 0 ? p.tb : p.mb;
-      for (int t = ta; t < tb; ++t) {
-        if ((t & 1) != group) continue;
+      const int ta = pass == 0 ? p.ta : p.ma, tb = pass == 0 ? p.tb : p.mb;
+      // what a key's slot holds already and its page, loaded a tile ahead
+      auto held = [&](int t) {
         const int j = t * kTileKeys + key;
-        const bool inside = j < p.it.n;
-        float total = 0.0f, before = 0.0f;
-        if (inside) before = rb > 0 ? out[j] : prior ? prior[j] : 0.0f;
+        return t < tb && j < p.n ? (pass > 0 ? out[j] : prior ? prior[j] : 0.0f) : 0.0f;
+      };
+      auto page_of = [&](int t) {
+        const int j = t * kTileKeys + key;
+        return t < p.mb && j >= p.first && j <= p.last
+                   ? __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page))
+                   : 0;
+      };
+      int t = ta + ((ta ^ group) & 1);
+      float before = held(t);
+      int page = page_of(t);
+#pragma unroll 1
+      for (; t < tb; t += 2) {
+        const float next_before = held(t + 2);
+        const int next_page = page_of(t + 2);
+        const int j = t * kTileKeys + key;
+        float total = 0.0f;
         if (t >= p.ma && t < p.mb) {
-          bool bad = false;
-          if (j >= p.it.first && j <= p.it.last) {
-            const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
-            bad = page < 0 || page >= A.num_pages;
-          }
-          const bool edge = edge_tile(p.it, A.rule.window, t);
+          const bool edge = edge_tile(p, A.rule.window, t);
           wait_phase(&sh.s_full[0][group], (uint32_t)used & 1u, &sh.dead);
           ++used;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < S::N; q += 16) {
             float s[16];
             tmem_ld16(lane_base + group * S::N + q, s);
             tmem_wait_ld();
-            apply_rule<16>(s, A.rule, (float)(p.it.pos0 - j), &T.slope[q], &T.ahead[q]);
-            float part = 0.0f;
+            float scale = A.rule.scale * kLog2e;
+            if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
+              apply_rule<16>(s, A.rule, (float)(p.pos0 - j), &T.slope[q], &T.ahead[q]);
+              scale = 1.0f;
+              if (edge) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float e = ex2(s[c] - T.m[q + c]);
-              if (edge && (j > T.hi[q + c] || j <= T.lo[q + c])) e = 0.0f;
-              part += e;
+                for (int c = 0; c < 16; ++c)
+                  if (j > T.hi[q + c] || j <= T.lo[q + c]) s[c] = -INFINITY;
+              }
             }
-            total += part;
+            const Two sc = two(scale, scale);
+            Two part = 0ull;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) {
+              const float2 m = *reinterpret_cast<const float2*>(&T.m[q + c]);
+              const float2 e = split(two_fma(two(s[c], s[c + 1]), sc, two(m.x, m.y)));
+              part = two_add(part, two(ex2(e.x), ex2(e.y)));
+            }
+            total += split(part).x + split(part).y;
           }
           tc_fence_before();
           mbar_arrive(&sh.s_empty[0][group]);
-          if (bad || *(volatile int*)&sh.dead) total = nan;
+          if (page < 0 || page >= A.num_pages || *(volatile int*)&sh.dead) total = nan;
         }
-        if (inside) out[j] = before + total;
+        if (j < p.n) out[j] = before + total;
+        before = next_before;
+        page = next_page;
       }
     }
   }
@@ -1221,15 +1354,14 @@ __global__ void __launch_bounds__(S::Threads, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
 
   if (tid == 0) {
+#pragma unroll 1
     for (int s = 0; s < S::NU; ++s) {
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.empty[s], 1);
-      sh.issued[s] = 0;
     }
     for (int s = 0; s < S::NQ; ++s) {
       mbar_init(&sh.q_full[s], 1);
       mbar_init(&sh.q_empty[s], 1);
-      sh.q_issued[s] = 0;
     }
     for (int t = 0; t < S::Teams; ++t) {
       for (int s = 0; s < 2; ++s) {
@@ -1244,6 +1376,11 @@ __global__ void __launch_bounds__(S::Threads, 1)
     for (int t = 0; t < S::Teams; ++t) mbar_init(&sh.v_ready[t], 1);
     mbar_init(&sh.o_done[0], 1);
     mbar_init(&sh.o_done[1], 1);
+    for (int s = 0; s < kPieceQueue; ++s) {
+      mbar_init(&sh.piece_full[s], 1);
+      // taken by the softmax warps, the issuing threads and the value copies
+      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : 3));
+    }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
     sh.dead = 0;
@@ -1256,7 +1393,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
     prefetch_map(&mk);
     if (!S::Weigh) prefetch_map(&mv);
   }
-  if (warp == S::SoftWarps + 1) tmem_alloc(&sh.tmem, S::TmemCols);
+  if (warp == S::ScoreWarp) tmem_alloc(&sh.tmem, S::TmemCols);
   // columns past the query rows multiply zeros: the copies never write them
   {
     const int rows = A.G * A.pos_block;
@@ -1277,17 +1414,19 @@ __global__ void __launch_bounds__(S::Threads, 1)
   }
   if (sh.start.left <= 0) {
     if (!S::Weigh && tid == 0) A.joins[blockIdx.x] = JoinItem{};
-    if (warp == S::SoftWarps + 1) tmem_free(sh.tmem, S::TmemCols);
+    if (warp == S::ScoreWarp) tmem_free(sh.tmem, S::TmemCols);
     return;
   }
 
-  if (warp == S::SoftWarps) {
-    copy_role<S>(A, sh, qbuf, ring, &mq, &mk, &mv);
-  } else if (warp == S::SoftWarps + 1) {
-    if ((tid & 31) == 0) score_role<S>(A, issuer<S>(A, sh, qbuf, pbuf, ring), sh);
+  if (warp == S::KeyWarp) {
+    copy_role<S, false>(A, sh, qbuf, ring, &mq, &mk);
+  } else if (warp == S::ScoreWarp) {
+    if ((tid & 31) == 0) score_role<S>(A, sh, qbuf, ring);
     __syncwarp();
-  } else if (!S::Weigh && warp == S::SoftWarps + 2) {
-    if ((tid & 31) == 0) value_role<S>(A, issuer<S>(A, sh, qbuf, pbuf, ring), sh);
+  } else if (!S::Weigh && warp == S::CopyVWarp) {
+    copy_role<S, true>(A, sh, qbuf, ring, &mq, &mv);
+  } else if (!S::Weigh && warp == S::ValueWarp) {
+    if ((tid & 31) == 0) value_role<S>(A, sh, pbuf, ring);
     __syncwarp();
   } else if constexpr (S::Weigh) {
     weigh_role<S>(A, sh);
@@ -1303,7 +1442,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
   __syncthreads();
   tc_fence_after();
   if (!S::Weigh && tid == 0) A.joins[blockIdx.x] = sh.join;
-  if (warp == S::SoftWarps + 1) tmem_free(sh.tmem, S::TmemCols);
+  if (warp == S::ScoreWarp) tmem_free(sh.tmem, S::TmemCols);
 }
 
 // ---- joining the pieces of split items --------------------------------------------------------
@@ -1392,6 +1531,10 @@ sv_status encode_pool(CUtensorMap* map, const sv_kv_shape* s, const sv_kv_pool* 
 // Query rows per pass: as many whole positions as 128 columns hold (64 in an attention of
 // D = 256, where the weights of more columns would leave no room for two tiles), evenly over
 // the passes.
+inline bool ranges_fit(const sv_kv_shape* s, int blocks) {
+  const double tiles = (double)s->max_pages * s->page_size / kTileKeys + 1;
+  return (double)s->B * s->Hkv * blocks * (tiles * 4 + 16) < 1.5e11;  // 2^30 units per CTA
+}
 inline void row_blocks(const sv_kv_shape* s, bool weigh, int* pos_block, int* blocks,
                        int* columns) {
   const int G = s->Hq / s->Hkv, most = (s->D == 256 && !weigh ? 64 : 128) / G;

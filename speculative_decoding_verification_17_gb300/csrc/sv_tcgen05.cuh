@@ -111,8 +111,8 @@ constexpr uint64_t kTileWaitNs = 2000000000ull;  // 2 s: far past any legitimate
 // Wait for a phase of an mbarrier unless the CTA has given up (*dead); a wait that runs out
 // makes the CTA give up. After that every wait returns at once, so each role still walks its
 // whole loop and every CTA barrier is met; the results are then replaced by NaN.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
+static __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity,
+                                                volatile int* dead) {
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -122,6 +122,9 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, dead);
 }
 
 }  // namespace sv
