@@ -50,6 +50,7 @@ call) that it grows as needed: calls in flight on different streams never share 
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 
 import torch
@@ -117,11 +118,16 @@ def _dtype_code(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _check_cuda(name, t, dtype=None, shape=None, device=None):
     if t is None:
+        return
+    if (type(t) is torch.Tensor and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)
+            and (t.device == device if device is not None else t.is_cuda) and t.is_contiguous()
+            and t.is_cuda):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -607,12 +613,14 @@ def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_
     if out is None:
         out = torch.empty((B, P, V), dtype=logits.dtype, device=dev)
     _check_strided("out", out, logits.dtype, (B, P, V), dev)
-    h, _ = _stream_handle(stream)
+    a, b, _ = logits.stride()
+    c, d, _ = out.stride()
     _ok(library().logit_adjust(
-        _ptr(logits), logits.stride(0), logits.stride(1), code, _ptr(history), _ptr(hist_len),
+        logits.data_ptr(), a, b, code, _ptr(history), _ptr(hist_len),
         _ptr(prompt_len), L_max, _ptr(draft_tokens), _ptr(num_draft), _ptr(repetition),
         _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), n_bias,
-        _ptr(allowed), B, P, V, _ptr(out), out.stride(0), out.stride(1), h), "logit_adjust")
+        _ptr(allowed), B, P, V, out.data_ptr(), c, d, _raw_stream(stream, dev)),
+        "logit_adjust")
     return out
 
 
@@ -625,52 +633,64 @@ def _check_strided(name, t, dtype=None, shape=None, device=None, last=True):
         raise ValueError(f"{name} must be contiguous in its last dimension")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _kv_dtype(t):
-    if t.dtype == torch.bfloat16:
-        return SV_BF16
-    if t.dtype == torch.float16:
-        return SV_F16
-    raise TypeError(f"keys and values must be bfloat16 or float16, got {t.dtype}")
+def _raw_stream(stream, device):
+    """The handle of a stream, of the device's current one for None."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _kv_pool(t):
-    return _native.KvPool(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+# the C structs of specverify_kv.h as bytes
+_pack_pool = struct.Struct("@Pqqq").pack
+_pack_shape = struct.Struct("@9i").pack
+_pack_rule = struct.Struct("@ffiP").pack
+_KV_DTYPE = {torch.bfloat16: SV_BF16, torch.float16: SV_F16}
 
 
-def _kv_shape(B, P, Hq, k_cache, page_table):
-    pages, page_size, Hkv, D = k_cache.shape
-    return _native.KvShape(_kv_dtype(k_cache), B, P, Hq, Hkv, D, page_size, pages,
-                           page_table.shape[-1])
+def _kv_pool(name, t, like):
+    """A pool [pages, page_size, Hkv, D] of k_cache's type, device and last three sizes."""
+    _check_strided(name, t, like.dtype, None, like.device)
+    if t.ndim != 4 or t.shape[1:] != like.shape[1:]:
+        raise ValueError(f"{name} must have shape [pages, {tuple(like.shape[1:])}], "
+                         f"got {tuple(t.shape)}")
+    a, b, c, _ = t.stride()
+    return _pack_pool(t.data_ptr(), a, b, c)
 
 
-def _score_rule(scale, softcap, window, slopes, D):
-    return _native.ScoreRule(float(D ** -0.5 if scale is None else scale), float(softcap),
-                             int(window), None if slopes is None else slopes.data_ptr())
-
-
-def _check_kv(q, k_cache, v_cache, page_table, seq_len, num_draft, slopes):
+def _kv_call(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window):
+    """Checks what the calls with queries share; returns their first arguments and sizes."""
     B, P, Hq, D = q.shape
+    pages, page_size, Hkv, d = k_cache.shape
     dev = q.device
-    pages, page_size, Hkv, _ = k_cache.shape
-    _check_strided("q", q, k_cache.dtype)
-    _check_strided("k_cache", k_cache, None, (pages, page_size, Hkv, D), dev)
-    if v_cache is not None:
-        _check_strided("v_cache", v_cache, k_cache.dtype, (pages, page_size, Hkv, D), dev)
+    dtype = _KV_DTYPE.get(q.dtype)
+    if dtype is None:
+        raise TypeError(f"queries must be bfloat16 or float16, got {q.dtype}")
+    _check_strided("q", q)
+    if d != D or k_cache.dtype is not q.dtype or k_cache.device != dev:
+        raise ValueError("k_cache must have q's width, type and device")
     _check_cuda("page_table", page_table, torch.int32, (B, page_table.shape[-1]), dev)
     _check_cuda("seq_len", seq_len, torch.int32, (B,), dev)
     _check_cuda("num_draft", num_draft, torch.int32, (B,), dev)
     _check_cuda("slopes", slopes, torch.float32, (Hq,), dev)
-    return B, P, Hq, D, dev
+    shape = _pack_shape(dtype, B, P, Hq, Hkv, D, page_size, pages, page_table.shape[1])
+    rule = _pack_rule(D ** -0.5 if scale is None else scale, softcap, window,
+                      0 if slopes is None else slopes.data_ptr())
+    a, b, c, _ = q.stride()
+    head = (shape, rule, q.data_ptr(), a, b, c, _kv_pool("k_cache", k_cache, k_cache))
+    return head, B, P, Hq, Hkv, D, dev
 
 
 def paged_attention_workspace(B: int, P: int, Hq: int, k_cache, page_table) -> int:
-    return int(library().paged_attention_workspace(_kv_shape(B, P, Hq, k_cache, page_table)))
+    pages, page_size, Hkv, D = k_cache.shape
+    return int(library().paged_attention_workspace(
+        _pack_shape(_KV_DTYPE[k_cache.dtype], B, P, Hq, Hkv, D, page_size, pages,
+                    page_table.shape[1])))
 
 
 def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None, scale=None,
@@ -680,23 +700,28 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None,
     page_size, Hkv, D] of any page, token and head stride, page_table [B, max_pages] int32,
     seq_len [B] int32 (the new positions included). ``scale`` defaults to D ** -0.5. Returns
     (out [B, P, Hq, D], lse [B, P, Hq] fp32 or None)."""
-    B, P, Hq, D, dev = _check_kv(q, k_cache, v_cache, page_table, seq_len, num_draft, slopes)
+    head, B, P, Hq, _, D, dev = _kv_call(q, k_cache, page_table, seq_len, num_draft, slopes,
+                                         scale, softcap, window)
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have k_cache's shape")
     if out is None:
         out = torch.empty((B, P, Hq, D), dtype=q.dtype, device=dev)
     if out_lse is None and want_lse:
         out_lse = torch.empty((B, P, Hq), dtype=torch.float32, device=dev)
     _check_cuda("out", out, q.dtype, (B, P, Hq, D), dev)
     _check_cuda("out_lse", out_lse, torch.float32, (B, P, Hq), dev)
-    shape = _kv_shape(B, P, Hq, k_cache, page_table)
-    h, st = _stream_handle(stream)
+    h = _raw_stream(stream, dev)
     L = library()
     ws = workspace
     if ws is None:
-        ws = _workspace("attention", int(L.paged_attention_workspace(shape)), dev, st)
+        need = L.paged_attention_workspace(head[0])
+        ws = _ws_cache.get(("attention", dev, h))  # (as _workspace, past its lock)
+        if ws is None or ws.numel() < need:
+            ws = _workspace("attention", need, dev, stream or torch.cuda.current_stream(dev))
     _ok(L.paged_attention(
-        shape, _score_rule(scale, softcap, window, slopes, D), _ptr(q), q.stride(0), q.stride(1),
-        q.stride(2), _kv_pool(k_cache), _kv_pool(v_cache), _ptr(page_table), _ptr(seq_len),
-        _ptr(num_draft), _ptr(out), _ptr(out_lse), _ptr(ws), ws.numel(), h), "paged_attention")
+        *head, _kv_pool("v_cache", v_cache, k_cache), page_table.data_ptr(), seq_len.data_ptr(),
+        _ptr(num_draft), out.data_ptr(), _ptr(out_lse), ws.data_ptr(), ws.numel(), h),
+        "paged_attention")
     return out, out_lse
 
 
@@ -706,8 +731,8 @@ def attention_weight_sum(q, k_cache, page_table, seq_len, lse, *, num_draft=None
     """Adds to ``prior`` [B, Hkv, N] fp32 (zeros if None) the softmax weight that the rows up to
     accept_len gave each cached key, with ``lse`` [B, P, Hq] as paged_attention returned it.
     Returns the sums [B, Hkv, N] (``out``, which may be ``prior``)."""
-    B, P, Hq, D, dev = _check_kv(q, k_cache, None, page_table, seq_len, num_draft, slopes)
-    Hkv = k_cache.shape[2]
+    head, B, P, Hq, Hkv, D, dev = _kv_call(q, k_cache, page_table, seq_len, num_draft, slopes,
+                                           scale, softcap, window)
     if out is None:
         N = page_table.shape[-1] * k_cache.shape[1] if prior is None else prior.shape[-1]
         out = torch.zeros((B, Hkv, N), dtype=torch.float32, device=dev)
@@ -716,13 +741,10 @@ def attention_weight_sum(q, k_cache, page_table, seq_len, lse, *, num_draft=None
     _check_cuda("accept_len", accept_len, torch.int32, (B,), dev)
     _check_cuda("prior", prior, torch.float32, (B, Hkv, N), dev)
     _check_cuda("out", out, torch.float32, (B, Hkv, N), dev)
-    h, _ = _stream_handle(stream)
     _ok(library().attention_weight_sum(
-        _kv_shape(B, P, Hq, k_cache, page_table),
-        _score_rule(scale, softcap, window, slopes, D), _ptr(q), q.stride(0), q.stride(1),
-        q.stride(2), _kv_pool(k_cache), _ptr(page_table), _ptr(seq_len), _ptr(num_draft),
-        _ptr(lse), *lse.stride(), _ptr(accept_len), _ptr(prior), _ptr(out), N, h),
-        "attention_weight_sum")
+        *head, page_table.data_ptr(), seq_len.data_ptr(), _ptr(num_draft), lse.data_ptr(),
+        *lse.stride(), _ptr(accept_len), _ptr(prior), out.data_ptr(), N,
+        _raw_stream(stream, dev)), "attention_weight_sum")
     return out
 
 
@@ -734,18 +756,21 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
     new_page_table in new_k and new_v (which may be the same pools). Returns (out_len [B],
     out_index [B, Hkv, budget] int32, out_weights [B, Hkv, budget] fp32)."""
     B, max_pages = page_table.shape
-    dev = k_cache.device
     pages, page_size, Hkv, D = k_cache.shape
+    dev = k_cache.device
     N = weights.shape[-1]
-    new_pages = new_k.shape[0]
-    _check_strided("k_cache", k_cache)
-    _check_strided("v_cache", v_cache, k_cache.dtype, (pages, page_size, Hkv, D), dev)
-    _check_strided("new_k", new_k, k_cache.dtype, (new_pages, page_size, Hkv, D), dev)
-    _check_strided("new_v", new_v, k_cache.dtype, (new_pages, page_size, Hkv, D), dev)
+    new_cols = new_page_table.shape[-1]
+    dtype = _KV_DTYPE.get(k_cache.dtype)
+    if dtype is None:
+        raise TypeError(f"keys and values must be bfloat16 or float16, got {k_cache.dtype}")
+    pools = [_kv_pool(name, t, k_cache) for name, t in
+             (("k_cache", k_cache), ("v_cache", v_cache), ("new_k", new_k), ("new_v", new_v))]
+    if v_cache.shape[0] != pages or new_v.shape[0] != new_k.shape[0]:
+        raise ValueError("keys and values must have the same number of pages")
     _check_cuda("page_table", page_table, torch.int32, (B, max_pages), dev)
     _check_cuda("seq_len", seq_len, torch.int32, (B,), dev)
     _check_cuda("weights", weights, torch.float32, (B, Hkv, N), dev)
-    _check_cuda("new_page_table", new_page_table, torch.int32, (B, new_page_table.shape[-1]), dev)
+    _check_cuda("new_page_table", new_page_table, torch.int32, (B, new_cols), dev)
     if out_len is None:
         out_len = torch.empty((B,), dtype=torch.int32, device=dev)
     if out_index is None:
@@ -755,11 +780,10 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
     _check_cuda("out_len", out_len, torch.int32, (B,), dev)
     _check_cuda("out_index", out_index, torch.int32, (B, Hkv, budget), dev)
     _check_cuda("out_weights", out_weights, torch.float32, (B, Hkv, budget), dev)
-    h, _ = _stream_handle(stream)
     _ok(library().kv_cache_evict(
-        _kv_shape(B, 1, Hkv, k_cache, page_table), _kv_pool(k_cache), _kv_pool(v_cache),
-        _ptr(page_table), _ptr(seq_len), _ptr(weights), N, int(budget), int(recent),
-        _kv_pool(new_k), _kv_pool(new_v), new_pages, _ptr(new_page_table),
-        new_page_table.shape[-1], _ptr(out_len), _ptr(out_index), _ptr(out_weights), h),
-        "kv_cache_evict")
+        _pack_shape(dtype, B, 1, Hkv, Hkv, D, page_size, pages, max_pages), pools[0], pools[1],
+        page_table.data_ptr(), seq_len.data_ptr(), weights.data_ptr(), N, budget, recent,
+        pools[2], pools[3], new_k.shape[0], new_page_table.data_ptr(), new_cols,
+        out_len.data_ptr(), out_index.data_ptr(), out_weights.data_ptr(),
+        _raw_stream(stream, dev)), "kv_cache_evict")
     return out_len, out_index, out_weights

@@ -177,7 +177,7 @@ def _declare(L):
     L.logit_adjust.restype = I
     L.logit_adjust.argtypes = [P, q, q, I, P, P, P, I, P, P, P, P, P, P, P, I, P, I, I, I, P, q,
                                q, P]
-    shape, rule, pool = (ctypes.POINTER(t) for t in (KvShape, ScoreRule, KvPool))
+    shape = rule = pool = P  # structs: byref() of those above, or their bytes
     L.paged_attention_workspace.restype = Z
     L.paged_attention_workspace.argtypes = [shape]
     L.paged_attention.restype = I

@@ -39,17 +39,17 @@ def test_logit_adjust_refusals(kw, status):
 def shape(**kw):
     s = dict(dtype=1, B=2, P=3, Hq=8, Hkv=2, D=128, page_size=16, num_pages=40, max_pages=10)
     s.update(kw)
-    return _native.KvShape(*s.values())
+    return ctypes.byref(_native.KvShape(*s.values()))
 
 
 def rule(**kw):
     r = dict(scale=0.1, softcap=0.0, window=0, slopes=None)
     r.update(kw)
-    return _native.ScoreRule(*r.values())
+    return ctypes.byref(_native.ScoreRule(*r.values()))
 
 
 def pool(data=0x20000, page=4096, token=256, head=128):
-    return _native.KvPool(data, page, token, head)
+    return ctypes.byref(_native.KvPool(data, page, token, head))
 
 
 WS = ctypes.c_void_p(0x100000)
