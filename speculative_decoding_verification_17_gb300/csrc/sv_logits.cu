@@ -5,14 +5,18 @@
 //   add[v]   = bias(v) - f * c(v) - pi * [c(v) > 0]  with c over the history's output part
 //   seen bits (v occurs in the history), touched bits (seen, biased or drafted), draft bits
 // by scanning the request's whole history (a few tens of KiB out of L2) and keeping the tokens
-// that fall into the chunk. The rows then stream through registers once, 16 bytes at a time:
-//   - a vector with no touched token is copied as it is, or set to -inf under the mask,
-//     without being read where the mask allows none of it;
-//   - one with touched tokens takes y = (seen ? (z > 0 ? z / rho : z * rho) : z) + add;
-//   - a token drafted in this step (at most 16 per request) takes its count at this row's
-//     position from the drafts themselves, so no row waits for another one.
-// The counts are integers until they are final, and the biases are entered in order by one
-// warp, so the result does not depend on the order of atomics.
+// that fall into the chunk. The counts are integers until they are final, and the biases are
+// entered in order by one warp, so the result does not depend on the order of atomics. A token
+// drafted in this step (at most 16 per request) takes its count at a row's position from the
+// drafts themselves, so no row waits for another one.
+//
+// The rows themselves never pass through registers as a whole: a ring of row pieces is copied
+// in and out of shared memory by bulk copies, and the threads only visit the 16-byte vectors
+// that the mask or a touched token changes, in place. Bound: reading and writing the rows. (A
+// first form that streamed every vector through registers, with the penalties inlined for all
+// its elements, ran at 46 % of the copy rate: its code did not fit the instruction cache.)
+// Rows whose V or addresses do not allow 16-byte copies take a second kernel, element by element.
+
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -22,6 +26,8 @@
 #include "sv_host.h"
 
 namespace sv {
+
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far past any legitimate wait
 
 int device_sm_count();
 
@@ -130,89 +136,125 @@ __device__ __forceinline__ float adjusted(const Tables& T, const RowRule& r, int
   return y + a;
 }
 
-template <typename T, bool kAligned>
-__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A) {
-  using X = Vec<T>;
-  constexpr int E = X::E;
-  extern __shared__ __align__(16) unsigned char adj_smem[];
-  __shared__ int32_t s_draft[kMaxDraft], s_said[kMaxDraft];
-  const int C = 1 << A.log_chunk;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int b = blockIdx.x % A.B, c0 = (blockIdx.x / A.B) << A.log_chunk;
-  const int c1 = c0 + C < A.V ? c0 + C : A.V;
+#ifndef SV_ADJ_STAGES
+#define SV_ADJ_STAGES 3
+#endif
+constexpr int kAdjStages = SV_ADJ_STAGES;
+// A chunk with up to kListed touched tokens lists them, and its threads share the list out; in one
+// with more each thread visits its own vectors. (Of text that repeats, the chunk of the most
+// frequent tokens is nearly full, the others hold a few percent: with the vectors alone a warp
+// walked some hit in almost every 32 of them.)
+constexpr int kListed = 1024;
 
-  const int n = A.hist_len ? __ldg(A.hist_len + b) : 0;
-  const int prompt = A.prompt_len ? __ldg(A.prompt_len + b) : 0;
-  const int nd = A.num_draft ? __ldg(A.num_draft + b) : A.P - 1;
-  const T* in = static_cast<const T*>(A.in) + b * A.in_req;
-  T* out = static_cast<T*>(A.out) + b * A.out_req;
-  if (n < 0 || n > A.L_max || prompt < 0 || prompt > n || nd < 0 || nd > A.P - 1) {
-    for (int i = 0; i < A.P; ++i)
-      for (int j = c0 + tid; j < c1; j += kAdjThreads)
-        X::store1(out + i * A.out_row + j, __uint_as_float(0x7fc00000u));
-    return;
-  }
+// What every thread of a CTA knows of its request and chunk.
+struct Chunk {
+  int b, c0, c1, n, prompt, nd;
+  bool bad;
+};
+__device__ __forceinline__ Chunk chunk_of(const AdjustArgs& A) {
+  Chunk c;
+  c.b = blockIdx.x % A.B;  // (the chunks of the lowest, most frequent tokens first)
+  c.c0 = (int)(blockIdx.x / A.B) << A.log_chunk;
+  c.c1 = c.c0 + (1 << A.log_chunk) < A.V ? c.c0 + (1 << A.log_chunk) : A.V;
+  c.n = A.hist_len ? __ldg(A.hist_len + c.b) : 0;
+  c.prompt = A.prompt_len ? __ldg(A.prompt_len + c.b) : 0;
+  c.nd = A.num_draft ? __ldg(A.num_draft + c.b) : A.P - 1;
+  c.bad = c.n < 0 || c.n > A.L_max || c.prompt < 0 || c.prompt > c.n || c.nd < 0 ||
+          c.nd > A.P - 1;
+  return c;
+}
 
-  // ---- the chunk's tables
-  Tables S;
-  S.add = reinterpret_cast<float*>(adj_smem);
-  S.seen = reinterpret_cast<uint32_t*>(adj_smem + 4 * (size_t)C);
+struct DraftShared {
+  int32_t x[kMaxDraft], said[kMaxDraft];
+};
+
+// Builds the chunk's tables (all threads; ends with a CTA barrier).
+__device__ __forceinline__ void build_tables(const AdjustArgs& A, const Chunk& c,
+                                             unsigned char* smem, DraftShared& D, Tables& S,
+                                             RowRule& r) {
+  const int C = 1 << A.log_chunk, tid = threadIdx.x, lane = tid & 31, b = c.b;
+  S.add = reinterpret_cast<float*>(smem);
+  S.seen = reinterpret_cast<uint32_t*>(smem + 4 * (size_t)C);
   S.touched = S.seen + C / 32;
   S.drafted = S.touched + C / 32;
   S.listed = S.drafted + C / 32;
   uint32_t* cnt = reinterpret_cast<uint32_t*>(S.add);
-  RowRule r;
   r.rho = A.rep ? __ldg(A.rep + b) : 1.0f;
   r.inv = 1.0f / r.rho;
   r.pi = A.pres ? __ldg(A.pres + b) : 0.0f;
   r.f = A.freq ? __ldg(A.freq + b) : 0.0f;
-  r.x = s_draft;
-  r.x_said = s_said;
-  const int ndraft = A.draft ? nd : 0;
+  r.x = D.x;
+  r.x_said = D.said;
+  const int ndraft = A.draft ? c.nd : 0;
   {
-    uint4* z = reinterpret_cast<uint4*>(adj_smem);
+    uint4* z = reinterpret_cast<uint4*>(smem);
     const int n16 = (C * 4 + 4 * (C / 32) * 4) / 16;
+#pragma unroll 4
     for (int q = tid; q < n16; q += kAdjThreads) z[q] = make_uint4(0u, 0u, 0u, 0u);
   }
   __syncthreads();
   if (A.history) {
     const int32_t* h = A.history + (int64_t)b * A.L_max;
-    constexpr int U = 4;
-    for (int q0 = 0; q0 < n; q0 += U * kAdjThreads) {
-      int t[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int q = q0 + u * kAdjThreads + tid;
-        t[u] = q < n ? __ldg(h + q) : -1;
+    const int here = c.c1 - c.c0;
+    auto enter = [&](int q, int t) {
+      const int v = t - c.c0;
+      if ((unsigned)v < (unsigned)here && q < c.n) {
+        atomicOr(&S.seen[v >> 5], 1u << (v & 31));
+        if (q >= c.prompt) atomicAdd(&cnt[v], 1u);
       }
+    };
+    constexpr int U = 8;
+    // four tokens a load where the row allows (the row's end is padded to L_max, a multiple of 4)
+    if (A.L_max % 4 == 0 && (reinterpret_cast<uintptr_t>(h) & 15) == 0) {
+#pragma unroll 1
+      for (int q0 = 4 * tid; q0 < c.n; q0 += 4 * U * kAdjThreads) {
+        int4 t[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int q = q0 + u * kAdjThreads + tid;
-        if (t[u] >= c0 && t[u] < c1) {
-          const int v = t[u] - c0;
-          atomicOr(&S.seen[v >> 5], 1u << (v & 31));
-          if (q >= prompt) atomicAdd(&cnt[v], 1u);
+        for (int u = 0; u < U; ++u) {
+          const int q = q0 + 4 * u * kAdjThreads;
+          t[u] = q < c.n ? __ldg(reinterpret_cast<const int4*>(h + q)) : make_int4(-1, -1, -1, -1);
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int q = q0 + 4 * u * kAdjThreads;
+          enter(q, t[u].x);
+          enter(q + 1, t[u].y);
+          enter(q + 2, t[u].z);
+          enter(q + 3, t[u].w);
+        }
+      }
+    } else {
+#pragma unroll 1
+      for (int q0 = tid; q0 < c.n; q0 += U * kAdjThreads) {
+        int t[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int q = q0 + u * kAdjThreads;
+          t[u] = q < c.n ? __ldg(h + q) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) enter(q0 + u * kAdjThreads, t[u]);
       }
     }
   }
   __syncthreads();
   if (tid < ndraft) {
-    const int t = __ldg(A.draft + (int64_t)b * (A.P - 1) + tid);
-    const bool here = t >= c0 && t < c1;
-    s_draft[tid] = here ? t - c0 : -1;
-    s_said[tid] = here && cnt[t - c0] > 0;
-    if (here) atomicOr(&S.drafted[(t - c0) >> 5], 1u << ((t - c0) & 31));
+    const int v = __ldg(A.draft + (int64_t)b * (A.P - 1) + tid) - c.c0;
+    const bool here = (unsigned)v < (unsigned)(c.c1 - c.c0);
+    D.x[tid] = here ? v : -1;
+    D.said[tid] = here && cnt[v] > 0;
+    if (here) atomicOr(&S.drafted[v >> 5], 1u << (v & 31));
   }
   __syncthreads();
+#pragma unroll 1
   for (int w = tid; w < C / 32; w += kAdjThreads) {
     uint32_t m = S.seen[w];
     S.touched[w] = m | S.drafted[w];
-    while (m) {
+#pragma unroll 1
+    for (; m; m &= m - 1) {
       const int v = 32 * w + __ffs(m) - 1;
-      m &= m - 1;
-      const uint32_t c = cnt[v];
-      S.add[v] = c ? -(r.f * (float)c) - r.pi : 0.0f;
+      const uint32_t k = cnt[v];
+      S.add[v] = k ? -(r.f * (float)k) - r.pi : 0.0f;
     }
   }
   if (A.n_bias > 0) {
@@ -221,17 +263,17 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
       const int32_t* bt = A.bias_tok + (int64_t)b * A.n_bias;
       const float* bv = A.bias_val + (int64_t)b * A.n_bias;
       // entries in order, 32 at a time: a token's first entry counts (listed bits)
+#pragma unroll 1
       for (int q0 = 0; q0 < A.n_bias; q0 += 32) {
         const int q = q0 + lane;
-        const int t = q < A.n_bias ? __ldg(bt + q) : -1;
-        const bool here = t >= c0 && t < c1;
+        const int v = (q < A.n_bias ? __ldg(bt + q) : -1) - c.c0;
+        const bool here = q < A.n_bias && (unsigned)v < (unsigned)(c.c1 - c.c0);
         if (!__any_sync(0xffffffffu, here)) continue;
-        const uint32_t same = __match_any_sync(0xffffffffu, here ? t : -1 - lane);
+        const uint32_t same = __match_any_sync(0xffffffffu, here ? v : -1 - lane);
         const bool first = here && (__ffs(same) - 1) == lane &&
-                           !((S.listed[(t - c0) >> 5] >> ((t - c0) & 31)) & 1u);
+                           !((S.listed[v >> 5] >> (v & 31)) & 1u);
         __syncwarp();
         if (first) {
-          const int v = t - c0;
           S.add[v] += __ldg(bv + q);
           atomicOr(&S.touched[v >> 5], 1u << (v & 31));
           atomicOr(&S.listed[v >> 5], 1u << (v & 31));
@@ -241,84 +283,250 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
     }
   }
   __syncthreads();
+}
 
-  // ---- the rows
-  const uint32_t full = (1u << E) - 1u;
-  const uint32_t* allowed = A.allowed ? A.allowed + (int64_t)b * A.P * A.W : nullptr;
-  if (kAligned) {
-    // vectors of the chunk, counted through all rows: 4 in flight per thread
-    constexpr int U = 4;
-    const int lv = A.log_chunk - (E == 8 ? 3 : 2);
-    const int items = (nd + 1) << lv;
-    for (int it0 = tid; it0 < items; it0 += U * kAdjThreads) {
-      uint32_t ok[U];
-      uint4 v[U];
+// Bulk copy of shared memory to global memory (both 16-byte aligned, a multiple of 16 bytes).
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
+}
+
+// Rows in 16-byte vectors.
+template <typename T>
+__global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A) {
+  using X = Vec<T>;
+  constexpr int E = X::E;
+  constexpr uint32_t kFull = (1u << E) - 1u;
+  extern __shared__ __align__(128) unsigned char adj_smem[];
+  __shared__ DraftShared D;
+  __shared__ __align__(8) uint64_t full[kAdjStages];
+  __shared__ uint16_t list[kListed];
+  __shared__ int warp_count[kAdjThreads / 32];
+  const int tid = threadIdx.x;
+  const Chunk c = chunk_of(A);
+  const T* in = static_cast<const T*>(A.in) + c.b * A.in_req + c.c0;
+  T* out = static_cast<T*>(A.out) + c.b * A.out_req + c.c0;
+  const int rows = c.bad ? A.P : c.nd + 1, nvec = (c.c1 - c.c0) / E;
+  const uint32_t bytes = (uint32_t)nvec * 16u;
+  unsigned char* ring = adj_smem;
+  const int stage = (int)sizeof(T) << A.log_chunk;
+  if (c.bad) {
+    const float nan[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
+    const uint4 v = X::pack(reinterpret_cast<const float(&)[E]>(nan));
+    for (int i = 0; i < rows; ++i)
+      for (int q = tid; q < nvec; q += kAdjThreads)
+        *reinterpret_cast<uint4*>(out + i * A.out_row + q * E) = v;
+    return;
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kAdjStages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+    for (int i = 0; i < kAdjStages && i < rows; ++i) {
+      mbar_arrive_expect_tx(&full[i], bytes);
+      bulk_g2s(ring + i * stage, in + i * A.in_row, bytes, &full[i]);
+    }
+  }
+  Tables S;
+  RowRule r;
+  build_tables(A, c, adj_smem + kAdjStages * stage, D, S, r);
+  const uint8_t* touched = reinterpret_cast<const uint8_t*>(S.touched);
+  const uint8_t* const allowed =
+      A.allowed ? reinterpret_cast<const uint8_t*>(A.allowed + (int64_t)c.b * A.P * A.W) + c.c0 / 8
+                : nullptr;
+
+  // The touched tokens in ascending order, a word of their bits per thread.
+  int count = 0;
+  {
+    const int lane = tid & 31, warp = tid >> 5;
+    uint32_t m = tid < (1 << A.log_chunk) / 32 ? S.touched[tid] : 0u;
+    int at = __popc(m);
+    const int mine = at;
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int it = it0 + u * kAdjThreads;
-        const int i = it >> lv, j = c0 + (it & ((1 << lv) - 1)) * E;
-        ok[u] = 0;
-        if (it < items && j < A.V) {
-          ok[u] = full;
-          if (allowed) {
-            const uint8_t byte =
-                __ldg(reinterpret_cast<const uint8_t*>(allowed + (int64_t)i * A.W) + (j >> 3));
-            ok[u] = (E == 8 ? byte : byte >> (j & 4)) & full;
-          }
-        }
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    if (lane == 31) warp_count[warp] = at;
+    __syncthreads();
+    at -= mine;
+#pragma unroll
+    for (int q = 0; q < kAdjThreads / 32; ++q) {
+      if (q < warp) at += warp_count[q];
+      count += warp_count[q];
+    }
+    if (count <= kListed)
+#pragma unroll 1
+      for (; m; m &= m - 1) list[at++] = (uint16_t)(32 * tid + __ffs(m) - 1);
+    __syncthreads();
+  }
+  const bool listed = count <= kListed;
+
+  // A thread's vectors are q = tid + u * kAdjThreads; kVecs of them cover the largest chunk. Their
+  // touched bits stay in registers, their masks are loaded a row ahead.
+  constexpr int kVecs = 4;
+  uint32_t touch[kVecs], next_ok[kVecs];
+  auto load_ok = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int q = tid + u * kAdjThreads, at = E == 8 ? q : q >> 1;
+      next_ok[u] = 0xffu;
+      if (allowed && i < rows && q < nvec) next_ok[u] = __ldg(allowed + (int64_t)i * A.W * 4 + at);
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int q = tid + u * kAdjThreads, at = E == 8 ? q : q >> 1;
+    touch[u] = q < nvec ? (uint32_t)(touched[at] >> (E == 8 ? 0 : 4 * (q & 1))) & kFull : 0u;
+  }
+  auto bits_of = [&](const uint32_t* bits, int q) {
+    const uint8_t byte = reinterpret_cast<const uint8_t*>(bits)[E == 8 ? q : q >> 1];
+    return (uint32_t)(byte >> (E == 8 ? 0 : 4 * (q & 1))) & kFull;
+  };
+  auto drafted_of = [&](int q) { return bits_of(S.drafted, q); };
+  auto seen_of = [&](int q) { return bits_of(S.seen, q); };
+  load_ok(0);
+  int s = 0;
+  uint32_t phase = 0;
+#pragma unroll 1
+  for (int i = 0; i < rows; ++i) {
+    unsigned char* buf = ring + s * stage;
+    uint32_t ok[kVecs];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      ok[u] = (next_ok[u] >> (E == 8 ? 0 : 4 * ((tid + u * kAdjThreads) & 1))) & kFull;
+    load_ok(i + 1);
+    if (!mbar_wait(&full[s], phase, kWaitLimitNs))
+      // the copy never came: the row reads as NaN
+      for (int q = tid; q < nvec * 4; q += kAdjThreads)
+        reinterpret_cast<uint32_t*>(buf)[q] = 0x7fc07fc0u;
+    if (listed && count > 0) {
+#pragma unroll 1
+      for (int e = tid; e < count; e += kAdjThreads) {
+        T* z = reinterpret_cast<T*>(buf) + list[e];
+        X::store1(z, adjusted(S, r, list[e], X::load1(z), i));
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int it = it0 + u * kAdjThreads;
-        const int i = it >> lv, j = c0 + (it & ((1 << lv) - 1)) * E;
-        v[u] = X::mask(make_uint4(0u, 0u, 0u, 0u), 0u);
-        if (ok[u]) v[u] = *reinterpret_cast<const uint4*>(in + i * A.in_row + j);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int it = it0 + u * kAdjThreads;
-        const int i = it >> lv, t = (it & ((1 << lv) - 1)) * E, j = c0 + t;
-        if (it >= items || j >= A.V) continue;
-        const uint32_t hit = (S.touched[t >> 5] >> (t & 31)) & full & ok[u];
-        if (hit) {
+      if (allowed) __syncthreads();  // the masks, by vectors, come last
+    }
+#pragma unroll 1
+    for (int u = 0; u < kVecs; ++u) {
+      const int q = tid + u * kAdjThreads;
+      if (q >= nvec) break;
+      uint4* v = reinterpret_cast<uint4*>(buf) + q;
+      const uint32_t may = u == 0 ? ok[0] : u == 1 ? ok[1] : u == 2 ? ok[2] : ok[3];
+      if (!listed) {
+        const uint32_t hit = u == 0 ? touch[0] : u == 1 ? touch[1] : u == 2 ? touch[2] : touch[3];
+        if (hit & may) {
+          const uint32_t drafts = drafted_of(q);
+          uint4 w = *v;
           float y[E];
 #pragma unroll
-          for (int l = 0; l < E; ++l) {
-            y[l] = X::get(v[u], l);
-            if ((hit >> l) & 1u) y[l] = adjusted(S, r, t + l, y[l], i);
+          for (int l = 0; l < E; ++l) y[l] = X::get(w, l);
+          if (__builtin_expect(drafts != 0, 0)) {
+#pragma unroll
+            for (int l = 0; l < E; ++l)
+              if ((hit >> l) & 1u) y[l] = adjusted(S, r, q * E + l, y[l], i);
+          } else {
+            const uint32_t seen = seen_of(q);
+#pragma unroll
+            for (int l = 0; l < E; ++l) {
+              const float z = y[l];
+              y[l] = ((seen >> l) & 1u ? (z > 0.0f ? z * r.inv : z * r.rho) : z) +
+                     S.add[q * E + l];
+            }
           }
-          v[u] = X::pack(y);
+          *v = X::pack(y);
         }
-        if (ok[u] != full) v[u] = X::mask(v[u], ok[u]);
-        *reinterpret_cast<uint4*>(out + i * A.out_row + j) = v[u];
+      }
+      if (may != kFull) *v = X::mask(may ? *v : make_uint4(0u, 0u, 0u, 0u), may);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+      bulk_s2g(out + i * A.out_row, buf, bytes);
+      // the piece before this one has left its buffer: the next row into it
+      const int next = i - 1 + kAdjStages;
+      if (i > 0 && next < rows) {
+        bulk_wait_read<1>();
+        const int sb = s == 0 ? kAdjStages - 1 : s - 1;
+        mbar_arrive_expect_tx(&full[sb], bytes);
+        bulk_g2s(ring + sb * stage, in + next * A.in_row, bytes, &full[sb]);
       }
     }
-  } else {
-    for (int i = 0; i <= nd; ++i) {
-      const T* zi = in + i * A.in_row;
-      T* yi = out + i * A.out_row;
-      const uint32_t* al = allowed ? allowed + (int64_t)i * A.W : nullptr;
-      for (int j = c0 + tid; j < c1; j += kAdjThreads) {
-        const int t = j - c0;
-        if (al && !((__ldg(al + (j >> 5)) >> (j & 31)) & 1u)) {
-          X::store1(yi + j, __uint_as_float(F32::kNegInfBits));
-          continue;
-        }
-        float z = X::load1(zi + j);
-        if ((S.touched[t >> 5] >> (t & 31)) & 1u) z = adjusted(S, r, t, z, i);
-        X::store1(yi + j, z);
+    if (++s == kAdjStages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  if (tid == 0) bulk_wait_read<0>();
+}
+
+// Rows that 16-byte vectors do not divide: element by element.
+template <typename T>
+__global__ void __launch_bounds__(kAdjThreads) adjust_any_kernel(const AdjustArgs A) {
+  using X = Vec<T>;
+  extern __shared__ __align__(128) unsigned char adj_smem[];
+  __shared__ DraftShared D;
+  const Chunk c = chunk_of(A);
+  const T* in = static_cast<const T*>(A.in) + c.b * A.in_req;
+  T* out = static_cast<T*>(A.out) + c.b * A.out_req;
+  if (c.bad) {
+    for (int i = 0; i < A.P; ++i)
+      for (int j = c.c0 + threadIdx.x; j < c.c1; j += kAdjThreads)
+        X::store1(out + i * A.out_row + j, NAN);
+    return;
+  }
+  Tables S;
+  RowRule r;
+  build_tables(A, c, adj_smem, D, S, r);
+  const uint32_t* allowed = A.allowed ? A.allowed + (int64_t)c.b * A.P * A.W : nullptr;
+#pragma unroll 1
+  for (int i = 0; i <= c.nd; ++i) {
+    const uint32_t* ok = allowed ? allowed + (int64_t)i * A.W : nullptr;
+    constexpr int U = 4;
+#pragma unroll 1
+    for (int j0 = c.c0 + threadIdx.x; j0 < c.c1; j0 += U * kAdjThreads) {
+      float z[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kAdjThreads;
+        z[u] = 0.0f;
+        if (j < c.c1)
+          z[u] = ok && !((__ldg(ok + (j >> 5)) >> (j & 31)) & 1u)
+                     ? __uint_as_float(F32::kNegInfBits)
+                     : X::load1(in + i * A.in_row + j);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * kAdjThreads, t = j - c.c0;
+        if (j >= c.c1) break;
+        const bool masked = ok && !((__ldg(ok + (j >> 5)) >> (j & 31)) & 1u);
+        if (!masked && ((S.touched[t >> 5] >> (t & 31)) & 1u)) z[u] = adjusted(S, r, t, z[u], i);
+        X::store1(out + i * A.out_row + j, z[u]);
       }
     }
   }
 }
 
 template <typename T>
-sv_status launch_adjust(const AdjustArgs& A, bool aligned, cudaStream_t st) {
+sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
+  // Chunks of 8192 bf16 or 4096 fp32 logits (three rows of it in flight), or shorter ones (each scans the history) while they would leave SMs
+  // without work: two CTAs are resident per SM.
+  const int64_t resident = 2 * (int64_t)device_sm_count();
+  A.log_chunk = sizeof(T) == 4 ? 12 : 13;
+  while (A.log_chunk > 11 && (((int64_t)A.V - 1) / (1 << A.log_chunk) + 1) * A.B < resident)
+    --A.log_chunk;
   const int64_t chunks = ((int64_t)A.V + (1 << A.log_chunk) - 1) >> A.log_chunk;
   const int64_t grid = chunks * A.B;
   if (grid >= (1ll << 31)) return SV_ERR_UNSUPPORTED;
-  const size_t smem = ((size_t)4 << A.log_chunk) + 4 * (((size_t)1 << A.log_chunk) / 8);
-  auto kernel = aligned ? adjust_kernel<T, true> : adjust_kernel<T, false>;
+  const size_t tables = ((size_t)4 << A.log_chunk) + 4 * (((size_t)1 << A.log_chunk) / 8);
+  const size_t smem = tables + (aligned ? kAdjStages * (sizeof(T) << A.log_chunk) : 0);
+  auto kernel = aligned ? adjust_kernel<T> : adjust_any_kernel<T>;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return cuda_fail(e);
