@@ -46,7 +46,7 @@ struct AdjustArgs {
   const float* bias_val;
   const uint32_t* allowed;
   int L_max, n_bias, B, P, V, W;
-  int log_chunk;  // tokens per chunk, a power of two >= 1024
+  int log_chunk;  // tokens per chunk, a power of two from 1024 to 4096
 };
 
 // E elements of a row as floats, and back (one rounding).
@@ -92,13 +92,20 @@ struct Vec<__nv_bfloat16> {
   __device__ static __forceinline__ void store1(__nv_bfloat16* p, float y) {
     *p = __float2bfloat16_rn(y);
   }
-  __device__ static __forceinline__ uint32_t mask2(uint32_t w, uint32_t ok) {
-    const uint32_t keep = ((ok & 1u) ? 0xffffu : 0u) | ((ok & 2u) ? 0xffff0000u : 0u);
-    return (w & keep) | (0xff80ff80u & ~keep);
+  // Two words of four elements under four bits: the bits go to the signs of four bytes, and a
+  // byte permutation that replicates signs widens each to an element.
+  __device__ static __forceinline__ void mask4(uint32_t& a, uint32_t& b, uint32_t ok) {
+    const uint32_t signs = ((ok & 15u) * 0x10204080u) & 0x80808080u;
+    uint32_t ka, kb;
+    asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(ka) : "r"(signs));
+    asm("prmt.b32 %0, %1, 0, 0xbbaa;" : "=r"(kb) : "r"(signs));
+    a = (a & ka) | (0xff80ff80u & ~ka);
+    b = (b & kb) | (0xff80ff80u & ~kb);
   }
   __device__ static __forceinline__ uint4 mask(uint4 v, uint32_t ok) {
-    return make_uint4(mask2(v.x, ok), mask2(v.y, ok >> 2), mask2(v.z, ok >> 4),
-                      mask2(v.w, ok >> 6));
+    mask4(v.x, v.y, ok);
+    mask4(v.z, v.w, ok >> 4);
+    return v;
   }
 };
 
@@ -136,10 +143,7 @@ __device__ __forceinline__ float adjusted(const Tables& T, const RowRule& r, int
   return y + a;
 }
 
-#ifndef SV_ADJ_STAGES
-#define SV_ADJ_STAGES 3
-#endif
-constexpr int kAdjStages = SV_ADJ_STAGES;
+constexpr int kAdjStages = 4;  // row pieces in flight (8 KiB each)
 // A chunk with up to kListed touched tokens lists them, and its threads share the list out; in one
 // with more each thread visits its own vectors. (Of text that repeats, the chunk of the most
 // frequent tokens is nearly full, the others hold a few percent: with the vectors alone a warp
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
 
   // A thread's vectors are q = tid + u * kAdjThreads; kVecs of them cover the largest chunk. Their
   // touched bits stay in registers, their masks are loaded a row ahead.
-  constexpr int kVecs = 4;
+  constexpr int kVecs = 2;
   uint32_t touch[kVecs], next_ok[kVecs];
   auto load_ok = [&](int i) {
 #pragma unroll
@@ -418,9 +422,9 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
       const int q = tid + u * kAdjThreads;
       if (q >= nvec) break;
       uint4* v = reinterpret_cast<uint4*>(buf) + q;
-      const uint32_t may = u == 0 ? ok[0] : u == 1 ? ok[1] : u == 2 ? ok[2] : ok[3];
+      const uint32_t may = u == 0 ? ok[0] : ok[1];
       if (!listed) {
-        const uint32_t hit = u == 0 ? touch[0] : u == 1 ? touch[1] : u == 2 ? touch[2] : touch[3];
+        const uint32_t hit = u == 0 ? touch[0] : touch[1];
         if (hit & may) {
           const uint32_t drafts = drafted_of(q);
           uint4 w = *v;
@@ -515,11 +519,12 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_any_kernel(const AdjustArg
 
 template <typename T>
 sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
-  // Chunks of 8192 bf16 or 4096 fp32 logits (three rows of it in flight), or shorter ones (each scans the history) while they would leave SMs
-  // without work: two CTAs are resident per SM.
-  const int64_t resident = 2 * (int64_t)device_sm_count();
-  A.log_chunk = sizeof(T) == 4 ? 12 : 13;
-  while (A.log_chunk > 11 && (((int64_t)A.V - 1) / (1 << A.log_chunk) + 1) * A.B < resident)
+  // Chunks of 4096 bf16 or 2048 fp32 logits, or shorter ones (each scans the history) while they
+  // would leave SMs without work: five CTAs are resident per SM.
+  const int64_t wanted = 2 * (int64_t)device_sm_count();
+  const int least = sizeof(T) == 4 ? 10 : 11;
+  A.log_chunk = least + 1;
+  while (A.log_chunk > least && (((int64_t)A.V - 1) / (1 << A.log_chunk) + 1) * A.B < wanted)
     --A.log_chunk;
   const int64_t chunks = ((int64_t)A.V + (1 << A.log_chunk) - 1) >> A.log_chunk;
   const int64_t grid = chunks * A.B;
