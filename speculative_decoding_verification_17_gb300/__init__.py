@@ -587,6 +587,16 @@ def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_
     apart (last dimension contiguous). ``allowed`` holds bits, [B, P, ceil(V/32)] int32.
     Returns the adjusted logits [B, P, V] (``out``, which may be ``logits`` itself; rows past a
     request's num_draft are left as they are in it)."""
+    if out is None and isinstance(logits, torch.Tensor):
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    status = (_native._calls or _native.calls()).adjust(
+        logits, history, hist_len, prompt_len, draft_tokens, num_draft, repetition, presence,
+        frequency, bias_tokens, bias_values, allowed, out, _raw_stream(stream, logits))
+    if status is not None:
+        if status:
+            raise SVError(status, "logit_adjust")
+        return out
+    # an argument that does not fit: the checks one by one
     B, P, V = logits.shape
     dev = logits.device
     code = _dtype_code(logits)
@@ -610,8 +620,6 @@ def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_
     if n_bias == 0:
         bias_tokens = bias_values = None
     _check_cuda("allowed", allowed, torch.int32, (B, P, (V + 31) // 32), dev)
-    if out is None:
-        out = torch.empty((B, P, V), dtype=logits.dtype, device=dev)
     _check_strided("out", out, logits.dtype, (B, P, V), dev)
     a, b, _ = logits.stride()
     c, d, _ = out.stride()
@@ -619,7 +627,7 @@ def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_
         logits.data_ptr(), a, b, code, _ptr(history), _ptr(hist_len),
         _ptr(prompt_len), L_max, _ptr(draft_tokens), _ptr(num_draft), _ptr(repetition),
         _ptr(presence), _ptr(frequency), _ptr(bias_tokens), _ptr(bias_values), n_bias,
-        _ptr(allowed), B, P, V, out.data_ptr(), c, d, _raw_stream(stream, dev)),
+        _ptr(allowed), B, P, V, out.data_ptr(), c, d, _raw_stream(stream, logits)),
         "logit_adjust")
     return out
 
@@ -639,11 +647,13 @@ def _check_strided(name, t, dtype=None, shape=None, device=None, last=True):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
-def _raw_stream(stream, device):
-    """The handle of a stream, of the device's current one for None."""
+def _raw_stream(stream, like):
+    """The handle of a stream; for None, of the current one of a tensor's device."""
     if stream is not None:
         return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    if not like.is_cuda:
+        return 0  # (refused by the checks)
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
 
 
 # the C structs of specverify_kv.h as bytes
@@ -700,24 +710,39 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None,
     page_size, Hkv, D] of any page, token and head stride, page_table [B, max_pages] int32,
     seq_len [B] int32 (the new positions included). ``scale`` defaults to D ** -0.5. Returns
     (out [B, P, Hq, D], lse [B, P, Hq] fp32 or None)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if out_lse is None and want_lse:
+        out_lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    h = _raw_stream(stream, q)
+    ws = workspace
+    if ws is None:
+        ws = _ws_cache.get(("attention", q.get_device(), h))
+    fast = (_native._calls or _native.calls()).attention
+    status = fast(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window,
+                  v_cache, out, out_lse, ws, h)
+    if status is not None and status < 0 and workspace is None:
+        # a first call on this stream, or one that needs more than the earlier ones did
+        ws = _workspace("attention", -status - 1, q.device,
+                        stream or torch.cuda.current_stream(q.device))
+        _ws_cache["attention", q.get_device(), h] = ws
+        status = fast(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window,
+                      v_cache, out, out_lse, ws, h)
+    if status is not None:
+        if status:
+            raise SVError(status if status > 0 else 3, "paged_attention")
+        return out, out_lse
+    # an argument that does not fit: the checks one by one
     head, B, P, Hq, _, D, dev = _kv_call(q, k_cache, page_table, seq_len, num_draft, slopes,
                                          scale, softcap, window)
     if v_cache.shape != k_cache.shape:
         raise ValueError("v_cache must have k_cache's shape")
-    if out is None:
-        out = torch.empty((B, P, Hq, D), dtype=q.dtype, device=dev)
-    if out_lse is None and want_lse:
-        out_lse = torch.empty((B, P, Hq), dtype=torch.float32, device=dev)
     _check_cuda("out", out, q.dtype, (B, P, Hq, D), dev)
     _check_cuda("out_lse", out_lse, torch.float32, (B, P, Hq), dev)
-    h = _raw_stream(stream, dev)
     L = library()
-    ws = workspace
     if ws is None:
-        need = L.paged_attention_workspace(head[0])
-        ws = _ws_cache.get(("attention", dev, h))  # (as _workspace, past its lock)
-        if ws is None or ws.numel() < need:
-            ws = _workspace("attention", need, dev, stream or torch.cuda.current_stream(dev))
+        ws = _workspace("attention", L.paged_attention_workspace(head[0]), dev,
+                        stream or torch.cuda.current_stream(dev))
     _ok(L.paged_attention(
         *head, _kv_pool("v_cache", v_cache, k_cache), page_table.data_ptr(), seq_len.data_ptr(),
         _ptr(num_draft), out.data_ptr(), _ptr(out_lse), ws.data_ptr(), ws.numel(), h),
@@ -731,11 +756,20 @@ def attention_weight_sum(q, k_cache, page_table, seq_len, lse, *, num_draft=None
     """Adds to ``prior`` [B, Hkv, N] fp32 (zeros if None) the softmax weight that the rows up to
     accept_len gave each cached key, with ``lse`` [B, P, Hq] as paged_attention returned it.
     Returns the sums [B, Hkv, N] (``out``, which may be ``prior``)."""
-    head, B, P, Hq, Hkv, D, dev = _kv_call(q, k_cache, page_table, seq_len, num_draft, slopes,
-                                           scale, softcap, window)
     if out is None:
         N = page_table.shape[-1] * k_cache.shape[1] if prior is None else prior.shape[-1]
-        out = torch.zeros((B, Hkv, N), dtype=torch.float32, device=dev)
+        out = torch.zeros((q.shape[0], k_cache.shape[2], N), dtype=torch.float32, device=q.device)
+    h = _raw_stream(stream, q)
+    status = (_native._calls or _native.calls()).weights(
+        q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window, lse,
+        accept_len, prior, out, h)
+    if status is not None:
+        if status:
+            raise SVError(status, "attention_weight_sum")
+        return out
+    # an argument that does not fit: the checks one by one
+    head, B, P, Hq, Hkv, D, dev = _kv_call(q, k_cache, page_table, seq_len, num_draft, slopes,
+                                           scale, softcap, window)
     N = out.shape[-1]
     _check_strided("lse", lse, torch.float32, (B, P, Hq), dev, last=False)
     _check_cuda("accept_len", accept_len, torch.int32, (B,), dev)
@@ -743,8 +777,8 @@ def attention_weight_sum(q, k_cache, page_table, seq_len, lse, *, num_draft=None
     _check_cuda("out", out, torch.float32, (B, Hkv, N), dev)
     _ok(library().attention_weight_sum(
         *head, page_table.data_ptr(), seq_len.data_ptr(), _ptr(num_draft), lse.data_ptr(),
-        *lse.stride(), _ptr(accept_len), _ptr(prior), out.data_ptr(), N,
-        _raw_stream(stream, dev)), "attention_weight_sum")
+        *lse.stride(), _ptr(accept_len), _ptr(prior), out.data_ptr(), N, h),
+        "attention_weight_sum")
     return out
 
 
@@ -755,6 +789,15 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
     heaviest others by ``weights`` [B, Hkv, N] fp32, and copies them in order to the pages of
     new_page_table in new_k and new_v (which may be the same pools). Returns (out_len [B],
     out_index [B, Hkv, budget] int32, out_weights [B, Hkv, budget] fp32)."""
+    h = _raw_stream(stream, k_cache)
+    made = (_native._calls or _native.calls()).evict(
+        k_cache, v_cache, page_table, seq_len, weights, budget, recent, new_k, new_v,
+        new_page_table, out_len, out_index, out_weights, h)
+    if made is not None:
+        if made[0]:
+            raise SVError(made[0], "kv_cache_evict")
+        return made[1:]
+    # an argument that does not fit: the checks one by one
     B, max_pages = page_table.shape
     pages, page_size, Hkv, D = k_cache.shape
     dev = k_cache.device
@@ -784,6 +827,6 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
         _pack_shape(dtype, B, 1, Hkv, Hkv, D, page_size, pages, max_pages), pools[0], pools[1],
         page_table.data_ptr(), seq_len.data_ptr(), weights.data_ptr(), N, budget, recent,
         pools[2], pools[3], new_k.shape[0], new_page_table.data_ptr(), new_cols,
-        out_len.data_ptr(), out_index.data_ptr(), out_weights.data_ptr(),
-        _raw_stream(stream, dev)), "kv_cache_evict")
+        out_len.data_ptr(), out_index.data_ptr(), out_weights.data_ptr(), h),
+        "kv_cache_evict")
     return out_len, out_index, out_weights

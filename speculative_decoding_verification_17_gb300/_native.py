@@ -1,4 +1,5 @@
-"""Build and load ``libspecverify.so``, the C-ABI library of the verify step.
+"""Build and load ``libspecverify.so``, the C-ABI library of the verify step, and ``_calls.so``,
+the checks and marshalling of the calls on logits and on the paged cache.
 
 The library is compiled in-tree from ``csrc/`` for sm_103a only (one ``-gencode``), one
 nvcc process per translation unit in parallel, and linked against the static CUDA runtime
@@ -20,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(BUILD, "libspecverify.so")
+BINDING = os.path.join(CSRC, "binding.cpp")
+CALLS = os.path.join(BUILD, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -40,8 +43,10 @@ def sources() -> list[str]:
 def _stale() -> bool:
     if not os.path.exists(SO):
         return True
-    t = os.path.getmtime(SO)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+    if not os.path.exists(CALLS):
+        return True
+    t = min(os.path.getmtime(SO), os.path.getmtime(CALLS))
+    deps = sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
         os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -66,8 +71,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    def compile_binding():
+        import sysconfig
+
+        import torch
+
+        root = os.path.dirname(torch.__file__)
+        tmp = CALLS + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+               "-I", os.path.join(root, "include"), "-I",
+               os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I",
+               sysconfig.get_paths()["include"], BINDING, "-o", tmp, "-L",
+               os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, CALLS)
+
+    with ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
+        binding.result()
     tmp = SO + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs],
                        capture_output=True, text=True)
@@ -79,6 +104,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 
 def lib():
@@ -95,6 +121,23 @@ def lib():
             _declare(L)
             _lib = L
     return _lib
+
+
+def calls():
+    """The marshalling module, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        import importlib.util
+
+        L = lib()
+        spec = importlib.util.spec_from_file_location("_calls", CALLS)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.logit_adjust, L.paged_attention, L.paged_attention_workspace,
+            L.attention_weight_sum, L.kv_cache_evict)))
+        _calls = m
+    return _calls
 
 
 class KvPool(ctypes.Structure):
