@@ -128,7 +128,7 @@ struct TileShape {
   // of the time a tile's bytes take (about 350 clocks per 64 columns; half that for the keys
   // alone).
   static constexpr int TileCost = 4;
-  static constexpr int PieceCost = (kWeigh ? 12 : Teams == 2 ? 4 : 10) / U + 1;
+  static constexpr int PieceCost = (kWeigh ? 20 : Teams == 2 ? 8 : 16) / U + 1;
   static_assert(TmemNeed <= 512 && NK >= 2 && Smem + kTables <= kSmemMax, "tile shape");
 };
 
@@ -340,7 +340,8 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
   }
   incl += before;
   // (a range of TileCost units or more holds a tile of any item that spans it)
-  const int wanted = (int)((total + gridDim.x - 1) / gridDim.x);
+  const int wanted = total >> 31 ? (int)((total + gridDim.x - 1) / gridDim.x)
+                                 : (int)(((unsigned)total + gridDim.x - 1) / gridDim.x);
   const int per = wanted < S::TileCost ? S::TileCost : wanted;
   const int64_t from = (int64_t)per * blockIdx.x;
   if (tid == 0) {

@@ -174,8 +174,8 @@ struct DraftShared {
 
 // Builds the chunk's tables (all threads; ends with a CTA barrier).
 __device__ __forceinline__ void build_tables(const AdjustArgs& A, const Chunk& c,
-                                             unsigned char* smem, DraftShared& D, Tables& S,
-                                             RowRule& r) {
+                                             unsigned char* smem, int my_draft,
+                                             DraftShared& D, Tables& S, RowRule& r) {
   const int C = 1 << A.log_chunk, tid = threadIdx.x, lane = tid & 31, b = c.b;
   S.add = reinterpret_cast<float*>(smem);
   S.seen = reinterpret_cast<uint32_t*>(smem + 4 * (size_t)C);
@@ -208,7 +208,7 @@ __device__ __forceinline__ void build_tables(const AdjustArgs& A, const Chunk& c
       }
     };
     constexpr int U = 8;
-    // four tokens a load where the row allows (the row's end is padded to L_max, a multiple of 4)
+    // four tokens a load where the row allows (rows are L_max long, a multiple of 4)
     if (A.L_max % 4 == 0 && (reinterpret_cast<uintptr_t>(h) & 15) == 0) {
 #pragma unroll 1
       for (int q0 = 4 * tid; q0 < c.n; q0 += 4 * U * kAdjThreads) {
@@ -221,6 +221,7 @@ __device__ __forceinline__ void build_tables(const AdjustArgs& A, const Chunk& c
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int q = q0 + 4 * u * kAdjThreads;
+          if (q >= c.n) break;
           enter(q, t[u].x);
           enter(q + 1, t[u].y);
           enter(q + 2, t[u].z);
@@ -243,7 +244,7 @@ __device__ __forceinline__ void build_tables(const AdjustArgs& A, const Chunk& c
   }
   __syncthreads();
   if (tid < ndraft) {
-    const int v = __ldg(A.draft + (int64_t)b * (A.P - 1) + tid) - c.c0;
+    const int v = my_draft - c.c0;
     const bool here = (unsigned)v < (unsigned)(c.c1 - c.c0);
     D.x[tid] = here ? v : -1;
     D.said[tid] = here && cnt[v] > 0;
@@ -313,6 +314,9 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
   __shared__ uint16_t list[kListed];
   __shared__ int warp_count[kAdjThreads / 32];
   const int tid = threadIdx.x;
+  const int b0 = blockIdx.x % A.B;
+  const int my_draft =
+      A.draft && threadIdx.x < A.P - 1 ? __ldg(A.draft + (int64_t)b0 * (A.P - 1) + threadIdx.x) : -1;
   const Chunk c = chunk_of(A);
   const T* in = static_cast<const T*>(A.in) + c.b * A.in_req + c.c0;
   T* out = static_cast<T*>(A.out) + c.b * A.out_req + c.c0;
@@ -336,13 +340,26 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
       bulk_g2s(ring + i * stage, in + i * A.in_row, bytes, &full[i]);
     }
   }
-  Tables S;
-  RowRule r;
-  build_tables(A, c, adj_smem + kAdjStages * stage, D, S, r);
-  const uint8_t* touched = reinterpret_cast<const uint8_t*>(S.touched);
+  // A thread's vectors are q = tid + u * kAdjThreads; kVecs of them cover the largest chunk. Their
+  // touched bits stay in registers, their masks are loaded a row ahead.
+  constexpr int kVecs = 2;
   const uint8_t* const allowed =
       A.allowed ? reinterpret_cast<const uint8_t*>(A.allowed + (int64_t)c.b * A.P * A.W) + c.c0 / 8
                 : nullptr;
+  uint32_t touch[kVecs], next_ok[kVecs];
+  auto load_ok = [&](int i) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int q = tid + u * kAdjThreads, at = E == 8 ? q : q >> 1;
+      next_ok[u] = 0xffu;
+      if (allowed && i < rows && q < nvec) next_ok[u] = __ldg(allowed + (int64_t)i * A.W * 4 + at);
+    }
+  };
+  load_ok(0);
+  Tables S;
+  RowRule r;
+  build_tables(A, c, adj_smem + kAdjStages * stage, my_draft, D, S, r);
+  const uint8_t* touched = reinterpret_cast<const uint8_t*>(S.touched);
 
   // The touched tokens in ascending order, a word of their bits per thread.
   int count = 0;
@@ -371,18 +388,6 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
   }
   const bool listed = count <= kListed;
 
-  // A thread's vectors are q = tid + u * kAdjThreads; kVecs of them cover the largest chunk. Their
-  // touched bits stay in registers, their masks are loaded a row ahead.
-  constexpr int kVecs = 2;
-  uint32_t touch[kVecs], next_ok[kVecs];
-  auto load_ok = [&](int i) {
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int q = tid + u * kAdjThreads, at = E == 8 ? q : q >> 1;
-      next_ok[u] = 0xffu;
-      if (allowed && i < rows && q < nvec) next_ok[u] = __ldg(allowed + (int64_t)i * A.W * 4 + at);
-    }
-  };
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     const int q = tid + u * kAdjThreads, at = E == 8 ? q : q >> 1;
@@ -394,7 +399,6 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
   };
   auto drafted_of = [&](int q) { return bits_of(S.drafted, q); };
   auto seen_of = [&](int q) { return bits_of(S.seen, q); };
-  load_ok(0);
   int s = 0;
   uint32_t phase = 0;
 #pragma unroll 1
@@ -476,6 +480,9 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_any_kernel(const AdjustArg
   using X = Vec<T>;
   extern __shared__ __align__(128) unsigned char adj_smem[];
   __shared__ DraftShared D;
+  const int b0 = blockIdx.x % A.B;
+  const int my_draft =
+      A.draft && threadIdx.x < A.P - 1 ? __ldg(A.draft + (int64_t)b0 * (A.P - 1) + threadIdx.x) : -1;
   const Chunk c = chunk_of(A);
   const T* in = static_cast<const T*>(A.in) + c.b * A.in_req;
   T* out = static_cast<T*>(A.out) + c.b * A.out_req;
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_any_kernel(const AdjustArg
   }
   Tables S;
   RowRule r;
-  build_tables(A, c, adj_smem, D, S, r);
+  build_tables(A, c, adj_smem, my_draft, D, S, r);
   const uint32_t* allowed = A.allowed ? A.allowed + (int64_t)c.b * A.P * A.W : nullptr;
 #pragma unroll 1
   for (int i = 0; i <= c.nd; ++i) {

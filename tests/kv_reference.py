@@ -198,3 +198,44 @@ def close(got, want, tol):
     got, want = got.double(), want.double()
     same = (got == want) | (got.isnan() & want.isnan())
     return bool((same | ((got - want).abs() <= tol)).all())
+
+
+def attention_on_device(q, k, v, table, lens, num_draft, *, scale, softcap=0.0, window=0,
+                        slopes=None):
+    """paged_attention's definition and bounds for many requests, in 64 bits with the pools (zeros
+    past every length) on q's device: (out, lse, bound on out, bound on lse, live rows)."""
+    B, P, Hq, D = q.shape
+    pages, page, Hkv, _ = k.shape
+    n = int(lens.max()) if B else 0
+    cols = max(1, -(-n // page))
+    row = lambda pool: pool[table[:, :cols].clamp(min=0).long()].flatten(1, 2)[:, :n].double()  # noqa: E731
+    kk, vv = row(k), row(v)  # [B, n, Hkv, D]
+    qq = q.double().unflatten(2, (Hkv, -1))
+    s = torch.einsum("bphgd,bnhd->bhgpn", qq, kk) * scale
+    err = (D + 4) * 2.0 ** -24 * abs(scale) * torch.einsum("bphgd,bnhd->bhgpn", qq.abs(), kk.abs())
+    if softcap:
+        s = softcap * torch.tanh(s / softcap)
+        err = err + softcap * 2.0 ** -21
+    i, j = torch.arange(P, device=q.device), torch.arange(n, device=q.device)
+    pos = (lens[:, None] - 1 - num_draft[:, None] + i)[:, None, None, :, None]
+    slope = 0.0 if slopes is None else slopes.double().view(1, Hkv, -1, 1, 1)
+    away = (pos - j).double()
+    err = err + 2.0 ** -22 * (away.abs() * abs(slope) + s.abs())
+    s = s - slope * away
+    sees = j <= pos
+    if window:
+        sees = sees & (j > pos - window)
+    s = s.masked_fill(~sees, -math.inf)
+    any_key = sees.any(-1, keepdim=True).expand(*s.shape[:-1], 1)
+    lse = torch.logsumexp(s, -1, keepdim=True)
+    p = torch.where(any_key, torch.exp(s - lse), 0.0).nan_to_num(0.0)
+    out = torch.einsum("bhgpn,bnhd->bphgd", p, vv).flatten(2, 3)
+    size = torch.einsum("bhgpn,bnhd->bphgd", p, vv.abs()).flatten(2, 3)
+    worst = torch.where(sees, err, 0.0).amax(-1)  # [B, Hkv, G, P]
+    worst = worst.flatten(1, 2).transpose(1, 2)
+    half = HALF_STEP[q.dtype]
+    w = 2 * worst[..., None] + 2.0 ** -21 + (n + 8) * 2.0 ** -23 + half
+    lse = lse[..., 0].flatten(1, 2).transpose(1, 2)
+    tol = w * size + half * out.abs() + (2.0 ** -24 if q.dtype == torch.float16 else 1e-30)
+    tol_lse = worst + (n + 8) * 2.0 ** -24 + 2.0 ** -21 * (1 + lse.abs().nan_to_num(0, 0, 0))
+    return out, lse, tol, tol_lse, i <= num_draft[:, None]

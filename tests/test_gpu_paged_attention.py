@@ -88,6 +88,54 @@ def test_many_rows_of_one_head():
     check_attention(cache, queries(2, 9, 48, 64, torch.float16), [8, 5])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D,G,P,page,rule", [
+    (64, 1, 1, 16, {}), (64, 5, 5, 8, {}), (64, 8, 6, 64, dict(window=300)), (64, 8, 13, 32, {}),
+    (128, 4, 1, 16, dict(softcap=20.0)), (128, 4, 6, 128, {}), (128, 8, 6, 32, {}),
+    (128, 16, 8, 256, dict(slopes=True)), (256, 2, 3, 16, {}), (256, 4, 7, 64, {}),
+    (256, 8, 6, 16, dict(window=129)), (256, 8, 9, 8, {}),
+])
+def test_many_requests_share_the_ranges(dtype, D, G, P, page, rule):
+    """Every width of the kernel with far more pieces than CTAs: short and long caches, empty ones
+    and ones shorter than the drafts, side by side."""
+    g = torch.Generator().manual_seed(D + G + P)
+    B, Hkv = 150, 2
+    lens = torch.cat([torch.tensor([0, 1, P, 128, 129]),
+                      torch.exp(torch.rand(B - 5, generator=g) * 7.6).int().clamp(1, 2000)]).int()
+    lens = lens[torch.randperm(B, generator=g)]
+    nd = torch.randint(0, P, (B,), generator=g).int()
+    cols = -(-int(lens.max()) // page)
+    counts = -(-lens.long() // page)
+    total = int(counts.sum())
+    ids, table = torch.randperm(total, generator=g).int(), torch.full((B, cols), -1, dtype=torch.int32)
+    at = 0
+    for b, c in enumerate(counts.tolist()):
+        table[b, :c] = ids[at:at + c]
+        at += c
+    dg = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn((total, page, Hkv, D), generator=dg, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn((B, P, Hkv * G, D), generator=dg, device="cuda").to(dtype)
+    table, lens, nd = table.cuda(), lens.cuda(), nd.cuda()
+    rule = dict(rule)
+    if rule.get("slopes"):
+        rule["slopes"] = torch.rand(Hkv * G, generator=dg, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((B, P, Hkv * G), 7.0, device="cuda")
+    for _ in range(2):  # (the second call finds what the first left in the workspace)
+        sv.paged_attention(q, k, v, table, lens, num_draft=nd, out=out, out_lse=lse, **rule)
+    acc = nd - (torch.arange(B, device="cuda") % 2).int()
+    want, want_lse, tol, tol_lse, live = ref.attention_on_device(q, k, v, table, lens, nd,
+                                                                 scale=D ** -0.5, **rule)
+    assert ref.close(out[live], want[live], tol[live])
+    assert ref.close(lse[live], want_lse[live], tol_lse[live])
+    assert bool((out[~live] == 7).all()) and bool((lse[~live] == 7).all())
+    # the weights of all rows up to the accepted ones: every row that sees a key gave 1 in all
+    w = sv.attention_weight_sum(q, k, table, lens, lse, num_draft=nd, accept_len=acc, **rule)
+    rows = torch.arange(P, device="cuda")
+    gave = ((rows <= acc[:, None]) & (lens[:, None] - 1 - nd[:, None] + rows >= 0)).sum(1) * G
+    assert torch.allclose(w.double().sum(-1), gave[:, None].double().expand(B, Hkv), rtol=2e-4,
+                          atol=1e-12)
+
+
 def test_large_scores_keep_their_range():
     cache = ref.Cache([400, 129], 16, 1, 128, torch.float16, seed=4)
     for pool in cache.pools[:1]:
