@@ -55,7 +55,7 @@ typedef struct {
 
 /* How a row scores a key. HOST memory, read during the call.
  *   scale    multiplies q.k; finite.
- *   softcap  0 for none, else c > 0: the scaled score s becomes c * tanh(s / c).
+ *   softcap  0 for none, else c >= 1e-6: the scaled score s becomes c * tanh(s / c).
  *   window   0 for none, else a row at position p sees keys p - window + 1 .. p only.
  *   slopes   DEVICE [Hq] fp32 or NULL: the capped score of a key at position j falls by
  *            slopes[h] * (p - j).
@@ -76,7 +76,7 @@ typedef struct {
  *
  * Arguments
  *   q            [B, P, Hq, D]; element strides q_req, q_row, q_head (multiples of 8), D
- *                contiguous, 16-byte aligned. Rows past n_r are not read.
+ *                contiguous, 16-byte aligned. What rows past n_r hold reaches no output.
  *   k, v         pools of num_pages pages.
  *   page_table   [B, max_pages] int32: page t of request r holds tokens t*page_size on. Only
  *                pages that hold a key some row sees are looked up.
@@ -84,14 +84,15 @@ typedef struct {
  *   num_draft    [B] int32 in [0, P-1], or NULL for all P-1.
  *   out          [B, P, Hq, D] contiguous. Rows past n_r are not written.
  *   out_lse      [B, P, Hq] fp32, or NULL.
- *   workspace    >= paged_attention_workspace(shape) bytes.
+ *   workspace    >= paged_attention_workspace(shape) bytes; needs no initialisation.
  * What slots past n hold never reaches an output (NaN included), nor does a drafted token's
  * value reach the rows ahead of it.
  * A request with seq_len or num_draft out of range gets NaN in out and out_lse in all its P
  * rows; one whose page table names a page outside [0, num_pages) for a key that is seen, NaN
- * in its rows 0 .. n_r.
- * Scores, their softmax and the sums over values are fp32; the weights exp(s_j - max) are
- * rounded for the product with the values (see the kernel).
+ * at least in the rows that see such a key.
+ * Scores, their softmax and the sums over values are fp32; the weights exp(s_j - max) enter the
+ * product with the values as a sum of two numbers of the values' type. The work is split over
+ * the SMs by a rule on the lengths alone and joined in order: equal calls give equal bits.
  * ---------------------------------------------------------------------------------------- */
 size_t paged_attention_workspace(const sv_kv_shape* shape);
 
@@ -121,7 +122,7 @@ sv_status paged_attention(const sv_kv_shape* shape, const sv_score_rule* rule, c
  *                least every seq_len; a request whose seq_len is above it is out of range.
  * A request with seq_len, num_draft or accept_len (above num_draft) out of range is left
  * unwritten but for out[r, :, 0] = NaN (stride >= 1); a page outside [0, num_pages) gives NaN
- * in the slots it would hold.
+ * in those of its slots that a counted row sees.
  * No workspace.
  * ---------------------------------------------------------------------------------------- */
 sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_score_rule* rule,
@@ -153,6 +154,7 @@ sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_score_rule* ru
  *   out_len      [B] int32: m, or -1 for a request with a data error.
  *   out_index    [B, Hkv, budget] int32: the old slot of each kept one, then -1.
  *   out_weights  [B, Hkv, budget] fp32: the kept slots' weights, then 0; or NULL.
+ * B * Hkv is at most 65535, else SV_ERR_UNSUPPORTED.
  * A request with seq_len out of range (or above stride) or with a page outside its pool's
  * range among those it needs, in either table, gets out_len = -1, out_index all -1 and
  * out_weights all 0, and nothing of it is copied.

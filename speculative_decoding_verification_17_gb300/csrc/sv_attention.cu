@@ -102,6 +102,7 @@ sv_status fill_tile_args(TileArgs& A, CUtensorMap* mq, CUtensorMap* mk, const sv
   A.max_pages = s->max_pages;
   int columns;
   row_blocks(s, weigh, &A.pos_block, &A.blocks, &columns);
+  if (!ranges_fit(s, A.blocks)) return SV_ERR_UNSUPPORTED;
   A.box = s->page_size < kTileKeys ? s->page_size : kTileKeys;
   A.bf16 = s->dtype == SV_KV_BF16;
   A.rule = score_rule(rule);

@@ -39,8 +39,8 @@ inline sv_status check_pool(const sv_kv_pool* p) {
 }
 
 inline sv_status check_rule(const sv_score_rule* r) {
-  if (!r || !std::isfinite(r->scale) || !std::isfinite(r->softcap) || r->softcap < 0.0f ||
-      r->window < 0 || !aligned_to(r->slopes, 4))
+  if (!r || !std::isfinite(r->scale) || !std::isfinite(r->softcap) ||
+      (r->softcap != 0.0f && r->softcap < 1e-6f) || r->window < 0 || !aligned_to(r->slopes, 4))
     return SV_ERR_INVALID_ARG;
   return SV_OK;
 }

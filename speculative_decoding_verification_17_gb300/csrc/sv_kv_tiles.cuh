@@ -51,6 +51,7 @@ constexpr int kUnitBytes = kTileKeys * 128;  // 64 columns of a tile
 constexpr int kSmemMax = 232448;             // shared memory of a CTA
 constexpr float kNoMax = -3.402823466e38f;   // a maximum below every finite score
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct JoinItem;
 
@@ -779,10 +780,16 @@ __device__ __forceinline__ void apply_rule(float (&s)[kC], const ScoreRule& r, f
                                            const float* slope, const float* ahead) {
   const float scale2 = r.scale * kLog2e;
   if (__builtin_expect(r.softcap > 0.0f, 0)) {
-    // c tanh(y) = c - 2 c / (1 + 2^(2 log2(e) y))
-    const float in = 2.0f * scale2 / r.softcap, c2 = r.softcap * kLog2e;
+    // c tanh(y) = c - 2 c / (1 + 2^(2 log2(e) y)); below |y| = 1/8, where that cancels, the series
+    // y (1 - y^2/3 + 2 y^4/15), off by y^6 / 18 (2^-22)
+    const float in = scale2 / r.softcap * kLn2, c2 = r.softcap * kLog2e;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) s[c] = fmaf(-2.0f * c2, rcp_fast(1.0f + ex2(s[c] * in)), c2);
+    for (int c = 0; c < kC; ++c) {
+      const float y = s[c] * in, y2 = y * y;
+      const float far = fmaf(-2.0f * c2, rcp_fast(1.0f + ex2(y * (2.0f * kLog2e))), c2);
+      const float near = s[c] * scale2 * fmaf(y2, fmaf(y2, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
+      s[c] = y2 < 1.0f / 64.0f ? near : far;
+    }
   } else {
 #pragma unroll
     for (int c = 0; c < kC; ++c) s[c] *= scale2;
@@ -1276,6 +1283,9 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
       set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
       bar_sync(kAllBar, S::SoftThreads);
       const int ta = pass == 0 ? p.ta : p.ma, tb = pass == 0 ? p.tb : p.mb;
+      // the columns from here on are of rows that do not count, whose products may be anything
+      // (those past the copied block are zero)
+      const int dead = p.live < A.pos_block ? p.live * A.G : S::N;
       // what a key's slot holds already and its page, loaded a tile ahead
       auto held = [&](int t) {
         const int j = t * kTileKeys + key;
@@ -1301,11 +1311,17 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
           wait_phase(&sh.s_full[0][group], (uint32_t)used & 1u, &sh.dead);
           ++used;
           tc_fence_after();
-#pragma unroll 1
+#pragma unroll 2
           for (int q = 0; q < S::N; q += 16) {
+            if (q >= dead) break;
             float s[16];
             tmem_ld16(lane_base + group * S::N + q, s);
             tmem_wait_ld();
+            if (__builtin_expect(q + 16 > dead, 0)) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (q + c >= dead) s[c] = 0.0f;
+            }
             float scale = A.rule.scale * kLog2e;
             if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
               apply_rule<16>(s, A.rule, (float)(p.pos0 - j), &T.slope[q], &T.ahead[q]);
@@ -1529,13 +1545,15 @@ sv_status fill_tile_args(TileArgs& A, CUtensorMap* mq, CUtensorMap* mk, const sv
                          const int32_t* seq_len, const int32_t* num_draft, bool weigh);
 sv_status encode_pool(CUtensorMap* map, const sv_kv_shape* s, const sv_kv_pool* pool);
 
+// Whether a CTA's share of the longest work list these sizes allow stays in 32 bits.
+inline bool ranges_fit(const sv_kv_shape* s, int blocks) {
+  const double tiles = (double)s->max_pages * s->page_size / kTileKeys + 1;
+  return (double)s->B * s->Hkv * blocks * (tiles * 4 + 32) < 1e9 * device_sm_count();
+}
+
 // Query rows per pass: as many whole positions as 128 columns hold (64 in an attention of
 // D = 256, where the weights of more columns would leave no room for two tiles), evenly over
 // the passes.
-inline bool ranges_fit(const sv_kv_shape* s, int blocks) {
-  const double tiles = (double)s->max_pages * s->page_size / kTileKeys + 1;
-  return (double)s->B * s->Hkv * blocks * (tiles * 4 + 16) < 1.5e11;  // 2^30 units per CTA
-}
 inline void row_blocks(const sv_kv_shape* s, bool weigh, int* pos_block, int* blocks,
                        int* columns) {
   const int G = s->Hq / s->Hkv, most = (s->D == 256 && !weigh ? 64 : 128) / G;

@@ -353,3 +353,46 @@ def test_key_weights_of_bad_requests():
     nan = w[2, 0].isnan()
     assert bool(nan[48:64].all()) and not bool(nan[:48].any()) and not bool(nan[64:].any())
     assert bool((w[3, 0, :100] == 0).all()) and bool((w[3, 0, 100:] == 7).all())
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf, 3e38])
+@pytest.mark.parametrize("G,P", [(4, 3), (8, 5), (16, 9)])
+def test_rows_that_do_not_count_may_hold_anything(value, G, P):
+    lens = [40, 130, 257, 300]
+    cache = ref.Cache(lens, 16, 2, 64, torch.bfloat16, seed=31)
+    nd, acc = [0, 1, P - 1, P - 1], [0, 0, 1, P - 2]
+    q = queries(4, P, 2 * G, 64, torch.bfloat16)
+    junk = q.clone()
+    for b, n in enumerate(nd):
+        junk[b, n + 1:] = value
+    out, lse = check_attention(cache, junk, nd)
+    for b, n in enumerate(acc):
+        junk[b, n + 1:] = value
+    a = dev_args(cache, nd)
+    got = sv.attention_weight_sum(junk.cuda(), a["k"], a["table"], a["seq_len"], lse.cuda(),
+                                  num_draft=a["num_draft"],
+                                  accept_len=torch.tensor(acc).int().cuda(),
+                                  out=torch.full((4, 2, 304), 7.0, device="cuda")).cpu()
+    want, tol = ref.weight_sum(cache, q, nd, acc, lse, torch.zeros((4, 2, 304)),
+                               scale=64 ** -0.5)
+    for b, n in enumerate(lens):
+        assert ref.close(got[b, :, :n], want[b, :, :n], tol[b, :, :n]), b
+
+
+def test_a_cap_far_above_the_scores_changes_nothing():
+    # c tanh(s / c) is s - s^3 / 3c^2: less than 2^-30 of a score of 100 at c = 10^7
+    cache = ref.Cache([1, 200, 513], 16, 2, 128, torch.float16, seed=32)
+    q = queries(3, 2, 8, 128, torch.float16)
+    a = dev_args(cache, None)
+    args = (q.cuda(), a["k"], a["v"], a["table"], a["seq_len"])
+    out, lse = sv.paged_attention(*args)
+    capped, lse_c = sv.paged_attention(*args, softcap=1e7)
+    want = ref.attention(cache, q, [1, 1, 1], scale=128 ** -0.5)
+    for b in range(3):
+        for i in range(2):
+            for head in range(8):
+                if not (b == 0 and i == 0):  # (the row of a cache of one that sees no key)
+                    o, l, tol, tol_l = want[b, i, head]
+                    assert ref.close(capped[b, i, head].cpu(), o, tol), (b, i, head)
+                    assert abs(float(lse_c[b, i, head]) - l) <= tol_l, (b, i, head)
+    assert bool((lse_c[0, 0] == -math.inf).all())

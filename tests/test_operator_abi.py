@@ -65,7 +65,7 @@ QUERY_SHAPES = SHAPES + [
     (dict(P=0), INVALID), (dict(P=18), UNSUPPORTED), (dict(Hq=7), INVALID),
     (dict(Hq=130), UNSUPPORTED),
 ]
-RULES = [dict(scale=float("nan")), dict(scale=float("inf")), dict(softcap=-1.0),
+RULES = [dict(scale=float("nan")), dict(scale=float("inf")), dict(softcap=-1.0), dict(softcap=1e-9),
          dict(softcap=float("nan")), dict(window=-1), dict(slopes=0x10002)]
 POOLS = [dict(data=0), dict(data=0x20008), dict(page=0), dict(page=-4096), dict(token=100),
          dict(head=4)]
@@ -117,6 +117,8 @@ def test_shapes_rules_and_pools_are_checked():
         for name in ("k", "v", "nk", "nv"):
             assert evict(**{name: pool(**kw)}) == INVALID, kw
     assert sv.library().paged_attention_workspace(shape()) > 0
+    huge = dict(B=4096, Hkv=1024, Hq=1024, page_size=1024, max_pages=1 << 19)
+    assert attend(shape(**huge)) == UNSUPPORTED and weigh(shape(**huge)) == UNSUPPORTED
 
 
 def test_pointers_and_strides_are_checked():
