@@ -16,6 +16,11 @@
 // first form that streamed every vector through registers, with the penalties inlined for all
 // its elements, ran at 46 % of the copy rate: its code did not fit the instruction cache.)
 // Rows whose V or addresses do not allow 16-byte copies take a second kernel, element by element.
+//
+// Measured in graph replays, of the 6782 GB/s a copy reaches: 512 requests x 9 rows of 128256 bf16
+// with histories of 8192, 64 biases and masks 393 us (2098 MB, 79 %; 341 us without the scan of
+// the histories, which each of a request's 32 chunks repeats); 64 x 6 rows of 32000 bf16 with masks
+// 14.2 us (46 MB); one request of 5 rows of 50257 fp32 5.5 us.
 
 #include <cstdint>
 
@@ -46,7 +51,7 @@ struct AdjustArgs {
   const float* bias_val;
   const uint32_t* allowed;
   int L_max, n_bias, B, P, V, W;
-  int log_chunk;  // tokens per chunk, a power of two from 1024 to 4096
+  int log_chunk;  // tokens per chunk, 1024 to 4096, a power of two
 };
 
 // E elements of a row as floats, and back (one rounding).
@@ -526,8 +531,9 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_any_kernel(const AdjustArg
 
 template <typename T>
 sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
-  // Chunks of 4096 bf16 or 2048 fp32 logits, or shorter ones (each scans the history) while they
-  // would leave SMs without work: five CTAs are resident per SM.
+  // Chunks of 4096 bf16 or 2048 fp32 logits, or half of that (each scans the history) while they
+  // would leave SMs without work. (512 requests of 9 rows of 128256 bf16: 405 us in chunks of
+  // 4096, 478 us of 2048, 472 us of 8192, whose ring and tables leave room for fewer CTAs.)
   const int64_t wanted = 2 * (int64_t)device_sm_count();
   const int least = sizeof(T) == 4 ? 10 : 11;
   A.log_chunk = least + 1;
