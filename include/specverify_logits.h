@@ -35,6 +35,7 @@ extern "C" {
  *                  request are not read.
  *   history        [B, L_max] int32, or NULL (then hist_len and prompt_len are NULL and
  *                  L_max is 0). Tokens outside [0, V) count for nothing (padding).
+ *                  L_max < 2^30, else SV_ERR_UNSUPPORTED.
  *   hist_len       [B] int32, in [0, L_max].
  *   prompt_len     [B] int32, in [0, hist_len[r]], or NULL for no prompt.
  *   draft_tokens   [B, P-1] int32, or NULL: no drafts count. Tokens outside [0, V) count for

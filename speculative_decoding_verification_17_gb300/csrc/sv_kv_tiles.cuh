@@ -104,12 +104,13 @@ struct TileShape {
   static constexpr bool Weigh = kWeigh;
   static constexpr int U = D / 64;  // units of a key or value tile
   // Softmax warps: two groups of four (one warp per quarter of the tile's keys). In the
-  // attention of up to 32 columns the groups are two teams that take the pieces in turn, each
+  // attention of 16 columns the groups are two teams that take the pieces in turn, each
   // with its own score, weight and output buffers, so one team's end of a piece (its last
   // product, its output, the next piece's tables) passes under the other's tiles; of wider
-  // tiles each group takes half of the columns and there is one team. In the key weights each
+  // tiles each group takes half of the columns and there is one team (6 positions of 64 requests,
+  // 24 of 32 columns: 98 us with one team, 111 us with two, whose buffers shorten the rings). In the key weights each
   // group takes every other tile.
-  static constexpr int Teams = !kWeigh && N <= 32 ? 2 : 1;
+  static constexpr int Teams = !kWeigh && N == 16 ? 2 : 1;
   static constexpr int SoftWarps = 8;
   static constexpr int SoftThreads = 32 * SoftWarps;
   static constexpr int Threads = SoftThreads + (kWeigh ? 64 : 128);
@@ -138,7 +139,8 @@ struct TileShape {
   // Two score buffers per team, two outputs. Where tensor memory has room, the products with the
   // high and the low halves of the weights are one instruction of twice the columns (the values,
   // whose read from shared memory bounds a narrow instruction, are read once) and are added at
-  // the end; else the second accumulates onto the first.
+  // the end; else the second accumulates onto the first. (9 positions over long caches, 64 columns:
+  // 163 us wide, 179 us in two; 16 columns: 94 and 96 us.)
   static constexpr bool Wide = !kWeigh && 2 * (Teams + 2 * MBlocks) * N <= 512;
   static constexpr int ON = Wide ? 2 * N : N;  // columns of an accumulator
   static constexpr int TmemNeed = 2 * (Teams * N + MBlocks * ON);

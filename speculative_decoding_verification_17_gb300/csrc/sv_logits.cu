@@ -18,8 +18,9 @@
 // Rows whose V or addresses do not allow 16-byte copies take a second kernel, element by element.
 //
 // Measured in graph replays, of the 6782 GB/s a copy reaches: 512 requests x 9 rows of 128256 bf16
-// with histories of 8192, 64 biases and masks 393 us (2098 MB, 79 %; 341 us without the scan of
-// the histories, which each of a request's 32 chunks repeats); 64 x 6 rows of 32000 bf16 with masks
+// with histories of 8192, 64 biases and masks 374 us (2098 MB, 83 %; the scan of the histories,
+// which each of a request's 32 chunks repeats, is about 50 us of it, but shared by clusters of 2, 4
+// or 8 CTAs, over distributed shared memory, the call took 467, 578 and 607 us); 64 x 6 rows of 32000 bf16 with masks
 // 14.2 us (46 MB); one request of 5 rows of 50257 fp32 5.5 us.
 
 #include <cstdint>
@@ -148,7 +149,9 @@ __device__ __forceinline__ float adjusted(const Tables& T, const RowRule& r, int
   return y + a;
 }
 
-constexpr int kAdjStages = 4;  // row pieces in flight (8 KiB each)
+// Row pieces in flight, of 8 KiB: five CTAs fit an SM with three, four with four (512 requests x 9
+// rows of 128256 bf16: 374 and 395 us; with two 455).
+constexpr int kAdjStages = 3;
 // A chunk with up to kListed touched tokens lists them, and its threads share the list out; in one
 // with more each thread visits its own vectors. (Of text that repeats, the chunk of the most
 // frequent tokens is nearly full, the others hold a few percent: with the vectors alone a warp
@@ -532,8 +535,9 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_any_kernel(const AdjustArg
 template <typename T>
 sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
   // Chunks of 4096 bf16 or 2048 fp32 logits, or half of that (each scans the history) while they
-  // would leave SMs without work. (512 requests of 9 rows of 128256 bf16: 405 us in chunks of
-  // 4096, 478 us of 2048, 472 us of 8192, whose ring and tables leave room for fewer CTAs.)
+  // would leave SMs without work. (512 requests of 9 rows of 128256 bf16, four pieces in flight:
+  // 405 us in chunks of 4096, 478 us of 2048, 472 us of 8192, whose tables leave room for fewer
+  // CTAs.)
   const int64_t wanted = 2 * (int64_t)device_sm_count();
   const int least = sizeof(T) == 4 ? 10 : 11;
   A.log_chunk = least + 1;
@@ -570,7 +574,7 @@ extern "C" sv_status logit_adjust(const void* logits, int64_t in_req_stride,
                                   sv_stream_t stream) {
   if (B < 0 || P < 1 || V < 1 || L_max < 0 || n_bias < 0) return SV_ERR_INVALID_ARG;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
-  if (P > SV_MAX_K + 1) return SV_ERR_UNSUPPORTED;
+  if (P > SV_MAX_K + 1 || L_max >= (1 << 30)) return SV_ERR_UNSUPPORTED;
   if (B == 0) return SV_OK;
   if (!logits || !out) return SV_ERR_INVALID_ARG;
   if (history ? (!hist_len || L_max < 1) : (hist_len || prompt_len || L_max != 0))

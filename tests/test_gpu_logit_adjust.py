@@ -70,6 +70,21 @@ def test_against_definition(dtype, B, P, V, H, bias, mask):
     check(d, call(d))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H", [1500, 2047, 5000])
+@pytest.mark.parametrize("V", [4104, 12296, 33000])
+def test_long_histories(dtype, H, V):
+    # (more than a thread's batch of loads, in fours and one by one; a short last chunk)
+    d = case(3, 4, V, dtype, H=H, bias=30, mask="half", seed=V + H, zipf=H != 5000)
+    d["hist_len"][0] = H
+    got = call(d)
+    check(d, got)
+    d["hist_len"][1] = H + 1  # refused; the others are as they were
+    again = call(d)
+    assert bool(again[1, :d["num_draft"][1] + 1].isnan().all())
+    assert torch.equal(again[0], got[0]) and torch.equal(again[2], got[2])
+
+
 def test_every_option_alone():
     full = case(3, 4, 640, torch.float32, H=200, bias=20, mask="half", seed=5)
     for keep in (("history", "hist_len"), ("draft",), ("bias_tokens", "bias_values"),

@@ -22,6 +22,7 @@ def adjust(**kw):
 
 
 @pytest.mark.parametrize("kw,status", [
+    (dict(L=1 << 30), UNSUPPORTED),
     (dict(B=-1), INVALID), (dict(P=0), INVALID), (dict(V=0), INVALID), (dict(dtype=2), INVALID),
     (dict(P=18, zr=99999, orq=99999), UNSUPPORTED), (dict(z=None), INVALID),
     (dict(out=None), INVALID), (dict(h=None), INVALID), (dict(hl=None), INVALID),
