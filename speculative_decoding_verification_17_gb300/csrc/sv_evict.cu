@@ -11,8 +11,8 @@
 // enough (request, head) pairs to fill the SMs the selecting CTA copies its own, so that one CTA's
 // selection (latency: about ten CTA barriers) passes under another's copies (bandwidth); with
 // fewer a second launch spreads the copies over all SMs. Bound: the copies. Measured in graph
-// replays: 64 requests x 8 heads of 128, 1000 .. 16384 keys cut to 2048, 187 us (1005 MB, 79 % of
-// the 6782 GB/s a copy reaches); one request of 5003 keys cut to 1024, 14.2 us.
+// replays: 64 requests x 8 heads of 128, 1000 .. 16384 keys cut to 2048, 169 us (1005 MB, 88 % of
+// the 6782 GB/s a copy reaches); one request of 5003 keys cut to 1024, 13.4 us.
 #include <cstdint>
 
 #include "specverify_kv.h"
@@ -30,7 +30,11 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kHeld = 16384;   // weights in shared memory (64 KiB)
-constexpr int kMoveBatch = 4;  // keys per thread in flight
+constexpr int kMoveBatch = 2;  // keys per thread in flight
+// CTAs of an SM that select and copy: with two (32 registers a thread) one's selection passes under
+// the other's copies. 64 requests x 8 heads of up to 16384 keys: 169 us; with one CTA and two or
+// four keys a thread 188 and 186 us; with two CTAs of 512 threads 216 and 190 us.
+constexpr int kBothCtas = 2;
 
 struct MoveArgs {
   const char *k, *v;
@@ -248,7 +252,7 @@ __device__ __forceinline__ int select_keys(const SelectArgs& A, int b, int h, fl
 }
 
 template <bool kMoves>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, kMoves ? kBothCtas : 1)
     select_kernel(const SelectArgs A, const __grid_constant__ MoveArgs M) {
   extern __shared__ float held_w[];
   if (!kMoves) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -316,8 +320,8 @@ extern "C" sv_status kv_cache_evict(const sv_kv_shape* shape, const sv_kv_pool* 
              2 * new_v->page_stride, 2 * new_v->token_stride, 2 * new_v->head_stride,
              page_table, new_table, out_len, out_index, shape->Hkv, budget, lp,
              shape->max_pages, new_max_pages, log2_of(shape->D / 8)};
-  // (64 requests x 8 heads of up to 16384 keys: 187 us fused, 204 us in two launches; 8 rows of
-  // 5003 keys: 14 us in two launches, of which the copies take 7)
+  // (64 requests x 8 heads of up to 16384 keys, one CTA per SM: 187 us fused, 204 us in two
+  // launches; 8 rows of 5003 keys: 13 us in two launches, of which the copies take 6)
   const bool fused = rows >= device_sm_count();
   auto select = fused ? select_kernel<true> : select_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
