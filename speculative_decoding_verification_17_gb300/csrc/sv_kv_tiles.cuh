@@ -237,13 +237,14 @@ struct Piece {
   int n;                                  // tokens of the request
   int ta, tb;                             // its tiles
   int ma, mb;                             // those that go through the tensor cores
-  int pass;    // (key weights) the row block
-  int turn;    // pieces before it with (or, of one without, without) such tiles
+  int turn;    // pieces before it with such tiles
   int x0;      // such tiles before it
   int pieces;  // CTAs that hold a part of the item
   int flags;
 };
-enum { kStarts = 1, kEnds = 2, kBad = 4, kEndOfList = 8 };
+// kFresh: (key weights) no earlier pass over its tiles took any through the tensor cores; kHollow:
+// nor does this one, the last of them.
+enum { kStarts = 1, kEnds = 2, kBad = 4, kEndOfList = 8, kFresh = 16, kHollow = 32 };
 
 // Walks a range of the flat work list, in which an item takes PieceCost + tiles * TileCost
 // units; tile k belongs to the range that holds the item's unit PieceCost + k * TileCost.
@@ -253,9 +254,9 @@ struct Walk {
   int b, h, rb, n = 0, nd = 0, acc = 0;
   int off, left, per;
   Item it;
-  int turns = 0, fills = 0, x = 0;
+  int turns = 0, x = 0;
   int pass = 0;  // (key weights) the pass last given out
-  bool more_passes = false;
+  bool more_passes = false, had = false;
   enum { kLoad, kStay, kAdvance } step = kLoad;
   __device__ __forceinline__ Walk(const TileArgs& a, const Start& s)
       : A(a), b(s.b), h(s.h), rb(s.rb), off(s.off), left(s.left), per(s.per) {}
@@ -303,6 +304,7 @@ struct Walk {
         p.ta = it.t0 + ka;
         p.tb = it.t0 + kb;
         pass = 0;
+        had = false;
         p.flags = (ka == 0 ? kStarts : 0) | (kb == it.tiles ? kEnds : 0) | (it.bad ? kBad : 0);
         // of an item that goes on in other CTAs: how many of the ranges, from this one on, hold
         // its tiles (the first lies at unit PieceCost of it)
@@ -311,7 +313,6 @@ struct Walk {
       off += take;
       left -= take;
     }
-    p.pass = pass;
     p.i0 = it.i0;
     p.live = it.live;
     p.pos0 = it.pos0;
@@ -324,7 +325,7 @@ struct Walk {
       p.mb = p.tb < hi ? p.tb : hi;
       if (p.mb < p.ma) p.mb = p.ma;
     }
-    p.turn = p.mb > p.ma ? turns++ : fills++;
+    p.turn = turns;
     p.x0 = x;
     x += p.mb - p.ma;
     if (S::Weigh) {
@@ -332,6 +333,11 @@ struct Walk {
       // (the next piece starts from the item of the first pass)
       if (!more_passes && pass > 0 && step == kStay) step = kLoad;
     }
+    const bool busy = p.mb > p.ma;
+    p.flags = (p.flags & ~(kFresh | kHollow)) | (had ? 0 : kFresh) |
+              (busy || had || more_passes ? 0 : kHollow);
+    turns += busy;
+    had |= busy;
     return true;
   }
 };
@@ -397,7 +403,12 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
   __syncthreads();
 }
 
-// Pieces handed out and not yet taken by every role.
+// Pieces handed out and not yet taken by every role. Only pieces with tiles for the tensor cores are
+// handed out, so the queue cannot stop the walk: the warp that copies the keys takes the next piece
+// before it copies the last tile of the one at hand, X, and all it then waits for is that every role
+// has taken the piece kPieceQueue - 1 before X, which needs no tile later than those of the piece
+// ahead of X. (Any number of pieces without tiles may follow X: in the queue they would fill it while
+// the other roles wait for X's last tile.)
 constexpr int kPieceQueue = 8;
 
 // ---- shared memory ------------------------------------------------------------------------------
@@ -411,6 +422,7 @@ struct TileShared {
   uint64_t o_done[2];  // a piece has its last product, by ordinal % 2
   uint32_t tmem;
   int dead;
+  int hollow;  // the range holds pieces without tiles for the tensor cores
   int bad_piece[8];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 8
   uint64_t drain[2];
   // the pieces, from the warp that walks the work list to the other roles
@@ -480,19 +492,16 @@ struct Reader {
     if (mine) mbar_arrive(&sh.piece_empty[at.slot]);
     at.next(kPieceQueue);
   }
-  // Takes the next piece with tiles, by one thread or (kWarp) by a whole warp; false at the end
-  // of the list or when the CTA has given up.
+  // Takes the next piece, by one thread or (kWarp) by a whole warp; false at the end of the list
+  // or when the CTA has given up.
   template <bool kWarp>
   __device__ __forceinline__ bool next(Piece& p) {
-#pragma unroll 1
-    for (;;) {
-      p = wait();
-      bool end = *(volatile int*)&sh.dead || (p.flags & kEndOfList);
-      if (kWarp) end = __any_sync(0xffffffffu, end);  // (and every lane has read the piece)
-      if (end) return false;
-      release(!kWarp || (threadIdx.x & 31) == 0);
-      if (p.mb > p.ma) return true;
-    }
+    p = wait();
+    bool end = *(volatile int*)&sh.dead || (p.flags & kEndOfList);
+    if (kWarp) end = __any_sync(0xffffffffu, end);  // (and every lane has read the piece)
+    if (end) return false;
+    release(!kWarp || (threadIdx.x & 31) == 0);
+    return true;
   }
 };
 
@@ -521,23 +530,23 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
   unsigned char* dst = ring + kBase * kUnitBytes + lane * A.box * 128;
   Walk<S> walk(A, sh.start);
   Reader<S> reader(sh);
-  // the next piece with tiles; all lanes
+  // the next piece with tiles for the tensor cores; all lanes
+  bool hollow = false;
   auto take = [&](Piece& p) -> bool {
+    if (kValues) return reader.template next<true>(p);
+    bool more;
 #pragma unroll 1
-    for (;;) {
-      if (kValues) return reader.template next<true>(p);
-      const bool more = walk.next(p);
-      if (!more) p.flags = kEndOfList;
-      bool ok = wait_phase(&sh.piece_empty[reader.at.slot], reader.at.phase ^ 1u, &sh.dead);
-      ok = __all_sync(0xffffffffu, ok);
-      if (lane == 0) {
-        sh.piece[reader.at.slot] = p;
-        mbar_arrive(&sh.piece_full[reader.at.slot]);
-      }
-      reader.at.next(kPieceQueue);
-      if (!more || !ok) return false;
-      if (p.mb > p.ma) return true;
+    while ((more = walk.next(p)) && p.mb == p.ma) hollow |= (p.flags & kHollow) != 0;
+    if (!more) p.flags = kEndOfList;
+    bool ok = wait_phase(&sh.piece_empty[reader.at.slot], reader.at.phase ^ 1u, &sh.dead);
+    ok = __all_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      sh.hollow = hollow;
+      sh.piece[reader.at.slot] = p;
+      mbar_arrive(&sh.piece_full[reader.at.slot]);
     }
+    reader.at.next(kPieceQueue);
+    return more && ok;
   };
   Piece p;
   bool more = take(p);
@@ -1091,21 +1100,6 @@ struct Attend {
     return ((int64_t)p.b * A.P + p.i0) * A.Hq + p.h * A.G;
   }
 
-  // Rows without a visible key, or of a request with bad counts.
-  __device__ __forceinline__ void fill(const Table& T, const Piece& p) const {
-    const int64_t row0 = first_row(p);
-    const bool bad = p.flags & kBad;
-    const float v = bad ? __uint_as_float(0x7fc00000u) : 0.0f;
-    const int rows = p.live * A.G;
-#pragma unroll 1
-    for (int e = me; e < rows * S::D; e += S::TeamThreads)
-      store16<S::Bf16>(A.out, (row0 + T.row[e / S::D]) * S::D + e % S::D, v);
-    if (A.out_lse)
-#pragma unroll 1
-      for (int c = me; c < rows; c += S::TeamThreads)
-        A.out_lse[row0 + T.row[c]] = bad ? v : -INFINITY;
-  }
-
   // The end of a piece (its sums' warp parts are in T.red): O and the sums leave for the output
   // or for the workspace.
   __device__ __forceinline__ void finish(Table& T, const Piece& p) {
@@ -1232,17 +1226,15 @@ struct Attend {
             if (S::Teams == 1) more = !bar_or(kAllBar, S::SoftThreads, !more);
             if (!more) break;
             reader.release(lane == 0);
-            const int tiles = p.mb - p.ma;
-            if (p.turn % S::Teams != team) continue;
-            // (a piece without tiles borrows the table that is not the ended piece's)
-            Table& T = table(tiles > 0 ? p.turn : pending ? ended.turn + 1 : 0);
+            if (p.turn % S::Teams == team) break;
+          }
+          if (more) {
+            Table& T = table(p.turn);
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
             if (me == 0) T.odd_keys = 0;
             team_sync();
             i = 0;
-            if (tiles > 0) break;
-            fill(T, p);
           }
 #pragma unroll
           for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
@@ -1295,22 +1287,19 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
     const int64_t row = ((int64_t)p.b * A.Hkv + p.h) * A.stride;
     float* out = A.weights + row;
     const float* prior = A.prior ? A.prior + row : nullptr;
-    const int pass = p.pass;
+    // the first pass that has tiles here writes every tile of the piece, later ones add to theirs
+    const bool fresh = p.flags & kFresh;
     {
-      if (p.flags & kBad) {
-        if (threadIdx.x == 0) out[0] = nan;
-        continue;
-      }
       set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
       bar_sync(kAllBar, S::SoftThreads);
-      const int ta = pass == 0 ? p.ta : p.ma, tb = pass == 0 ? p.tb : p.mb;
+      const int ta = fresh ? p.ta : p.ma, tb = fresh ? p.tb : p.mb;
       // the columns from here on are of rows that do not count, whose products may be anything
       // (those past the copied block are zero)
       const int dead = p.live < A.pos_block ? p.live * A.G : S::N;
       // what a key's slot holds already and its page, loaded a tile ahead
       auto held = [&](int t) {
         const int j = t * kTileKeys + key;
-        return t < tb && j < p.n ? (pass > 0 ? out[j] : prior ? prior[j] : 0.0f) : 0.0f;
+        return t < tb && j < p.n ? (!fresh ? out[j] : prior ? prior[j] : 0.0f) : 0.0f;
       };
       auto page_of = [&](int t) {
         const int j = t * kTileKeys + key;
@@ -1375,6 +1364,50 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
   }
 }
 
+// ---- pieces without tiles for the tensor cores ---------------------------------------------------
+// Rows that see no key get 0 and a log-sum-exp of -inf, keys that no counted row sees keep what they
+// held, requests with bad counts get NaN. All threads, once the roles are done.
+template <class S>
+__device__ __noinline__ void write_hollow(const TileArgs& A, const TileShared<S>& sh) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float nan = __uint_as_float(0x7fc00000u);
+  Walk<S> walk(A, sh.start);
+  Piece p;
+  int at = 0;
+#pragma unroll 1
+  while (walk.next(p)) {
+    if (!(p.flags & kHollow)) continue;
+    const bool bad = p.flags & kBad;
+    if constexpr (S::Weigh) {
+      const int64_t row = ((int64_t)p.b * A.Hkv + p.h) * A.stride;
+      if (bad) {
+        if (threadIdx.x == 0) A.weights[row] = nan;
+        continue;
+      }
+      const int end = p.tb * kTileKeys < p.n ? p.tb * kTileKeys : p.n;
+#pragma unroll 4
+      for (int j = p.ta * kTileKeys + (int)threadIdx.x; j < end; j += S::Threads)
+        A.weights[row + j] = A.prior ? A.prior[row + j] : 0.0f;
+    } else {
+      if (at++ % (S::Threads / 32) != warp) continue;  // (a warp per piece)
+      const int64_t row0 = ((int64_t)p.b * A.P + p.i0) * A.Hq + p.h * A.G;
+      const uint32_t w = pack16<S::Bf16>(bad ? nan : 0.0f, bad ? nan : 0.0f);
+      constexpr int kVecs = S::D / 8;
+      const int rows = p.live * A.G;
+#pragma unroll 1
+      for (int e = lane; e < rows * kVecs; e += 32) {
+        const int c = e / kVecs;
+        const int64_t r = row0 + c / A.G * A.Hq + c % A.G;
+        reinterpret_cast<uint4*>(A.out)[r * kVecs + e % kVecs] = make_uint4(w, w, w, w);
+      }
+      if (A.out_lse)
+#pragma unroll 1
+        for (int c = lane; c < rows; c += 32)
+          A.out_lse[row0 + c / A.G * A.Hq + c % A.G] = bad ? nan : -INFINITY;
+    }
+  }
+}
+
 // ---- the kernel ---------------------------------------------------------------------------------
 template <class S>
 __global__ void __launch_bounds__(S::Threads, 1)
@@ -1421,7 +1454,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
     }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
-    sh.dead = 0;
+    sh.dead = sh.hollow = 0;
     sh.join.rows = 0;
     for (int i = 0; i < 8; ++i) sh.bad_piece[i] = 0;
     fence_barrier_init();
@@ -1481,6 +1514,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
   tc_fence_after();
   if (!S::Weigh && tid == 0) A.joins[blockIdx.x] = sh.join;
   if (warp == S::ScoreWarp) tmem_free(sh.tmem, S::TmemCols);
+  if (sh.hollow) write_hollow<S>(A, sh);
 }
 
 // ---- joining the pieces of split items --------------------------------------------------------
