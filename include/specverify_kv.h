@@ -104,6 +104,28 @@ sv_status paged_attention(const sv_kv_shape* shape, const sv_score_rule* rule, c
                           sv_stream_t stream);
 
 /* ------------------------------------------------------------------------------------------
+ * Self-tests of the bounded waits inside paged_attention and attention_weight_sum: the same calls
+ * with each wait limited to wait_us microseconds (1 .. 100000) instead of 2 s, so that ordinary
+ * waits run out. No fault and no hang: a CTA whose wait ran out waits for its own copies and
+ * instructions, writes NaN to everything in its share of the work and ends. Every row, and every
+ * key weight, is then either what the call gives or NaN, and the device stays usable.
+ * Returns SV_ERR_INVALID_ARG for wait_us out of range, else what the call returns.
+ * ---------------------------------------------------------------------------------------- */
+sv_status paged_attention_wait_selftest(
+    const sv_kv_shape* shape, const sv_score_rule* rule, const void* q, int64_t q_req,
+    int64_t q_row, int64_t q_head, const sv_kv_pool* k, const sv_kv_pool* v,
+    const int32_t* page_table, const int32_t* seq_len, const int32_t* num_draft, void* out,
+    float* out_lse, void* workspace, size_t workspace_bytes, unsigned int wait_us,
+    sv_stream_t stream);
+
+sv_status attention_weight_sum_wait_selftest(
+    const sv_kv_shape* shape, const sv_score_rule* rule, const void* q, int64_t q_req,
+    int64_t q_row, int64_t q_head, const sv_kv_pool* k, const int32_t* page_table,
+    const int32_t* seq_len, const int32_t* num_draft, const float* lse, int64_t lse_req,
+    int64_t lse_row, int64_t lse_head, const int32_t* accept_len, const float* prior, float* out,
+    int64_t stride, unsigned int wait_us, sv_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
  * The weight each key received. With rows and scores as in paged_attention, for every slot
  * j < seq_len[r] of kv head h:
  *   out[r, h, j] = prior[r, h, j] + sum over rows i <= accept_len[r] and the G query heads of

@@ -228,6 +228,11 @@ def _declare(L):
     L.attention_weight_sum.restype = I
     L.attention_weight_sum.argtypes = [shape, rule, P, q, q, q, pool, P, P, P, P, q, q, q, P, P,
                                        P, q, P]
+    L.paged_attention_wait_selftest.restype = I
+    L.paged_attention_wait_selftest.argtypes = [*L.paged_attention.argtypes[:-1], ctypes.c_uint, P]
+    L.attention_weight_sum_wait_selftest.restype = I
+    L.attention_weight_sum_wait_selftest.argtypes = [*L.attention_weight_sum.argtypes[:-1],
+                                                     ctypes.c_uint, P]
     L.kv_cache_evict.restype = I
     L.kv_cache_evict.argtypes = [shape, pool, pool, P, P, P, q, I, I, pool, pool, I, P, I, P, P,
                                  P, P]

@@ -106,6 +106,7 @@ sv_status fill_tile_args(TileArgs& A, CUtensorMap* mq, CUtensorMap* mk, const sv
   A.box = s->page_size < kTileKeys ? s->page_size : kTileKeys;
   A.bf16 = s->dtype == SV_KV_BF16;
   A.rule = score_rule(rule);
+  A.wait_ns = kTileWaitNs;
   const sv_status ok = encode_map(
       mq, q, A.bf16, {(uint64_t)s->D, (uint64_t)s->Hq, (uint64_t)s->P, (uint64_t)s->B},
       {q_head, q_row, q_req}, {64u, (uint32_t)A.G, (uint32_t)A.pos_block, 1u});
@@ -185,22 +186,11 @@ sv_status launch_width(int D, int columns, const TileArgs& A, const CUtensorMap&
   return launch_columns<256, kBf16>(columns, A, mq, mk, mv, v, st);
 }
 
-}  // namespace
-}  // namespace sv
-
-using namespace sv;
-
-extern "C" size_t paged_attention_workspace(const sv_kv_shape* shape) {
-  return check_kv_shape(shape, true) == SV_OK ? attn_layout(shape).total : 0;
-}
-
-extern "C" sv_status paged_attention(const sv_kv_shape* shape, const sv_score_rule* rule,
-                                     const void* q, int64_t q_req, int64_t q_row,
-                                     int64_t q_head, const sv_kv_pool* k, const sv_kv_pool* v,
-                                     const int32_t* page_table, const int32_t* seq_len,
-                                     const int32_t* num_draft, void* out, float* out_lse,
-                                     void* workspace, size_t workspace_bytes,
-                                     sv_stream_t stream) {
+sv_status attend(const sv_kv_shape* shape, const sv_score_rule* rule, const void* q,
+                 int64_t q_req, int64_t q_row, int64_t q_head, const sv_kv_pool* k,
+                 const sv_kv_pool* v, const int32_t* page_table, const int32_t* seq_len,
+                 const int32_t* num_draft, void* out, float* out_lse, void* workspace,
+                 size_t workspace_bytes, uint64_t wait_ns, sv_stream_t stream) {
   const sv_status ok = check_tile_call(shape, rule, q, q_req, q_row, q_head, k, page_table,
                                        seq_len, num_draft);
   if (ok != SV_OK) return ok;
@@ -217,6 +207,7 @@ extern "C" sv_status paged_attention(const sv_kv_shape* shape, const sv_score_ru
                                seq_len, num_draft, false);
   if (s == SV_OK) s = encode_pool(&mv, shape, v);
   if (s != SV_OK) return s;
+  A.wait_ns = wait_ns;
   char* ws = static_cast<char*>(workspace);
   A.joins = reinterpret_cast<JoinItem*>(ws);
   A.part = reinterpret_cast<float*>(ws + L.part);
@@ -228,4 +219,35 @@ extern "C" sv_status paged_attention(const sv_kv_shape* shape, const sv_score_ru
   row_blocks(shape, false, &pos_block, &blocks, &columns);
   return A.bf16 ? launch_width<true>(shape->D, columns, A, mq, mk, mv, vp, st)
                 : launch_width<false>(shape->D, columns, A, mq, mk, mv, vp, st);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t paged_attention_workspace(const sv_kv_shape* shape) {
+  return check_kv_shape(shape, true) == SV_OK ? attn_layout(shape).total : 0;
+}
+
+extern "C" sv_status paged_attention(const sv_kv_shape* shape, const sv_score_rule* rule,
+                                     const void* q, int64_t q_req, int64_t q_row,
+                                     int64_t q_head, const sv_kv_pool* k, const sv_kv_pool* v,
+                                     const int32_t* page_table, const int32_t* seq_len,
+                                     const int32_t* num_draft, void* out, float* out_lse,
+                                     void* workspace, size_t workspace_bytes,
+                                     sv_stream_t stream) {
+  return attend(shape, rule, q, q_req, q_row, q_head, k, v, page_table, seq_len, num_draft, out,
+                out_lse, workspace, workspace_bytes, kTileWaitNs, stream);
+}
+
+extern "C" sv_status paged_attention_wait_selftest(
+    const sv_kv_shape* shape, const sv_score_rule* rule, const void* q, int64_t q_req,
+    int64_t q_row, int64_t q_head, const sv_kv_pool* k, const sv_kv_pool* v,
+    const int32_t* page_table, const int32_t* seq_len, const int32_t* num_draft, void* out,
+    float* out_lse, void* workspace, size_t workspace_bytes, unsigned int wait_us,
+    sv_stream_t stream) {
+  if (wait_us < 1 || wait_us > 100000) return SV_ERR_INVALID_ARG;
+  return attend(shape, rule, q, q_req, q_row, q_head, k, v, page_table, seq_len, num_draft, out,
+                out_lse, workspace, workspace_bytes, (uint64_t)wait_us * 1000ull, stream);
 }

@@ -40,19 +40,12 @@ sv_status launch_columns(int columns, const TileArgs& A, const CUtensorMap& mq,
   }
 }
 
-}  // namespace
-}  // namespace sv
-
-using namespace sv;
-
-extern "C" sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_score_rule* rule,
-                                          const void* q, int64_t q_req, int64_t q_row,
-                                          int64_t q_head, const sv_kv_pool* k,
-                                          const int32_t* page_table, const int32_t* seq_len,
-                                          const int32_t* num_draft, const float* lse,
-                                          int64_t lse_req, int64_t lse_row, int64_t lse_head,
-                                          const int32_t* accept_len, const float* prior,
-                                          float* out, int64_t stride, sv_stream_t stream) {
+sv_status weigh(const sv_kv_shape* shape, const sv_score_rule* rule, const void* q, int64_t q_req,
+                int64_t q_row, int64_t q_head, const sv_kv_pool* k, const int32_t* page_table,
+                const int32_t* seq_len, const int32_t* num_draft, const float* lse,
+                int64_t lse_req, int64_t lse_row, int64_t lse_head, const int32_t* accept_len,
+                const float* prior, float* out, int64_t stride, uint64_t wait_ns,
+                sv_stream_t stream) {
   const sv_status ok = check_tile_call(shape, rule, q, q_req, q_row, q_head, k, page_table,
                                        seq_len, num_draft);
   if (ok != SV_OK) return ok;
@@ -74,6 +67,7 @@ extern "C" sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_sco
   A.prior = prior;
   A.weights = out;
   A.stride = stride;
+  A.wait_ns = wait_ns;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   int pos_block, blocks, columns;
   row_blocks(shape, true, &pos_block, &blocks, &columns);
@@ -82,4 +76,33 @@ extern "C" sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_sco
     case 128: return launch_columns<128>(columns, A, mq, mk, st);
     default: return launch_columns<256>(columns, A, mq, mk, st);
   }
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_score_rule* rule,
+                                          const void* q, int64_t q_req, int64_t q_row,
+                                          int64_t q_head, const sv_kv_pool* k,
+                                          const int32_t* page_table, const int32_t* seq_len,
+                                          const int32_t* num_draft, const float* lse,
+                                          int64_t lse_req, int64_t lse_row, int64_t lse_head,
+                                          const int32_t* accept_len, const float* prior,
+                                          float* out, int64_t stride, sv_stream_t stream) {
+  return weigh(shape, rule, q, q_req, q_row, q_head, k, page_table, seq_len, num_draft, lse,
+               lse_req, lse_row, lse_head, accept_len, prior, out, stride, kTileWaitNs, stream);
+}
+
+extern "C" sv_status attention_weight_sum_wait_selftest(
+    const sv_kv_shape* shape, const sv_score_rule* rule, const void* q, int64_t q_req,
+    int64_t q_row, int64_t q_head, const sv_kv_pool* k, const int32_t* page_table,
+    const int32_t* seq_len, const int32_t* num_draft, const float* lse, int64_t lse_req,
+    int64_t lse_row, int64_t lse_head, const int32_t* accept_len, const float* prior, float* out,
+    int64_t stride, unsigned int wait_us, sv_stream_t stream) {
+  if (wait_us < 1 || wait_us > 100000) return SV_ERR_INVALID_ARG;
+  return weigh(shape, rule, q, q_req, q_row, q_head, k, page_table, seq_len, num_draft, lse,
+               lse_req, lse_row, lse_head, accept_len, prior, out, stride,
+               (uint64_t)wait_us * 1000ull, stream);
 }

@@ -48,7 +48,9 @@
 // pushed one another out of the instruction cache, which cost 20 to 30 % of every case.
 //
 // Waits. Every wait on a barrier is bounded (sv_tcgen05.cuh): one that runs out marks the CTA
-// dead, after which no wait blocks, the CTA leaves NaN in what it still has to write and ends. A
+// dead, after which no wait blocks, a role whose wait failed starts no copy and no instruction any
+// more, and all leave their loops at the end of the piece at hand. The CTA then waits for its copies and instructions in flight, walks its range
+// once more and writes NaN to everything in it: rows, key weights, its parts of split items. A
 // barrier's phase is one bit, so each ring has a single consumer that takes every phase in order:
 // a reader that skipped phases could take a later one for its own.
 #pragma once
@@ -81,6 +83,7 @@ struct TileArgs {
   int box;                // slots per copy
   int bf16;
   ScoreRule rule;
+  uint64_t wait_ns;  // the limit of a wait
   // attention
   void* out;
   float *out_lse, *part;
@@ -421,7 +424,7 @@ struct TileShared {
   uint64_t v_ready[S::Teams];  // the values of a tile that some rows see in part have landed
   uint64_t o_done[2];  // a piece has its last product, by ordinal % 2
   uint32_t tmem;
-  int dead;
+  Waits waits;
   int hollow;  // the range holds pieces without tiles for the tensor cores
   int bad_piece[8];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 8
   uint64_t drain[2];
@@ -484,7 +487,7 @@ struct Reader {
   RingPos at;
   __device__ __forceinline__ explicit Reader(TileShared<S>& s) : sh(s) {}
   __device__ __forceinline__ const Piece& wait() {
-    wait_phase(&sh.piece_full[at.slot], at.phase, &sh.dead);
+    wait_phase(&sh.piece_full[at.slot], at.phase, &sh.waits);
     return sh.piece[at.slot];
   }
   // One thread of each role (of the softmax, of each warp) gives the place back.
@@ -497,7 +500,7 @@ struct Reader {
   template <bool kWarp>
   __device__ __forceinline__ bool next(Piece& p) {
     p = wait();
-    bool end = *(volatile int*)&sh.dead || (p.flags & kEndOfList);
+    bool end = *(volatile int*)&sh.waits.dead || (p.flags & kEndOfList);
     if (kWarp) end = __any_sync(0xffffffffu, end);  // (and every lane has read the piece)
     if (end) return false;
     release(!kWarp || (threadIdx.x & 31) == 0);
@@ -538,15 +541,16 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll 1
     while ((more = walk.next(p)) && p.mb == p.ma) hollow |= (p.flags & kHollow) != 0;
     if (!more) p.flags = kEndOfList;
-    bool ok = wait_phase(&sh.piece_empty[reader.at.slot], reader.at.phase ^ 1u, &sh.dead);
+    bool ok = wait_phase(&sh.piece_empty[reader.at.slot], reader.at.phase ^ 1u, &sh.waits);
     ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
     if (lane == 0) {
       sh.hollow = hollow;
       sh.piece[reader.at.slot] = p;
       mbar_arrive(&sh.piece_full[reader.at.slot]);
     }
     reader.at.next(kPieceQueue);
-    return more && ok;
+    return more;
   };
   Piece p;
   bool more = take(p);
@@ -557,23 +561,22 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
   int issued = 0, q_issued = 0;
   bool ok = true;
 #pragma unroll 1
-  while (more) {
+  while (more && ok) {
     const int head = p.h, turn = p.turn;
     const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
     if (!kValues && i == 0) {
       const int qs = turn % S::NQ;
-      ok = wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u, &sh.dead);
+      ok = wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u, &sh.waits);
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&sh.q_full[qs], (uint32_t)(A.G * A.pos_block * S::D * 2));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full[qs], (uint32_t)(A.G * A.pos_block * S::D * 2));
 #pragma unroll 1
-          for (int c = 0; c < S::U; ++c)
-            tile_g2s(qbuf + qs * S::QBytes + c * S::N * 128, mq, &sh.q_full[qs], c * 64,
-                     head * A.G, p.i0, p.b);
-        }
-        ++q_issued;
+        for (int c = 0; c < S::U; ++c)
+          tile_g2s(qbuf + qs * S::QBytes + c * S::N * 128, mq, &sh.q_full[qs], c * 64,
+                   head * A.G, p.i0, p.b);
       }
+      ++q_issued;
       __syncwarp();
     }
     if (__builtin_expect(++i == p.mb - p.ma, 0)) {
@@ -590,23 +593,22 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
     const uint32_t bytes =
         (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
 #pragma unroll 1
-    for (int c = 0; c < S::U; ++c) {
+    for (int c = 0; ok && c < S::U; ++c) {
       uint64_t* full = &sh.full[kBase + at.slot];
-      ok = wait_phase(&sh.empty[kBase + at.slot], at.phase ^ 1u, &sh.dead);
+      ok = wait_phase(&sh.empty[kBase + at.slot], at.phase ^ 1u, &sh.waits);
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-        ++issued;
-      }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+      ++issued;
       __syncwarp();
-      if (ok && mine) tile_g2s(dst + at.slot * kUnitBytes, map, full, c * 64, slot, head, page);
+      if (mine) tile_g2s(dst + at.slot * kUnitBytes, map, full, c * 64, slot, head, page);
       at.next(kUnits);
     }
     page = next_page;
     seen = next_seen;
   }
-  if (*(volatile int*)&sh.dead && lane == 0) {
-    // given up: no copy may outlive the CTA
+  if (lane == 0) {
+    // no copy may outlive the CTA, should the others give up before they have seen it land
 #pragma unroll 1
     for (int u = issued > kUnits ? issued - kUnits : 0; u < issued; ++u)
       mbar_wait(&sh.full[kBase + u % kUnits], (uint32_t)(u / kUnits) & 1u, kTileWaitNs);
@@ -619,10 +621,11 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
 
 // ---- the threads that issue the matrix instructions -------------------------------------------
 // One issues the scores, as far ahead as their buffers allow, one the products with the values.
-// Given up: no instruction may outlive the tensor memory.
+// One whose wait failed issues nothing any more (what it then waits for is not what its loop is at).
+// At the end each waits for its own: no instruction may outlive the tensor memory, should the others
+// give up before they have seen it finish.
 template <class S>
 __device__ __forceinline__ void drain(TileShared<S>& sh, int which) {
-  if (!*(volatile int*)&sh.dead) return;
   mma_commit(&sh.drain[which]);
   mbar_wait(&sh.drain[which], 0, kTileWaitNs);
 }
@@ -642,19 +645,19 @@ __device__ __forceinline__ void score_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll 1
   while (reader.template next<false>(p)) {
     const int qs = p.turn % S::NQ, team = p.turn % S::Teams, tiles = p.mb - p.ma;
-    wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.dead);
+    ok &= wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits);
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int of = S::Weigh ? tile_at<S>(p, i) & 1 : team;
       const int y = of ? used[1]++ : used[0]++;
       const int buf = S::Weigh ? of : y & 1, turn = S::Weigh ? y : y >> 1;
-      wait_phase(&sh.s_empty[team][buf], ((uint32_t)turn & 1u) ^ 1u, &sh.dead);
+      ok &= wait_phase(&sh.s_empty[team][buf], ((uint32_t)turn & 1u) ^ 1u, &sh.waits);
       tc_fence_after();
       const uint32_t d = sh.tmem + (2 * team + buf) * S::N;
       uint64_t b = b0 + qs * (S::QBytes >> 4);
 #pragma unroll 1
       for (int c = 0; c < S::U; ++c, b += S::N * 8) {
-        ok = wait_phase(&sh.full[at.slot], at.phase, &sh.dead);
+        ok &= wait_phase(&sh.full[at.slot], at.phase, &sh.waits);
         tc_fence_after();
         const uint64_t a = a0 + at.slot * (kUnitBytes >> 4);
         if (ok) {
@@ -686,6 +689,7 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
   Reader<S> reader(sh);
   RingPos at;
   int used[2] = {0, 0};
+  bool ok = true;
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
@@ -694,17 +698,16 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int y = team ? used[1]++ : used[0]++, pb = y % S::NP;
-      bool ok = true;
       if (__builtin_expect(edge_tile(p, A.rule.window, tile_at<S>(p, i)), 0)) {
         RingPos look = at;
 #pragma unroll 1
         for (int c = 0; c < S::U; ++c) {
-          ok = wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.dead);
+          ok &= wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.waits);
           look.next(S::NV);
         }
         if (ok) mbar_arrive(&sh.v_ready[team]);
       }
-      ok = wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.dead);
+      ok &= wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits);
       const uint64_t b = b0 + (team * S::NP + pb) * (S::PBytes >> 4);
       uint32_t d = o;
 #pragma unroll 1
@@ -713,7 +716,7 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
         uint64_t* empty = &sh.empty[S::NK + at.slot];
 #pragma unroll 1
         for (int c = 0; c < kPer; ++c) {
-          ok = wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.dead);
+          ok &= wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.waits);
           at.next(S::NV);
         }
         tc_fence_after();
@@ -729,7 +732,7 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
       }
       if (ok) mma_commit(&sh.pv_done[team][pb]);
     }
-    if (!*(volatile int*)&sh.dead) mma_commit(&sh.o_done[p.turn & 1]);
+    if (ok) mma_commit(&sh.o_done[p.turn & 1]);
   }
   drain<S>(sh, 1);
 }
@@ -910,7 +913,7 @@ struct Attend {
 
   // Wait until the products of the team's tile y have read P and are in O.
   __device__ __forceinline__ void wait_values(int y) const {
-    wait_phase(&sh.pv_done[team][y % S::NP], (uint32_t)(y / S::NP) & 1u, &sh.dead);
+    wait_phase(&sh.pv_done[team][y % S::NP], (uint32_t)(y / S::NP) & 1u, &sh.waits);
   }
   __device__ __forceinline__ void group_sync() const { bar_sync(1 + group, 128); }
   __device__ __forceinline__ void team_sync() const {
@@ -1008,7 +1011,7 @@ struct Attend {
     const bool edge = edge_tile(p, A.rule.window, t);
     unsigned char* const pb =
         pbuf + (team * S::NP + y % S::NP) * S::PBytes + col0 / 16 * (kTileKeys * 32) + key * 32;
-    wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.dead);
+    wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.waits);
     tc_fence_after();
 #pragma unroll
     for (int k = 0; k < S::NC; k += S::CH) {
@@ -1087,7 +1090,7 @@ struct Attend {
       }
     }
     if (__builtin_expect(edge, 0)) {
-      wait_phase(&sh.v_ready[team], (uint32_t)(edges++) & 1u, &sh.dead);
+      wait_phase(&sh.v_ready[team], (uint32_t)(edges++) & 1u, &sh.waits);
       if (S::Teams == 2 || group == 0) clean_values(T, p, x, j);
     }
     fence_proxy_async();
@@ -1104,8 +1107,7 @@ struct Attend {
   // or for the workspace.
   __device__ __forceinline__ void finish(Table& T, const Piece& p) {
     group_sync();
-    const bool poison = *(volatile int*)&sh.dead ||
-                        *(volatile int*)&sh.bad_piece[p.turn & 7] == p.turn + 1;
+    const bool poison = *(volatile int*)&sh.bad_piece[p.turn & 7] == p.turn + 1;
     const bool starts = p.flags & kStarts, whole = starts && (p.flags & kEnds);
     const int rows = p.live * A.G;
     const int64_t row0 = first_row(p);
@@ -1133,7 +1135,7 @@ struct Attend {
       sh.join.rows = rows;
     }
     group_sync();
-    wait_phase(&sh.o_done[p.turn & 1], (uint32_t)(p.turn >> 1) & 1u, &sh.dead);
+    wait_phase(&sh.o_done[p.turn & 1], (uint32_t)(p.turn >> 1) & 1u, &sh.waits);
     tc_fence_after();
     if (S::D >= 128 || quarter < 2) {
       int d = quarter * 32 + lane;
@@ -1221,7 +1223,7 @@ struct Attend {
 #pragma unroll 1
           for (;;) {
             p = reader.wait();
-            more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.dead;
+            more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.waits.dead;
             more = !bar_or(1 + group, 128, !more);
             if (S::Teams == 1) more = !bar_or(kAllBar, S::SoftThreads, !more);
             if (!more) break;
@@ -1280,7 +1282,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
 #pragma unroll 1
   for (;;) {
     p = reader.wait();
-    bool more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.dead;
+    bool more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.waits.dead;
     more = !bar_or(kAllBar, S::SoftThreads, !more);  // (the last piece's tables have been read)
     if (!more) return;
     reader.release(lane == 0);
@@ -1318,7 +1320,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
         float total = 0.0f;
         if (t >= p.ma && t < p.mb) {
           const bool edge = edge_tile(p, A.rule.window, t);
-          wait_phase(&sh.s_full[0][group], (uint32_t)used & 1u, &sh.dead);
+          wait_phase(&sh.s_full[0][group], (uint32_t)used & 1u, &sh.waits);
           ++used;
           tc_fence_after();
 #pragma unroll 2
@@ -1354,7 +1356,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
           }
           tc_fence_before();
           mbar_arrive(&sh.s_empty[0][group]);
-          if (page < 0 || page >= A.num_pages || *(volatile int*)&sh.dead) total = nan;
+          if (page < 0 || page >= A.num_pages) total = nan;
         }
         if (j < p.n) out[j] = before + total;
         before = next_before;
@@ -1364,36 +1366,49 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
   }
 }
 
-// ---- pieces without tiles for the tensor cores ---------------------------------------------------
-// Rows that see no key get 0 and a log-sum-exp of -inf, keys that no counted row sees keep what they
-// held, requests with bad counts get NaN. All threads, once the roles are done.
+// ---- what the roles leave ------------------------------------------------------------------------
+// Pieces without tiles for the tensor cores: rows that see no key get 0 and a log-sum-exp of -inf,
+// keys that no counted row sees keep what they held, requests with bad counts get NaN. Of a CTA that
+// gave up, all pieces: NaN in rows, key weights and the parts of split items, whose join then gives
+// NaN as well. All threads, once the roles are done.
 template <class S>
-__device__ __noinline__ void write_hollow(const TileArgs& A, const TileShared<S>& sh) {
+__device__ __noinline__ void write_rest(const TileArgs& A, const TileShared<S>& sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float nan = __uint_as_float(0x7fc00000u);
+  const bool dead = sh.waits.dead;
   Walk<S> walk(A, sh.start);
   Piece p;
+  JoinItem join{};
   int at = 0;
 #pragma unroll 1
   while (walk.next(p)) {
-    if (!(p.flags & kHollow)) continue;
-    const bool bad = p.flags & kBad;
+    if (!dead && !(p.flags & kHollow)) continue;
+    const bool bad = dead || (p.flags & kBad);
     if constexpr (S::Weigh) {
       const int64_t row = ((int64_t)p.b * A.Hkv + p.h) * A.stride;
-      if (bad) {
+      if (p.flags & kBad) {
         if (threadIdx.x == 0) A.weights[row] = nan;
         continue;
       }
       const int end = p.tb * kTileKeys < p.n ? p.tb * kTileKeys : p.n;
 #pragma unroll 4
       for (int j = p.ta * kTileKeys + (int)threadIdx.x; j < end; j += S::Threads)
-        A.weights[row + j] = A.prior ? A.prior[row + j] : 0.0f;
+        A.weights[row + j] = dead ? nan : A.prior ? A.prior[row + j] : 0.0f;
     } else {
-      if (at++ % (S::Threads / 32) != warp) continue;  // (a warp per piece)
       const int64_t row0 = ((int64_t)p.b * A.P + p.i0) * A.Hq + p.h * A.G;
+      const int rows = p.live * A.G;
+      const bool starts = p.flags & kStarts, whole = starts && (p.flags & kEnds);
+      if (starts && !whole) join = JoinItem{rows, p.pieces, row0};
+      if (at++ % (S::Threads / 32) != warp) continue;  // (a warp per piece)
+      if (!whole) {
+        float* part = A.part + (2 * (int64_t)blockIdx.x + (starts ? 1 : 0)) * (S::N * (S::D + 2));
+#pragma unroll 1
+        for (int c = lane; c < rows; c += 32)
+          *reinterpret_cast<float2*>(part + S::N * S::D + 2 * c) = make_float2(0.0f, nan);
+        continue;
+      }
       const uint32_t w = pack16<S::Bf16>(bad ? nan : 0.0f, bad ? nan : 0.0f);
       constexpr int kVecs = S::D / 8;
-      const int rows = p.live * A.G;
 #pragma unroll 1
       for (int e = lane; e < rows * kVecs; e += 32) {
         const int c = e / kVecs;
@@ -1406,6 +1421,7 @@ __device__ __noinline__ void write_hollow(const TileArgs& A, const TileShared<S>
           A.out_lse[row0 + c / A.G * A.Hq + c % A.G] = bad ? nan : -INFINITY;
     }
   }
+  if (!S::Weigh && dead && threadIdx.x == 0) A.joins[blockIdx.x] = join;
 }
 
 // ---- the kernel ---------------------------------------------------------------------------------
@@ -1454,7 +1470,8 @@ __global__ void __launch_bounds__(S::Threads, 1)
     }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
-    sh.dead = sh.hollow = 0;
+    sh.waits.dead = sh.hollow = 0;
+    sh.waits.limit_ns = A.wait_ns;
     sh.join.rows = 0;
     for (int i = 0; i < 8; ++i) sh.bad_piece[i] = 0;
     fence_barrier_init();
@@ -1514,7 +1531,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
   tc_fence_after();
   if (!S::Weigh && tid == 0) A.joins[blockIdx.x] = sh.join;
   if (warp == S::ScoreWarp) tmem_free(sh.tmem, S::TmemCols);
-  if (sh.hollow) write_hollow<S>(A, sh);
+  if (sh.hollow || sh.waits.dead) write_rest<S>(A, sh);
 }
 
 // ---- joining the pieces of split items --------------------------------------------------------

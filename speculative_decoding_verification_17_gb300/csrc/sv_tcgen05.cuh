@@ -108,23 +108,29 @@ __device__ __forceinline__ void fence_proxy_async() {
 // ---- waits ------------------------------------------------------------------------------------
 constexpr uint64_t kTileWaitNs = 2000000000ull;  // 2 s: far past any legitimate wait
 
-// Wait for a phase of an mbarrier unless the CTA has given up (*dead); a wait that runs out
-// makes the CTA give up. After that every wait returns at once, so each role still walks its
-// whole loop and every CTA barrier is met; the results are then replaced by NaN.
+// What the waits of a CTA share (in shared memory): whether it has given up, and a wait's limit.
+struct Waits {
+  int dead;
+  uint64_t limit_ns;
+};
+
+// Wait for a phase of an mbarrier unless the CTA has given up; a wait that runs out makes the CTA
+// give up. After that no wait blocks, every role leaves its loop and every CTA barrier is met; what
+// the CTA owes is then written as NaN. (A wait that fails has seen or set `dead`.)
 static __device__ __noinline__ bool wait_longer(uint64_t* bar, uint32_t parity,
-                                                volatile int* dead) {
-  const uint64_t t0 = globaltimer_ns();
+                                                volatile Waits* w) {
+  const uint64_t t0 = globaltimer_ns(), limit = w->limit_ns;
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*dead) return false;
-    if (globaltimer_ns() - t0 > kTileWaitNs) {
-      *dead = 1;
+    if (w->dead) return false;
+    if (globaltimer_ns() - t0 > limit) {
+      w->dead = 1;
       return false;
     }
   }
 }
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, dead);
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile Waits* w) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, w);
 }
 
 }  // namespace sv
