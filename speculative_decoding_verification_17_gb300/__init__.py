@@ -579,6 +579,15 @@ def ngram_propose(history, hist_len, n_max: int, n_min: int, k: int, *, out_draf
     return out_draft, out_num_draft
 
 
+def _made(make, shape, dtype, device, stream):
+    """A new tensor (torch.empty or torch.zeros) of the stream the call runs on: what fills it runs
+    there, and the allocator hands out no block that another stream still uses."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
+
+
 # ------------------------------------------------------------------------------ logits
 def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_tokens=None,
                  num_draft=None, repetition=None, presence=None, frequency=None,
@@ -588,7 +597,7 @@ def logit_adjust(logits, history=None, hist_len=None, *, prompt_len=None, draft_
     Returns the adjusted logits [B, P, V] (``out``, which may be ``logits`` itself; rows past a
     request's num_draft are left as they are in it)."""
     if out is None and isinstance(logits, torch.Tensor):
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        out = _made(torch.empty, logits.shape, logits.dtype, logits.device, stream)
     status = (_native._calls or _native.calls()).adjust(
         logits, history, hist_len, prompt_len, draft_tokens, num_draft, repetition, presence,
         frequency, bias_tokens, bias_values, allowed, out, _raw_stream(stream, logits))
@@ -711,9 +720,9 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None,
     seq_len [B] int32 (the new positions included). ``scale`` defaults to D ** -0.5. Returns
     (out [B, P, Hq, D], lse [B, P, Hq] fp32 or None)."""
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _made(torch.empty, q.shape, q.dtype, q.device, stream)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+        out_lse = _made(torch.empty, q.shape[:3], torch.float32, q.device, stream)
     h = _raw_stream(stream, q)
     ws = workspace
     if ws is None:
@@ -758,7 +767,7 @@ def attention_weight_sum(q, k_cache, page_table, seq_len, lse, *, num_draft=None
     Returns the sums [B, Hkv, N] (``out``, which may be ``prior``)."""
     if out is None:
         N = page_table.shape[-1] * k_cache.shape[1] if prior is None else prior.shape[-1]
-        out = torch.zeros((q.shape[0], k_cache.shape[2], N), dtype=torch.float32, device=q.device)
+        out = _made(torch.zeros, (q.shape[0], k_cache.shape[2], N), torch.float32, q.device, stream)
     h = _raw_stream(stream, q)
     status = (_native._calls or _native.calls()).weights(
         q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window, lse,
@@ -789,6 +798,11 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
     heaviest others by ``weights`` [B, Hkv, N] fp32, and copies them in order to the pages of
     new_page_table in new_k and new_v (which may be the same pools). Returns (out_len [B],
     out_index [B, Hkv, budget] int32, out_weights [B, Hkv, budget] fp32)."""
+    if stream is not None and (out_len is None or out_index is None or out_weights is None):
+        with torch.cuda.stream(stream):  # (what is made here belongs to the call's stream)
+            return kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget, recent,
+                                  new_k, new_v, new_page_table, out_len=out_len,
+                                  out_index=out_index, out_weights=out_weights)
     h = _raw_stream(stream, k_cache)
     made = (_native._calls or _native.calls()).evict(
         k_cache, v_cache, page_table, seq_len, weights, budget, recent, new_k, new_v,
