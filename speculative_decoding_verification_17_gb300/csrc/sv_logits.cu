@@ -539,7 +539,7 @@ sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
   // 405 us in chunks of 4096, 478 us of 2048, 472 us of 8192, whose tables leave room for fewer
   // CTAs.)
   const int64_t wanted = 2 * (int64_t)device_sm_count();
-  const int least = sizeof(T) == 4 ? 10 : 11;
+  constexpr int least = sizeof(T) == 4 ? 10 : 11;
   A.log_chunk = least + 1;
   while (A.log_chunk > least && (((int64_t)A.V - 1) / (1 << A.log_chunk) + 1) * A.B < wanted)
     --A.log_chunk;
@@ -548,10 +548,14 @@ sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
   if (grid >= (1ll << 31)) return SV_ERR_UNSUPPORTED;
   const size_t tables = ((size_t)4 << A.log_chunk) + 4 * (((size_t)1 << A.log_chunk) / 8);
   const size_t smem = tables + (aligned ? kAdjStages * (sizeof(T) << A.log_chunk) : 0);
+  // The largest chunk's tables and ring and the static shared memory stay within what every launch
+  // may have: no limit is raised (one raised per call could be lowered under another thread's launch).
+  constexpr int kMost = least + 1;
+  constexpr size_t kStatic = sizeof(DraftShared) + 8 * kAdjStages + 2 * kListed + kAdjThreads / 8;
+  static_assert((4u << kMost) + (1u << kMost) / 2 + kAdjStages * (sizeof(T) << kMost) + kStatic + 64 <=
+                    48 * 1024,
+                "shared memory");
   auto kernel = aligned ? adjust_kernel<T> : adjust_any_kernel<T>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return cuda_fail(e);
   kernel<<<(unsigned)grid, kAdjThreads, smem, st>>>(A);
   return launch_status();
 }
