@@ -267,39 +267,47 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !len.fits(at::kInt, dev, {B}) || !index.fits(at::kInt, dev, {B, Hkv, budget}) ||
       !kept.fits(at::kFloat, dev, {B, Hkv, budget}))
     return none();
+  const auto made = [&](const Arg& given, at::IntArrayRef sizes, at::ScalarType type) {
+    return given ? *given.t : at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
+  };
+  const at::Tensor o_len = made(len, {B}, at::kInt);
+  const at::Tensor o_index = made(index, {B, Hkv, budget}, at::kInt);
+  const at::Tensor o_kept = made(kept, {B, Hkv, budget}, at::kFloat);
+  shape.B = (int)B;
+  shape.P = 1;
+  shape.Hq = shape.Hkv = (int)Hkv;
+  shape.D = (int)k.t->size(3);
+  shape.page_size = (int)k.t->size(1);
+  shape.num_pages = (int)k.t->size(0);
+  shape.max_pages = (int)cols;
+  const sv_status s = p_evict(
+      &shape, &pools[0], &pools[1], table.ptr<int32_t>(), lens.ptr<int32_t>(), w.ptr<float>(), N,
+      budget, recent, &pools[2], &pools[3], (int)nk.t->size(0), ntable.ptr<int32_t>(),
+      (int)ncols, static_cast<int32_t*>(o_len.data_ptr()),
+      static_cast<int32_t*>(o_index.data_ptr()), static_cast<float*>(o_kept.data_ptr()),
+      reinterpret_cast<sv_stream_t>(stream));
+  return Py_BuildValue("(iNNN)", (int)s, THPVariable_Wrap(o_len), THPVariable_Wrap(o_index),
+                       THPVariable_Wrap(o_kept));
+}
+
+// No exception may pass into the interpreter: a tensor without storage (of a transform, a sparse one)
+// throws where its address or strides are read, an allocation where memory is short. The Python side
+// then meets the same and raises it.
+template <PyObject* (*kCall)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   try {
-    const auto made = [&](const Arg& given, at::IntArrayRef sizes, at::ScalarType type) {
-      return given ? *given.t : at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
-    };
-    const at::Tensor o_len = made(len, {B}, at::kInt);
-    const at::Tensor o_index = made(index, {B, Hkv, budget}, at::kInt);
-    const at::Tensor o_kept = made(kept, {B, Hkv, budget}, at::kFloat);
-    shape.B = (int)B;
-    shape.P = 1;
-    shape.Hq = shape.Hkv = (int)Hkv;
-    shape.D = (int)k.t->size(3);
-    shape.page_size = (int)k.t->size(1);
-    shape.num_pages = (int)k.t->size(0);
-    shape.max_pages = (int)cols;
-    const sv_status s = p_evict(
-        &shape, &pools[0], &pools[1], table.ptr<int32_t>(), lens.ptr<int32_t>(), w.ptr<float>(), N,
-        budget, recent, &pools[2], &pools[3], (int)nk.t->size(0), ntable.ptr<int32_t>(),
-        (int)ncols, static_cast<int32_t*>(o_len.data_ptr()),
-        static_cast<int32_t*>(o_index.data_ptr()), static_cast<float*>(o_kept.data_ptr()),
-        reinterpret_cast<sv_stream_t>(stream));
-    return Py_BuildValue("(iNNN)", (int)s, THPVariable_Wrap(o_len), THPVariable_Wrap(o_index),
-                         THPVariable_Wrap(o_kept));
-  } catch (const std::exception& e) {  // (an allocation that failed)
-    return PyErr_Format(PyExc_RuntimeError, "%s", e.what());
+    return kCall(self, a, n);
+  } catch (...) {
+    return none();
   }
 }
 
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
-    {"adjust", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adjust)), METH_FASTCALL, nullptr},
-    {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)), METH_FASTCALL, nullptr},
-    {"weights", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(weights)), METH_FASTCALL, nullptr},
-    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict)), METH_FASTCALL, nullptr},
+    {"adjust", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<adjust>)), METH_FASTCALL, nullptr},
+    {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<attention>)), METH_FASTCALL, nullptr},
+    {"weights", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<weights>)), METH_FASTCALL, nullptr},
+    {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<evict>)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
