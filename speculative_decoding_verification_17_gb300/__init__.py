@@ -748,14 +748,15 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None,
         raise ValueError("v_cache must have k_cache's shape")
     _check_cuda("out", out, q.dtype, (B, P, Hq, D), dev)
     _check_cuda("out_lse", out_lse, torch.float32, (B, P, Hq), dev)
+    _check_cuda("workspace", ws, None, None, dev)
     L = library()
     if ws is None:
         ws = _workspace("attention", L.paged_attention_workspace(head[0]), dev,
                         stream or torch.cuda.current_stream(dev))
     _ok(L.paged_attention(
         *head, _kv_pool("v_cache", v_cache, k_cache), page_table.data_ptr(), seq_len.data_ptr(),
-        _ptr(num_draft), out.data_ptr(), _ptr(out_lse), ws.data_ptr(), ws.numel(), h),
-        "paged_attention")
+        _ptr(num_draft), out.data_ptr(), _ptr(out_lse), ws.data_ptr(),
+        ws.numel() * ws.element_size(), h), "paged_attention")
     return out, out_lse
 
 

@@ -204,12 +204,13 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t B = Q.shape.B, P = Q.shape.P, Hq = Q.shape.Hq, D = Q.shape.D;
   if (!out.fits(Q.q.t->scalar_type(), dev, {B, P, Hq, D}) || !lse.fits(at::kFloat, dev, {B, P, Hq}))
     return none();
+  if (ws && (ws.t->device() != dev || !ws.t->is_contiguous())) return none();
   const size_t need = p_workspace(&Q.shape);
-  if (!ws || (size_t)ws.t->numel() < need) return PyLong_FromLongLong(-(long long)need - 1);
+  if (!ws || ws.t->nbytes() < need) return PyLong_FromLongLong(-(long long)need - 1);
   const sv_status s = p_attention(
       &Q.shape, &Q.rule, Q.q.ptr<void>(), Q.q.t->stride(0), Q.q.t->stride(1), Q.q.t->stride(2),
       &Q.pool, &vp, Q.table.ptr<int32_t>(), Q.lens.ptr<int32_t>(), Q.nd.ptr<int32_t>(),
-      out.ptr<void>(), lse.ptr<float>(), ws.ptr<void>(), (size_t)ws.t->numel(),
+      out.ptr<void>(), lse.ptr<float>(), ws.ptr<void>(), ws.t->nbytes(),
       reinterpret_cast<sv_stream_t>(stream));
   return PyLong_FromLong(s);
 }

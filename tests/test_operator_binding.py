@@ -46,3 +46,18 @@ def test_a_transformed_tensor_is_refused(fake, name):
     fn, sizes = calls(fake)[name]
     with pytest.raises((RuntimeError, TypeError, ValueError)):
         torch.func.vmap(fn)(fake(2, *sizes))
+
+
+@pytest.mark.parametrize("workspace", [dict(device="cpu", dtype=torch.uint8), "strided", "text"])
+def test_a_workspace_off_the_device_is_refused(fake, workspace):
+    """Its address would be written by the kernel."""
+    k, table, n = fake(4, 16, 1, 64), fake(1, 4, dtype=torch.int32), fake(1, dtype=torch.int32)
+    if workspace == "strided":
+        ws = fake(1 << 21, 8, dtype=torch.uint8)[:, 0]
+    elif workspace == "text":
+        ws = "workspace"
+    else:
+        ws = fake(1 << 24, **workspace)
+    with pytest.raises((TypeError, ValueError)):
+        sv.paged_attention(fake(1, 1, 2, 64), k, k, table, n, out=fake(1, 1, 2, 64),
+                           out_lse=fake(1, 1, 2, dtype=torch.float32), workspace=ws, stream=STREAM)
