@@ -45,7 +45,9 @@ The paged key-value cache around a verify (C ABI in ``include/specverify_kv.h``)
 Workspaces: pass ``workspace=`` (a uint8 CUDA tensor of at least the size the matching
 ``*_workspace`` query returns, 256-byte aligned, not shared by calls in flight at the same
 time; it needs no initialisation), or let the binding keep one cached per (device, stream,
-call) that it grows as needed: calls in flight on different streams never share one.
+call) that it grows as needed: calls in flight on different streams never share one. A call that
+is captured into a CUDA graph gets one of the graph's own memory instead, so replays of different
+graphs never share one either, and none is freed under a graph.
 """
 from __future__ import annotations
 
@@ -151,10 +153,23 @@ _ws_lock = threading.Lock()
 _ws_cache: dict = {}
 
 
+def _capturing(handle: int, stream) -> bool:
+    """Whether a stream (None: the current one), whose handle is given, is being captured."""
+    if stream is None or handle == torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()):
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with torch.cuda.stream(stream):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def _workspace(kind: str, nbytes: int, device, stream):
     """Cached zero-filled workspace for (device, stream, kind) of at least ``nbytes`` bytes.
     Calls on one stream run in order, so they may share it; calls on two streams may overlap,
     so each stream has its own."""
+    if _capturing(stream.cuda_stream, stream):
+        # the graph's memory pool keeps it (one kept here would be shared with whatever else runs on
+        # this stream, and freed under the graph once a larger call replaces it)
+        with torch.cuda.stream(stream):
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     key = (kind, device, stream.cuda_stream)
     with _ws_lock:
         ws = _ws_cache.get(key)
@@ -727,14 +742,17 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None,
     ws = workspace
     if ws is None:
         ws = _ws_cache.get(("attention", q.get_device(), h))
+        if ws is not None and _capturing(h, stream):
+            ws = None
     fast = (_native._calls or _native.calls()).attention
     status = fast(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window,
                   v_cache, out, out_lse, ws, h)
     if status is not None and status < 0 and workspace is None:
-        # a first call on this stream, or one that needs more than the earlier ones did
+        # a first call on this stream, one that needs more than the earlier ones did, or a captured one
         ws = _workspace("attention", -status - 1, q.device,
                         stream or torch.cuda.current_stream(q.device))
-        _ws_cache["attention", q.get_device(), h] = ws
+        if _ws_cache.get(("attention", q.device, h)) is ws:
+            _ws_cache["attention", q.get_device(), h] = ws
         status = fast(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window,
                       v_cache, out, out_lse, ws, h)
     if status is not None:
@@ -748,9 +766,9 @@ def paged_attention(q, k_cache, v_cache, page_table, seq_len, *, num_draft=None,
         raise ValueError("v_cache must have k_cache's shape")
     _check_cuda("out", out, q.dtype, (B, P, Hq, D), dev)
     _check_cuda("out_lse", out_lse, torch.float32, (B, P, Hq), dev)
-    _check_cuda("workspace", ws, None, None, dev)
+    _check_cuda("workspace", workspace, None, None, dev)
     L = library()
-    if ws is None:
+    if workspace is None:
         ws = _workspace("attention", L.paged_attention_workspace(head[0]), dev,
                         stream or torch.cuda.current_stream(dev))
     _ok(L.paged_attention(
