@@ -1295,9 +1295,9 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
       set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
       bar_sync(kAllBar, S::SoftThreads);
       const int ta = fresh ? p.ta : p.ma, tb = fresh ? p.tb : p.mb;
-      // the columns from here on are of rows that do not count, whose products may be anything
-      // (those past the copied block are zero)
-      const int dead = p.live < A.pos_block ? p.live * A.G : S::N;
+      // the columns from here on are of rows that do not count, or of none: their products may be
+      // anything (a zero query times an infinite key is NaN)
+      const int dead = p.live * A.G;
       // what a key's slot holds already and its page, loaded a tile ahead
       auto held = [&](int t) {
         const int j = t * kTileKeys + key;
