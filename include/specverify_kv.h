@@ -86,7 +86,8 @@ typedef struct {
  *   out_lse      [B, P, Hq] fp32, or NULL.
  *   workspace    >= paged_attention_workspace(shape) bytes; needs no initialisation.
  * What slots past n hold never reaches an output (NaN included), nor does a drafted token's
- * value reach the rows ahead of it.
+ * value reach the rows ahead of it. A value that is infinite or NaN makes what it enters infinite or
+ * NaN: the sum, over the keys a row sees, of that component's values that are not finite.
  * A request with seq_len or num_draft out of range gets NaN in out and out_lse in all its P
  * rows; one whose page table names a page outside [0, num_pages) for a key that is seen, NaN
  * at least in the rows that see such a key.

@@ -441,7 +441,7 @@ struct TileShared {
     alignas(16) float red[4][S::N];  // per-warp maxima or sums
     int hi[S::N], lo[S::N];          // the column sees keys j with lo < j <= hi
     int row[S::N];                   // output row of the column, from the item's first
-    unsigned int odd_keys;           // partly visible keys whose values are not finite
+    int odd;                         // a partly visible key has values that are not finite
   } table[2];                        // by ordinal % 2 (with two teams: one each)
   JoinItem join;
 };
@@ -896,6 +896,53 @@ struct ValuePool {
   int64_t page, token, head;
 };
 
+// The outputs of a piece that values make infinite or NaN. In the tensor cores such a value meets
+// weights of 0: the low half of an exact weight, or a weight that is too small for its type. So the
+// values of the piece's keys that are not finite are summed here, for one thread's share of D: those
+// of the keys that all rows see, and for each row of its columns those of the others it sees. What
+// comes out not finite is the row's output (times a positive weight, and plus finite numbers, it is
+// the same); a row whose values are finite keeps what it has.
+template <class S>
+__device__ __noinline__ void special_values(const TileArgs& A, const ValuePool& vpool,
+                                            const typename TileShared<S>::Table& T, int b, int h,
+                                            int pos0, int first, int last, int ma, int mb, int col0,
+                                            int rows, int d0, float* part, int64_t row0) {
+  const int j0 = first > ma * kTileKeys ? first : ma * kTileKeys;
+  const int j1 = last < mb * kTileKeys - 1 ? last : mb * kTileKeys - 1;
+  // keys [f0, f1] are seen by all rows; where there are none, [j0, j1] are all looked at row by row
+  int f0 = last - A.rule.window + 1 > j0 ? last - A.rule.window + 1 : j0, f1 = pos0 < j1 ? pos0 : j1;
+  if (f0 > f1) f0 = j1 + 1, f1 = j1;
+#pragma unroll 1
+  for (int d = d0; d < S::D; d += 128) {
+    auto odd_part = [&](int j) {  // the value if it is not finite, else 0
+      const int page = __ldg(A.table + (int64_t)b * A.max_pages + (j >> A.log_page));
+      if (page < 0 || page >= A.num_pages) return 0.0f;
+      const int64_t at = page * vpool.page + (j & ((1 << A.log_page) - 1)) * vpool.token +
+                         h * vpool.head + d;
+      const float v = unpack16<S::Bf16>(__ldg(static_cast<const unsigned short*>(vpool.data) + at)).x;
+      return isfinite(v) ? 0.0f : v;
+    };
+    float all = 0.0f;
+#pragma unroll 8
+    for (int j = f0; j <= f1; ++j) all += odd_part(j);
+#pragma unroll 1
+    for (int n = col0; n < col0 + S::NC && n < rows; ++n) {
+      if (T.red[0][n] == 0.0f) continue;
+      float sum = all;
+#pragma unroll 1
+      for (int j = j0; j <= j1; ++j) {
+        if (j == f0) j = f1 + 1;
+        if (j <= j1 && j <= T.hi[n] && j > T.lo[n]) sum += odd_part(j);
+      }
+      if (isfinite(sum)) continue;
+      if (part)
+        part[n * S::D + d] = sum;
+      else
+        store16<S::Bf16>(A.out, (row0 + T.row[n]) * S::D + d, sum);
+    }
+  }
+}
+
 // ---- attention --------------------------------------------------------------------------------
 // What one softmax thread does for the attention: its key of every tile, its share of O.
 template <class S>
@@ -963,8 +1010,8 @@ struct Attend {
   }
 
   // Values of keys that some row of a tile does not see: what no row sees becomes 0; of a key
-  // that only some rows see, the values that are not finite become 0 and are added to the rows
-  // that see it at the end (0 times infinity would reach the others).
+  // that only some rows see, the values that are not finite become 0 (times a weight of 0 they would
+  // reach the others) and special_values adds them at the end to the rows that see it.
   __device__ __forceinline__ void clean_values(Table& T, const Piece& p, int x, int j) {
     const bool none = j > p.last || j < p.first;
     const bool some = !none && (j > p.pos0 || j < first_full(p, A.rule.window));
@@ -987,8 +1034,7 @@ struct Attend {
       }
     }
     if (odd) {
-      atomicOr(&T.odd_keys,
-               1u << (j > p.pos0 ? j - p.pos0 - 1 : 16 + j - p.first));
+      *(volatile int*)&T.odd = 1;
 #pragma unroll 1
       for (int c = 0; c < S::U; ++c) {
         uint32_t* w = reinterpret_cast<uint32_t*>(ring + value_slot<S>(x, c) * kUnitBytes +
@@ -1127,6 +1173,7 @@ struct Attend {
                 sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
         }
         T.alpha[c] = !whole ? 1.0f : sum == 0.0f ? 0.0f : rcp_fast(sum);
+        T.red[0][c] = c < rows && sum == sum ? 1.0f : 0.0f;  // its output is a number unless a value is not
       }
     }
     if (me == 0 && starts && !whole) {
@@ -1139,6 +1186,7 @@ struct Attend {
     tc_fence_after();
     if (S::D >= 128 || quarter < 2) {
       int d = quarter * 32 + lane;
+      float odd = *(volatile int*)&T.odd ? __uint_as_float(0x7fc00000u) : 0.0f;
 #pragma unroll 1
       for (int m = 0; m < S::MBlocks; ++m, d += 128)
 #pragma unroll 1
@@ -1155,6 +1203,9 @@ struct Attend {
             tmem_wait_ld();
           }
           const int n0 = col0 + q;
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            if (T.red[0][n0 + c] != 0.0f) odd = fmaf(o[c], 0.0f, odd);
           if (whole) {
             uint16_t* out = static_cast<uint16_t*>(A.out) + row0 * S::D + d;
 #pragma unroll
@@ -1170,38 +1221,11 @@ struct Attend {
               if (n0 + c < rows) part[(n0 + c) * S::D + d] = o[c];
           }
         }
-      const unsigned int odd = *(volatile unsigned int*)&T.odd_keys;
-      if (odd && !poison) add_odd(T, p, odd, whole ? nullptr : part, row0, rows);
+      if (__builtin_expect(odd != odd && !poison, 0))
+        special_values<S>(A, vpool, T, p.b, p.h, p.pos0, p.first, p.last, p.ma, p.mb, col0, rows,
+                          quarter * 32 + lane, whole ? nullptr : part, row0);
     }
     tc_fence_before();
-  }
-
-  // The values that are not finite of keys only some rows see: what such a row's sum is then.
-  __device__ __forceinline__ void add_odd(const Table& T, const Piece& p, unsigned int odd,
-                                          float* part, int64_t row0, int rows) const {
-#pragma unroll 1
-    for (int d = quarter * 32 + lane; d < S::D; d += 128)
-#pragma unroll 1
-      for (int n = col0; n < col0 + S::NC && n < rows; ++n) {
-        float sum = 0.0f;
-#pragma unroll 1
-        for (unsigned int left = odd; left; left &= left - 1) {
-          const int bit = __ffs(left) - 1;
-          const int j = bit < 16 ? p.pos0 + 1 + bit : p.first + bit - 16;
-          if (j > T.hi[n] || j <= T.lo[n]) continue;
-          const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
-          if (page < 0 || page >= A.num_pages) continue;
-          const int64_t at = page * vpool.page + (j & ((1 << A.log_page) - 1)) * vpool.token +
-                             p.h * vpool.head + d;
-          const float v = unpack16<S::Bf16>(static_cast<const uint16_t*>(vpool.data)[at]).x;
-          if (!isfinite(v)) sum += v;
-        }
-        if (isfinite(sum)) continue;
-        if (part)
-          part[n * S::D + d] = sum;
-        else
-          store16<S::Bf16>(A.out, (row0 + T.row[n]) * S::D + d, sum);
-      }
   }
 
   // The pieces in turn. With one team the end of a piece waits until the first tile of the next
@@ -1234,7 +1258,7 @@ struct Attend {
             Table& T = table(p.turn);
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
-            if (me == 0) T.odd_keys = 0;
+            if (me == 0) T.odd = 0;
             team_sync();
             i = 0;
           }
@@ -1582,7 +1606,8 @@ __global__ void __launch_bounds__(kJoinThreads)
     acc.w *= a;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const float w = ex2(ml[i].x - m);
+      // (never 0: a part that an infinite value made infinite stays so)
+      const float w = fmaxf(ex2(ml[i].x - m), 1.17549435e-38f);
       sum += w * ml[i].y;
       acc.x = fmaf(w, v[i].x, acc.x);
       acc.y = fmaf(w, v[i].y, acc.y);
