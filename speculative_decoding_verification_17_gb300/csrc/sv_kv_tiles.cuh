@@ -24,13 +24,15 @@
 // the join (4 us). Pages of 16 slots, copied in eight pieces per unit, reach 82 % where pages of
 // 64 reach 88 %, pages of 8 reach 69 %.
 //
-// Running maximum. m[c] only moves when a score passes it by 2^8: the products of a tile are
-// at most 2^8, far inside fp32 and the 16-bit types, and the accumulators are rescaled only in
-// the first tiles of a row instead of in every tile.
+// Running maximum. m[c] only moves when a score passes it by 2^8: the accumulators are rescaled only
+// in the first tiles of a row instead of in every tile. The weights are 2^(s - m + lift), with a lift
+// of 7 for fp16, whose numbers end at 2^-24: a weight is at most 2^15, and 2^-32 of the largest score's
+// still counts (without the lift 2^-25: 131072 keys of that weight, 0.4 % of a row, came to 0).
 //
 // Rounding. The weights P are given to the tensor core as two 16-bit numbers, p = hi + lo, and
-// V^T is multiplied by both: 16 bits of the weight instead of 8 (bf16), so the output carries
-// no error but its own rounding. The second product costs tensor time that the memory hides.
+// V^T is multiplied by both. Each rounding leaves at most half a step of what it rounds: a weight is
+// off by 2^-16 of it (bf16) or 2^-22 (fp16, or by 2^-32 of the largest), where the output's own rounding
+// is 2^-8 or 2^-11 of it. The second product costs tensor time that the memory hides.
 //
 // Work. All tiles of all (request, kv head, row block) items are one flat range, cut into equal
 // costs over one CTA per SM: ragged lengths balance by construction. A CTA walks its range piece
@@ -105,6 +107,7 @@ struct TileShape {
   static constexpr int D = kD, N = kN;
   static constexpr bool Bf16 = kBf16;  // (attention) the type is bf16, else fp16
   static constexpr bool Weigh = kWeigh;
+  static constexpr float Lift = kBf16 ? 0.0f : 7.0f;  // (attention) of the weights' exponents
   static constexpr int U = D / 64;  // units of a key or value tile
   // Softmax warps: two groups of four (one warp per quarter of the tile's keys). In the
   // attention of 16 columns the groups are two teams that take the pieces in turn, each
@@ -434,7 +437,7 @@ struct TileShared {
   int64_t scratch[16];
   Start start;
   struct Table {
-    alignas(16) float m[S::N];       // minus the running maximum, or the row's lse (log2)
+    alignas(16) float m[S::N];       // lift - the running maximum, or minus the row's lse (log2)
     alignas(16) float slope[S::N];   // log2(e) * slope
     alignas(16) float ahead[S::N];   // the column's position less the block's first
     alignas(16) float alpha[S::N];
@@ -891,6 +894,14 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
 // Named barriers: 1 and 2 for the two groups of softmax warps, 3 for all of them.
 constexpr int kAllBar = 3;
 
+// The log-sum-exp of a row from m (its maximum less the lift) and its lifted sum.
+template <bool kBf16>
+__device__ __forceinline__ float row_lse(float m, float sum) {
+  constexpr float kLift = TileShape<64, 16, false, kBf16>::Lift;
+  if (sum == 0.0f) return -INFINITY;
+  return (m + kLift + log2f(kBf16 ? sum : sum * 0.0078125f)) * (1.0f / kLog2e);
+}
+
 struct ValuePool {
   const void* data;
   int64_t page, token, head;
@@ -981,8 +992,8 @@ struct Attend {
     if (quarter == 0 && lane < S::CH) {
       const int c = c0 + lane;
       const float was = -T.m[c];
-      const float m =
-          fmaxf(fmaxf(fmaxf(T.red[0][c], T.red[1][c]), fmaxf(T.red[2][c], T.red[3][c])), was);
+      const float top = fmaxf(fmaxf(T.red[0][c], T.red[1][c]), fmaxf(T.red[2][c], T.red[3][c]));
+      const float m = fmaxf(top - S::Lift, was);
       T.alpha[c] = ex2(was - m);
       T.m[c] = -m;
     }
@@ -1099,7 +1110,7 @@ struct Attend {
         const float2 v = split(e[c]);
         top = fmaxf(top, fmaxf(v.x, v.y));
       }
-      if (__builtin_expect(bar_or(1 + group, 128, top > 8.0f), 0)) {
+      if (__builtin_expect(bar_or(1 + group, 128, top > 8.0f + S::Lift), 0)) {
         if (!first) wait_values(y - 1);
 #pragma unroll
         for (int c = 0; c < S::CH; ++c) s[c] *= scale;
@@ -1170,7 +1181,7 @@ struct Attend {
             *reinterpret_cast<float2*>(part + S::N * S::D + 2 * c) = make_float2(m, sum);
           else if (A.out_lse)
             A.out_lse[row0 + T.row[c]] =
-                sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
+                row_lse<S::Bf16>(m, sum);
         }
         T.alpha[c] = !whole ? 1.0f : sum == 0.0f ? 0.0f : rcp_fast(sum);
         T.red[0][c] = c < rows && sum == sum ? 1.0f : 0.0f;  // its output is a number unless a value is not
@@ -1620,7 +1631,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   *reinterpret_cast<uint2*>(static_cast<char*>(out) + 2 * (row * kD + d)) =
       make_uint2(pack16<kBf16>(acc.x * inv, acc.y * inv), pack16<kBf16>(acc.z * inv, acc.w * inv));
   if (out_lse && d == 0)
-    out_lse[row] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * (1.0f / kLog2e);
+    out_lse[row] = row_lse<kBf16>(m, sum);
 }
 
 // ---- the host side ------------------------------------------------------------------------------
