@@ -1214,9 +1214,10 @@ struct Attend {
             tmem_wait_ld();
           }
           const int n0 = col0 + q;
+          float all = 0.0f;
 #pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (T.red[0][n0 + c] != 0.0f) odd = fmaf(o[c], 0.0f, odd);
+          for (int c = 0; c < 16; ++c) all = fmaf(o[c], T.red[0][n0 + c], all);
+          odd = fmaf(all, 0.0f, odd);  // (NaN from here on if one of them is not finite)
           if (whole) {
             uint16_t* out = static_cast<uint16_t*>(A.out) + row0 * S::D + d;
 #pragma unroll
