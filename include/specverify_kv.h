@@ -177,7 +177,8 @@ sv_status attention_weight_sum(const sv_kv_shape* shape, const sv_score_rule* ru
  *   out_len      [B] int32: m, or -1 for a request with a data error.
  *   out_index    [B, Hkv, budget] int32: the old slot of each kept one, then -1.
  *   out_weights  [B, Hkv, budget] fp32: the kept slots' weights, then 0; or NULL.
- * B * Hkv is at most 65535, else SV_ERR_UNSUPPORTED.
+ * B * Hkv is at most 65535, else SV_ERR_UNSUPPORTED. out_len must not overlap seq_len, nor
+ * out_weights weights, else SV_ERR_INVALID_ARG.
  * A request with seq_len out of range (or above stride) or with a page outside its pool's
  * range among those it needs, in either table, gets out_len = -1, out_index all -1 and
  * out_weights all 0, and nothing of it is copied.

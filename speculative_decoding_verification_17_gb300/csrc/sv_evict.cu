@@ -263,6 +263,12 @@ __global__ void __launch_bounds__(kSelThreads, kMoves ? kBothCtas : 1)
   }
 }
 
+// Whether two ranges of bytes share one (no range: NULL).
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 constexpr int kMoveThreads = 256;
 
 __global__ void __launch_bounds__(kMoveThreads)
@@ -306,6 +312,11 @@ extern "C" sv_status kv_cache_evict(const sv_kv_shape* shape, const sv_kv_pool* 
       !aligned_to(out_weights, 4))
     return SV_ERR_INVALID_ARG;
   const int rows = shape->B * shape->Hkv;
+  // one head's CTA writes a request's length while another may still read it, and rows of weights
+  // move
+  if (overlap(out_len, 4 * (size_t)shape->B, seq_len, 4 * (size_t)shape->B) ||
+      overlap(out_weights, 4 * (size_t)rows * budget, weights, 4 * (size_t)rows * stride))
+    return SV_ERR_INVALID_ARG;
   if (rows > 65535) return SV_ERR_UNSUPPORTED;
   const int lp = log2_of(shape->page_size);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

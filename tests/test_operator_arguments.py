@@ -1,0 +1,30 @@
+"""Refusals of kv_cache_evict and its binding that come before anything is launched or made (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+import speculative_decoding_verification_17_gb300 as sv
+from speculative_decoding_verification_17_gb300 import _native
+
+INVALID = 1
+
+
+def evict(**kw):
+    """2 requests of 2 heads, tables of 10 and 3 pages of 16, every array in a place of its own."""
+    shape = ctypes.byref(_native.KvShape(1, 2, 1, 2, 2, 128, 16, 40, 10))
+    pool = lambda at: ctypes.byref(_native.KvPool(at, 4096, 256, 128))  # noqa: E731
+    a = dict(k=pool(0x100000), v=pool(0x200000), table=0x300000, lens=0x310000, w=0x320000,
+             stride=160, budget=40, recent=8, nk=pool(0x400000), nv=pool(0x500000), npages=20,
+             ntable=0x600000, ncols=3, ol=0x610000, oi=0x620000, ow=0x630000, st=None)
+    a.update(kw)
+    return sv.library().kv_cache_evict(shape, *a.values())
+
+
+@pytest.mark.parametrize("kw", [
+    dict(ol=0x310000), dict(ol=0x310004), dict(ol=0x30fffc), dict(ow=0x320000),
+    dict(ow=0x320000 + 4 * (2 * 2 * 160 - 1)), dict(ow=0x320000 - 4 * (2 * 2 * 40 - 1)),
+])
+def test_outputs_over_what_is_read_are_refused(kw):
+    """In place, one head's CTA would overwrite what another still reads."""
+    assert evict(**kw) == INVALID
