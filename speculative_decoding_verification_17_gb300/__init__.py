@@ -847,6 +847,8 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
     _check_cuda("seq_len", seq_len, torch.int32, (B,), dev)
     _check_cuda("weights", weights, torch.float32, (B, Hkv, N), dev)
     _check_cuda("new_page_table", new_page_table, torch.int32, (B, new_cols), dev)
+    if not 1 <= budget <= new_cols * page_size:
+        raise SVError(1, "kv_cache_evict")
     if out_len is None:
         out_len = torch.empty((B,), dtype=torch.int32, device=dev)
     if out_index is None:

@@ -268,6 +268,9 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !len.fits(at::kInt, dev, {B}) || !index.fits(at::kInt, dev, {B, Hkv, budget}) ||
       !kept.fits(at::kFloat, dev, {B, Hkv, budget}))
     return none();
+  // (before outputs of that size are made)
+  if (budget < 1 || budget > ncols * k.t->size(1))
+    return Py_BuildValue("(iOOO)", (int)SV_ERR_INVALID_ARG, Py_None, Py_None, Py_None);
   const auto made = [&](const Arg& given, at::IntArrayRef sizes, at::ScalarType type) {
     return given ? *given.t : at::empty(sizes, at::TensorOptions().dtype(type).device(dev));
   };

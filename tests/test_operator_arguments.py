@@ -3,6 +3,8 @@ import ctypes
 
 import pytest
 import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.utils._python_dispatch import TorchDispatchMode
 
 import speculative_decoding_verification_17_gb300 as sv
 from speculative_decoding_verification_17_gb300 import _native
@@ -28,3 +30,23 @@ def evict(**kw):
 def test_outputs_over_what_is_read_are_refused(kw):
     """In place, one head's CTA would overwrite what another still reads."""
     assert evict(**kw) == INVALID
+
+
+class NothingMade(TorchDispatchMode):
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        assert "empty" not in str(func) and "zeros" not in str(func), func
+        return func(*args, **(kwargs or {}))
+
+
+@pytest.mark.parametrize("budget", [0, -1, 65, 10 ** 9, 2 ** 31 - 1])
+def test_a_budget_its_pages_cannot_hold_makes_no_outputs(budget, monkeypatch):
+    if torch.cuda.is_available():
+        pytest.skip("fakes stand in for the tensors of a GPU")
+    monkeypatch.setattr(sv, "_raw_stream", lambda stream, like: 0)
+    with FakeTensorMode():
+        new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        kv, table, n = new(4, 16, 2, 64), new(1, 4, dtype=torch.int32), new(1, dtype=torch.int32)
+        w, length = new(1, 2, 64, dtype=torch.float32), new(1, dtype=torch.int32)
+        with NothingMade(), pytest.raises(sv.SVError) as e:
+            sv.kv_cache_evict(kv, kv, table, n, w, budget, 0, kv, kv, table, out_len=length)
+        assert e.value.status == INVALID
