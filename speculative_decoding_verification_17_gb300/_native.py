@@ -1,10 +1,11 @@
-"""Build and load ``libspecverify.so``, the C-ABI library of the verify step, and ``_calls.so``,
-the checks and marshalling of the calls on logits and on the paged cache.
+"""Build and load ``libspecverify.so``, the C-ABI library of the verify step, and ``_calls``, the
+checks and marshalling of the calls on logits and on the paged cache.
 
 The library is compiled in-tree from ``csrc/`` for sm_103a only (one ``-gencode``), one
 nvcc process per translation unit in parallel, and linked against the static CUDA runtime
 so loading it needs no CUDA library path. Loading never falls back to anything: a missing
-or stale library is an error.
+or stale library is an error. ``_calls`` is a Python module against torch's C++ interface, so its
+file is named after the versions of both; the calls that do not use it do not need it.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import ctypes
 import glob
 import os
 import subprocess
+import sys
 import threading
 from concurrent.futures import ThreadPoolExecutor
 
@@ -22,7 +24,13 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 SO = os.path.join(BUILD, "libspecverify.so")
 BINDING = os.path.join(CSRC, "binding.cpp")
-CALLS = os.path.join(BUILD, "_calls.so")
+
+
+def _calls_path() -> str:
+    import torch
+
+    return os.path.join(BUILD, f"_calls.{sys.implementation.cache_tag}-torch{torch.__version__}.so")
+
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
@@ -40,21 +48,56 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _older(path: str, deps) -> bool:
+    """Whether a built file is missing or older than what it is made of."""
+    return not os.path.exists(path) or any(
+        os.path.getmtime(d) > os.path.getmtime(path) for d in deps)
+
+
 def _stale() -> bool:
-    if not os.path.exists(SO):
-        return True
-    if not os.path.exists(CALLS):
-        return True
-    t = min(os.path.getmtime(SO), os.path.getmtime(CALLS))
-    deps = sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
-        os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(d) > t for d in deps)
+    return _older(SO, sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(
+        os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _calls_stale() -> bool:
+    return _older(_calls_path(), [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every ``csrc/*.cu`` and link ``_build/libspecverify.so``."""
-    if not force and not _stale():
-        return SO
+    """Compile what is missing or older than its sources: the library and ``_calls``."""
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_build_calls) if force or _calls_stale() else None
+        if force or _stale():
+            _build_library(verbose)
+        if binding:
+            binding.result()
+    return SO
+
+
+def _build_calls() -> None:
+    import sysconfig
+
+    import torch
+
+    os.makedirs(BUILD, exist_ok=True)
+    path, root = _calls_path(), os.path.dirname(torch.__file__)
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I",
+           os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I",
+           sysconfig.get_paths()["include"], BINDING, "-o", tmp, "-L",
+           os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{cmd[0]} could not be run on {BINDING}: {e}") from e
+    if r.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, path)
+
+
+def _build_library(verbose: bool) -> None:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     objs = []
@@ -71,35 +114,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stdout + r.stderr)
         return obj
 
-    def compile_binding():
-        import sysconfig
-
-        import torch
-
-        root = os.path.dirname(torch.__file__)
-        tmp = CALLS + f".tmp{os.getpid()}"
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC",
-               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
-               "-I", os.path.join(root, "include"), "-I",
-               os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I",
-               sysconfig.get_paths()["include"], BINDING, "-o", tmp, "-L",
-               os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"{cmd[0]} failed on {BINDING}:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, CALLS)
-
     with ThreadPoolExecutor(max_workers=max(1, min(16, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(compile_binding)
         objs = list(ex.map(compile_one, sources()))
-        binding.result()
     tmp = SO + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs],
                        capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, SO)
-    return SO
 
 
 _lock = threading.Lock()
@@ -114,7 +136,7 @@ def lib():
         if _lib is None:
             path = SO
             if _stale():
-                build()
+                _build_library(False)
             if not os.path.exists(path):
                 raise RuntimeError("libspecverify.so is missing and could not be built")
             L = ctypes.CDLL(path)
@@ -124,19 +146,23 @@ def lib():
 
 
 def calls():
-    """The marshalling module, bound to the loaded library."""
+    """The marshalling module (built first if absent or older than its sources), bound to the loaded
+    library."""
     global _calls
-    if _calls is None:
-        import importlib.util
+    L = lib()
+    with _lock:
+        if _calls is None:
+            import importlib.util
 
-        L = lib()
-        spec = importlib.util.spec_from_file_location("_calls", CALLS)
-        m = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(m)
-        m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
-            L.logit_adjust, L.paged_attention, L.paged_attention_workspace,
-            L.attention_weight_sum, L.kv_cache_evict)))
-        _calls = m
+            if _calls_stale():
+                _build_calls()
+            spec = importlib.util.spec_from_file_location("_calls", _calls_path())
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.logit_adjust, L.paged_attention, L.paged_attention_workspace,
+                L.attention_weight_sum, L.kv_cache_evict)))
+            _calls = m
     return _calls
 
 
