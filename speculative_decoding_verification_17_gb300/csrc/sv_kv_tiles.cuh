@@ -130,7 +130,7 @@ struct TileShape {
   static constexpr int NQ = N * D <= 64 * 128 ? 2 : 1;  // query buffers
   static constexpr int PBytes = kWeigh ? 0 : 2 * kTileKeys * N * 2;
   // two buffers of weights per team where the ring keeps three tensors (two tiles of D = 256)
-  static constexpr int kTables = 96 * N + 1664;  // (the size of TileShared, at most)
+  static constexpr int kTables = 96 * N + 1792;  // (the size of TileShared, at most)
   static constexpr int kLeft = kSmemMax - kTables - 1024 - NQ * QBytes;
   static constexpr int NP =
       kWeigh ? 1 : (kLeft - 2 * Teams * PBytes) / kUnitBytes >= (U == 4 ? 8 : 6) ? 2 : 1;
@@ -444,6 +444,7 @@ struct TileShared {
     alignas(16) float red[4][S::N];  // per-warp maxima or sums
     int hi[S::N], lo[S::N];          // the column sees keys j with lo < j <= hi
     int row[S::N];                   // output row of the column, from the item's first
+    Piece piece;                     // whose columns these are (its end reads it from here)
     int odd;                         // a partly visible key has values that are not finite
   } table[2];                        // by ordinal % 2 (with two teams: one each)
   JoinItem join;
@@ -562,16 +563,15 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
   int page = seen ? group_page(A, p, tile_at<S>(p, 0), lane) : 0;
   RingPos at;
   int issued = 0, q_issued = 0;
-  bool ok = true;
 #pragma unroll 1
-  while (more && ok) {
+  while (more) {
     const int head = p.h, turn = p.turn;
     const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
     if (!kValues && i == 0) {
       const int qs = turn % S::NQ;
-      ok = wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u, &sh.waits);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u,
+                                              &sh.waits)))
+        goto end;
       if (lane == 0) {
         mbar_arrive_expect_tx(&sh.q_full[qs], (uint32_t)(A.G * A.pos_block * S::D * 2));
 #pragma unroll 1
@@ -596,11 +596,10 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
     const uint32_t bytes =
         (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
 #pragma unroll 1
-    for (int c = 0; ok && c < S::U; ++c) {
+    for (int c = 0; c < S::U; ++c) {
       uint64_t* full = &sh.full[kBase + at.slot];
-      ok = wait_phase(&sh.empty[kBase + at.slot], at.phase ^ 1u, &sh.waits);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, wait_phase(&sh.empty[kBase + at.slot], at.phase ^ 1u, &sh.waits)))
+        goto end;
       if (lane == 0) mbar_arrive_expect_tx(full, bytes);
       ++issued;
       __syncwarp();
@@ -610,6 +609,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
     page = next_page;
     seen = next_seen;
   }
+end:
   if (lane == 0) {
     // no copy may outlive the CTA, should the others give up before they have seen it land
 #pragma unroll 1
@@ -643,37 +643,35 @@ __device__ __forceinline__ void score_role(const TileArgs& A, TileShared<S>& sh,
   Reader<S> reader(sh);
   RingPos at;
   int used[2] = {0, 0};  // tiles so far per team (attention) or per score buffer (key weights)
-  bool ok = true;
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
     const int qs = p.turn % S::NQ, team = p.turn % S::Teams, tiles = p.mb - p.ma;
-    ok &= wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits);
+    if (!wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits)) goto end;
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int of = S::Weigh ? tile_at<S>(p, i) & 1 : team;
       const int y = of ? used[1]++ : used[0]++;
       const int buf = S::Weigh ? of : y & 1, turn = S::Weigh ? y : y >> 1;
-      ok &= wait_phase(&sh.s_empty[team][buf], ((uint32_t)turn & 1u) ^ 1u, &sh.waits);
+      if (!wait_phase(&sh.s_empty[team][buf], ((uint32_t)turn & 1u) ^ 1u, &sh.waits)) goto end;
       tc_fence_after();
       const uint32_t d = sh.tmem + (2 * team + buf) * S::N;
       uint64_t b = b0 + qs * (S::QBytes >> 4);
 #pragma unroll 1
       for (int c = 0; c < S::U; ++c, b += S::N * 8) {
-        ok &= wait_phase(&sh.full[at.slot], at.phase, &sh.waits);
+        if (!wait_phase(&sh.full[at.slot], at.phase, &sh.waits)) goto end;
         tc_fence_after();
         const uint64_t a = a0 + at.slot * (kUnitBytes >> 4);
-        if (ok) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16(d, a + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
-          mma_commit(&sh.empty[at.slot]);
-        }
+        for (int k = 0; k < 4; ++k) mma_f16(d, a + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
+        mma_commit(&sh.empty[at.slot]);
         at.next(S::NK);
       }
-      if (ok) mma_commit(&sh.s_full[team][buf]);
+      mma_commit(&sh.s_full[team][buf]);
     }
-    if (ok) mma_commit(&sh.q_empty[qs]);
+    mma_commit(&sh.q_empty[qs]);
   }
+end:
   drain<S>(sh, 0);
 }
 
@@ -692,7 +690,6 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
   Reader<S> reader(sh);
   RingPos at;
   int used[2] = {0, 0};
-  bool ok = true;
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
@@ -705,12 +702,12 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
         RingPos look = at;
 #pragma unroll 1
         for (int c = 0; c < S::U; ++c) {
-          ok &= wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.waits);
+          if (!wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.waits)) goto end;
           look.next(S::NV);
         }
-        if (ok) mbar_arrive(&sh.v_ready[team]);
+        mbar_arrive(&sh.v_ready[team]);
       }
-      ok &= wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits);
+      if (!wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits)) goto end;
       const uint64_t b = b0 + (team * S::NP + pb) * (S::PBytes >> 4);
       uint32_t d = o;
 #pragma unroll 1
@@ -719,11 +716,10 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
         uint64_t* empty = &sh.empty[S::NK + at.slot];
 #pragma unroll 1
         for (int c = 0; c < kPer; ++c) {
-          ok &= wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.waits);
+          if (!wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.waits)) goto end;
           at.next(S::NV);
         }
         tc_fence_after();
-        if (!ok) continue;
 #pragma unroll 1
         for (int part = 0; part < (S::Wide ? 1 : 2); ++part)  // the weights' high and low halves
 #pragma unroll 4
@@ -733,10 +729,11 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll
         for (int c = 0; c < kPer; ++c) mma_commit(empty + c);  // (a pair lies side by side)
       }
-      if (ok) mma_commit(&sh.pv_done[team][pb]);
+      mma_commit(&sh.pv_done[team][pb]);
     }
-    if (ok) mma_commit(&sh.o_done[p.turn & 1]);
+    mma_commit(&sh.o_done[p.turn & 1]);
   }
+end:
   drain<S>(sh, 1);
 }
 
@@ -1162,7 +1159,8 @@ struct Attend {
 
   // The end of a piece (its sums' warp parts are in T.red): O and the sums leave for the output
   // or for the workspace.
-  __device__ __forceinline__ void finish(Table& T, const Piece& p) {
+  __device__ __forceinline__ void finish(Table& T) {
+    const Piece& p = T.piece;
     group_sync();
     const bool poison = *(volatile int*)&sh.bad_piece[p.turn & 7] == p.turn + 1;
     const bool starts = p.flags & kStarts, whole = starts && (p.flags & kEnds);
@@ -1245,8 +1243,8 @@ struct Attend {
   // tile; with two the other team's tiles cover it.
   __device__ __forceinline__ void run() {
     Reader<S> reader(sh);
-    Piece p{}, ended{};
-    int y = 0, i = 0;
+    Piece p{};
+    int y = 0, i = 0, ended = 0;
     bool pending = false;
     Two l[S::NC / 2];
     auto table = [&](int turn) -> Table& { return sh.table[S::Teams == 2 ? team : turn & 1]; };
@@ -1270,7 +1268,7 @@ struct Attend {
             Table& T = table(p.turn);
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
-            if (me == 0) T.odd = 0;
+            if (me == 0) T.piece = p, T.odd = 0;
             team_sync();
             i = 0;
           }
@@ -1284,7 +1282,7 @@ struct Attend {
         }
       }
       if (pending) {
-        finish(table(ended.turn), ended);
+        finish(table(ended));
         pending = false;
       }
       if (!more) break;
@@ -1297,7 +1295,7 @@ struct Attend {
           sums[c + 1] = v.y;
         }
         column_reduce<S::NC, false>(sums, &table(p.turn).red[quarter][col0], lane);
-        ended = p;
+        ended = p.turn;
         pending = true;
       }
     }
