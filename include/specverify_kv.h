@@ -92,8 +92,9 @@ typedef struct {
  * rows; one whose page table names a page outside [0, num_pages) for a key that is seen, NaN
  * at least in the rows that see such a key.
  * Scores, their softmax and the sums over values are fp32; the weights exp(s_j - max) enter the
- * product with the values as a sum of two numbers of the values' type. The work is split over
- * the SMs by a rule on the lengths alone and joined in order: equal calls give equal bits.
+ * product with the values as a sum of numbers of the values' type: off by 2^-22 of a weight (fp16),
+ * or 2^-24 (bf16, up to 32 query rows per kv head and pass) or 2^-16 (bf16, more). The work is split
+ * over the SMs by a rule on the lengths alone and joined in order: equal calls give equal bits.
  * ---------------------------------------------------------------------------------------- */
 size_t paged_attention_workspace(const sv_kv_shape* shape);
 

@@ -29,10 +29,13 @@
 // of 7 for fp16, whose numbers end at 2^-24: a weight is at most 2^15, and 2^-32 of the largest score's
 // still counts (without the lift 2^-25: 131072 keys of that weight, 0.4 % of a row, came to 0).
 //
-// Rounding. The weights P are given to the tensor core as two 16-bit numbers, p = hi + lo, and
-// V^T is multiplied by both. Each rounding leaves at most half a step of what it rounds: a weight is
-// off by 2^-16 of it (bf16) or 2^-22 (fp16, or by 2^-32 of the largest), where the output's own rounding
-// is 2^-8 or 2^-11 of it. The second product costs tensor time that the memory hides.
+// Rounding. The weights P are given to the tensor core as a sum of 16-bit numbers, each the rest that
+// those before it leave, and V^T is multiplied by all. Every rounding leaves at most half a step of what
+// it rounds. fp16 takes two: a weight is off by 2^-22 of it (or by 2^-32 of the largest). bf16 takes
+// three up to 32 columns, 2^-24, as fp32 itself, at next to no cost (1 token of 64 requests 97.4 us
+// with two, 97.3 with three, D = 256 in a window 49.4 and 49.1, 24 rows 100.6 and 101.8), and two
+// above, 2^-16 (the output's own rounding is 2^-8), where the softmax and its buffers bound and a
+// third cost 2 to 17 % (9 positions over long caches 166 -> 172 us, 64 rows 109 -> 119).
 //
 // Work. All tiles of all (request, kv head, row block) items are one flat range, cut into equal
 // costs over one CTA per SM: ragged lengths balance by construction. A CTA walks its range piece
@@ -128,12 +131,14 @@ struct TileShape {
   static constexpr int CH = NC < 32 ? NC : 32;                 // of which at a time
   static constexpr int QBytes = N * D * 2;
   static constexpr int NQ = N * D <= 64 * 128 ? 2 : 1;  // query buffers
-  static constexpr int PBytes = kWeigh ? 0 : 2 * kTileKeys * N * 2;
-  // two buffers of weights per team where the ring keeps three tensors (two tiles of D = 256)
+  static constexpr int Parts = kBf16 && N <= 32 ? 3 : 2;  // 16-bit numbers a weight is given in
+  static constexpr int PBytes = kWeigh ? 0 : Parts * kTileKeys * N * 2;
+  // two buffers of weights per team where the ring keeps three tensors (of D = 256 two tiles, or ten
+  // units beside weights of three parts: in a window 49.1 us with one buffer, 51.0 with two)
   static constexpr int kTables = 96 * N + 1792;  // (the size of TileShared, at most)
   static constexpr int kLeft = kSmemMax - kTables - 1024 - NQ * QBytes;
   static constexpr int NP =
-      kWeigh ? 1 : (kLeft - 2 * Teams * PBytes) / kUnitBytes >= (U == 4 ? 8 : 6) ? 2 : 1;
+      kWeigh ? 1 : (kLeft - 2 * Teams * PBytes) / kUnitBytes >= (U == 4 ? 2 * Parts + 4 : 6) ? 2 : 1;
   static constexpr int Room = (kLeft - Teams * NP * PBytes) / kUnitBytes;
   // Ring units: one ring for keys, one for values, as each has its own consumer. (A consumer
   // that skipped some phases of a unit's barrier could not tell a phase from the one after next.)
@@ -143,12 +148,12 @@ struct TileShape {
   static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * kUnitBytes;
   static constexpr int MBlocks = kWeigh ? 0 : (D + 127) / 128;  // accumulators of 128 of D
   // Two score buffers per team, two outputs. Where tensor memory has room, the products with the
-  // high and the low halves of the weights are one instruction of twice the columns (the values,
-  // whose read from shared memory bounds a narrow instruction, are read once) and are added at
-  // the end; else the second accumulates onto the first. (9 positions over long caches, 64 columns:
+  // parts of the weights are one instruction of as many times the columns (the values, whose read
+  // from shared memory bounds a narrow instruction, are read once) and are added at the end; else
+  // they accumulate onto one another. (9 positions over long caches, 64 columns:
   // 163 us wide, 179 us in two; 16 columns: 94 and 96 us.)
-  static constexpr bool Wide = !kWeigh && 2 * (Teams + 2 * MBlocks) * N <= 512;
-  static constexpr int ON = Wide ? 2 * N : N;  // columns of an accumulator
+  static constexpr bool Wide = !kWeigh && 2 * (Teams + Parts * MBlocks) * N <= 512;
+  static constexpr int ON = Wide ? Parts * N : N;  // columns of an accumulator
   static constexpr int TmemNeed = 2 * (Teams * N + MBlocks * ON);
   static constexpr int TmemCols = TmemNeed <= 32 ? 32 : TmemNeed <= 64 ? 64 : TmemNeed <= 128 ? 128
                                   : TmemNeed <= 256 ? 256 : 512;
@@ -721,7 +726,7 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
         }
         tc_fence_after();
 #pragma unroll 1
-        for (int part = 0; part < (S::Wide ? 1 : 2); ++part)  // the weights' high and low halves
+        for (int part = 0; part < (S::Wide ? 1 : S::Parts); ++part)  // the weights' parts
 #pragma unroll 4
           for (int k = 0; k < kTileKeys / 16; ++k)
             mma_f16(d, a + k * 128, b + part * (kTileKeys * S::N * 2 >> 4) + k * 32, idesc,
@@ -1003,7 +1008,7 @@ struct Attend {
     }
     tc_fence_after();
 #pragma unroll 1
-    for (int m = 0; m < S::MBlocks * (S::Wide ? 2 : 1); ++m)  // (wide: high and low products)
+    for (int m = 0; m < S::MBlocks * (S::Wide ? S::Parts : 1); ++m)  // (wide: a product per part)
 #pragma unroll 1
       for (int q = 0; q < S::CH; q += 16) {
         float o[16];
@@ -1115,17 +1120,20 @@ struct Attend {
         raise(T, s, l, k, first, output(p.turn));
         exponents();
       }
-      uint32_t hi[S::CH / 2], lo[S::CH / 2];
+      uint32_t w16[S::Parts][S::CH / 2];
 #pragma unroll
       for (int c = 0; c < S::CH / 2; ++c) {
         const float2 v = split(e[c]);
         const float a = ex2(v.x), b = ex2(v.y);
-        const Two w = two(a, b);
+        Two w = two(a, b);  // what the parts so far leave of the weights
         l[k / 2 + c] = two_add(l[k / 2 + c], w);
-        hi[c] = pack16<S::Bf16>(a, b);
-        const float2 h = unpack16<S::Bf16>(hi[c]);
-        const float2 r = split(two_fma(two(h.x, h.y), two(-1.0f, -1.0f), w));
-        lo[c] = pack16<S::Bf16>(r.x, r.y);
+#pragma unroll
+        for (int part = 0; part < S::Parts; ++part) {
+          const float2 r = split(w);
+          w16[part][c] = pack16<S::Bf16>(r.x, r.y);
+          const float2 h = unpack16<S::Bf16>(w16[part][c]);
+          if (part + 1 < S::Parts) w = two_fma(two(h.x, h.y), two(-1.0f, -1.0f), w);
+        }
       }
       // the product that last read this buffer
       if (k == 0 && y >= S::NP) wait_values(y - S::NP);
@@ -1134,13 +1142,12 @@ struct Attend {
         // 16 columns of a key: 32 bytes, their 16-byte halves swapped in every other 4 keys
         unsigned char* at = pb + (k + q) / 16 * (kTileKeys * 32);
         const int sw = ((key >> 2) & 1) * 16, w = q / 2;
-        *reinterpret_cast<uint4*>(at + sw) = make_uint4(hi[w], hi[w + 1], hi[w + 2], hi[w + 3]);
-        *reinterpret_cast<uint4*>(at + (16 - sw)) =
-            make_uint4(hi[w + 4], hi[w + 5], hi[w + 6], hi[w + 7]);
-        at += kTileKeys * S::N * 2;
-        *reinterpret_cast<uint4*>(at + sw) = make_uint4(lo[w], lo[w + 1], lo[w + 2], lo[w + 3]);
-        *reinterpret_cast<uint4*>(at + (16 - sw)) =
-            make_uint4(lo[w + 4], lo[w + 5], lo[w + 6], lo[w + 7]);
+#pragma unroll
+        for (int part = 0; part < S::Parts; ++part, at += kTileKeys * S::N * 2) {
+          const uint32_t* v = &w16[part][w];
+          *reinterpret_cast<uint4*>(at + sw) = make_uint4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<uint4*>(at + (16 - sw)) = make_uint4(v[4], v[5], v[6], v[7]);
+        }
       }
     }
     if (__builtin_expect(edge, 0)) {
@@ -1202,14 +1209,16 @@ struct Attend {
         for (int q = 0; q < S::NC && col0 + q < rows; q += 16) {
           float o[16];
           tmem_ld16(output(p.turn) + m * S::ON + q, o);
+          tmem_wait_ld();
           if (S::Wide) {
-            float low[16];
-            tmem_ld16(output(p.turn) + m * S::ON + S::N + q, low);
-            tmem_wait_ld();
+#pragma unroll 1
+            for (int part = 1; part < S::Parts; ++part) {
+              float low[16];
+              tmem_ld16(output(p.turn) + m * S::ON + part * S::N + q, low);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 16; ++c) o[c] += low[c];
-          } else {
-            tmem_wait_ld();
+              for (int c = 0; c < 16; ++c) o[c] += low[c];
+            }
           }
           const int n0 = col0 + q;
           float all = 0.0f;

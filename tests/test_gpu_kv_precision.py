@@ -63,3 +63,34 @@ def test_a_long_tail_of_small_fp16_weights(D, G, P, below):
     assert ref.close(out, want, tol)
     assert torch.allclose(lse.double(), (scale + torch.log1p(tail))[None, :, None].expand(B, P, G),
                           rtol=0, atol=2.0 ** -16)
+
+
+@pytest.mark.parametrize("D,G,P", [(64, 1, 1), (64, 8, 4), (128, 4, 1), (128, 4, 6), (128, 16, 2),
+                                   (256, 2, 5), (256, 8, 3)])
+def test_bf16_weights_keep_the_bits_of_fp32(D, G, P):
+    """Up to 32 rows per kv head. Three keys: weights 1, 1 and p, values -c1, -c2 and 1, where c1 and c2
+    are the first 16 bits of p: what is left is p's third part."""
+    x = torch.arange(0xbc00, 0xbf80).to(torch.int16).view(torch.bfloat16)  # all in (-1, -2^-7]
+    p = torch.exp(x.double())
+    c1 = p.bfloat16()
+    c2 = (p - c1.double()).bfloat16()
+    # the scores whose weight has the largest third parts, up to 2^-18
+    some = (p - c1.double() - c2.double()).abs().topk(96).indices
+    x, p, c1, c2, B = x[some], p[some], c1[some], c2[some], 96
+    n, page = 2 + P, 8 if P <= 6 else 16  # the drafts' own keys come last: of no weight to anything
+    k = torch.zeros((B, page, 1, D), dtype=torch.bfloat16)
+    v = torch.zeros_like(k)
+    k[:, 2, 0, 0] = x
+    k[:, 3:, 0, 0] = -1000.0
+    v[:, 0, 0], v[:, 1, 0], v[:, 2, 0] = -c1[:, None], -c2[:, None], 1.0
+    q = torch.zeros((B, P, G, D), dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    table = torch.arange(B).int()[:, None]
+    lens = torch.full((B,), n).int()
+    out, _ = sv.paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lens.cuda(), scale=1.0)
+    want = ((p - c1.double() - c2.double()) / (2 + p))[:, None, None, None].expand(B, P, G, D)
+    # the exponential and its argument 2^-21, the three parts 2^-24, sums of numbers near 1 in fp32
+    # 2^-22; the output's rounding
+    tol = ((2.0 ** -21 + 2.0 ** -24 + 2.0 ** -22) / (2 + p))[:, None, None, None] + 2.0 ** -8 * want.abs()
+    assert bool((want.abs() > 2 * tol).all())  # (two parts would leave it out)
+    assert ref.close(out.cpu(), want, tol)
