@@ -53,8 +53,9 @@ extern "C" {
  *                  same strides, and must not overlap it otherwise. Rows past n_r are not
  *                  written.
  * A request with hist_len, prompt_len or num_draft out of range gets NaN in all its P rows.
- * Any alignment of the rows works; 16-byte accesses are used where a row's input and output
- * start at the same offset from a 16-byte boundary. No workspace; one launch.
+ * Any alignment of the rows works. Rows move in 16-byte pieces where logits and out, their strides
+ * and V are all multiples of 16 bytes (4 fp32 or 8 bf16 elements); else element by element, which is
+ * slower. No workspace; one launch.
  * ---------------------------------------------------------------------------------------- */
 sv_status logit_adjust(const void* logits, int64_t in_req_stride, int64_t in_row_stride,
                        sv_dtype dtype, const int32_t* history, const int32_t* hist_len,
