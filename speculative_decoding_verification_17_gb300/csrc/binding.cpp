@@ -58,8 +58,9 @@ bool number(PyObject* o, double* x) {
   }
   return true;
 }
+// An integer, or what has one's value (numpy's).
 bool whole(PyObject* o, long long* x) {
-  if (!PyLong_Check(o)) return false;
+  if (!PyIndex_Check(o)) return false;
   *x = PyLong_AsLongLong(o);
   if (*x == -1 && PyErr_Occurred()) {
     PyErr_Clear();

@@ -1,6 +1,7 @@
 """Refusals of kv_cache_evict and its binding that come before anything is launched or made (no GPU)."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
@@ -50,3 +51,15 @@ def test_a_budget_its_pages_cannot_hold_makes_no_outputs(budget, monkeypatch):
         with NothingMade(), pytest.raises(sv.SVError) as e:
             sv.kv_cache_evict(kv, kv, table, n, w, budget, 0, kv, kv, table, out_len=length)
         assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("make", [int, np.int64, np.int32])
+def test_integers_of_numpy_take_the_short_way(make):
+    if torch.cuda.is_available():
+        pytest.skip("fakes stand in for the tensors of a GPU")
+    with FakeTensorMode():
+        new = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device="cuda")  # noqa: E731
+        kv, table, n = new(4, 16, 2, 64), new(1, 4, dtype=torch.int32), new(1, dtype=torch.int32)
+        made = _native.calls().evict(kv, kv, table, n, new(1, 2, 64, dtype=torch.float32), make(65),
+                                     make(0), kv, kv, table, None, None, None, 0)
+    assert made == (INVALID, None, None, None)  # (judged, not handed to the slow checks)
