@@ -66,6 +66,23 @@ sv_status logit_adjust(const void* logits, int64_t in_req_stride, int64_t in_row
                        const uint32_t* allowed, int B, int P, int V, void* out,
                        int64_t out_req_stride, int64_t out_row_stride, sv_stream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Self-test of the bounded waits inside logit_adjust: the same call, except that each wait for a
+ * copy is limited to wait_us microseconds (1000 .. 100000: the copies have landed by then) instead of
+ * 2 s and that those for the third row of a request cannot be over. Where rows move in 16-byte pieces,
+ * rows 0 and 1 come out as ever and the others are NaN, with no fault and no hang; other calls are as
+ * logit_adjust's. Returns SV_ERR_INVALID_ARG for wait_us out of range, else what the call returns.
+ * ---------------------------------------------------------------------------------------- */
+sv_status logit_adjust_wait_selftest(
+    const void* logits, int64_t in_req_stride, int64_t in_row_stride, sv_dtype dtype,
+    const int32_t* history, const int32_t* hist_len, const int32_t* prompt_len,
+    int L_max, const int32_t* draft_tokens, const int32_t* num_draft,
+    const float* repetition, const float* presence, const float* frequency,
+    const int32_t* bias_tokens, const float* bias_values, int n_bias,
+    const uint32_t* allowed, int B, int P, int V, void* out,
+    int64_t out_req_stride, int64_t out_row_stride, unsigned int wait_us,
+    sv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

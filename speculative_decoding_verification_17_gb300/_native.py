@@ -246,6 +246,8 @@ def _declare(L):
     L.logit_adjust.restype = I
     L.logit_adjust.argtypes = [P, q, q, I, P, P, P, I, P, P, P, P, P, P, P, I, P, I, I, I, P, q,
                                q, P]
+    L.logit_adjust_wait_selftest.restype = I
+    L.logit_adjust_wait_selftest.argtypes = [*L.logit_adjust.argtypes[:-1], ctypes.c_uint, P]
     shape = rule = pool = P  # structs: byref() of those above, or their bytes
     L.paged_attention_workspace.restype = Z
     L.paged_attention_workspace.argtypes = [shape]

@@ -53,6 +53,8 @@ struct AdjustArgs {
   const uint32_t* allowed;
   int L_max, n_bias, B, P, V, W;
   int log_chunk;  // tokens per chunk, 1024 to 4096, a power of two
+  uint64_t wait_ns;          // the limit of a wait
+  unsigned int more_arrivals;  // (self-test) the last stage's barrier waits for as many more
 };
 
 // E elements of a row as floats, and back (one rounding).
@@ -310,6 +312,33 @@ __device__ __forceinline__ void bulk_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kPending) : "memory");
 }
 
+// The rest of a wait for row i's copy.
+__device__ __noinline__ void wait_row(uint64_t* bar, uint32_t phase, uint64_t limit_ns, int* lost_row,
+                                      int i) {
+  if (!mbar_wait(bar, phase, limit_ns)) atomicMin(lost_row, i);
+}
+
+// The copy of row i never came: that row and those after it are NaN, once no copy is in flight any
+// more. All threads.
+template <typename T>
+__device__ __noinline__ void give_up(const AdjustArgs& A, uint64_t* full, int i, int rows, int nvec,
+                                     T* out) {
+  using X = Vec<T>;
+  if (threadIdx.x == 0) {
+    const int issued = kAdjStages + (i > 1 ? i - 1 : 0);
+    for (int r = i; r < issued && r < rows; ++r)
+      mbar_wait(&full[r % kAdjStages], (uint32_t)(r / kAdjStages) & 1u, A.wait_ns);
+    bulk_wait_read<0>();
+  }
+  const float nan[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
+  const uint4 v = X::pack(reinterpret_cast<const float(&)[X::E]>(nan));
+#pragma unroll 1
+  for (int r = i; r < rows; ++r)
+#pragma unroll 1
+    for (int q = threadIdx.x; q < nvec; q += kAdjThreads)
+      *reinterpret_cast<uint4*>(out + r * A.out_row + q * X::E) = v;
+}
+
 // Rows in 16-byte vectors.
 template <typename T>
 __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A) {
@@ -321,6 +350,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
   __shared__ __align__(8) uint64_t full[kAdjStages];
   __shared__ uint16_t list[kListed];
   __shared__ int warp_count[kAdjThreads / 32];
+  __shared__ int lost_row;  // the first whose copy never came
   const int tid = threadIdx.x;
   const int b0 = blockIdx.x % A.B;
   const int my_draft =
@@ -341,7 +371,9 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
     return;
   }
   if (tid == 0) {
-    for (int s = 0; s < kAdjStages; ++s) mbar_init(&full[s], 1);
+    lost_row = INT32_MAX;
+    for (int s = 0; s < kAdjStages; ++s)
+      mbar_init(&full[s], s == kAdjStages - 1 ? 1 + A.more_arrivals : 1);
     fence_barrier_init();
     for (int i = 0; i < kAdjStages && i < rows; ++i) {
       mbar_arrive_expect_tx(&full[i], bytes);
@@ -417,10 +449,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
     for (int u = 0; u < kVecs; ++u)
       ok[u] = (next_ok[u] >> (E == 8 ? 0 : 4 * ((tid + u * kAdjThreads) & 1))) & kFull;
     load_ok(i + 1);
-    if (!mbar_wait(&full[s], phase, kWaitLimitNs))
-      // the copy never came: the row reads as NaN
-      for (int q = tid; q < nvec * 4; q += kAdjThreads)
-        reinterpret_cast<uint32_t*>(buf)[q] = 0x7fc07fc0u;
+    if (!mbar_try_wait(&full[s], phase)) wait_row(&full[s], phase, A.wait_ns, &lost_row, i);
     if (listed && count > 0) {
 #pragma unroll 1
       for (int e = tid; e < count; e += kAdjThreads) {
@@ -463,6 +492,11 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
+    // (a thread ahead may have lost a later row: that one's barrier tells all)
+    if (__builtin_expect(*(volatile int*)&lost_row <= i, 0)) {
+      give_up<T>(A, full, i, rows, nvec, out);
+      return;
+    }
     if (tid == 0) {
       bulk_s2g(out + i * A.out_row, buf, bytes);
       // the piece before this one has left its buffer: the next row into it
@@ -560,22 +594,14 @@ sv_status launch_adjust(AdjustArgs A, bool aligned, cudaStream_t st) {
   return launch_status();
 }
 
-}  // namespace
-}  // namespace sv
-
-using namespace sv;
-
-extern "C" sv_status logit_adjust(const void* logits, int64_t in_req_stride,
-                                  int64_t in_row_stride, sv_dtype dtype,
-                                  const int32_t* history, const int32_t* hist_len,
-                                  const int32_t* prompt_len, int L_max,
-                                  const int32_t* draft_tokens, const int32_t* num_draft,
-                                  const float* repetition, const float* presence,
-                                  const float* frequency, const int32_t* bias_tokens,
-                                  const float* bias_values, int n_bias,
-                                  const uint32_t* allowed, int B, int P, int V, void* out,
-                                  int64_t out_req_stride, int64_t out_row_stride,
-                                  sv_stream_t stream) {
+sv_status adjust(const void* logits, int64_t in_req_stride, int64_t in_row_stride, sv_dtype dtype,
+                 const int32_t* history, const int32_t* hist_len, const int32_t* prompt_len,
+                 int L_max, const int32_t* draft_tokens, const int32_t* num_draft,
+                 const float* repetition, const float* presence, const float* frequency,
+                 const int32_t* bias_tokens, const float* bias_values, int n_bias,
+                 const uint32_t* allowed, int B, int P, int V, void* out,
+                 int64_t out_req_stride, int64_t out_row_stride,
+                 uint64_t wait_ns, unsigned int more_arrivals, sv_stream_t stream) {
   if (B < 0 || P < 1 || V < 1 || L_max < 0 || n_bias < 0) return SV_ERR_INVALID_ARG;
   if (dtype != SV_F32 && dtype != SV_BF16) return SV_ERR_INVALID_ARG;
   if (P > SV_MAX_K + 1 || L_max >= (1 << 30)) return SV_ERR_UNSUPPORTED;
@@ -603,7 +629,7 @@ extern "C" sv_status logit_adjust(const void* logits, int64_t in_req_stride,
   AdjustArgs A{logits, out, in_req_stride, in_row_stride, out_req_stride, out_row_stride,
                history, hist_len, prompt_len, draft_tokens, num_draft, repetition, presence,
                frequency, bias_tokens, bias_values, allowed, L_max, n_bias, B, P, V,
-               (V + 31) / 32, 13};
+               (V + 31) / 32, 13, wait_ns, more_arrivals};
   const int E = 16 / (int)eb;
   const bool aligned = aligned_to(logits, 16) && aligned_to(out, 16) && V % E == 0 &&
                        (P == 1 || (in_row_stride % E == 0 && out_row_stride % E == 0)) &&
@@ -611,4 +637,42 @@ extern "C" sv_status logit_adjust(const void* logits, int64_t in_req_stride,
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return dtype == SV_F32 ? launch_adjust<float>(A, aligned, st)
                          : launch_adjust<__nv_bfloat16>(A, aligned, st);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" sv_status logit_adjust(const void* logits, int64_t in_req_stride,
+                                  int64_t in_row_stride, sv_dtype dtype,
+                                  const int32_t* history, const int32_t* hist_len,
+                                  const int32_t* prompt_len, int L_max,
+                                  const int32_t* draft_tokens, const int32_t* num_draft,
+                                  const float* repetition, const float* presence,
+                                  const float* frequency, const int32_t* bias_tokens,
+                                  const float* bias_values, int n_bias,
+                                  const uint32_t* allowed, int B, int P, int V, void* out,
+                                  int64_t out_req_stride, int64_t out_row_stride,
+                                  sv_stream_t stream) {
+  return adjust(logits, in_req_stride, in_row_stride, dtype, history, hist_len, prompt_len, L_max,
+                draft_tokens, num_draft, repetition, presence, frequency, bias_tokens,
+                bias_values, n_bias, allowed, B, P, V, out, out_req_stride, out_row_stride,
+                kWaitLimitNs, 0u, stream);
+}
+
+extern "C" sv_status logit_adjust_wait_selftest(
+    const void* logits, int64_t in_req_stride, int64_t in_row_stride, sv_dtype dtype,
+    const int32_t* history, const int32_t* hist_len, const int32_t* prompt_len,
+    int L_max, const int32_t* draft_tokens, const int32_t* num_draft,
+    const float* repetition, const float* presence, const float* frequency,
+    const int32_t* bias_tokens, const float* bias_values, int n_bias,
+    const uint32_t* allowed, int B, int P, int V, void* out,
+    int64_t out_req_stride, int64_t out_row_stride, unsigned int wait_us,
+    sv_stream_t stream) {
+  if (wait_us < 1000 || wait_us > 100000) return SV_ERR_INVALID_ARG;
+  return adjust(logits, in_req_stride, in_row_stride, dtype, history, hist_len, prompt_len, L_max,
+                draft_tokens, num_draft, repetition, presence, frequency, bias_tokens,
+                bias_values, n_bias, allowed, B, P, V, out, out_req_stride, out_row_stride,
+                (uint64_t)wait_us * 1000ull, 1u, stream);
 }
