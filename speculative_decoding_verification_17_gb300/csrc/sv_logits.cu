@@ -325,11 +325,11 @@ __device__ __noinline__ void give_up(const AdjustArgs& A, uint64_t* full, int i,
                                      T* out) {
   using X = Vec<T>;
   if (threadIdx.x == 0) {
-    const int issued = kAdjStages + (i > 1 ? i - 1 : 0);
-    for (int r = i; r < issued && r < rows; ++r)
+    for (int r = i; r < kAdjStages + i && r < rows; ++r)
       mbar_wait(&full[r % kAdjStages], (uint32_t)(r / kAdjStages) & 1u, A.wait_ns);
-    bulk_wait_read<0>();
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // (row i is on its way out)
   }
+  __syncthreads();
   const float nan[8] = {NAN, NAN, NAN, NAN, NAN, NAN, NAN, NAN};
   const uint4 v = X::pack(reinterpret_cast<const float(&)[X::E]>(nan));
 #pragma unroll 1
@@ -492,11 +492,7 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    // (a thread ahead may have lost a later row: that one's barrier tells all)
-    if (__builtin_expect(*(volatile int*)&lost_row <= i, 0)) {
-      give_up<T>(A, full, i, rows, nvec, out);
-      return;
-    }
+    const int lost = *(volatile int*)&lost_row;
     if (tid == 0) {
       bulk_s2g(out + i * A.out_row, buf, bytes);
       // the piece before this one has left its buffer: the next row into it
@@ -507,6 +503,11 @@ __global__ void __launch_bounds__(kAdjThreads) adjust_kernel(const AdjustArgs A)
         mbar_arrive_expect_tx(&full[sb], bytes);
         bulk_g2s(ring + sb * stage, in + next * A.in_row, bytes, &full[sb]);
       }
+    }
+    // (a thread ahead may have lost a later row: that one's barrier tells all)
+    if (__builtin_expect(lost <= i, 0)) {
+      give_up<T>(A, full, i, rows, nvec, out);
+      return;
     }
     if (++s == kAdjStages) {
       s = 0;
