@@ -12,14 +12,14 @@
 // Bound: reading K and V once. 64 KiB per tile of D = 128 at this card's bandwidth is 2800
 // clocks of one SM; the instructions of a tile take 256 + 512 clocks (the operand read from
 // shared memory bounds a narrow instruction), the softmax about 1000. Measured, in graph
-// replays, of the 6782 GB/s a copy reaches (D = 128, 16-bit):
-//   1 token of 64 requests, 200 .. 8192 keys, 32 / 8 heads   567 MB   94.5 us  5998 GB/s  88 %
-//   6 positions of 32, 500 .. 16384 keys, 64 / 8 heads       570 MB  103.5 us  5512 GB/s  81 %
-//   9 positions of 2, 100001 .. 131072 keys, 32 / 8 heads   1052 MB  163.4 us  6438 GB/s  95 %
-//   5 positions of 16, window 4096, 16 / 8 heads of 256      214 MB   47.0 us  4547 GB/s  67 %
-//   1 token of 1 request of 777 keys                         3.2 MB   12.9 us  (latency)
-//   key weights, 6 positions of 64, 1000 .. 8192 keys        463 MB   87.2 us  5307 GB/s  78 %
-//   key weights, 1 request of 1501 keys                      3.2 MB    7.9 us  (latency)
+// replays, of the 6782 GB/s a copy reaches (D = 128, 16-bit; boxes differ by 3 %):
+//   1 token of 64 requests, 200 .. 8192 keys, 32 / 8 heads   567 MB   95.1 us  5959 GB/s  88 %
+//   6 positions of 32, 500 .. 16384 keys, 64 / 8 heads       570 MB  104.3 us  5465 GB/s  81 %
+//   9 positions of 2, 100001 .. 131072 keys, 32 / 8 heads   1052 MB  167.7 us  6275 GB/s  93 %
+//   5 positions of 16, window 4096, 16 / 8 heads of 256      214 MB   47.3 us  4520 GB/s  67 %
+//   1 token of 1 request of 777 keys                         3.2 MB   13.0 us  (latency)
+//   key weights, 6 positions of 64, 1000 .. 8192 keys        463 MB   85.4 us  5420 GB/s  80 %
+//   key weights, 1 request of 1501 keys                      3.2 MB    8.2 us  (latency)
 // About 10 us of a call do not depend on its size: the launch, the work list's sums (2.5 us) and
 // the join (4 us). Pages of 16 slots, copied in eight pieces per unit, reach 82 % where pages of
 // 64 reach 88 %, pages of 8 reach 69 %.
@@ -48,7 +48,8 @@
 // that looks up the pages and starts the tiled copies, and a thread each that issues the matrix
 // instructions; 8 warps do the softmax and the outputs. S is double buffered: the scores of tile
 // t+1 are computed while tile t is in the softmax. The key copies' warp alone walks the work list
-// and hands the pieces to the others through a queue. The roles' loops are kept rolled and their
+// and hands the pieces with tiles to the others through a queue (write_rest does the rest at the
+// end). The roles' loops are kept rolled and their
 // rare parts out of line: all five run at once, and at 139 KB of code (79 KB now) their loops
 // pushed one another out of the instruction cache, which cost 20 to 30 % of every case.
 //
@@ -117,8 +118,8 @@ struct TileShape {
   // with its own score, weight and output buffers, so one team's end of a piece (its last
   // product, its output, the next piece's tables) passes under the other's tiles; of wider
   // tiles each group takes half of the columns and there is one team (6 positions of 64 requests,
-  // 24 of 32 columns: 98 us with one team, 111 us with two, whose buffers shorten the rings). In the key weights each
-  // group takes every other tile.
+  // 24 of 32 columns: 98 us with one team, 111 us with two, whose buffers shorten the rings). In
+  // the key weights each group takes every other tile.
   static constexpr int Teams = !kWeigh && N == 16 ? 2 : 1;
   static constexpr int SoftWarps = 8;
   static constexpr int SoftThreads = 32 * SoftWarps;

@@ -18,10 +18,10 @@
 // Rows whose V or addresses do not allow 16-byte copies take a second kernel, element by element.
 //
 // Measured in graph replays, of the 6782 GB/s a copy reaches: 512 requests x 9 rows of 128256 bf16
-// with histories of 8192, 64 biases and masks 374 us (2098 MB, 83 %; the scan of the histories,
+// with histories of 8192, 64 biases and masks 377 us (2098 MB, 82 %; the scan of the histories,
 // which each of a request's 32 chunks repeats, is about 50 us of it, but shared by clusters of 2, 4
 // or 8 CTAs, over distributed shared memory, the call took 467, 578 and 607 us); 64 x 6 rows of 32000 bf16 with masks
-// 14.2 us (46 MB); one request of 5 rows of 50257 fp32 5.5 us.
+// 14.2 us (46 MB); one request of 5 rows of 50257 fp32 5.3 us.
 
 #include <cstdint>
 
