@@ -6,6 +6,8 @@ import sys
 
 import torch
 
+import speculative_decoding_verification_17_gb300 as sv
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PKG = "speculative_decoding_verification_17_gb300"
 
@@ -23,6 +25,7 @@ except RuntimeError as e:
 
 def test_the_verify_calls_do_not_need_a_host_compiler_for_the_others(tmp_path):
     """A copy of the package with the library built, no module and no compiler for it."""
+    sv.library()
     for name in (PKG, "include"):
         shutil.copytree(os.path.join(ROOT, name), tmp_path / name,
                         ignore=shutil.ignore_patterns("_calls*", "__pycache__"))
