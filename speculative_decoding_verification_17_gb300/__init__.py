@@ -42,6 +42,16 @@ The paged key-value cache around a verify (C ABI in ``include/specverify_kv.h``)
 - :func:`attention_weight_sum` — the weight the accepted positions gave each cached key.
 - :func:`kv_cache_evict`       — keeps the most recent and the heaviest keys.
 
+The same cache in 8 bits (C ABI in ``include/specverify_kv8.h``):
+
+- :func:`kv_cache_append_q8` — rounds new keys and values to 8 bits, a scale per block and head.
+- :func:`paged_attention_q8` — attention of the new positions over it.
+
+What a step does ahead of its attention (C ABI in ``include/specverify_step.h``):
+
+- :func:`kv_page_map`    — pages and slots of the new positions, from the requests' lengths.
+- :func:`qk_norm_rotate` — the norm of every query and key head, and its rotation by position.
+
 Workspaces: pass ``workspace=`` (a uint8 CUDA tensor of at least the size the matching
 ``*_workspace`` query returns, 256-byte aligned, not shared by calls in flight at the same
 time; it needs no initialisation), or let the binding keep one cached per (device, stream,
@@ -70,7 +80,8 @@ __all__ = [
     "conformal_quantile", "conformal_admit_workspace", "conformal_admit", "gate_points_dict",
     "ReadyCacheTable", "ready_cache_record_workspace", "SV_CACHE_VALID", "SV_CACHE_DECODED",
     "SV_CACHE_CONSUMED", "CACHE_STATS", "SV_F16", "logit_adjust", "paged_attention_workspace",
-    "paged_attention", "attention_weight_sum", "kv_cache_evict",
+    "paged_attention", "attention_weight_sum", "kv_cache_evict", "kv_page_map", "qk_norm_rotate",
+    "kv_cache_append_q8", "paged_attention_q8_workspace", "paged_attention_q8",
 ]
 
 SV_F32 = 0
@@ -865,3 +876,240 @@ def kv_cache_evict(k_cache, v_cache, page_table, seq_len, weights, budget: int, 
         out_len.data_ptr(), out_index.data_ptr(), out_weights.data_ptr(), h),
         "kv_cache_evict")
     return out_len, out_index, out_weights
+
+
+# ------------------------------------------------------------------------------ 8-bit cache
+def _check_codes(k_cache, v_cache, k_scale, v_scale, like):
+    """Checks a cache of e4m3 codes [pages, page_size, Hkv, D] and its scales [pages, blocks, Hkv];
+    returns its two pools and the slots of a block."""
+    _check_strided("k_cache", k_cache, torch.float8_e4m3fn, None, like.device)
+    if k_cache.ndim != 4:
+        raise ValueError("k_cache must have shape [pages, page_size, Hkv, D]")
+    pages, page_size, Hkv, _ = k_cache.shape
+    pools = [_kv_pool("k_cache", k_cache, k_cache), _kv_pool("v_cache", v_cache, k_cache)]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("v_cache must have k_cache's shape")
+    blocks = k_scale.shape[1] if k_scale.ndim == 3 else 0
+    if blocks < 1 or page_size % blocks:
+        raise ValueError("k_scale must have shape [pages, page_size / block, Hkv]")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        _check_cuda(name, t, torch.float32, (pages, blocks, Hkv), like.device)
+    return *pools, page_size // blocks
+
+
+def kv_cache_append_q8(k, v, slots, k_cache, v_cache, k_scale, v_scale, *, stream=None):
+    """Rounds new keys and values, [T, Hkv, D] or [B, P, Hkv, D] (rows one stride apart), to 8 bits
+    and puts row t into slot ``slots[t]`` (int64, page * page_size + slot; -1: left out) of the pools
+    k_cache and v_cache, float8_e4m3fn views [pages, page_size, Hkv, D], with scales k_scale and
+    v_scale [pages, page_size / block, Hkv] fp32. All four are updated in place. Rows of one block
+    stand side by side in ascending order of slots."""
+    h = _raw_stream(stream, k)
+    status = (_native._calls or _native.calls()).append(k, v, slots, k_cache, v_cache, k_scale,
+                                                        v_scale, h)
+    if status is not None:
+        if status:
+            raise SVError(status, "kv_cache_append_q8")
+        return
+    # an argument that does not fit: the checks one by one
+    dtype = _KV_DTYPE.get(k.dtype)
+    if dtype is None:
+        raise TypeError(f"keys and values must be bfloat16 or float16, got {k.dtype}")
+    if k.ndim not in (3, 4):
+        raise ValueError("k must have shape [T, Hkv, D] or [B, P, Hkv, D]")
+    strides = []
+    for name, x in (("k", k), ("v", v)):
+        _check_strided(name, x, k.dtype, k.shape, k.device)
+        if x.ndim == 4 and x.shape[0] > 1 and x.shape[1] > 1 and \
+                x.stride(0) != x.shape[1] * x.stride(1):
+            raise ValueError(f"the rows of {name} must lie one stride apart")
+        strides.append(x.stride(0) if x.ndim == 4 and x.shape[1] == 1 else x.stride(-3))
+    if slots is None:
+        raise TypeError("slots must be a CUDA tensor")
+    _check_cuda("slots", slots, torch.int64, k.shape[:-2], k.device)
+    kp, vp, block = _check_codes(k_cache, v_cache, k_scale, v_scale, k)
+    pages, page_size, Hkv, D = k_cache.shape
+    if k.shape[-2:] != (Hkv, D):
+        raise ValueError("k must have the cache's heads and width")
+    _ok(library().kv_cache_append_q8(
+        _pack_shape(dtype, 1, 1, 1, Hkv, D, page_size, pages, 1), slots.numel(), k.data_ptr(),
+        strides[0], k.stride(-2), v.data_ptr(), strides[1], v.stride(-2), slots.data_ptr(), kp, vp,
+        k_scale.data_ptr(), v_scale.data_ptr(), block, h), "kv_cache_append_q8")
+
+
+def paged_attention_q8_workspace(B: int, P: int, Hq: int, dtype, k_cache, page_table) -> int:
+    pages, page_size, Hkv, D = k_cache.shape
+    return int(library().paged_attention_q8_workspace(
+        _pack_shape(_KV_DTYPE[dtype], B, P, Hq, Hkv, D, page_size, pages, page_table.shape[1])))
+
+
+def paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_len, *,
+                       num_draft=None, scale=None, softcap: float = 0.0, window: int = 0,
+                       slopes=None, out=None, out_lse=None, want_lse: bool = True, workspace=None,
+                       stream=None):
+    """paged_attention over a cache in 8 bits: k_cache and v_cache are float8_e4m3fn views [pages,
+    page_size, Hkv, D] with scales k_scale and v_scale [pages, page_size / block, Hkv] fp32; q and
+    out are bfloat16 or float16. Returns (out [B, P, Hq, D], lse [B, P, Hq] fp32 or None)."""
+    if out is None:
+        out = _made(torch.empty, q.shape, q.dtype, q.device, stream)
+    if out_lse is None and want_lse:
+        out_lse = _made(torch.empty, q.shape[:3], torch.float32, q.device, stream)
+    h = _raw_stream(stream, q)
+    ws = workspace
+    if ws is None:
+        ws = _ws_cache.get(("attention8", q.get_device(), h))
+        if ws is not None and _capturing(h, stream):
+            ws = None
+    fast = (_native._calls or _native.calls()).attention8
+    status = fast(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window,
+                  v_cache, k_scale, v_scale, out, out_lse, ws, h)
+    if status is not None and status < 0 and workspace is None:
+        # a first call on this stream, one that needs more than the earlier ones did, or a captured one
+        ws = _workspace("attention8", -status - 1, q.device,
+                        stream or torch.cuda.current_stream(q.device))
+        if _ws_cache.get(("attention8", q.device, h)) is ws:
+            _ws_cache["attention8", q.get_device(), h] = ws
+        status = fast(q, k_cache, page_table, seq_len, num_draft, slopes, scale, softcap, window,
+                      v_cache, k_scale, v_scale, out, out_lse, ws, h)
+    if status is not None:
+        if status:
+            raise SVError(status if status > 0 else 3, "paged_attention_q8")
+        return out, out_lse
+    # an argument that does not fit: the checks one by one
+    B, P, Hq, D = q.shape
+    dev = q.device
+    dtype = _KV_DTYPE.get(q.dtype)
+    if dtype is None:
+        raise TypeError(f"queries must be bfloat16 or float16, got {q.dtype}")
+    _check_strided("q", q)
+    kp, vp, block = _check_codes(k_cache, v_cache, k_scale, v_scale, q)
+    pages, page_size, Hkv, d = k_cache.shape
+    if d != D:
+        raise ValueError("k_cache must have q's width")
+    _check_cuda("page_table", page_table, torch.int32, (B, page_table.shape[-1]), dev)
+    _check_cuda("seq_len", seq_len, torch.int32, (B,), dev)
+    _check_cuda("num_draft", num_draft, torch.int32, (B,), dev)
+    _check_cuda("slopes", slopes, torch.float32, (Hq,), dev)
+    _check_cuda("out", out, q.dtype, (B, P, Hq, D), dev)
+    _check_cuda("out_lse", out_lse, torch.float32, (B, P, Hq), dev)
+    _check_cuda("workspace", workspace, None, None, dev)
+    shape = _pack_shape(dtype, B, P, Hq, Hkv, D, page_size, pages, page_table.shape[1])
+    L = library()
+    if workspace is None:
+        ws = _workspace("attention8", L.paged_attention_q8_workspace(shape), dev,
+                        stream or torch.cuda.current_stream(dev))
+    rule = _pack_rule(D ** -0.5 if scale is None else scale, softcap, window, _ptr(slopes) or 0)
+    a, b, c, _ = q.stride()
+    _ok(L.paged_attention_q8(
+        shape, rule, q.data_ptr(), a, b, c, kp, vp, k_scale.data_ptr(), v_scale.data_ptr(), block,
+        page_table.data_ptr(), seq_len.data_ptr(), _ptr(num_draft), out.data_ptr(), _ptr(out_lse),
+        ws.data_ptr(), ws.numel() * ws.element_size(), h), "paged_attention_q8")
+    return out, out_lse
+
+
+# ------------------------------------------------------------------------------ ahead of a step
+def kv_page_map(page_table, old_len, seq_len, num_new, ring, ring_state, page_size: int,
+                num_pages: int, *, P: int | None = None, rows: int | None = None, out_slots=None,
+                out_positions=None, out_len=None, out_first=None, out_state=None, stream=None):
+    """Pages and slots of the new positions. Request r holds the pages of ``old_len`` tokens in its
+    row of page_table [B, max_pages] int32 (updated in place) and is to have ``seq_len`` tokens, the
+    last ``num_new`` of them new: it takes the pages it lacks from the front of ``ring`` (int32, the
+    free pages, updated in place; ``ring_state`` [2] int32 holds the first one's place and how many
+    there are) or gives pages back to its end. Rows are [B, P], or packed in ``rows`` rows.
+    Returns (slots [B, P] or [rows] int64, positions int32 likewise, both -1 in rows of no new
+    token; out_len [B] int32: seq_len, old_len where no pages were left, -1 for a data error;
+    first rows [B + 1] int32; the ring's new state [2] int32)."""
+    if out_slots is None:
+        if (P is None) == (rows is None):
+            raise ValueError("give P (rows per request) or rows (packed)")
+        size = (page_table.shape[0], P) if rows is None else (rows,)
+        out_slots = _made(torch.empty, size, torch.int64, page_table.device, stream)
+    B = page_table.shape[0]
+    made = [_made(torch.empty, size, torch.int32, page_table.device, stream) if t is None else t
+            for t, size in ((out_positions, out_slots.shape), (out_len, (B,)),
+                            (out_first, (B + 1,)), (out_state, (2,)))]
+    h = _raw_stream(stream, page_table)
+    status = (_native._calls or _native.calls()).page_map(
+        page_table, old_len, seq_len, num_new, ring, ring_state, page_size, num_pages, out_slots,
+        *made, h)
+    if status is not None:
+        if status:
+            raise SVError(status, "kv_page_map")
+        return out_slots, *made
+    # an argument that does not fit: the checks one by one
+    dev = page_table.device
+    padded = out_slots.ndim == 2
+    if out_slots.ndim not in (1, 2) or padded and (out_slots.shape[0] != B or out_slots.shape[1] < 1):
+        raise ValueError("slots must have shape [B, P] or [rows]")
+    for name, t, dtype, shape in (
+            ("page_table", page_table, torch.int32, (B, page_table.shape[-1])),
+            ("old_len", old_len, torch.int32, (B,)), ("seq_len", seq_len, torch.int32, (B,)),
+            ("num_new", num_new, torch.int32, (B,)), ("ring", ring, torch.int32, (ring.numel(),)),
+            ("ring_state", ring_state, torch.int32, (2,)),
+            ("out_slots", out_slots, torch.int64, out_slots.shape),
+            ("out_positions", made[0], torch.int32, out_slots.shape),
+            ("out_len", made[1], torch.int32, (B,)), ("out_first", made[2], torch.int32, (B + 1,)),
+            ("out_state", made[3], torch.int32, (2,))):
+        if t is None:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        _check_cuda(name, t, dtype, shape, dev)
+    _ok(library().kv_page_map(
+        B, page_size, num_pages, page_table.data_ptr(), page_table.shape[1], old_len.data_ptr(),
+        seq_len.data_ptr(), num_new.data_ptr(), ring.data_ptr(), ring.numel(),
+        ring_state.data_ptr(), out_slots.shape[1] if padded else 0, out_slots.numel(),
+        out_slots.data_ptr(), *(t.data_ptr() for t in made), h), "kv_page_map")
+    return out_slots, *made
+
+
+def qk_norm_rotate(q, k, positions, inv_freq=None, *, q_weight=None, k_weight=None,
+                   eps: float = 1e-6, norm: bool = True, interleaved: bool = False, out_q=None,
+                   out_k=None, stream=None):
+    """Divides every head of q [..., Hq, D] and k [..., Hkv, D] by its root mean square, multiplies
+    by the weights [D] (fp32 or q's type), and rotates its first 2 * len(inv_freq) components by
+    position * inv_freq (fp32 or fp64): component i with i + R/2, or 2i with 2i + 1 where
+    ``interleaved``. ``positions`` [...] int32; rows at a negative one are left as they are.
+    Returns (out_q, out_k), which may be q and k themselves."""
+    if out_q is None:
+        out_q = _made(torch.empty, q.shape, q.dtype, q.device, stream)
+    if out_k is None:
+        out_k = _made(torch.empty, k.shape, k.dtype, k.device, stream)
+    h = _raw_stream(stream, q)
+    status = (_native._calls or _native.calls()).rotate(
+        q, k, positions, inv_freq, q_weight, k_weight, eps, interleaved, norm, out_q, out_k, h)
+    if status is not None:
+        if status:
+            raise SVError(status, "qk_norm_rotate")
+        return out_q, out_k
+    # an argument that does not fit: the checks one by one
+    dtype = _KV_DTYPE.get(q.dtype)
+    if dtype is None:
+        raise TypeError(f"queries must be bfloat16 or float16, got {q.dtype}")
+    if q.ndim not in (3, 4) or k.ndim != q.ndim:
+        raise ValueError("q and k must have shape [T, heads, D] or [B, P, heads, D]")
+    lead, D, dev = q.shape[:-2], q.shape[-1], q.device
+    _check_strided("q", q)
+    _check_strided("k", k, q.dtype, (*lead, k.shape[-2], D), dev)
+    _check_strided("out_q", out_q, q.dtype, q.shape, dev)
+    _check_strided("out_k", out_k, q.dtype, k.shape, dev)
+    if positions is None:
+        raise TypeError("positions must be a CUDA tensor")
+    _check_cuda("positions", positions, torch.int32, lead, dev)
+    wide = inv_freq is not None and inv_freq.dtype == torch.float64
+    half = 0 if inv_freq is None else inv_freq.numel()
+    _check_cuda("inv_freq", inv_freq, torch.float64 if wide else torch.float32, (half,), dev)
+    w = q_weight if q_weight is not None else k_weight
+    w32 = w is not None and w.dtype == torch.float32
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _check_cuda(name, t, torch.float32 if w32 else q.dtype, (D,), dev)
+    rows = []
+    for x, out, weight in ((q, out_q, q_weight), (k, out_k, k_weight)):
+        rows.append(_native.HeadRows(
+            x.data_ptr(), x.stride(0) if x.ndim == 4 else 0, x.stride(-3), x.stride(-2),
+            out.data_ptr(), out.stride(0) if x.ndim == 4 else 0, out.stride(-3), out.stride(-2),
+            x.shape[-2], _ptr(weight)))
+    _ok(library().qk_norm_rotate(
+        dtype, lead[0] if q.ndim == 4 else 1, lead[-1], D, 2 * half, ctypes.byref(rows[0]),
+        ctypes.byref(rows[1]), int(w32), positions.data_ptr(), _ptr(inv_freq), int(wide),
+        int(bool(norm)), float(eps), int(bool(interleaved)), h), "qk_norm_rotate")
+    return out_q, out_k

@@ -1,5 +1,5 @@
 """Build and load ``libspecverify.so``, the C-ABI library of the verify step, and ``_calls``, the
-checks and marshalling of the calls on logits and on the paged cache.
+checks and marshalling of the calls on logits, on the paged cache and around its attention.
 
 The library is compiled in-tree from ``csrc/`` for sm_103a only (one ``-gencode``), one
 nvcc process per translation unit in parallel, and linked against the static CUDA runtime
@@ -161,7 +161,8 @@ def calls():
             spec.loader.exec_module(m)
             m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 L.logit_adjust, L.paged_attention, L.paged_attention_workspace,
-                L.attention_weight_sum, L.kv_cache_evict)))
+                L.attention_weight_sum, L.kv_cache_evict, L.kv_page_map, L.qk_norm_rotate,
+                L.kv_cache_append_q8, L.paged_attention_q8, L.paged_attention_q8_workspace)))
             _calls = m
     return _calls
 
@@ -185,6 +186,15 @@ class ScoreRule(ctypes.Structure):
 
     _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int),
                 ("slopes", ctypes.c_void_p)]
+
+
+class HeadRows(ctypes.Structure):
+    """sv_head_rows"""
+
+    _fields_ = [("data", ctypes.c_void_p), ("req", ctypes.c_int64), ("row", ctypes.c_int64),
+                ("head", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_req", ctypes.c_int64),
+                ("out_row", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("heads", ctypes.c_int), ("weight", ctypes.c_void_p)]
 
 
 def _declare(L):
@@ -264,3 +274,18 @@ def _declare(L):
     L.kv_cache_evict.restype = I
     L.kv_cache_evict.argtypes = [shape, pool, pool, P, P, P, q, I, I, pool, pool, I, P, I, P, P,
                                  P, P]
+    L.kv_page_map.restype = I
+    L.kv_page_map.argtypes = [I, I, I, P, I, P, P, P, P, I, P, I, I, P, P, P, P, P, P]
+    rows = P
+    L.qk_norm_rotate.restype = I
+    L.qk_norm_rotate.argtypes = [I, I, I, I, I, rows, rows, I, P, P, I, I, F, I, P]
+    L.kv_cache_append_q8.restype = I
+    L.kv_cache_append_q8.argtypes = [shape, I, P, q, q, P, q, q, P, pool, pool, P, P, I, P]
+    L.paged_attention_q8_workspace.restype = Z
+    L.paged_attention_q8_workspace.argtypes = [shape]
+    L.paged_attention_q8.restype = I
+    L.paged_attention_q8.argtypes = [shape, rule, P, q, q, q, pool, pool, P, P, I, P, P, P, P, P,
+                                     P, Z, P]
+    L.paged_attention_q8_wait_selftest.restype = I
+    L.paged_attention_q8_wait_selftest.argtypes = [*L.paged_attention_q8.argtypes[:-1],
+                                                   ctypes.c_uint, P]

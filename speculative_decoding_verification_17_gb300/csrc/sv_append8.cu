@@ -1,0 +1,259 @@
+// sv_append8.cu — new keys and values into a paged cache of 8 bits, with a scale for each block of
+// tokens and kv head.
+//
+// Mathematics: scale = the smallest power of two that brings the block's largest magnitude within
+// 448, or the block's scale so far where earlier tokens hold it up; code = x / scale, rounded to e4m3.
+// A power of two is read off the bits of the largest magnitude, divides exactly, and re-rounds
+// earlier codes exactly but for those that become subnormal.
+//
+// Work: rows of one block stand side by side, so the first of them (its predecessor is in another
+// block) finds the others. A warp takes one such run for one head of keys or values: it reads the
+// run's rows once for the largest magnitude and codes them from registers, or again from L2 where
+// there are more than eight loads of them. No two warps share a block.
+//
+// Bound: 3 bytes an element (2 read, 1 written).
+#include <cstdint>
+
+#include <cuda_fp8.h>
+
+#include "specverify_kv8.h"
+#include "sv_kv8.h"
+#include "sv_kv_tiles.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kAppThreads = 256, kAppWarps = kAppThreads / 32;
+
+struct AppendArgs {
+  const uint16_t* x[2];  // keys, values
+  int64_t row[2], head[2];
+  unsigned char* pool[2];
+  int64_t page[2], token[2], pool_head[2];
+  float* scale[2];
+  const int64_t* slots;
+  int64_t num_slots;  // of the pools
+  int rows, Hkv, log_page, log_block;
+};
+
+// Eight numbers as e4m3 codes; what is not finite, or too large for any scale, becomes NaN.
+template <bool kBf16>
+__device__ __forceinline__ uint2 code8(const uint4& v, float scale, float inverse, bool exact,
+                                       uint32_t limit) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float2 f = unpack16<kBf16>(w[k]);
+    if (exact) {
+      f.x *= inverse;
+      f.y *= inverse;
+    } else {
+      f.x = __fdiv_rn(f.x, scale);
+      f.y = __fdiv_rn(f.y, scale);
+    }
+    if ((w[k] & 0x7fffu) > limit) f.x = __uint_as_float(0x7fc00000u);
+    if ((w[k] >> 16 & 0x7fffu) > limit) f.y = __uint_as_float(0x7fc00000u);
+    out[k >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << 16 * (k & 1);
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendArgs A) {
+  constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
+  constexpr int kKeep = 8;                           // loads of a run kept in registers
+  // the largest finite magnitude that a scale reaches (448 * 2^40 in bf16)
+  constexpr uint32_t kLimit = kBf16 ? 0x57e0u : 0x7bffu;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int block = 1 << A.log_block;
+  const int t0 = blockIdx.x * 32;
+  // the block of a row's slot, -1 for a row that is left out
+  auto slot_of = [&](int t) {
+    const int64_t s = t >= 0 && t < A.rows ? __ldg(A.slots + t) : -1;
+    return s < A.num_slots ? s : -1;
+  };
+  const int64_t slot = slot_of(t0 + lane), before = slot_of(t0 + lane - 1);
+  uint32_t starts = __ballot_sync(0xffffffffu, slot >= 0 && (before < 0 || slot >> A.log_block != before >> A.log_block));
+  const int runs = __popc(starts), units = runs * A.Hkv * 2;
+  int taken = -1, cur = -1;  // the run at hand
+  int64_t first = 0;
+  int n = 0;
+  bool ordered = true;
+#pragma unroll 1
+  for (int u = blockIdx.y * kAppWarps + warp; u < units; u += gridDim.y * kAppWarps) {
+    const int run = u / (2 * A.Hkv), h = (u - run * 2 * A.Hkv) >> 1, which = u & 1;
+    if (run != taken) {
+      // the run's first row, its rows and whether their slots ascend
+      taken = run;
+      cur = __fns(starts, 0, run + 1);
+      first = __shfl_sync(0xffffffffu, slot, cur);
+      n = 0;
+      ordered = true;
+#pragma unroll 1
+      for (int i0 = 0; i0 <= block; i0 += 32) {
+        const int t = t0 + cur + i0 + lane;
+        const int64_t s = slot_of(t), p = slot_of(t - 1);
+        const bool in = s >= 0 && s >> A.log_block == first >> A.log_block;
+        const uint32_t all = __ballot_sync(0xffffffffu, in);
+        const int more = all == 0xffffffffu ? 32 : __ffs(~all) - 1;
+        ordered = ordered && !__any_sync(0xffffffffu, in && lane < more && (i0 + lane > 0) && s <= p);
+        n += more;
+        if (more < 32) break;
+      }
+      ordered = ordered && n <= block;
+    }
+    const int64_t page = first >> A.log_page;
+    const int at = (int)(first & ((1 << A.log_page) - 1));
+    float* scale_at = A.scale[which] + (page * (1 << (A.log_page - A.log_block)) + (at >> A.log_block)) * A.Hkv + h;
+    if (!ordered) {
+      if (lane == 0) *scale_at = __uint_as_float(0x7fc00000u);
+      continue;
+    }
+    const int earlier = at & (block - 1);  // slots of the block below the first new one
+    const float old = earlier ? *scale_at : 0.0f;
+    const uint16_t* x = A.x[which] + (int64_t)(t0 + cur) * A.row[which] + h * A.head[which] + lane % kLanes * 8;
+    const int mine = lane / kLanes;  // the lane's row of a load
+    auto load = [&](int i) {
+      return i < n ? *reinterpret_cast<const uint4*>(x + i * A.row[which]) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 keep[kKeep];
+    uint32_t top = 0;
+    auto raise = [&](const uint4& v) {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = w[k] & 0x7fffu, hi = w[k] >> 16 & 0x7fffu;
+        top = max(top, max(lo > kLimit ? 0u : lo, hi > kLimit ? 0u : hi));
+      }
+    };
+#pragma unroll
+    for (int s = 0; s < kKeep; ++s) keep[s] = load(s * kPer + mine);
+#pragma unroll
+    for (int s = 0; s < kKeep; ++s) raise(keep[s]);
+#pragma unroll 1
+    for (int s0 = kKeep; s0 * kPer < n; s0 += kKeep) {
+      uint4 v[kKeep];
+#pragma unroll
+      for (int s = 0; s < kKeep; ++s) v[s] = load((s0 + s) * kPer + mine);
+#pragma unroll
+      for (int s = 0; s < kKeep; ++s) raise(v[s]);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 448 = 1.75 * 2^8
+    const uint32_t bits = __float_as_uint(unpack16<kBf16>(top).x);
+    const int e = max(-40, (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u));
+    float scale = __uint_as_float((uint32_t)(127 + e) << 23);
+    unsigned char* pool = A.pool[which] + page * A.page[which] + h * A.pool_head[which];
+    const int64_t token = A.token[which];
+    if (earlier) {
+      if (!(old >= 0.0f && old <= 1099511627776.0f)) {
+        scale = __uint_as_float(0x7fc00000u);
+      } else if (old >= scale) {
+        scale = old;
+      } else {
+        // earlier codes, four at a time (those of a scale of 0 stand for 0, and become 0)
+        const float ratio = old / scale;
+        unsigned char* p = pool + (int64_t)(at - earlier) * token;
+#pragma unroll 4
+        for (int q = lane; q < earlier * (D / 4); q += 32) {
+          uint32_t* w = reinterpret_cast<uint32_t*>(p + (int64_t)(q / (D / 4)) * token + q % (D / 4) * 4);
+          const uint32_t v = *w;
+          uint32_t out = 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v >> 16 * k), __NV_E4M3);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+            out |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(f.x * ratio, f.y * ratio),
+                                                      __NV_SATFINITE, __NV_E4M3) << 16 * k;
+          }
+          *w = out;
+        }
+      }
+    }
+    if (lane == 0) *scale_at = scale;
+    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
+    const float inverse = 1.0f / scale;
+    // slots ascend, but need not be neighbours
+    auto store = [&](int i, const uint4& v) {
+      if (i >= n) return;
+      const int64_t s = __ldg(A.slots + t0 + cur + i);
+      *reinterpret_cast<uint2*>(pool + (s & ((1 << A.log_page) - 1)) * token + lane % kLanes * 8) =
+          code8<kBf16>(v, scale, inverse, exact, kLimit);
+    };
+#pragma unroll
+    for (int s = 0; s < kKeep; ++s) store(s * kPer + mine, keep[s]);
+#pragma unroll 1
+    for (int s0 = kKeep; s0 * kPer < n; s0 += kKeep) {
+      uint4 v[kKeep];
+#pragma unroll
+      for (int s = 0; s < kKeep; ++s) v[s] = load((s0 + s) * kPer + mine);
+#pragma unroll
+      for (int s = 0; s < kKeep; ++s) store((s0 + s) * kPer + mine, v[s]);
+    }
+  }
+}
+
+template <int D, bool kBf16>
+sv_status launch_append(const AppendArgs& A, cudaStream_t st) {
+  const int64_t chunks = (A.rows + 31) / 32;
+  // enough CTAs for the SMs; a chunk has at most 32 runs of 2 Hkv units, 8 warps to a CTA
+  int64_t split = (16 * (int64_t)device_sm_count() + chunks - 1) / chunks;
+  const int64_t most = (64 * (int64_t)A.Hkv + kAppWarps - 1) / kAppWarps;
+  const int64_t least = (2 * (int64_t)A.Hkv + kAppWarps - 1) / kAppWarps;
+  split = split > most ? most : split < least ? least : split;
+  append_kernel<D, kBf16><<<dim3((unsigned)chunks, (unsigned)split), kAppThreads, 0, st>>>(A);
+  return launch_status();
+}
+
+template <bool kBf16>
+sv_status launch_append_width(int D, const AppendArgs& A, cudaStream_t st) {
+  switch (D) {
+    case 64: return launch_append<64, kBf16>(A, st);
+    case 128: return launch_append<128, kBf16>(A, st);
+  }
+  return launch_append<256, kBf16>(A, st);
+}
+
+}  // namespace
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" sv_status kv_cache_append_q8(const sv_kv_shape* shape, int rows, const void* k,
+                                        int64_t k_row, int64_t k_head, const void* v, int64_t v_row,
+                                        int64_t v_head, const int64_t* slots,
+                                        const sv_kv_pool* k_pool, const sv_kv_pool* v_pool,
+                                        float* k_scale, float* v_scale, int block,
+                                        sv_stream_t stream) {
+  sv_status s = check_kv_shape(shape, false);
+  if (s == SV_OK) s = check_block(shape, block);
+  if (s != SV_OK) return s;
+  if (rows < 0) return SV_ERR_INVALID_ARG;
+  if (rows > 1 << 30) return SV_ERR_UNSUPPORTED;
+  if (rows == 0) return SV_OK;
+  if (check_pool8(k_pool) != SV_OK || check_pool8(v_pool) != SV_OK) return SV_ERR_INVALID_ARG;
+  if (!k || !v || !slots || !k_scale || !v_scale || !aligned_to(k, 16) || !aligned_to(v, 16) ||
+      !aligned_to(slots, 8) || !aligned_to(k_scale, 4) || !aligned_to(v_scale, 4))
+    return SV_ERR_INVALID_ARG;
+  for (int64_t st : {k_row, k_head, v_row, v_head})
+    if (st < 0 || st % 8 != 0 || st >= (1ll << 39)) return SV_ERR_INVALID_ARG;
+  const AppendArgs A{{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v)},
+                     {k_row, v_row},
+                     {k_head, v_head},
+                     {static_cast<unsigned char*>(k_pool->data), static_cast<unsigned char*>(v_pool->data)},
+                     {k_pool->page_stride, v_pool->page_stride},
+                     {k_pool->token_stride, v_pool->token_stride},
+                     {k_pool->head_stride, v_pool->head_stride},
+                     {k_scale, v_scale},
+                     slots,
+                     (int64_t)shape->num_pages * shape->page_size,
+                     rows,
+                     shape->Hkv,
+                     log2_of(shape->page_size),
+                     log2_of(block)};
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return shape->dtype == SV_KV_BF16 ? launch_append_width<true>(shape->D, A, st)
+                                    : launch_append_width<false>(shape->D, A, st);
+}

@@ -1,0 +1,492 @@
+// sv_kv8_tiles.cuh — what the tile kernel (sv_kv_tiles.cuh) does otherwise over a cache in 8 bits.
+//
+// Mathematics. Keys and values are e4m3 codes with a scale for each block of tokens and kv head.
+// With ks_j and vs_j the scales of key j's block, and codes k, v,
+//   s_j = scale * ks_j * (q . k_j)                    a thread per key: one factor more
+//   w_j = 2^(s_j - m) * vs_j,  O = sum w_j v_j        the values' scale goes into the weight
+//   l   = sum 2^(s_j - m)                             the softmax's sum does not have it
+// so the codes go to the tensor cores as they lie in the cache (kind::f8f6f4, 32 deep), and no tile
+// is ever widened: 32 KiB per 128 keys of D = 128 instead of 64.
+//
+// Rounding. Both operands of the instruction are 8 bits wide, so queries and weights are given to it
+// as sums of e4m3 numbers.
+// - A query row is scaled by a power of two to a largest magnitude in [128, 256) and split into two
+//   numbers (bf16) or three (fp16): its 8 or 11 bits exactly, or for an element below 2^-9 (bf16) or
+//   2^-6 (fp16) of the row's largest, to 2^-17 of that at worst.
+// - A weight, in units in which the largest possible is below 1, becomes an fp16 number y and what
+//   that leaves. y is three e4m3 numbers exactly, each 16 times finer than the one before (cut, not
+//   rounded: 4 + 4 + 3 bits), the rest a fourth: a weight is off by 2^-16 of it, or by 2^-30 of the
+//   largest possible (2^-27 of the largest there is, as the maximum below moves).
+// The four products are one instruction of four times the columns and are added, each by its unit,
+// at the end of a piece. The instruction adds up in fp32, cut: measured 2^-20.7 of sum |a b| over 128
+// products, and sums that fp32 holds exactly come out exact.
+//
+// Running maximum. Of s_j + log2 vs_j, as that is what bounds a weight: m is the maximum less 5 when
+// it moves, which it does when a weight passes 2^7.98 (8 times the largest so far). log2 vs_j counts
+// as -40 .. 40; a scale above 2^40, negative or not a number makes what sees the key NaN.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "sv_kv_tiles.cuh"
+
+namespace sv {
+
+constexpr float kMaxScale = 1099511627776.0f;  // 2^40
+
+template <int kD, int kN, bool kBf16>
+struct TileShape8 {
+  static constexpr int D = kD, N = kN;
+  static constexpr bool Bf16 = kBf16, Weigh = false, Quant = true;  // (the queries' and outputs' type)
+  static constexpr float Lift = 5.0f;
+  static constexpr float Top = 7.984375f;  // log2 of the largest weight: below 2^8 when rounded
+  static constexpr int UnitCols = D < 128 ? D : 128, RowBytes = UnitCols, UnitBytes = kTileKeys * RowBytes;
+  static constexpr int U = D / UnitCols;
+  // teams as over 16 bits: two that take the pieces in turn at 16 columns, one beyond
+  static constexpr int Teams = N == 16 ? 2 : 1;
+  static constexpr int SoftWarps = 8;
+  static constexpr int SoftThreads = 32 * SoftWarps;
+  // the softmax, then a warp each: key copies, scores, value copies, values, queries
+  static constexpr int KeyWarp = SoftWarps, ScoreWarp = KeyWarp + 1, CopyVWarp = KeyWarp + 2,
+                       ValueWarp = KeyWarp + 3;
+  static constexpr int Threads = SoftThreads + 160;
+  static constexpr int TeamThreads = SoftThreads / Teams;
+  static constexpr int NC = Teams == 2 ? N : N / 2;  // columns per softmax thread
+  static constexpr int CH = 16;                      // of which at a time
+  static constexpr int QParts = kBf16 ? 2 : 3;       // e4m3 numbers of a query element
+  static constexpr int QBytes = QParts * N * D;
+  static constexpr int NQ = 2;
+  static constexpr int Parts = 4;  // of a weight
+  static constexpr int PBytes = Parts * kTileKeys * N;
+  static constexpr int NP = 2;
+  static constexpr int kTables = 112 * N + 1792;
+  static constexpr int Room =
+      (kSmemMax - kTables - 1024 - NQ * QBytes - Teams * NP * PBytes) / UnitBytes;
+  static constexpr int NU = Room > 16 ? 16 : Room;
+  static constexpr int NV = NU / 2, NK = NU - NV;
+  static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * UnitBytes;
+  static constexpr int MBlocks = (D + 127) / 128;
+  static constexpr bool Wide = true;
+  static constexpr int ON = Parts * N;
+  // one set of accumulators where tensor memory has no room for two: a piece's output is then
+  // written before the next one's first product
+  static constexpr int Outs = 2 * Teams * N + 2 * MBlocks * ON <= 512 ? 2 : 1;
+  static constexpr int TmemNeed = 2 * Teams * N + Outs * MBlocks * ON;
+  static constexpr int TmemCols = TmemNeed <= 128 ? 128 : TmemNeed <= 256 ? 256 : 512;
+  // a tile's bytes take half the time of one in 16 bits, a piece's start as long
+  static constexpr int TileCost = 4;
+  static constexpr int PieceCost = (Teams == 2 ? 16 : 32) * 64 / D + 1;
+  static_assert(TmemNeed <= 512 && NV >= U && NK >= U && Smem + kTables <= kSmemMax, "tile shape");
+};
+
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       bool accumulate) {
+  asm volatile(
+      "{ .reg .pred p;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+// The instruction descriptor: fp32 accumulator, both operands e4m3.
+__device__ __forceinline__ uint32_t mma_desc8(bool mn, int M, int N) {
+  return 1u << 4 | (mn ? 3u << 15 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+}
+constexpr uint32_t kSwizzle64 = 4;
+// Operand rows of RowBytes bytes: their swizzle, and the bytes of eight of them.
+template <class S>
+constexpr uint32_t kRowSwizzle = S::RowBytes == 128 ? kSwizzle128 : kSwizzle64;
+template <class S>
+constexpr uint32_t kRows8 = 8 * S::RowBytes;
+
+// ---- the queries ---------------------------------------------------------------------------------
+// One warp reads each piece's query rows and leaves them as e4m3 numbers, part by part, in the
+// layout of the instruction's operand: rows of RowBytes, 16-byte pieces swapped by the row.
+template <class S>
+__device__ __forceinline__ void query_role8(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* qbuf) {
+  constexpr int kLanes = S::D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
+  constexpr int kSteps = S::N / kPer, kBatch = kSteps < 8 ? kSteps : 8;
+  const int lane = threadIdx.x & 31, col = lane % kLanes * 8;
+  Reader<S> reader(sh);
+  Piece p;
+#pragma unroll 1
+  while (reader.template next<true>(p)) {
+    const int qs = p.turn % S::NQ, rows = p.live * A.G;
+    if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs],
+                                            ((uint32_t)(p.turn / S::NQ) & 1u) ^ 1u, &sh.waits)))
+      return;
+    const uint16_t* q = static_cast<const uint16_t*>(A.q) + p.b * A.q_req + p.i0 * A.q_row +
+                        (int64_t)p.h * A.G * A.q_head + col;
+    unsigned char* buf = qbuf + qs * S::QBytes + col / S::UnitCols * (S::N * S::RowBytes);
+#pragma unroll 1
+    for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const int c = (s0 + s) * kPer + lane / kLanes, i = c / A.G;
+        x[s] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < rows)
+          x[s] = *reinterpret_cast<const uint4*>(q + i * A.q_row + (c - i * A.G) * A.q_head);
+      }
+#pragma unroll
+      for (int s = 0; s < kBatch; ++s) {
+        const int c = (s0 + s) * kPer + lane / kLanes;
+        const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+        // the row's largest magnitude, by its bits (those of what is not finite are the largest)
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+#pragma unroll
+        for (int o = kLanes / 2; o >= 1; o >>= 1)
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const bool odd = top >= (S::Bf16 ? 0x7f80u : 0x7c00u);
+        // 2^e <= top < 2^(e+1), e at least -100 (what is smaller counts as 0)
+        const int e = top == 0 ? 0 : max(-100, (int)(__float_as_uint(unpack16<S::Bf16>(top).x) >> 23) - 127);
+        const float up = odd ? 1.0f : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack16<S::Bf16>(w[k]);
+          f[2 * k] = v.x * up;
+          f[2 * k + 1] = v.y * up;
+        }
+        const uint32_t row = c * S::RowBytes + col % S::UnitCols;
+        const uint32_t at = row ^ ((row >> 7 & (S::RowBytes == 128 ? 7u : 3u)) << 4);
+#pragma unroll
+        for (int part = 0; part < S::QParts; ++part) {
+          uint32_t out[2];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __nv_fp8x2_storage_t b =
+                __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            f[2 * k] -= back.x;
+            f[2 * k + 1] -= back.y;
+            out[k / 2] = k & 1 ? out[k / 2] | (uint32_t)b << 16 : (uint32_t)b;
+          }
+          if (odd) out[0] = out[1] = 0x7f7f7f7fu;  // NaN
+          *reinterpret_cast<uint2*>(buf + part * (S::N * S::D) + at) = make_uint2(out[0], out[1]);
+        }
+        if (lane % kLanes == 0)
+          sh.q_scale[qs][c] = __uint_as_float((uint32_t)(127 - 7 + (odd ? 7 : e)) << 23);
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.q_full[qs]);
+  }
+}
+
+// ---- the threads that issue the matrix instructions -------------------------------------------
+// S^T = K Q^T of every tile, over the queries' parts.
+template <class S>
+__device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* qbuf, unsigned char* ring) {
+  const uint32_t idesc = mma_desc8(false, 128, S::N);
+  const uint64_t rows = smem_desc(0, 16, kRows8<S>, kRowSwizzle<S>);
+  const uint64_t a0 = rows + (smem_u32(ring) >> 4), b0 = rows + (smem_u32(qbuf) >> 4);
+  Reader<S> reader(sh);
+  RingPos at;
+  int used[2] = {0, 0};  // tiles so far per team
+  Piece p;
+#pragma unroll 1
+  while (reader.template next<false>(p)) {
+    const int qs = p.turn % S::NQ, team = p.turn % S::Teams, tiles = p.mb - p.ma;
+    if (!wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits)) goto end;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int y = team ? used[1]++ : used[0]++, buf = y & 1;
+      if (!wait_phase(&sh.s_empty[team][buf], ((uint32_t)(y >> 1) & 1u) ^ 1u, &sh.waits)) goto end;
+      tc_fence_after();
+      const uint32_t d = sh.tmem + (2 * team + buf) * S::N;
+      uint64_t b = b0 + qs * (S::QBytes >> 4);
+#pragma unroll 1
+      for (int c = 0; c < S::U; ++c, b += S::N * S::RowBytes >> 4) {
+        if (!wait_phase(&sh.full[at.slot], at.phase, &sh.waits)) goto end;
+        tc_fence_after();
+        const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
+#pragma unroll
+        for (int part = 0; part < S::QParts; ++part)
+#pragma unroll
+          for (int k = 0; k < S::RowBytes / 32; ++k)
+            mma_f8(d, a + 2 * k, b + part * (S::N * S::D >> 4) + 2 * k, idesc,
+                   c > 0 || part > 0 || k > 0);
+        mma_commit(&sh.empty[at.slot]);
+        at.next(S::NK);
+      }
+      mma_commit(&sh.s_full[team][buf]);
+    }
+    mma_commit(&sh.q_empty[qs]);
+  }
+end:
+  drain<S>(sh, 0);
+}
+
+// O^T (+)= V^T P^T of every tile, the weights' parts side by side as columns.
+template <class S>
+__device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* pbuf, unsigned char* ring) {
+  const uint32_t idesc = mma_desc8(true, 128, S::ON);
+  // (with D = 64 both halves of the instruction's rows read the same columns, and the upper half is
+  // not used)
+  const uint64_t a0 = smem_desc(0, 0, kRows8<S>, kRowSwizzle<S>) +
+                      ((smem_u32(ring) + S::NK * S::UnitBytes) >> 4);
+  const uint64_t b0 = smem_desc(0, kTileKeys * 32, 256, kSwizzle32) + (smem_u32(pbuf) >> 4);
+  Reader<S> reader(sh);
+  RingPos at;
+  int used[2] = {0, 0};
+  Piece p;
+#pragma unroll 1
+  while (reader.template next<false>(p)) {
+    const int team = p.turn % S::Teams, tiles = p.mb - p.ma;
+    const uint32_t o = sh.tmem + 2 * S::Teams * S::N + (p.turn & (S::Outs - 1)) * S::MBlocks * S::ON;
+#pragma unroll 1
+    for (int i = 0; i < tiles; ++i) {
+      const int y = team ? used[1]++ : used[0]++, pb = y % S::NP;
+      if (__builtin_expect(edge_tile(p, A.rule.window, tile_at<S>(p, i)), 0)) {
+        RingPos look = at;
+#pragma unroll 1
+        for (int c = 0; c < S::U; ++c) {
+          if (!wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.waits)) goto end;
+          look.next(S::NV);
+        }
+        mbar_arrive(&sh.v_ready[team]);
+      }
+      if (!wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits)) goto end;
+      const uint64_t b = b0 + (team * S::NP + pb) * (S::PBytes >> 4);
+      uint32_t d = o;
+#pragma unroll 1
+      for (int m = 0; m < S::MBlocks; ++m, d += S::ON) {
+        if (!wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.waits)) goto end;
+        tc_fence_after();
+        const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
+#pragma unroll
+        for (int k = 0; k < kTileKeys / 32; ++k)
+          mma_f8(d, a + k * (4 * kRows8<S> >> 4), b + k * 64, idesc, !(i == 0 && k == 0));
+        mma_commit(&sh.empty[S::NK + at.slot]);
+        at.next(S::NV);
+      }
+      mma_commit(&sh.pv_done[team][pb]);
+    }
+    mma_commit(&sh.o_done[p.turn & 1]);
+  }
+end:
+  drain<S>(sh, 1);
+}
+
+// ---- the softmax threads ------------------------------------------------------------------------
+// The scales of the thread's key in a tile, loaded a tile ahead, and the page of the key after it.
+template <class S>
+struct KeyScales<S, true> {
+  float k, v;      // of the tile at hand
+  int64_t next;    // where those of the next tile lie; -1: none
+};
+
+template <class S>
+__device__ __forceinline__ int64_t scale_of(const Attend<S>& me, const Piece& p, int i) {
+  const TileArgs& A = me.A;
+  const int j = tile_at<S>(p, i) * kTileKeys + me.key;
+  if (i >= p.mb - p.ma || j < p.first || j > p.last) return -1;
+  const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
+  if (page < 0 || page >= A.num_pages) return -1;
+  return scale_at(A, page, j & ((1 << A.log_page) - 1), p.h);
+}
+
+// The start of a piece: the columns' powers of two, and the scales of the first tile's keys.
+template <class S>
+__device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p) {
+  auto& sh = me.sh;
+  const int64_t at = scale_of(me, p, 0);
+  me.scales.next = scale_of(me, p, 1);
+  me.scales.k = at < 0 ? 0.0f : __ldg(me.A.k_scale + at);
+  me.scales.v = at < 0 ? 0.0f : __ldg(me.A.v_scale + at);
+  const int qs = p.turn % S::NQ;
+  wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits);
+#pragma unroll 1
+  for (int c = me.me; c < S::N; c += S::TeamThreads) sh.column_scale[table][c] = sh.q_scale[qs][c];
+}
+
+__device__ __forceinline__ Two two_mul(Two a, Two b) {
+  Two v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+// Four e4m3 codes, which lie in bits 7 to 14 of the halves of a and b.
+__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b) {
+  return __byte_perm(a + a, b + b, 0x7531);
+}
+
+template <class S>
+__device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>::Table& T,
+                                           const Piece& p, int t, int i, int x, int y,
+                                           Two (&l)[S::NC / 2]) {
+  const TileArgs& A = me.A;
+  auto& sh = me.sh;
+  const int team = me.team, buf = y & 1, j = t * kTileKeys + me.key;
+  const bool edge = edge_tile(p, A.rule.window, t);
+  unsigned char* const pb = me.pbuf + (team * S::NP + y % S::NP) * S::PBytes + me.key * 32;
+  const float* columns = sh.column_scale[S::Teams == 2 ? team : p.turn & 1];
+  // (every team thread has read the queries' scales by now: the barriers around set_columns)
+  if (i == 0 && me.me == 0) mbar_arrive(&sh.q_empty[p.turn % S::NQ]);
+  float ks = me.scales.k, vs = me.scales.v;
+  const int64_t at = me.scales.next;
+  me.scales.k = at < 0 ? 0.0f : __ldg(A.k_scale + at);
+  me.scales.v = at < 0 ? 0.0f : __ldg(A.v_scale + at);
+  me.scales.next = scale_of(me, p, i + 2);
+  if (!(vs >= 0.0f && vs <= kMaxScale && fabsf(ks) < INFINITY)) {
+    ks = __uint_as_float(0x7fc00000u);
+    vs = 1.0f;
+  }
+  const float lv = vs < 1.0f / kMaxScale ? -40.0f : __log2f(vs);
+  const float unit = vs * 0.00390625f;  // (the largest weight possible below 1)
+  wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.waits);
+  tc_fence_after();
+#pragma unroll
+  for (int k = 0; k < S::NC; k += S::CH) {
+    const int c0 = me.col0 + k;
+    float s[S::CH];
+    tmem_ld16(me.lane_base + (2 * team + buf) * S::N + c0, s);
+    tmem_wait_ld();
+    if (k + S::CH == S::NC) {
+      tc_fence_before();
+      mbar_arrive(&sh.s_empty[team][buf]);
+    }
+    float scale = A.rule.scale * kLog2e * ks;  // to what the thread holds in s
+#pragma unroll
+    for (int c = 0; c < S::CH; c += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(&columns[c0 + c]);
+      s[c] *= q.x;
+      s[c + 1] *= q.y;
+      s[c + 2] *= q.z;
+      s[c + 3] *= q.w;
+    }
+    if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
+#pragma unroll
+      for (int c = 0; c < S::CH; ++c) s[c] *= ks;
+      apply_rule<S::CH>(s, A.rule, (float)(p.pos0 - j), &T.slope[c0], &T.ahead[c0]);
+      scale = 1.0f;
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c)
+          if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[c] = -INFINITY;
+      }
+    }
+    Two e[S::CH / 2];
+    auto exponents = [&]() {
+      const Two sc = two(scale, scale);
+#pragma unroll
+      for (int c = 0; c < S::CH; c += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&T.m[c0 + c]);
+        e[c / 2] = two_fma(two(s[c], s[c + 1]), sc, two(m.x, m.y));
+        e[c / 2 + 1] = two_fma(two(s[c + 2], s[c + 3]), sc, two(m.z, m.w));
+      }
+    };
+    exponents();
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < S::CH / 2; ++c) {
+      const float2 v = split(e[c]);
+      top = fmaxf(top, fmaxf(v.x, v.y));
+    }
+    if (__builtin_expect(bar_or(1 + me.group, 128, top + lv > S::Top), 0)) {
+      if (i > 0) me.wait_values(y - 1);
+#pragma unroll
+      for (int c = 0; c < S::CH; ++c) s[c] = fmaf(s[c], scale, lv);
+      me.raise(T, s, l, k, i == 0, me.output(p.turn));
+#pragma unroll
+      for (int c = 0; c < S::CH; ++c) s[c] -= lv;
+      scale = 1.0f;
+      exponents();
+    }
+    uint32_t part[3][S::CH / 2], rest[S::CH / 4];
+    const Two unit2 = two(unit, unit);
+#pragma unroll
+    for (int c = 0; c < S::CH / 2; ++c) {
+      const float2 v = split(e[c]);
+      const Two w = two(ex2(v.x), ex2(v.y));
+      l[k / 2 + c] = two_add(l[k / 2 + c], w);
+      const Two y2 = two_mul(w, unit2);
+      const float2 yf = split(y2);
+      const __half2 h = __floats2half2_rn(yf.x, yf.y);
+      const float2 back = __half22float2(h);
+      const float2 left = split(two_mul(two_fma(two(back.x, back.y), two(-1.0f, -1.0f), y2),
+                                        two(1048576.0f, 1048576.0f)));
+      const uint32_t b =
+          __nv_cvt_float2_to_fp8x2(make_float2(left.x, left.y), __NV_SATFINITE, __NV_E4M3);
+      rest[c / 2] = c & 1 ? rest[c / 2] | b << 16 : b;
+      // y is at most 1, so its e4m3 digits of exponent -8 are bits 7 .. 14 as they are
+      const __half2 sixteen = __float2half2_rn(16.0f);
+      uint32_t d = *reinterpret_cast<const uint32_t*>(&h) & 0xff80ff80u;
+      part[0][c] = d;
+      __half2 r = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&d)), sixteen);
+      d = *reinterpret_cast<const uint32_t*>(&r) & 0xff80ff80u;
+      part[1][c] = d;
+      r = __hmul2(__hsub2(r, *reinterpret_cast<const __half2*>(&d)), sixteen);
+      part[2][c] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    // the product that last read this buffer
+    if (k == 0 && y >= S::NP) me.wait_values(y - S::NP);
+    // 32 columns of a key are 32 bytes, their 16-byte halves swapped in every other 4 keys
+#pragma unroll
+    for (int q = 0; q < S::Parts; ++q) {
+      const int n = q * S::N + c0;
+      uint4 v;
+      if (q < 3)
+        v = make_uint4(codes4(part[q][0], part[q][1]), codes4(part[q][2], part[q][3]),
+                       codes4(part[q][4], part[q][5]), codes4(part[q][6], part[q][7]));
+      else
+        v = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+      *reinterpret_cast<uint4*>(pb + n / 32 * (kTileKeys * 32) +
+                                ((n / 16 ^ me.key >> 2) & 1) * 16) = v;
+    }
+  }
+  if (__builtin_expect(edge, 0)) {
+    wait_phase(&sh.v_ready[team], (uint32_t)(me.edges++) & 1u, &sh.waits);
+    if (S::Teams == 2 || me.group == 0) me.clean_values(T, p, x, j);
+  }
+  fence_proxy_async();
+  tc_fence_before();
+  mbar_arrive(&sh.p_full[team][y % S::NP]);
+}
+
+// The outputs that NaN codes among the values of partly visible keys make NaN (those codes went to
+// the tensor cores as 0): of the keys that some rows of the piece see and others do not.
+template <class S>
+__device__ __noinline__ void special_values8(const TileArgs& A, const ValuePool& vpool,
+                                             const typename TileShared<S>::Table& T,
+                                             const Piece& p, int col0, int rows, int d0,
+                                             float* part, int64_t row0) {
+  const int j0 = p.first > p.ma * kTileKeys ? p.first : p.ma * kTileKeys;
+  const int j1 = p.last < p.mb * kTileKeys - 1 ? p.last : p.mb * kTileKeys - 1;
+  // keys [f0, f1] are seen by all rows
+  int f0 = first_full(p, A.rule.window) > j0 ? first_full(p, A.rule.window) : j0;
+  int f1 = p.pos0 < j1 ? p.pos0 : j1;
+  if (f0 > f1) f0 = j1 + 1, f1 = j1;
+  const float nan = __uint_as_float(0x7fc00000u);
+#pragma unroll 1
+  for (int d = d0; d < S::D; d += 128) {
+#pragma unroll 1
+    for (int j = j0; j <= j1; ++j) {
+      if (j == f0) j = f1 + 1;
+      if (j > j1) break;
+      const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
+      if (page < 0 || page >= A.num_pages) continue;
+      const int64_t at = page * vpool.page + (j & ((1 << A.log_page) - 1)) * vpool.token +
+                         p.h * vpool.head + d;
+      if ((__ldg(static_cast<const unsigned char*>(vpool.data) + at) & 0x7f) != 0x7f) continue;
+#pragma unroll 1
+      for (int n = col0; n < col0 + S::NC && n < rows; ++n) {
+        if (j > T.hi[n] || j <= T.lo[n]) continue;
+        if (part)
+          part[n * S::D + d] = nan;
+        else
+          store16<S::Bf16>(A.out, (row0 + T.row[n]) * S::D + d, nan);
+      }
+    }
+  }
+}
+
+}  // namespace sv

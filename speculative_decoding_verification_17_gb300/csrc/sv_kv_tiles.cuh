@@ -94,6 +94,11 @@ struct TileArgs {
   void* out;
   float *out_lse, *part;
   struct JoinItem* joins;
+  // attention over 8 bits: [num_pages, slots / block, Hkv]
+  const float *k_scale, *v_scale;
+  const void* q;
+  int64_t q_req, q_row, q_head;  // of q, in elements
+  int log_block;
   // key weights
   const float *lse, *prior;
   float* weights;
@@ -111,8 +116,10 @@ struct TileShape {
   static constexpr int D = kD, N = kN;
   static constexpr bool Bf16 = kBf16;  // (attention) the type is bf16, else fp16
   static constexpr bool Weigh = kWeigh;
+  static constexpr bool Quant = false;  // keys and values in 16 bits (in 8: sv_kv8_tiles.cuh)
   static constexpr float Lift = kBf16 ? 0.0f : 7.0f;  // (attention) of the weights' exponents
   static constexpr int U = D / 64;  // units of a key or value tile
+  static constexpr int UnitCols = 64, RowBytes = 128, UnitBytes = kUnitBytes;
   // Softmax warps: two groups of four (one warp per quarter of the tile's keys). In the
   // attention of 16 columns the groups are two teams that take the pieces in turn, each
   // with its own score, weight and output buffers, so one team's end of a piece (its last
@@ -148,6 +155,7 @@ struct TileShape {
   static constexpr int NK = NU - NV;
   static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * kUnitBytes;
   static constexpr int MBlocks = kWeigh ? 0 : (D + 127) / 128;  // accumulators of 128 of D
+  static constexpr int Outs = 2;  // sets of them
   // Two score buffers per team, two outputs. Where tensor memory has room, the products with the
   // parts of the weights are one instruction of as many times the columns (the values, whose read
   // from shared memory bounds a narrow instruction, are read once) and are added at the end; else
@@ -424,8 +432,16 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
 constexpr int kPieceQueue = 8;
 
 // ---- shared memory ------------------------------------------------------------------------------
+// Of an attention over 8 bits: the columns' powers of two, by query buffer and by table.
+template <bool kQuant, int kN>
+struct QueryScales {};
+template <int kN>
+struct QueryScales<true, kN> {
+  alignas(16) float q_scale[2][kN], column_scale[2][kN];
+};
+
 template <class S>
-struct TileShared {
+struct TileShared : QueryScales<S::Quant, S::N> {
   uint64_t full[S::NU], empty[S::NU];
   uint64_t q_full[S::NQ], q_empty[S::NQ];
   uint64_t s_full[S::Teams][2], s_empty[S::Teams][2];
@@ -518,6 +534,25 @@ struct Reader {
   }
 };
 
+// Where the scales of a block of slots lie: of a page's slot and a kv head.
+__device__ __forceinline__ int64_t scale_at(const TileArgs& A, int page, int slot, int head) {
+  return ((int64_t)page * (1 << (A.log_page - A.log_block)) + (slot >> A.log_block)) * A.Hkv + head;
+}
+// The scales of a tile's blocks into L2, for the softmax threads' loads some tiles later: the lanes
+// share the blocks (page and slot are those of the lane's group of keys, -1 for a group not copied).
+__device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int slot, int head) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int j0 = 0; j0 < kTileKeys; j0 += 32 << A.log_block) {
+    const int j = j0 + (lane << A.log_block), from = (j / A.box) & 31;
+    const int of = __shfl_sync(0xffffffffu, page, from), at0 = __shfl_sync(0xffffffffu, slot, from);
+    if (j >= kTileKeys || of < 0) continue;
+    const int64_t at = scale_at(A, of, at0 + j % A.box, head);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.k_scale + at));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.v_scale + at));
+  }
+}
+
 // ---- the copying warps ------------------------------------------------------------------------
 // Whether some row sees a key of the lane's group of `box` keys in a tile, and that group's page
 // (not looked at here: the load is a tile ahead of its use).
@@ -540,7 +575,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
                                           const CUtensorMap* mq, const CUtensorMap* map) {
   constexpr int kBase = kValues ? S::NK : 0, kUnits = kValues ? S::NV + S::Weigh : S::NK;
   const int lane = threadIdx.x & 31;
-  unsigned char* dst = ring + kBase * kUnitBytes + lane * A.box * 128;
+  unsigned char* dst = ring + kBase * S::UnitBytes + lane * A.box * S::RowBytes;
   Walk<S> walk(A, sh.start);
   Reader<S> reader(sh);
   // the next piece with tiles for the tensor cores; all lanes
@@ -573,7 +608,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
   while (more) {
     const int head = p.h, turn = p.turn;
     const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
-    if (!kValues && i == 0) {
+    if (!S::Quant && !kValues && i == 0) {
       const int qs = turn % S::NQ;
       if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u,
                                               &sh.waits)))
@@ -599,8 +634,11 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
       if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
         *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
     }
+    if constexpr (S::Quant) {
+      if (!kValues) prefetch_scales(A, mine ? page : -1, slot, head);
+    }
     const uint32_t bytes =
-        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
+        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
 #pragma unroll 1
     for (int c = 0; c < S::U; ++c) {
       uint64_t* full = &sh.full[kBase + at.slot];
@@ -609,7 +647,8 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
       if (lane == 0) mbar_arrive_expect_tx(full, bytes);
       ++issued;
       __syncwarp();
-      if (mine) tile_g2s(dst + at.slot * kUnitBytes, map, full, c * 64, slot, head, page);
+      if (mine)
+        tile_g2s(dst + at.slot * S::UnitBytes, map, full, c * S::UnitCols, slot, head, page);
       at.next(kUnits);
     }
     page = next_page;
@@ -621,9 +660,11 @@ end:
 #pragma unroll 1
     for (int u = issued > kUnits ? issued - kUnits : 0; u < issued; ++u)
       mbar_wait(&sh.full[kBase + u % kUnits], (uint32_t)(u / kUnits) & 1u, kTileWaitNs);
+    if constexpr (!S::Quant) {
 #pragma unroll 1
-    for (int u = q_issued > S::NQ ? q_issued - S::NQ : 0; u < q_issued; ++u)
-      mbar_wait(&sh.q_full[u % S::NQ], (uint32_t)(u / S::NQ) & 1u, kTileWaitNs);
+      for (int u = q_issued > S::NQ ? q_issued - S::NQ : 0; u < q_issued; ++u)
+        mbar_wait(&sh.q_full[u % S::NQ], (uint32_t)(u / S::NQ) & 1u, kTileWaitNs);
+    }
   }
   __syncwarp();
 }
@@ -894,6 +935,15 @@ __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
                : ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
 }
 
+// The same of four 8-bit values (e4m3 has no infinity; NaN is the largest magnitude): bit 7 of each.
+__device__ __forceinline__ uint32_t not_finite4(uint32_t w) {
+  return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+template <class S>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return S::Quant ? not_finite4(w) : not_finite2<S::Bf16>(w);
+}
+
 // Named barriers: 1 and 2 for the two groups of softmax warps, 3 for all of them.
 constexpr int kAllBar = 3;
 
@@ -957,6 +1007,24 @@ __device__ __noinline__ void special_values(const TileArgs& A, const ValuePool& 
   }
 }
 
+// Of an attention over 8 bits: what a softmax thread keeps of the scales of its keys, and its part
+// of a tile (sv_kv8_tiles.cuh).
+template <class S, bool kQuant = S::Quant>
+struct KeyScales {};
+template <class S>
+struct Attend;
+template <class S>
+__device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>::Table& T,
+                                           const Piece& p, int t, int i, int x, int y,
+                                           Two (&l)[S::NC / 2]);
+template <class S>
+__device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p);
+template <class S>
+__device__ __noinline__ void special_values8(const TileArgs& A, const ValuePool& vpool,
+                                             const typename TileShared<S>::Table& T,
+                                             const Piece& p, int col0, int rows, int d0,
+                                             float* part, int64_t row0);
+
 // ---- attention --------------------------------------------------------------------------------
 // What one softmax thread does for the attention: its key of every tile, its share of O.
 template <class S>
@@ -971,6 +1039,7 @@ struct Attend {
   int team, me;        // the team, the thread's index in it
   int col0;            // the group's first column
   int edges = 0;       // edge tiles so far
+  KeyScales<S> scales{};  // (8 bits) of the thread's key
 
   // Wait until the products of the team's tile y have read P and are in O.
   __device__ __forceinline__ void wait_values(int y) const {
@@ -982,7 +1051,7 @@ struct Attend {
   }
   // The accumulator of a piece, the group's first column.
   __device__ __forceinline__ uint32_t output(int turn) const {
-    return lane_base + 2 * S::Teams * S::N + (turn & 1) * S::MBlocks * S::ON + col0;
+    return lane_base + 2 * S::Teams * S::N + (turn & (S::Outs - 1)) * S::MBlocks * S::ON + col0;
   }
 
   // Raise the maxima of the CH columns from c0 to those of this tile's scores s, and scale what
@@ -1030,20 +1099,22 @@ struct Attend {
     const bool none = j > p.last || j < p.first;
     const bool some = !none && (j > p.pos0 || j < first_full(p, A.rule.window));
     if (!__any_sync(0xffffffffu, none || some)) return;
+    constexpr int kVecs = S::RowBytes / 16;
     uint32_t odd = 0;
 #pragma unroll 1
     for (int c = 0; c < S::U; ++c) {
-      uint4* row = reinterpret_cast<uint4*>(ring + value_slot<S>(x, c) * kUnitBytes + key * 128);
+      uint4* row = reinterpret_cast<uint4*>(ring + value_slot<S>(x, c) * S::UnitBytes +
+                                            key * S::RowBytes);
       // (each lane starts with another 16 bytes of its row: no bank conflicts)
       if (none) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) row[(q + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
+        for (int q = 0; q < kVecs; ++q)
+          row[(q + lane) & (kVecs - 1)] = make_uint4(0u, 0u, 0u, 0u);
       } else if (some) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 v = row[(q + lane) & 7];
-          odd |= not_finite2<S::Bf16>(v.x) | not_finite2<S::Bf16>(v.y) |
-                 not_finite2<S::Bf16>(v.z) | not_finite2<S::Bf16>(v.w);
+        for (int q = 0; q < kVecs; ++q) {
+          const uint4 v = row[(q + lane) & (kVecs - 1)];
+          odd |= not_finite<S>(v.x) | not_finite<S>(v.y) | not_finite<S>(v.z) | not_finite<S>(v.w);
         }
       }
     }
@@ -1051,12 +1122,12 @@ struct Attend {
       *(volatile int*)&T.odd = 1;
 #pragma unroll 1
       for (int c = 0; c < S::U; ++c) {
-        uint32_t* w = reinterpret_cast<uint32_t*>(ring + value_slot<S>(x, c) * kUnitBytes +
-                                                  key * 128);
+        uint32_t* w = reinterpret_cast<uint32_t*>(ring + value_slot<S>(x, c) * S::UnitBytes +
+                                                  key * S::RowBytes);
 #pragma unroll 1
-        for (int e = 0; e < 32; ++e) {
-          const uint32_t bad = not_finite2<S::Bf16>(w[e]);
-          if (bad) w[e] &= ~((bad >> 15) * 0xffffu);
+        for (int e = 0; e < S::RowBytes / 4; ++e) {
+          const uint32_t bad = not_finite<S>(w[e]);
+          if (bad) w[e] &= S::Quant ? ~((bad >> 7) * 0xffu) : ~((bad >> 15) * 0xffffu);
         }
       }
     }
@@ -1212,13 +1283,15 @@ struct Attend {
           tmem_ld16(output(p.turn) + m * S::ON + q, o);
           tmem_wait_ld();
           if (S::Wide) {
+            float unit = 1.0f;  // (8 bits: each part is given 16 times its size)
 #pragma unroll 1
             for (int part = 1; part < S::Parts; ++part) {
               float low[16];
               tmem_ld16(output(p.turn) + m * S::ON + part * S::N + q, low);
               tmem_wait_ld();
+              if (S::Quant) unit *= 0.0625f;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] += low[c];
+              for (int c = 0; c < 16; ++c) o[c] = S::Quant ? fmaf(low[c], unit, o[c]) : o[c] + low[c];
             }
           }
           const int n0 = col0 + q;
@@ -1241,7 +1314,11 @@ struct Attend {
               if (n0 + c < rows) part[(n0 + c) * S::D + d] = o[c];
           }
         }
-      if (__builtin_expect(odd != odd && !poison, 0))
+      if constexpr (S::Quant) {
+        if (__builtin_expect(*(volatile int*)&T.odd && !poison, 0))
+          special_values8<S>(A, vpool, T, p, col0, rows, quarter * 32 + lane, whole ? nullptr : part,
+                             row0);
+      } else if (__builtin_expect(odd != odd && !poison, 0))
         special_values<S>(A, vpool, T, p.b, p.h, p.pos0, p.first, p.last, p.ma, p.mb, col0, rows,
                           quarter * 32 + lane, whole ? nullptr : part, row0);
     }
@@ -1260,7 +1337,7 @@ struct Attend {
     auto table = [&](int turn) -> Table& { return sh.table[S::Teams == 2 ? team : turn & 1]; };
 #pragma unroll 1
     for (;;) {
-      const bool flush = S::Teams == 2 && pending;  // the end first
+      const bool flush = (S::Teams == 2 || S::Outs == 1) && pending;  // the end first
       bool more = true;
       if (!flush) {
         if (__builtin_expect(i == p.mb - p.ma, 0)) {
@@ -1279,6 +1356,7 @@ struct Attend {
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
             if (me == 0) T.piece = p, T.odd = 0;
+            if constexpr (S::Quant) quant_columns<S>(*this, S::Teams == 2 ? team : p.turn & 1, p);
             team_sync();
             i = 0;
           }
@@ -1286,7 +1364,10 @@ struct Attend {
           for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
         }
         if (more) {
-          tile(table(p.turn), p, tile_at<S>(p, i), i == 0, p.x0 + i, y, l);
+          if constexpr (S::Quant)
+            quant_tile<S>(*this, table(p.turn), p, tile_at<S>(p, i), i, p.x0 + i, y, l);
+          else
+            tile(table(p.turn), p, tile_at<S>(p, i), i == 0, p.x0 + i, y, l);
           ++i;
           ++y;
         }
@@ -1469,6 +1550,17 @@ __device__ __noinline__ void write_rest(const TileArgs& A, const TileShared<S>& 
 }
 
 // ---- the kernel ---------------------------------------------------------------------------------
+// The roles that differ over 8 bits (sv_kv8_tiles.cuh).
+template <class S>
+__device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* qbuf, unsigned char* ring);
+template <class S>
+__device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* pbuf, unsigned char* ring);
+template <class S>
+__device__ __forceinline__ void query_role8(const TileArgs& A, TileShared<S>& sh,
+                                            unsigned char* qbuf);
+
 template <class S>
 __global__ void __launch_bounds__(S::Threads, 1)
     tile_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -1492,7 +1584,7 @@ __global__ void __launch_bounds__(S::Threads, 1)
     }
     for (int s = 0; s < S::NQ; ++s) {
       mbar_init(&sh.q_full[s], 1);
-      mbar_init(&sh.q_empty[s], 1);
+      mbar_init(&sh.q_empty[s], S::Quant ? 2 : 1);
     }
     for (int t = 0; t < S::Teams; ++t) {
       for (int s = 0; s < 2; ++s) {
@@ -1509,8 +1601,8 @@ __global__ void __launch_bounds__(S::Threads, 1)
     mbar_init(&sh.o_done[1], 1);
     for (int s = 0; s < kPieceQueue; ++s) {
       mbar_init(&sh.piece_full[s], 1);
-      // taken by the softmax warps, the issuing threads and the value copies
-      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : 3));
+      // taken by the softmax warps, the issuing threads, the value copies and (8 bits) the queries' warp
+      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : 3) + S::Quant);
     }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
@@ -1521,13 +1613,13 @@ __global__ void __launch_bounds__(S::Threads, 1)
     fence_barrier_init();
   }
   if (tid == 32) {
-    prefetch_map(&mq);
+    if (!S::Quant) prefetch_map(&mq);
     prefetch_map(&mk);
     if (!S::Weigh) prefetch_map(&mv);
   }
   if (warp == S::ScoreWarp) tmem_alloc(&sh.tmem, S::TmemCols);
   // columns past the query rows multiply zeros: the copies never write them
-  {
+  if (!S::Quant) {
     const int rows = A.G * A.pos_block;
     for (int q = 0; q < S::NQ; ++q)
       for (int c = 0; c < S::U; ++c) {
@@ -1553,15 +1645,27 @@ __global__ void __launch_bounds__(S::Threads, 1)
   if (warp == S::KeyWarp) {
     copy_role<S, false>(A, sh, qbuf, ring, &mq, &mk);
   } else if (warp == S::ScoreWarp) {
-    if ((tid & 31) == 0) score_role<S>(A, sh, qbuf, ring);
+    if ((tid & 31) == 0) {
+      if constexpr (S::Quant)
+        score_role8<S>(A, sh, qbuf, ring);
+      else
+        score_role<S>(A, sh, qbuf, ring);
+    }
     __syncwarp();
   } else if (!S::Weigh && warp == S::CopyVWarp) {
     copy_role<S, true>(A, sh, qbuf, ring, &mq, &mv);
   } else if (!S::Weigh && warp == S::ValueWarp) {
-    if ((tid & 31) == 0) value_role<S>(A, sh, pbuf, ring);
+    if ((tid & 31) == 0) {
+      if constexpr (S::Quant)
+        value_role8<S>(A, sh, pbuf, ring);
+      else
+        value_role<S>(A, sh, pbuf, ring);
+    }
     __syncwarp();
   } else if constexpr (S::Weigh) {
     weigh_role<S>(A, sh);
+  } else if (S::Quant && warp == S::SoftWarps + 4) {
+    if constexpr (S::Quant) query_role8<S>(A, sh, qbuf);
   } else {
     const int lane = tid & 31, quarter = warp & 3, group = warp >> 2;
     const int team = S::Teams == 2 ? group : 0;
@@ -1646,7 +1750,11 @@ __global__ void __launch_bounds__(kJoinThreads)
 // ---- the host side ------------------------------------------------------------------------------
 int device_sm_count();
 
-// A 4-D tensor map of 16-bit elements, 64 wide boxes of 128-byte swizzled rows.
+// A 4-D tensor map of elements of `size` bytes.
+sv_status encode_tiles(CUtensorMap* map, const void* data, CUtensorMapDataType type, int size,
+                       CUtensorMapSwizzle swizzle, const uint64_t (&dims)[4],
+                       const int64_t (&strides)[3], const uint32_t (&box)[4]);
+// Of 16-bit elements, 64 wide boxes of 128-byte swizzled rows.
 sv_status encode_map(CUtensorMap* map, const void* data, bool bf16, const uint64_t (&dims)[4],
                      const int64_t (&strides)[3], const uint32_t (&box)[4]);
 
