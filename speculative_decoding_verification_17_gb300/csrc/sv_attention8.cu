@@ -17,7 +17,7 @@ void row_blocks8(const sv_kv_shape* s, int* pos_block, int* blocks, int* columns
   *blocks = (s->P + most - 1) / most;
   *pos_block = (s->P + *blocks - 1) / *blocks;
   const int rows = G * *pos_block;
-  *columns = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  *columns = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 sv_status check_shape8(const sv_kv_shape* s) {
@@ -33,7 +33,7 @@ struct Layout8 {
 Layout8 layout8(const sv_kv_shape* s) {
   int pos_block, blocks, columns;
   row_blocks8(s, &pos_block, &blocks, &columns);
-  const size_t ctas = (size_t)device_sm_count();
+  const size_t ctas = 2 * (size_t)device_sm_count();  // (at most)
   Layout8 L{};
   L.part = round_up(ctas * sizeof(JoinItem), 256);
   L.total = round_up(L.part + 2 * ctas * columns * (s->D + 2) * sizeof(float), 256);
@@ -65,7 +65,7 @@ sv_status launch8(const TileArgs& A, const CUtensorMap& mk, const CUtensorMap& m
     if (e != cudaSuccess) return cuda_fail(e);
     ready.fetch_or(bit);
   }
-  const unsigned ctas = (unsigned)device_sm_count();
+  const unsigned ctas = S::CtasPerSm * (unsigned)device_sm_count();
   kernel<<<ctas, S::Threads, S::Smem, st>>>(mk, mk, mv, A, v);  // (queries come without a map)
   const sv_status s = launch_status();
   if (s != SV_OK) return s;
@@ -90,6 +90,7 @@ sv_status launch_columns8(int columns, const TileArgs& A, const CUtensorMap& mk,
   switch (columns) {
     case 16: return launch8<D, 16, kBf16>(A, mk, mv, v, st);
     case 32: return launch8<D, 32, kBf16>(A, mk, mv, v, st);
+    case 48: return launch8<D, D == 256 ? 32 : 48, kBf16>(A, mk, mv, v, st);
   }
   return launch8<D, D == 256 ? 32 : 64, kBf16>(A, mk, mv, v, st);
 }

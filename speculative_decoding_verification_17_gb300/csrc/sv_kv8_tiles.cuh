@@ -42,41 +42,45 @@ struct TileShape8 {
   static constexpr float Top = 7.984375f;  // log2 of the largest weight: below 2^8 when rounded
   static constexpr int UnitCols = D < 128 ? D : 128, RowBytes = UnitCols, UnitBytes = kTileKeys * RowBytes;
   static constexpr int U = D / UnitCols;
-  // teams as over 16 bits: two that take the pieces in turn at 16 columns, one beyond
-  static constexpr int Teams = N == 16 ? 2 : 1;
-  static constexpr int SoftWarps = 8;
+  // A softmax thread per key and 16 columns: a group of four warps for each 16. Two CTAs share an SM
+  // up to 32 columns (16 where D is 256), so that one's chain of a tile passes under the other's.
+  static constexpr int Teams = 1, Groups = N / 16, SoftWarps = 4 * Groups;
+  static constexpr int CtasPerSm = N == 16 || (N == 32 && D <= 128) ? 2 : 1;
   static constexpr int SoftThreads = 32 * SoftWarps;
-  // the softmax, then a warp each: key copies, scores, value copies, values, queries
+  // the softmax, then a warp each: key (and query) copies, scores, value copies, values
   static constexpr int KeyWarp = SoftWarps, ScoreWarp = KeyWarp + 1, CopyVWarp = KeyWarp + 2,
                        ValueWarp = KeyWarp + 3;
-  static constexpr int Threads = SoftThreads + 160;
-  static constexpr int TeamThreads = SoftThreads / Teams;
-  static constexpr int NC = Teams == 2 ? N : N / 2;  // columns per softmax thread
-  static constexpr int CH = 16;                      // of which at a time
-  static constexpr int QParts = kBf16 ? 2 : 3;       // e4m3 numbers of a query element
+  static constexpr int Threads = SoftThreads + 128;
+  static constexpr int TeamThreads = SoftThreads;
+  static constexpr int NC = 16, CH = 16;        // columns per softmax thread
+  static constexpr int QParts = kBf16 ? 2 : 3;  // e4m3 numbers of a query element
   static constexpr int QBytes = QParts * N * D;
   static constexpr int NQ = 2;
   static constexpr int Parts = 4;  // of a weight
   static constexpr int PBytes = Parts * kTileKeys * N;
-  static constexpr int NP = 2;
   static constexpr int kTables = 112 * N + 1792;
-  static constexpr int Room =
-      (kSmemMax - kTables - 1024 - NQ * QBytes - Teams * NP * PBytes) / UnitBytes;
+  static constexpr int kRoom = kSmemMax / CtasPerSm - (CtasPerSm == 2 ? 512 : 0) - kTables - 1024 -
+                               NQ * QBytes;
+  static constexpr int NP = (kRoom - 2 * PBytes) / UnitBytes >= 6 ? 2 : 1;
+  static constexpr int Room = (kRoom - NP * PBytes) / UnitBytes;
   static constexpr int NU = Room > 16 ? 16 : Room;
   static constexpr int NV = NU / 2, NK = NU - NV;
-  static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * UnitBytes;
+  static constexpr int Smem = 1024 + NQ * QBytes + NP * PBytes + NU * UnitBytes;
   static constexpr int MBlocks = (D + 127) / 128;
   static constexpr bool Wide = true;
   static constexpr int ON = Parts * N;
+  // two score buffers, whose two parts of the queries lie side by side (a third adds to the first)
+  static constexpr int OBase = 4 * N;
   // one set of accumulators where tensor memory has no room for two: a piece's output is then
   // written before the next one's first product
-  static constexpr int Outs = 2 * Teams * N + 2 * MBlocks * ON <= 512 ? 2 : 1;
-  static constexpr int TmemNeed = 2 * Teams * N + Outs * MBlocks * ON;
+  static constexpr int Outs = OBase + 2 * MBlocks * ON <= 512 / CtasPerSm ? 2 : 1;
+  static constexpr int TmemNeed = OBase + Outs * MBlocks * ON;
   static constexpr int TmemCols = TmemNeed <= 128 ? 128 : TmemNeed <= 256 ? 256 : 512;
   // a tile's bytes take half the time of one in 16 bits, a piece's start as long
   static constexpr int TileCost = 4;
-  static constexpr int PieceCost = (Teams == 2 ? 16 : 32) * 64 / D + 1;
-  static_assert(TmemNeed <= 512 && NV >= U && NK >= U && Smem + kTables <= kSmemMax, "tile shape");
+  static constexpr int PieceCost = 16 * 64 / D + 1;
+  static_assert(CtasPerSm * TmemCols <= 512 && NV >= U && NK >= U &&
+                CtasPerSm * (Smem + kTables) <= kSmemMax, "tile shape");
 };
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -100,84 +104,82 @@ template <class S>
 constexpr uint32_t kRows8 = 8 * S::RowBytes;
 
 // ---- the queries ---------------------------------------------------------------------------------
-// One warp reads each piece's query rows and leaves them as e4m3 numbers, part by part, in the
-// layout of the instruction's operand: rows of RowBytes, 16-byte pieces swapped by the row.
+// The warp that copies the keys reads each piece's query rows and leaves them as e4m3 numbers, part
+// by part (per unit of the row's columns), in the layout of the instruction's operand: rows of
+// RowBytes, 16-byte pieces swapped by the row. False when a wait failed.
 template <class S>
-__device__ __forceinline__ void query_role8(const TileArgs& A, TileShared<S>& sh,
-                                            unsigned char* qbuf) {
+__device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& sh,
+                                              unsigned char* qbuf, const Piece& p) {
   constexpr int kLanes = S::D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-  constexpr int kSteps = S::N / kPer, kBatch = kSteps < 8 ? kSteps : 8;
+  constexpr int kSteps = S::N / kPer, kBatch = kSteps % 8 == 0 ? 8 : 4;
+  static_assert(kSteps % kBatch == 0, "whole batches");
   const int lane = threadIdx.x & 31, col = lane % kLanes * 8;
-  Reader<S> reader(sh);
-  Piece p;
+  const int qs = p.turn % S::NQ, rows = p.live * A.G;
+  if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs],
+                                          ((uint32_t)(p.turn / S::NQ) & 1u) ^ 1u, &sh.waits)))
+    return false;
+  const uint16_t* q = static_cast<const uint16_t*>(A.q) + p.b * A.q_req + p.i0 * A.q_row +
+                      (int64_t)p.h * A.G * A.q_head + col;
+  unsigned char* buf = qbuf + qs * S::QBytes + col / S::UnitCols * (S::QParts * S::N * S::RowBytes);
 #pragma unroll 1
-  while (reader.template next<true>(p)) {
-    const int qs = p.turn % S::NQ, rows = p.live * A.G;
-    if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs],
-                                            ((uint32_t)(p.turn / S::NQ) & 1u) ^ 1u, &sh.waits)))
-      return;
-    const uint16_t* q = static_cast<const uint16_t*>(A.q) + p.b * A.q_req + p.i0 * A.q_row +
-                        (int64_t)p.h * A.G * A.q_head + col;
-    unsigned char* buf = qbuf + qs * S::QBytes + col / S::UnitCols * (S::N * S::RowBytes);
-#pragma unroll 1
-    for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
-      uint4 x[kBatch];
+  for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+    uint4 x[kBatch];
 #pragma unroll
-      for (int s = 0; s < kBatch; ++s) {
-        const int c = (s0 + s) * kPer + lane / kLanes, i = c / A.G;
-        x[s] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < rows)
-          x[s] = *reinterpret_cast<const uint4*>(q + i * A.q_row + (c - i * A.G) * A.q_head);
+    for (int s = 0; s < kBatch; ++s) {
+      const int c = (s0 + s) * kPer + lane / kLanes, i = c / A.G;
+      x[s] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < rows)
+        x[s] = *reinterpret_cast<const uint4*>(q + i * A.q_row + (c - i * A.G) * A.q_head);
+    }
+#pragma unroll
+    for (int s = 0; s < kBatch; ++s) {
+      const int c = (s0 + s) * kPer + lane / kLanes;
+      const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
+      // the row's largest magnitude, by its bits (those of what is not finite are the largest)
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+#pragma unroll
+      for (int o = kLanes / 2; o >= 1; o >>= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const bool odd = top >= (S::Bf16 ? 0x7f80u : 0x7c00u);
+      // 2^e <= top < 2^(e+1), e at least -100 (what is smaller counts as 0)
+      const int e = top == 0 ? 0 : max(-100, (int)(__float_as_uint(unpack16<S::Bf16>(top).x) >> 23) - 127);
+      const float up = odd ? 1.0f : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = unpack16<S::Bf16>(w[k]);
+        f[2 * k] = v.x * up;
+        f[2 * k + 1] = v.y * up;
       }
+      const uint32_t row = c * S::RowBytes + col % S::UnitCols;
+      const uint32_t at = row ^ ((row >> 7 & (S::RowBytes == 128 ? 7u : 3u)) << 4);
 #pragma unroll
-      for (int s = 0; s < kBatch; ++s) {
-        const int c = (s0 + s) * kPer + lane / kLanes;
-        const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-        // the row's largest magnitude, by its bits (those of what is not finite are the largest)
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
-#pragma unroll
-        for (int o = kLanes / 2; o >= 1; o >>= 1)
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const bool odd = top >= (S::Bf16 ? 0x7f80u : 0x7c00u);
-        // 2^e <= top < 2^(e+1), e at least -100 (what is smaller counts as 0)
-        const int e = top == 0 ? 0 : max(-100, (int)(__float_as_uint(unpack16<S::Bf16>(top).x) >> 23) - 127);
-        const float up = odd ? 1.0f : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
-        float f[8];
+      for (int part = 0; part < S::QParts; ++part) {
+        uint32_t out[2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 v = unpack16<S::Bf16>(w[k]);
-          f[2 * k] = v.x * up;
-          f[2 * k + 1] = v.y * up;
+          const __nv_fp8x2_storage_t b =
+              __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+          f[2 * k] -= back.x;
+          f[2 * k + 1] -= back.y;
+          out[k / 2] = k & 1 ? out[k / 2] | (uint32_t)b << 16 : (uint32_t)b;
         }
-        const uint32_t row = c * S::RowBytes + col % S::UnitCols;
-        const uint32_t at = row ^ ((row >> 7 & (S::RowBytes == 128 ? 7u : 3u)) << 4);
-#pragma unroll
-        for (int part = 0; part < S::QParts; ++part) {
-          uint32_t out[2];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const __nv_fp8x2_storage_t b =
-                __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
-            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-            f[2 * k] -= back.x;
-            f[2 * k + 1] -= back.y;
-            out[k / 2] = k & 1 ? out[k / 2] | (uint32_t)b << 16 : (uint32_t)b;
-          }
-          if (odd) out[0] = out[1] = 0x7f7f7f7fu;  // NaN
-          *reinterpret_cast<uint2*>(buf + part * (S::N * S::D) + at) = make_uint2(out[0], out[1]);
-        }
-        if (lane % kLanes == 0)
-          sh.q_scale[qs][c] = __uint_as_float((uint32_t)(127 - 7 + (odd ? 7 : e)) << 23);
+        if (odd) out[0] = out[1] = 0x7f7f7f7fu;  // NaN
+        *reinterpret_cast<uint2*>(buf + part * (S::N * S::RowBytes) + at) = make_uint2(out[0], out[1]);
       }
+      if (lane % kLanes == 0)
+        sh.q_scale[qs][c] = __uint_as_float((uint32_t)(127 - 7 + (odd ? 7 : e)) << 23);
     }
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_full[qs]);
   }
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.q_full[qs]);
+  return true;
 }
 
 // ---- the threads that issue the matrix instructions -------------------------------------------
@@ -185,39 +187,40 @@ __device__ __forceinline__ void query_role8(const TileArgs& A, TileShared<S>& sh
 template <class S>
 __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh,
                                             unsigned char* qbuf, unsigned char* ring) {
-  const uint32_t idesc = mma_desc8(false, 128, S::N);
+  const uint32_t idesc = mma_desc8(false, 128, 2 * S::N), third = mma_desc8(false, 128, S::N);
   const uint64_t rows = smem_desc(0, 16, kRows8<S>, kRowSwizzle<S>);
   const uint64_t a0 = rows + (smem_u32(ring) >> 4), b0 = rows + (smem_u32(qbuf) >> 4);
   Reader<S> reader(sh);
   RingPos at;
-  int used[2] = {0, 0};  // tiles so far per team
+  int y = 0;  // tiles so far
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
-    const int qs = p.turn % S::NQ, team = p.turn % S::Teams, tiles = p.mb - p.ma;
+    const int qs = p.turn % S::NQ, tiles = p.mb - p.ma;
     if (!wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits)) goto end;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      const int y = team ? used[1]++ : used[0]++, buf = y & 1;
-      if (!wait_phase(&sh.s_empty[team][buf], ((uint32_t)(y >> 1) & 1u) ^ 1u, &sh.waits)) goto end;
+    for (int i = 0; i < tiles; ++i, ++y) {
+      const int buf = y & 1;
+      if (!wait_phase(&sh.s_empty[0][buf], ((uint32_t)(y >> 1) & 1u) ^ 1u, &sh.waits)) goto end;
       tc_fence_after();
-      const uint32_t d = sh.tmem + (2 * team + buf) * S::N;
+      const uint32_t d = sh.tmem + buf * 2 * S::N;
       uint64_t b = b0 + qs * (S::QBytes >> 4);
 #pragma unroll 1
-      for (int c = 0; c < S::U; ++c, b += S::N * S::RowBytes >> 4) {
+      for (int c = 0; c < S::U; ++c, b += S::QParts * S::N * S::RowBytes >> 4) {
         if (!wait_phase(&sh.full[at.slot], at.phase, &sh.waits)) goto end;
         tc_fence_after();
         const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
 #pragma unroll
-        for (int part = 0; part < S::QParts; ++part)
+        for (int k = 0; k < S::RowBytes / 32; ++k) mma_f8(d, a + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
+        if (S::QParts == 3) {
 #pragma unroll
           for (int k = 0; k < S::RowBytes / 32; ++k)
-            mma_f8(d, a + 2 * k, b + part * (S::N * S::D >> 4) + 2 * k, idesc,
-                   c > 0 || part > 0 || k > 0);
+            mma_f8(d, a + 2 * k, b + (2 * S::N * S::RowBytes >> 4) + 2 * k, third, true);
+        }
         mma_commit(&sh.empty[at.slot]);
         at.next(S::NK);
       }
-      mma_commit(&sh.s_full[team][buf]);
+      mma_commit(&sh.s_full[0][buf]);
     }
     mma_commit(&sh.q_empty[qs]);
   }
@@ -237,15 +240,15 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
   const uint64_t b0 = smem_desc(0, kTileKeys * 32, 256, kSwizzle32) + (smem_u32(pbuf) >> 4);
   Reader<S> reader(sh);
   RingPos at;
-  int used[2] = {0, 0};
+  int y = 0;
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
-    const int team = p.turn % S::Teams, tiles = p.mb - p.ma;
-    const uint32_t o = sh.tmem + 2 * S::Teams * S::N + (p.turn & (S::Outs - 1)) * S::MBlocks * S::ON;
+    const int tiles = p.mb - p.ma;
+    const uint32_t o = sh.tmem + S::OBase + (p.turn & (S::Outs - 1)) * S::MBlocks * S::ON;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      const int y = team ? used[1]++ : used[0]++, pb = y % S::NP;
+    for (int i = 0; i < tiles; ++i, ++y) {
+      const int pb = y % S::NP;
       if (__builtin_expect(edge_tile(p, A.rule.window, tile_at<S>(p, i)), 0)) {
         RingPos look = at;
 #pragma unroll 1
@@ -253,10 +256,10 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
           if (!wait_phase(&sh.full[S::NK + look.slot], look.phase, &sh.waits)) goto end;
           look.next(S::NV);
         }
-        mbar_arrive(&sh.v_ready[team]);
+        mbar_arrive(&sh.v_ready[0]);
       }
-      if (!wait_phase(&sh.p_full[team][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits)) goto end;
-      const uint64_t b = b0 + (team * S::NP + pb) * (S::PBytes >> 4);
+      if (!wait_phase(&sh.p_full[0][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits)) goto end;
+      const uint64_t b = b0 + pb * (S::PBytes >> 4);
       uint32_t d = o;
 #pragma unroll 1
       for (int m = 0; m < S::MBlocks; ++m, d += S::ON) {
@@ -269,7 +272,7 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
         mma_commit(&sh.empty[S::NK + at.slot]);
         at.next(S::NV);
       }
-      mma_commit(&sh.pv_done[team][pb]);
+      mma_commit(&sh.pv_done[0][pb]);
     }
     mma_commit(&sh.o_done[p.turn & 1]);
   }
@@ -278,31 +281,42 @@ end:
 }
 
 // ---- the softmax threads ------------------------------------------------------------------------
-// The scales of the thread's key in a tile, loaded a tile ahead, and the page of the key after it.
+// The scales of the thread's key in the tile at hand, and the page of its key in the next one: each
+// loaded a tile before it is looked at.
 template <class S>
 struct KeyScales<S, true> {
-  float k, v;      // of the tile at hand
-  int64_t next;    // where those of the next tile lie; -1: none
+  float k, v;
+  int page;
 };
 
+// The page of the thread's key in the i-th tile of a piece, -1 where no row sees it.
 template <class S>
-__device__ __forceinline__ int64_t scale_of(const Attend<S>& me, const Piece& p, int i) {
-  const TileArgs& A = me.A;
+__device__ __forceinline__ int key_page(const Attend<S>& me, const Piece& p, int i) {
   const int j = tile_at<S>(p, i) * kTileKeys + me.key;
-  if (i >= p.mb - p.ma || j < p.first || j > p.last) return -1;
-  const int page = __ldg(A.table + (int64_t)p.b * A.max_pages + (j >> A.log_page));
-  if (page < 0 || page >= A.num_pages) return -1;
-  return scale_at(A, page, j & ((1 << A.log_page) - 1), p.h);
+  return i < p.mb - p.ma && j >= p.first && j <= p.last
+             ? __ldg(me.A.table + (int64_t)p.b * me.A.max_pages + (j >> me.A.log_page))
+             : -1;
+}
+// Its scales (0 without a page: what no row sees is masked, and a bad page makes the piece NaN).
+template <class S>
+__device__ __forceinline__ void load_scales(Attend<S>& me, const Piece& p, int i, int page) {
+  const TileArgs& A = me.A;
+  me.scales.k = me.scales.v = 0.0f;
+  if (page >= 0 && page < A.num_pages) {
+    const int j = tile_at<S>(p, i) * kTileKeys + me.key;
+    const int64_t at = scale_at(A, page, j & ((1 << A.log_page) - 1), p.h);
+    me.scales.k = __ldg(A.k_scale + at);
+    me.scales.v = __ldg(A.v_scale + at);
+  }
 }
 
 // The start of a piece: the columns' powers of two, and the scales of the first tile's keys.
 template <class S>
 __device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p) {
   auto& sh = me.sh;
-  const int64_t at = scale_of(me, p, 0);
-  me.scales.next = scale_of(me, p, 1);
-  me.scales.k = at < 0 ? 0.0f : __ldg(me.A.k_scale + at);
-  me.scales.v = at < 0 ? 0.0f : __ldg(me.A.v_scale + at);
+  const int page = key_page(me, p, 0);
+  me.scales.page = key_page(me, p, 1);
+  load_scales(me, p, 0, page);
   const int qs = p.turn % S::NQ;
   wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits);
 #pragma unroll 1
@@ -325,44 +339,43 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
                                            Two (&l)[S::NC / 2]) {
   const TileArgs& A = me.A;
   auto& sh = me.sh;
-  const int team = me.team, buf = y & 1, j = t * kTileKeys + me.key;
+  const int buf = y & 1, j = t * kTileKeys + me.key;
   const bool edge = edge_tile(p, A.rule.window, t);
-  unsigned char* const pb = me.pbuf + (team * S::NP + y % S::NP) * S::PBytes + me.key * 32;
-  const float* columns = sh.column_scale[S::Teams == 2 ? team : p.turn & 1];
-  // (every team thread has read the queries' scales by now: the barriers around set_columns)
+  unsigned char* const pb = me.pbuf + y % S::NP * S::PBytes + me.key * 32;
+  const float* columns = sh.column_scale[p.turn & 1];
+  // (every softmax thread has read the queries' scales by now: the barriers around set_columns)
   if (i == 0 && me.me == 0) mbar_arrive(&sh.q_empty[p.turn % S::NQ]);
   float ks = me.scales.k, vs = me.scales.v;
-  const int64_t at = me.scales.next;
-  me.scales.k = at < 0 ? 0.0f : __ldg(A.k_scale + at);
-  me.scales.v = at < 0 ? 0.0f : __ldg(A.v_scale + at);
-  me.scales.next = scale_of(me, p, i + 2);
+  load_scales(me, p, i + 1, me.scales.page);
+  me.scales.page = key_page(me, p, i + 2);
   if (!(vs >= 0.0f && vs <= kMaxScale && fabsf(ks) < INFINITY)) {
     ks = __uint_as_float(0x7fc00000u);
     vs = 1.0f;
   }
   const float lv = vs < 1.0f / kMaxScale ? -40.0f : __log2f(vs);
   const float unit = vs * 0.00390625f;  // (the largest weight possible below 1)
-  wait_phase(&sh.s_full[team][buf], (uint32_t)(y >> 1) & 1u, &sh.waits);
+  wait_phase(&sh.s_full[0][buf], (uint32_t)(y >> 1) & 1u, &sh.waits);
   tc_fence_after();
-#pragma unroll
-  for (int k = 0; k < S::NC; k += S::CH) {
-    const int c0 = me.col0 + k;
+  const int c0 = me.col0;
+  {
     float s[S::CH];
-    tmem_ld16(me.lane_base + (2 * team + buf) * S::N + c0, s);
-    tmem_wait_ld();
-    if (k + S::CH == S::NC) {
-      tc_fence_before();
-      mbar_arrive(&sh.s_empty[team][buf]);
-    }
-    float scale = A.rule.scale * kLog2e * ks;  // to what the thread holds in s
+    Two e[S::CH / 2];
+    {
+      float low[S::CH];
+      tmem_ld16(me.lane_base + buf * 2 * S::N + c0, s);
+      tmem_ld16(me.lane_base + buf * 2 * S::N + S::N + c0, low);
+      tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < S::CH; c += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(&columns[c0 + c]);
-      s[c] *= q.x;
-      s[c + 1] *= q.y;
-      s[c + 2] *= q.z;
-      s[c + 3] *= q.w;
+      for (int c = 0; c < S::CH; c += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(&columns[c0 + c]);
+        const float2 a = split(two_mul(two_add(two(s[c], s[c + 1]), two(low[c], low[c + 1])), two(q.x, q.y)));
+        const float2 b = split(two_mul(two_add(two(s[c + 2], s[c + 3]), two(low[c + 2], low[c + 3])), two(q.z, q.w)));
+        s[c] = a.x, s[c + 1] = a.y, s[c + 2] = b.x, s[c + 3] = b.y;
+      }
     }
+    tc_fence_before();
+    mbar_arrive(&sh.s_empty[0][buf]);
+    float scale = A.rule.scale * kLog2e * ks;  // to what the thread holds in s
     if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
 #pragma unroll
       for (int c = 0; c < S::CH; ++c) s[c] *= ks;
@@ -374,7 +387,6 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
           if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[c] = -INFINITY;
       }
     }
-    Two e[S::CH / 2];
     auto exponents = [&]() {
       const Two sc = two(scale, scale);
 #pragma unroll
@@ -395,7 +407,7 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
       if (i > 0) me.wait_values(y - 1);
 #pragma unroll
       for (int c = 0; c < S::CH; ++c) s[c] = fmaf(s[c], scale, lv);
-      me.raise(T, s, l, k, i == 0, me.output(p.turn));
+      me.raise(T, s, l, 0, i == 0, me.output(p.turn));
 #pragma unroll
       for (int c = 0; c < S::CH; ++c) s[c] -= lv;
       scale = 1.0f;
@@ -407,7 +419,7 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
     for (int c = 0; c < S::CH / 2; ++c) {
       const float2 v = split(e[c]);
       const Two w = two(ex2(v.x), ex2(v.y));
-      l[k / 2 + c] = two_add(l[k / 2 + c], w);
+      l[c] = two_add(l[c], w);
       const Two y2 = two_mul(w, unit2);
       const float2 yf = split(y2);
       const __half2 h = __floats2half2_rn(yf.x, yf.y);
@@ -428,7 +440,7 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
       part[2][c] = *reinterpret_cast<const uint32_t*>(&r);
     }
     // the product that last read this buffer
-    if (k == 0 && y >= S::NP) me.wait_values(y - S::NP);
+    if (y >= S::NP) me.wait_values(y - S::NP);
     // 32 columns of a key are 32 bytes, their 16-byte halves swapped in every other 4 keys
 #pragma unroll
     for (int q = 0; q < S::Parts; ++q) {
@@ -444,12 +456,12 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
     }
   }
   if (__builtin_expect(edge, 0)) {
-    wait_phase(&sh.v_ready[team], (uint32_t)(me.edges++) & 1u, &sh.waits);
-    if (S::Teams == 2 || me.group == 0) me.clean_values(T, p, x, j);
+    wait_phase(&sh.v_ready[0], (uint32_t)(me.edges++) & 1u, &sh.waits);
+    if (me.group == 0) me.clean_values(T, p, x, j);
   }
   fence_proxy_async();
   tc_fence_before();
-  mbar_arrive(&sh.p_full[team][y % S::NP]);
+  mbar_arrive(&sh.p_full[0][y % S::NP]);
 }
 
 // The outputs that NaN codes among the values of partly visible keys make NaN (those codes went to

@@ -156,6 +156,8 @@ struct TileShape {
   static constexpr int Smem = 1024 + NQ * QBytes + Teams * NP * PBytes + NU * kUnitBytes;
   static constexpr int MBlocks = kWeigh ? 0 : (D + 127) / 128;  // accumulators of 128 of D
   static constexpr int Outs = 2;  // sets of them
+  static constexpr int OBase = 2 * Teams * N;  // the first one's column in tensor memory
+  static constexpr int Groups = 2, CtasPerSm = 1;
   // Two score buffers per team, two outputs. Where tensor memory has room, the products with the
   // parts of the weights are one instruction of as many times the columns (the values, whose read
   // from shared memory bounds a narrow instruction, are read once) and are added at the end; else
@@ -456,7 +458,7 @@ struct TileShared : QueryScales<S::Quant, S::N> {
   // the pieces, from the warp that walks the work list to the other roles
   Piece piece[kPieceQueue];
   uint64_t piece_full[kPieceQueue], piece_empty[kPieceQueue];
-  int64_t scratch[16];
+  int64_t scratch[S::Threads / 32];
   Start start;
   struct Table {
     alignas(16) float m[S::N];       // lift - the running maximum, or minus the row's lse (log2)
@@ -553,6 +555,11 @@ __device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int
   }
 }
 
+// (8 bits) A piece's query rows as the instruction takes them (sv_kv8_tiles.cuh).
+template <class S>
+__device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& sh,
+                                              unsigned char* qbuf, const Piece& p);
+
 // ---- the copying warps ------------------------------------------------------------------------
 // Whether some row sees a key of the lane's group of `box` keys in a tile, and that group's page
 // (not looked at here: the load is a tile ahead of its use).
@@ -607,6 +614,11 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll 1
   while (more) {
     const int head = p.h, turn = p.turn;
+    const bool first = i == 0;
+    Piece at_hand;
+    if constexpr (S::Quant && !kValues) {
+      if (first) at_hand = p;
+    }
     const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
     if (!S::Quant && !kValues && i == 0) {
       const int qs = turn % S::NQ;
@@ -650,6 +662,10 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
       if (mine)
         tile_g2s(dst + at.slot * S::UnitBytes, map, full, c * S::UnitCols, slot, head, page);
       at.next(kUnits);
+    }
+    if constexpr (S::Quant && !kValues) {
+      // a piece's queries, once its first keys are on their way
+      if (first && !give_queries8<S>(A, sh, qbuf, at_hand)) goto end;
     }
     page = next_page;
     seen = next_seen;
@@ -741,7 +757,7 @@ __device__ __forceinline__ void value_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll 1
   while (reader.template next<false>(p)) {
     const int team = p.turn % S::Teams, tiles = p.mb - p.ma;
-    const uint32_t o = sh.tmem + 2 * S::Teams * S::N + (p.turn & 1) * S::MBlocks * S::ON;
+    const uint32_t o = sh.tmem + S::OBase + (p.turn & 1) * S::MBlocks * S::ON;
 #pragma unroll 1
     for (int i = 0; i < tiles; ++i) {
       const int y = team ? used[1]++ : used[0]++, pb = y % S::NP;
@@ -944,8 +960,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w) {
   return S::Quant ? not_finite4(w) : not_finite2<S::Bf16>(w);
 }
 
-// Named barriers: 1 and 2 for the two groups of softmax warps, 3 for all of them.
-constexpr int kAllBar = 3;
+// Named barriers: from 1 on for the groups of softmax warps, the one after them for all.
+template <class S>
+constexpr int kAllBar = 1 + S::Groups;
 
 // The log-sum-exp of a row from m (its maximum less the lift) and its lifted sum.
 template <bool kBf16>
@@ -1047,11 +1064,11 @@ struct Attend {
   }
   __device__ __forceinline__ void group_sync() const { bar_sync(1 + group, 128); }
   __device__ __forceinline__ void team_sync() const {
-    bar_sync(S::Teams == 2 ? 1 + group : kAllBar, S::TeamThreads);
+    bar_sync(S::Teams == 2 ? 1 + group : kAllBar<S>, S::TeamThreads);
   }
   // The accumulator of a piece, the group's first column.
   __device__ __forceinline__ uint32_t output(int turn) const {
-    return lane_base + 2 * S::Teams * S::N + (turn & (S::Outs - 1)) * S::MBlocks * S::ON + col0;
+    return lane_base + S::OBase + (turn & (S::Outs - 1)) * S::MBlocks * S::ON + col0;
   }
 
   // Raise the maxima of the CH columns from c0 to those of this tile's scores s, and scale what
@@ -1346,7 +1363,7 @@ struct Attend {
             p = reader.wait();
             more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.waits.dead;
             more = !bar_or(1 + group, 128, !more);
-            if (S::Teams == 1) more = !bar_or(kAllBar, S::SoftThreads, !more);
+            if (S::Teams == 1) more = !bar_or(kAllBar<S>, S::SoftThreads, !more);
             if (!more) break;
             reader.release(lane == 0);
             if (p.turn % S::Teams == team) break;
@@ -1408,7 +1425,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
   for (;;) {
     p = reader.wait();
     bool more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.waits.dead;
-    more = !bar_or(kAllBar, S::SoftThreads, !more);  // (the last piece's tables have been read)
+    more = !bar_or(kAllBar<S>, S::SoftThreads, !more);  // (the last piece's tables have been read)
     if (!more) return;
     reader.release(lane == 0);
     const int64_t row = ((int64_t)p.b * A.Hkv + p.h) * A.stride;
@@ -1418,7 +1435,7 @@ __device__ __forceinline__ void weigh_role(const TileArgs& A, TileShared<S>& sh)
     const bool fresh = p.flags & kFresh;
     {
       set_columns<S>(A, T, p, threadIdx.x, S::SoftThreads);
-      bar_sync(kAllBar, S::SoftThreads);
+      bar_sync(kAllBar<S>, S::SoftThreads);
       const int ta = fresh ? p.ta : p.ma, tb = fresh ? p.tb : p.mb;
       // the columns from here on are of rows that do not count, or of none: their products may be
       // anything (a zero query times an infinite key is NaN)
@@ -1558,11 +1575,7 @@ template <class S>
 __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh,
                                             unsigned char* pbuf, unsigned char* ring);
 template <class S>
-__device__ __forceinline__ void query_role8(const TileArgs& A, TileShared<S>& sh,
-                                            unsigned char* qbuf);
-
-template <class S>
-__global__ void __launch_bounds__(S::Threads, 1)
+__global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
     tile_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ TileArgs A,
                 const __grid_constant__ ValuePool vpool) {
@@ -1601,8 +1614,8 @@ __global__ void __launch_bounds__(S::Threads, 1)
     mbar_init(&sh.o_done[1], 1);
     for (int s = 0; s < kPieceQueue; ++s) {
       mbar_init(&sh.piece_full[s], 1);
-      // taken by the softmax warps, the issuing threads, the value copies and (8 bits) the queries' warp
-      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : 3) + S::Quant);
+      // taken by the softmax warps, the issuing threads and the value copies
+      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : 3));
     }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
@@ -1664,8 +1677,6 @@ __global__ void __launch_bounds__(S::Threads, 1)
     __syncwarp();
   } else if constexpr (S::Weigh) {
     weigh_role<S>(A, sh);
-  } else if (S::Quant && warp == S::SoftWarps + 4) {
-    if constexpr (S::Quant) query_role8<S>(A, sh, qbuf);
   } else {
     const int lane = tid & 31, quarter = warp & 3, group = warp >> 2;
     const int team = S::Teams == 2 ? group : 0;
