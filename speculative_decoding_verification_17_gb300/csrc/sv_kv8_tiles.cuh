@@ -38,8 +38,7 @@ template <int kD, int kN, bool kBf16>
 struct TileShape8 {
   static constexpr int D = kD, N = kN;
   static constexpr bool Bf16 = kBf16, Weigh = false, Quant = true;  // (the queries' and outputs' type)
-  static constexpr float Lift = 5.0f;
-  static constexpr float Top = 7.984375f;  // log2 of the largest weight: below 2^8 when rounded
+  static constexpr float Lift = 12.0f, Top = 15.875f;  // log2 of the largest weight when the maximum moves, and at most
   static constexpr int UnitCols = D < 128 ? D : 128, RowBytes = UnitCols, UnitBytes = kTileKeys * RowBytes;
   static constexpr int U = D / UnitCols;
   // A softmax thread per key and 16 columns: a group of four warps for each 16. Two CTAs share an SM
@@ -92,9 +91,9 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
       "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
-// The instruction descriptor: fp32 accumulator, both operands e4m3.
-__device__ __forceinline__ uint32_t mma_desc8(bool mn, int M, int N) {
-  return 1u << 4 | (mn ? 3u << 15 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+// The instruction descriptor: fp32 accumulator, A of e4m3, B of e4m3 or e5m2.
+__device__ __forceinline__ uint32_t mma_desc8(bool mn, bool b_e5m2, int M, int N) {
+  return 1u << 4 | (b_e5m2 ? 1u << 10 : 0u) | (mn ? 3u << 15 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 constexpr uint32_t kSwizzle64 = 4;
 // Operand rows of RowBytes bytes: their swizzle, and the bytes of eight of them.
@@ -187,7 +186,8 @@ __device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& 
 template <class S>
 __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh,
                                             unsigned char* qbuf, unsigned char* ring) {
-  const uint32_t idesc = mma_desc8(false, 128, 2 * S::N), third = mma_desc8(false, 128, S::N);
+  const uint32_t idesc = mma_desc8(false, false, 128, 2 * S::N),
+                 third = mma_desc8(false, false, 128, S::N);
   const uint64_t rows = smem_desc(0, 16, kRows8<S>, kRowSwizzle<S>);
   const uint64_t a0 = rows + (smem_u32(ring) >> 4), b0 = rows + (smem_u32(qbuf) >> 4);
   Reader<S> reader(sh);
@@ -232,7 +232,7 @@ end:
 template <class S>
 __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh,
                                             unsigned char* pbuf, unsigned char* ring) {
-  const uint32_t idesc = mma_desc8(true, 128, S::ON);
+  const uint32_t idesc = mma_desc8(true, true, 128, S::ON);
   // (with D = 64 both halves of the instruction's rows read the same columns, and the upper half is
   // not used)
   const uint64_t a0 = smem_desc(0, 0, kRows8<S>, kRowSwizzle<S>) +
@@ -328,9 +328,11 @@ __device__ __forceinline__ Two two_mul(Two a, Two b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
-// Four e4m3 codes, which lie in bits 7 to 14 of the halves of a and b.
-__device__ __forceinline__ uint32_t codes4(uint32_t a, uint32_t b) {
-  return __byte_perm(a + a, b + b, 0x7531);
+// The scores of a thread's key under the rule, in place (out of line: few calls have one).
+template <class S>
+__device__ __noinline__ void apply_rule8(float* s, const ScoreRule& r, float away, const float* slope,
+                                         const float* ahead) {
+  apply_rule<S::CH>(*reinterpret_cast<float(*)[S::CH]>(s), r, away, slope, ahead);
 }
 
 template <class S>
@@ -353,7 +355,6 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
     vs = 1.0f;
   }
   const float lv = vs < 1.0f / kMaxScale ? -40.0f : __log2f(vs);
-  const float unit = vs * 0.00390625f;  // (the largest weight possible below 1)
   wait_phase(&sh.s_full[0][buf], (uint32_t)(y >> 1) & 1u, &sh.waits);
   tc_fence_after();
   const int c0 = me.col0;
@@ -379,7 +380,17 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
     if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
 #pragma unroll
       for (int c = 0; c < S::CH; ++c) s[c] *= ks;
-      apply_rule<S::CH>(s, A.rule, (float)(p.pos0 - j), &T.slope[c0], &T.ahead[c0]);
+      if (A.rule.softcap > 0.0f || A.rule.slopes) {
+        float held[S::CH];
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) held[c] = s[c];
+        apply_rule8<S>(held, A.rule, (float)(p.pos0 - j), &T.slope[c0], &T.ahead[c0]);
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) s[c] = held[c];
+      } else {
+#pragma unroll
+        for (int c = 0; c < S::CH; ++c) s[c] *= A.rule.scale * kLog2e;
+      }
       scale = 1.0f;
       if (edge) {
 #pragma unroll
@@ -413,31 +424,23 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
       scale = 1.0f;
       exponents();
     }
-    uint32_t part[3][S::CH / 2], rest[S::CH / 4];
-    const Two unit2 = two(unit, unit);
+    uint32_t part[S::Parts][S::CH / 2];
+    // (what is below the last part's step of 2^-16 is rounded)
+    const Two unit2 = two(vs, vs), half2 = two(7.62939453125e-6f, 7.62939453125e-6f);
 #pragma unroll
     for (int c = 0; c < S::CH / 2; ++c) {
       const float2 v = split(e[c]);
       const Two w = two(ex2(v.x), ex2(v.y));
       l[c] = two_add(l[c], w);
-      const Two y2 = two_mul(w, unit2);
-      const float2 yf = split(y2);
-      const __half2 h = __floats2half2_rn(yf.x, yf.y);
-      const float2 back = __half22float2(h);
-      const float2 left = split(two_mul(two_fma(two(back.x, back.y), two(-1.0f, -1.0f), y2),
-                                        two(1048576.0f, 1048576.0f)));
-      const uint32_t b =
-          __nv_cvt_float2_to_fp8x2(make_float2(left.x, left.y), __NV_SATFINITE, __NV_E4M3);
-      rest[c / 2] = c & 1 ? rest[c / 2] | b << 16 : b;
-      // y is at most 1, so its e4m3 digits of exponent -8 are bits 7 .. 14 as they are
-      const __half2 sixteen = __float2half2_rn(16.0f);
-      uint32_t d = *reinterpret_cast<const uint32_t*>(&h) & 0xff80ff80u;
-      part[0][c] = d;
-      __half2 r = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&d)), sixteen);
-      d = *reinterpret_cast<const uint32_t*>(&r) & 0xff80ff80u;
-      part[1][c] = d;
-      r = __hmul2(__hsub2(r, *reinterpret_cast<const __half2*>(&d)), sixteen);
-      part[2][c] = *reinterpret_cast<const uint32_t*>(&r);
+      const float2 y2 = split(two_fma(w, unit2, half2));
+      __half2 r = __floats2half2_rn(y2.x, y2.y);
+#pragma unroll
+      for (int q = 0; q < S::Parts; ++q) {
+        // the upper byte of an fp16 number is an e5m2 number: what is left has three bits less
+        const uint32_t bits = *reinterpret_cast<const uint32_t*>(&r), top3 = bits & 0xff00ff00u;
+        part[q][c] = bits;
+        if (q + 1 < S::Parts) r = __hsub2(r, *reinterpret_cast<const __half2*>(&top3));
+      }
     }
     // the product that last read this buffer
     if (y >= S::NP) me.wait_values(y - S::NP);
@@ -445,14 +448,10 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
 #pragma unroll
     for (int q = 0; q < S::Parts; ++q) {
       const int n = q * S::N + c0;
-      uint4 v;
-      if (q < 3)
-        v = make_uint4(codes4(part[q][0], part[q][1]), codes4(part[q][2], part[q][3]),
-                       codes4(part[q][4], part[q][5]), codes4(part[q][6], part[q][7]));
-      else
-        v = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-      *reinterpret_cast<uint4*>(pb + n / 32 * (kTileKeys * 32) +
-                                ((n / 16 ^ me.key >> 2) & 1) * 16) = v;
+      const uint32_t* w = part[q];
+      *reinterpret_cast<uint4*>(pb + n / 32 * (kTileKeys * 32) + ((n / 16 ^ me.key >> 2) & 1) * 16) =
+          make_uint4(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531),
+                     __byte_perm(w[4], w[5], 0x7531), __byte_perm(w[6], w[7], 0x7531));
     }
   }
   if (__builtin_expect(edge, 0)) {

@@ -1300,15 +1300,13 @@ struct Attend {
           tmem_ld16(output(p.turn) + m * S::ON + q, o);
           tmem_wait_ld();
           if (S::Wide) {
-            float unit = 1.0f;  // (8 bits: each part is given 16 times its size)
 #pragma unroll 1
             for (int part = 1; part < S::Parts; ++part) {
               float low[16];
               tmem_ld16(output(p.turn) + m * S::ON + part * S::N + q, low);
               tmem_wait_ld();
-              if (S::Quant) unit *= 0.0625f;
 #pragma unroll
-              for (int c = 0; c < 16; ++c) o[c] = S::Quant ? fmaf(low[c], unit, o[c]) : o[c] + low[c];
+              for (int c = 0; c < 16; ++c) o[c] += low[c];
             }
           }
           const int n0 = col0 + q;
