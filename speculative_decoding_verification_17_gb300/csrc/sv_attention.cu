@@ -34,7 +34,8 @@ EncodeFn encoder() {
 }  // namespace
 
 sv_status encode_tiles(CUtensorMap* map, const void* data, CUtensorMapDataType type, int size,
-                       CUtensorMapSwizzle swizzle, const uint64_t (&dims)[4],
+                       CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                       const uint64_t (&dims)[4],
                        const int64_t (&strides)[3], const uint32_t (&box)[4]) {
   const EncodeFn f = encoder();
   if (!f) return cuda_fail(cudaErrorSymbolNotFound);
@@ -48,7 +49,7 @@ sv_status encode_tiles(CUtensorMap* map, const void* data, CUtensorMapDataType t
   // a dimension of one element is never stepped along: any stride will do
   for (int i = 0; i < 3; ++i) s[i] = dims[i + 1] == 1 ? 16 : (cuuint64_t)strides[i] * size;
   const CUresult r = f(map, type, 4, const_cast<void*>(data), d, s, b, ones,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SV_OK : cuda_fail(cudaErrorInvalidValue);
 }
@@ -57,7 +58,8 @@ sv_status encode_map(CUtensorMap* map, const void* data, bool bf16, const uint64
                      const int64_t (&strides)[3], const uint32_t (&box)[4]) {
   return encode_tiles(map, data,
                       bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                      CU_TENSOR_MAP_SWIZZLE_128B, dims, strides, box);
+                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, dims, strides,
+                      box);
 }
 
 sv_status encode_pool(CUtensorMap* map, const sv_kv_shape* s, const sv_kv_pool* pool) {

@@ -44,6 +44,7 @@ sv_status encode_pool8(CUtensorMap* map, const sv_kv_shape* s, const sv_kv_pool*
   const uint32_t box = s->page_size < kTileKeys ? s->page_size : kTileKeys;
   return encode_tiles(map, pool->data, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1,
                       s->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                       {(uint64_t)s->D, (uint64_t)s->page_size, (uint64_t)s->Hkv,
                        (uint64_t)(s->num_pages > 0 ? s->num_pages : 1)},
                       {pool->token_stride, pool->head_stride, pool->page_stride},

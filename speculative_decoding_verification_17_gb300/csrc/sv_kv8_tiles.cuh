@@ -328,6 +328,14 @@ __device__ __forceinline__ Two two_mul(Two a, Two b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
   return v;
 }
+// One arrival per warp: those of single threads queue up (384 of them on two barriers per tile were a
+// third of the time of the long caches).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // The scores of a thread's key under the rule, in place (out of line: few calls have one).
 template <class S>
 __device__ __noinline__ void apply_rule8(float* s, const ScoreRule& r, float away, const float* slope,
@@ -374,8 +382,7 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
         s[c] = a.x, s[c + 1] = a.y, s[c + 2] = b.x, s[c + 3] = b.y;
       }
     }
-    tc_fence_before();
-    mbar_arrive(&sh.s_empty[0][buf]);
+    warp_arrive(&sh.s_empty[0][buf], me.lane);
     float scale = A.rule.scale * kLog2e * ks;  // to what the thread holds in s
     if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
 #pragma unroll
@@ -459,8 +466,7 @@ __device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>
     if (me.group == 0) me.clean_values(T, p, x, j);
   }
   fence_proxy_async();
-  tc_fence_before();
-  mbar_arrive(&sh.p_full[0][y % S::NP]);
+  warp_arrive(&sh.p_full[0][y % S::NP], me.lane);
 }
 
 // The outputs that NaN codes among the values of partly visible keys make NaN (those codes went to

@@ -1600,10 +1600,10 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
     for (int t = 0; t < S::Teams; ++t) {
       for (int s = 0; s < 2; ++s) {
         mbar_init(&sh.s_full[t][s], 1);
-        mbar_init(&sh.s_empty[t][s], S::Weigh ? 128 : S::TeamThreads);
+        mbar_init(&sh.s_empty[t][s], S::Weigh ? 128 : S::Quant ? S::SoftWarps : S::TeamThreads);
       }
       for (int s = 0; s < S::NP; ++s) {
-        mbar_init(&sh.p_full[t][s], S::TeamThreads);
+        mbar_init(&sh.p_full[t][s], S::Quant ? S::SoftWarps : S::TeamThreads);
         mbar_init(&sh.pv_done[t][s], 1);
       }
     }
@@ -1761,7 +1761,8 @@ int device_sm_count();
 
 // A 4-D tensor map of elements of `size` bytes.
 sv_status encode_tiles(CUtensorMap* map, const void* data, CUtensorMapDataType type, int size,
-                       CUtensorMapSwizzle swizzle, const uint64_t (&dims)[4],
+                       CUtensorMapSwizzle swizzle, CUtensorMapL2promotion promotion,
+                       const uint64_t (&dims)[4],
                        const int64_t (&strides)[3], const uint32_t (&box)[4]);
 // Of 16-bit elements, 64 wide boxes of 128-byte swizzled rows.
 sv_status encode_map(CUtensorMap* map, const void* data, bool bf16, const uint64_t (&dims)[4],
