@@ -17,7 +17,7 @@ void row_blocks8(const sv_kv_shape* s, int* pos_block, int* blocks, int* columns
   *blocks = (s->P + most - 1) / most;
   *pos_block = (s->P + *blocks - 1) / *blocks;
   const int rows = G * *pos_block;
-  *columns = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
+  *columns = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 sv_status check_shape8(const sv_kv_shape* s) {
@@ -89,6 +89,7 @@ template <int D, bool kBf16>
 sv_status launch_columns8(int columns, const TileArgs& A, const CUtensorMap& mk,
                           const CUtensorMap& mv, const ValuePool& v, cudaStream_t st) {
   switch (columns) {
+    case 8: return launch8<D, 8, kBf16>(A, mk, mv, v, st);
     case 16: return launch8<D, 16, kBf16>(A, mk, mv, v, st);
     case 32: return launch8<D, 32, kBf16>(A, mk, mv, v, st);
     case 48: return launch8<D, D == 256 ? 32 : 48, kBf16>(A, mk, mv, v, st);

@@ -41,35 +41,37 @@ struct TileShape8 {
   static constexpr float Lift = 12.0f, Top = 15.875f;  // log2 of the largest weight when the maximum moves, and at most
   static constexpr int UnitCols = D < 128 ? D : 128, RowBytes = UnitCols, UnitBytes = kTileKeys * RowBytes;
   static constexpr int U = D / UnitCols;
-  // A softmax thread per key and 16 columns: a group of four warps for each 16. Two CTAs share an SM
-  // up to 32 columns (16 where D is 256), so that one's chain of a tile passes under the other's.
-  static constexpr int Teams = 1, Groups = N / 16, SoftWarps = 4 * Groups;
-  static constexpr int CtasPerSm = N == 16 || (N == 32 && D <= 128) ? 2 : 1;
+  // Softmax threads take a key and 16 columns (8 where there are no more) of two tiles at a time: a
+  // group of four warps for each 16. Two CTAs share an SM up to 16 columns, so that one's chain of
+  // dependent steps passes under the other's.
+  static constexpr int Teams = 1, Groups = N == 8 ? 1 : N / 16, SoftWarps = 4 * Groups;
+  static constexpr int CtasPerSm = N <= 16 ? 2 : 1;
   static constexpr int SoftThreads = 32 * SoftWarps;
   // the softmax, then a warp each: key (and query) copies, scores, value copies, values
   static constexpr int KeyWarp = SoftWarps, ScoreWarp = KeyWarp + 1, CopyVWarp = KeyWarp + 2,
                        ValueWarp = KeyWarp + 3;
   static constexpr int Threads = SoftThreads + 128;
   static constexpr int TeamThreads = SoftThreads;
-  static constexpr int NC = 16, CH = 16;        // columns per softmax thread
-  static constexpr int QParts = kBf16 ? 2 : 3;  // e4m3 numbers of a query element
-  static constexpr int QBytes = QParts * N * D;
+  static constexpr int NC = N == 8 ? 8 : 16, CH = NC;  // columns per softmax thread
+  // e4m3 numbers of a query element, and how many of them are columns of the score instruction (whose
+  // columns are a multiple of 16): a third is added in a pass of its own, or beside a row of zeros
+  static constexpr int QParts = kBf16 ? 2 : 3, QWide = N == 8 && !kBf16 ? 4 : 2;
+  static constexpr int QRows = QParts > QWide ? QParts : QWide;  // parts in the buffer
+  static constexpr int QBytes = QRows * N * D;
   static constexpr int NQ = 2;
   static constexpr int Parts = 4;  // of a weight
-  static constexpr int PBytes = Parts * kTileKeys * N;
-  static constexpr int kTables = 112 * N + 1792;
+  static constexpr int PTile = Parts * kTileKeys * N, PBytes = 2 * PTile, NP = 1;
+  static constexpr int kTables = 112 * N + 1920;
   static constexpr int kRoom = kSmemMax / CtasPerSm - (CtasPerSm == 2 ? 512 : 0) - kTables - 1024 -
-                               NQ * QBytes;
-  static constexpr int NP = (kRoom - 2 * PBytes) / UnitBytes >= 6 ? 2 : 1;
-  static constexpr int Room = (kRoom - NP * PBytes) / UnitBytes;
-  static constexpr int NU = Room > 16 ? 16 : Room;
+                               NQ * QBytes - PBytes;
+  static constexpr int NU = kRoom / UnitBytes > 16 ? 16 : kRoom / UnitBytes;
   static constexpr int NV = NU / 2, NK = NU - NV;
-  static constexpr int Smem = 1024 + NQ * QBytes + NP * PBytes + NU * UnitBytes;
+  static constexpr int Smem = 1024 + NQ * QBytes + PBytes + NU * UnitBytes;
   static constexpr int MBlocks = (D + 127) / 128;
   static constexpr bool Wide = true;
   static constexpr int ON = Parts * N;
-  // two score buffers, whose two parts of the queries lie side by side (a third adds to the first)
-  static constexpr int OBase = 4 * N;
+  // a score buffer of two tiles, read into registers before the next ones need it
+  static constexpr int SN = QWide * N, OBase = 2 * SN;
   // one set of accumulators where tensor memory has no room for two: a piece's output is then
   // written before the next one's first product
   static constexpr int Outs = OBase + 2 * MBlocks * ON <= 512 / CtasPerSm ? 2 : 1;
@@ -81,6 +83,14 @@ struct TileShape8 {
   static_assert(CtasPerSm * TmemCols <= 512 && NV >= U && NK >= U &&
                 CtasPerSm * (Smem + kTables) <= kSmemMax, "tile shape");
 };
+
+// The tiles of a piece that go together from its i-th on: two, but one alone where some row does not
+// see some key of either, and at the end of an odd number.
+template <class S>
+__device__ __forceinline__ int tiles_at(const Piece& p, int window, int i) {
+  return i + 1 < p.mb - p.ma && !edge_tile(p, window, tile_at<S>(p, i)) &&
+         !edge_tile(p, window, tile_at<S>(p, i + 1)) ? 2 : 1;
+}
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
@@ -110,7 +120,8 @@ template <class S>
 __device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& sh,
                                               unsigned char* qbuf, const Piece& p) {
   constexpr int kLanes = S::D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-  constexpr int kSteps = S::N / kPer, kBatch = kSteps % 8 == 0 ? 8 : 4;
+  constexpr int kSteps = S::N / kPer;
+  constexpr int kBatch = kSteps % 8 == 0 ? 8 : kSteps % 4 == 0 ? 4 : 2;
   static_assert(kSteps % kBatch == 0, "whole batches");
   const int lane = threadIdx.x & 31, col = lane % kLanes * 8;
   const int qs = p.turn % S::NQ, rows = p.live * A.G;
@@ -119,7 +130,7 @@ __device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& 
     return false;
   const uint16_t* q = static_cast<const uint16_t*>(A.q) + p.b * A.q_req + p.i0 * A.q_row +
                       (int64_t)p.h * A.G * A.q_head + col;
-  unsigned char* buf = qbuf + qs * S::QBytes + col / S::UnitCols * (S::QParts * S::N * S::RowBytes);
+  unsigned char* buf = qbuf + qs * S::QBytes + col / S::UnitCols * (S::QRows * S::N * S::RowBytes);
 #pragma unroll 1
   for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
     uint4 x[kBatch];
@@ -171,6 +182,8 @@ __device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& 
         if (odd) out[0] = out[1] = 0x7f7f7f7fu;  // NaN
         *reinterpret_cast<uint2*>(buf + part * (S::N * S::RowBytes) + at) = make_uint2(out[0], out[1]);
       }
+      if (S::QRows > S::QParts)
+        *reinterpret_cast<uint2*>(buf + S::QParts * (S::N * S::RowBytes) + at) = make_uint2(0u, 0u);
       if (lane % kLanes == 0)
         sh.q_scale[qs][c] = __uint_as_float((uint32_t)(127 - 7 + (odd ? 7 : e)) << 23);
     }
@@ -182,45 +195,51 @@ __device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& 
 }
 
 // ---- the threads that issue the matrix instructions -------------------------------------------
-// S^T = K Q^T of every tile, over the queries' parts.
+// S^T = K Q^T of every tile, the queries' parts side by side as columns.
 template <class S>
 __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh,
                                             unsigned char* qbuf, unsigned char* ring) {
-  const uint32_t idesc = mma_desc8(false, false, 128, 2 * S::N),
-                 third = mma_desc8(false, false, 128, S::N);
+  const uint32_t idesc = mma_desc8(false, false, 128, S::SN);
   const uint64_t rows = smem_desc(0, 16, kRows8<S>, kRowSwizzle<S>);
   const uint64_t a0 = rows + (smem_u32(ring) >> 4), b0 = rows + (smem_u32(qbuf) >> 4);
   Reader<S> reader(sh);
   RingPos at;
-  int y = 0;  // tiles so far
+  uint32_t y = 0;  // turns of the score buffer
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
     const int qs = p.turn % S::NQ, tiles = p.mb - p.ma;
     if (!wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits)) goto end;
+    int i = 0;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i, ++y) {
-      const int buf = y & 1;
-      if (!wait_phase(&sh.s_empty[0][buf], ((uint32_t)(y >> 1) & 1u) ^ 1u, &sh.waits)) goto end;
+    while (i < tiles) {
+      const int last = i + tiles_at<S>(p, A.rule.window, i);
+      if (!wait_phase(&sh.s_empty[0][0], (y & 1u) ^ 1u, &sh.waits)) goto end;
       tc_fence_after();
-      const uint32_t d = sh.tmem + buf * 2 * S::N;
-      uint64_t b = b0 + qs * (S::QBytes >> 4);
+      uint32_t d = sh.tmem;
 #pragma unroll 1
-      for (int c = 0; c < S::U; ++c, b += S::QParts * S::N * S::RowBytes >> 4) {
-        if (!wait_phase(&sh.full[at.slot], at.phase, &sh.waits)) goto end;
-        tc_fence_after();
-        const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
-#pragma unroll
-        for (int k = 0; k < S::RowBytes / 32; ++k) mma_f8(d, a + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
-        if (S::QParts == 3) {
+      for (; i < last; ++i, d += S::SN) {
+        uint64_t b = b0 + qs * (S::QBytes >> 4);
+#pragma unroll 1
+        for (int c = 0; c < S::U; ++c, b += S::QRows * S::N * S::RowBytes >> 4) {
+          if (!wait_phase(&sh.full[at.slot], at.phase, &sh.waits)) goto end;
+          tc_fence_after();
+          const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
 #pragma unroll
           for (int k = 0; k < S::RowBytes / 32; ++k)
-            mma_f8(d, a + 2 * k, b + (2 * S::N * S::RowBytes >> 4) + 2 * k, third, true);
+            mma_f8(d, a + 2 * k, b + 2 * k, idesc, c > 0 || k > 0);
+          if (S::QParts > S::QWide) {  // (onto the first part's)
+            const uint32_t third = mma_desc8(false, false, 128, S::N);
+#pragma unroll
+            for (int k = 0; k < S::RowBytes / 32; ++k)
+              mma_f8(d, a + 2 * k, b + (S::QWide * S::N * S::RowBytes >> 4) + 2 * k, third, true);
+          }
+          mma_commit(&sh.empty[at.slot]);
+          at.next(S::NK);
         }
-        mma_commit(&sh.empty[at.slot]);
-        at.next(S::NK);
       }
-      mma_commit(&sh.s_full[0][buf]);
+      mma_commit(&sh.s_full[0][0]);
+      ++y;
     }
     mma_commit(&sh.q_empty[qs]);
   }
@@ -240,15 +259,16 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
   const uint64_t b0 = smem_desc(0, kTileKeys * 32, 256, kSwizzle32) + (smem_u32(pbuf) >> 4);
   Reader<S> reader(sh);
   RingPos at;
-  int y = 0;
+  uint32_t y = 0;
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
     const int tiles = p.mb - p.ma;
     const uint32_t o = sh.tmem + S::OBase + (p.turn & (S::Outs - 1)) * S::MBlocks * S::ON;
+    int i = 0;
 #pragma unroll 1
-    for (int i = 0; i < tiles; ++i, ++y) {
-      const int pb = y % S::NP;
+    while (i < tiles) {
+      const int last = i + tiles_at<S>(p, A.rule.window, i);
       if (__builtin_expect(edge_tile(p, A.rule.window, tile_at<S>(p, i)), 0)) {
         RingPos look = at;
 #pragma unroll 1
@@ -258,21 +278,25 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
         }
         mbar_arrive(&sh.v_ready[0]);
       }
-      if (!wait_phase(&sh.p_full[0][pb], (uint32_t)(y / S::NP) & 1u, &sh.waits)) goto end;
-      const uint64_t b = b0 + pb * (S::PBytes >> 4);
-      uint32_t d = o;
+      if (!wait_phase(&sh.p_full[0][0], y & 1u, &sh.waits)) goto end;
+      uint64_t b = b0;
 #pragma unroll 1
-      for (int m = 0; m < S::MBlocks; ++m, d += S::ON) {
-        if (!wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.waits)) goto end;
-        tc_fence_after();
-        const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
+      for (; i < last; ++i, b += S::PTile >> 4) {
+        uint32_t d = o;
+#pragma unroll 1
+        for (int m = 0; m < S::MBlocks; ++m, d += S::ON) {
+          if (!wait_phase(&sh.full[S::NK + at.slot], at.phase, &sh.waits)) goto end;
+          tc_fence_after();
+          const uint64_t a = a0 + at.slot * (S::UnitBytes >> 4);
 #pragma unroll
-        for (int k = 0; k < kTileKeys / 32; ++k)
-          mma_f8(d, a + k * (4 * kRows8<S> >> 4), b + k * 64, idesc, !(i == 0 && k == 0));
-        mma_commit(&sh.empty[S::NK + at.slot]);
-        at.next(S::NV);
+          for (int k = 0; k < kTileKeys / 32; ++k)
+            mma_f8(d, a + k * (4 * kRows8<S> >> 4), b + k * 64, idesc, !(i == 0 && k == 0));
+          mma_commit(&sh.empty[S::NK + at.slot]);
+          at.next(S::NV);
+        }
       }
-      mma_commit(&sh.pv_done[0][pb]);
+      mma_commit(&sh.pv_done[0][0]);
+      ++y;
     }
     mma_commit(&sh.o_done[p.turn & 1]);
   }
@@ -281,12 +305,12 @@ end:
 }
 
 // ---- the softmax threads ------------------------------------------------------------------------
-// The scales of the thread's key in the tile at hand, and the page of its key in the next one: each
-// loaded a tile before it is looked at.
+// The scales of the thread's keys in the two tiles at hand, and the pages of its keys in the tiles
+// from the second of them on: each loaded a pass before it is looked at.
 template <class S>
 struct KeyScales<S, true> {
-  float k, v;
-  int page;
+  float k[2], v[2];
+  int page[3];
 };
 
 // The page of the thread's key in the i-th tile of a piece, -1 where no row sees it.
@@ -299,24 +323,32 @@ __device__ __forceinline__ int key_page(const Attend<S>& me, const Piece& p, int
 }
 // Its scales (0 without a page: what no row sees is masked, and a bad page makes the piece NaN).
 template <class S>
-__device__ __forceinline__ void load_scales(Attend<S>& me, const Piece& p, int i, int page) {
+__device__ __forceinline__ void load_scales(Attend<S>& me, const Piece& p, int which, int i, int page) {
   const TileArgs& A = me.A;
-  me.scales.k = me.scales.v = 0.0f;
+  me.scales.k[which] = me.scales.v[which] = 0.0f;
   if (page >= 0 && page < A.num_pages) {
     const int j = tile_at<S>(p, i) * kTileKeys + me.key;
     const int64_t at = scale_at(A, page, j & ((1 << A.log_page) - 1), p.h);
-    me.scales.k = __ldg(A.k_scale + at);
-    me.scales.v = __ldg(A.v_scale + at);
+    me.scales.k[which] = __ldg(A.k_scale + at);
+    me.scales.v[which] = __ldg(A.v_scale + at);
   }
 }
 
-// The start of a piece: the columns' powers of two, and the scales of the first tile's keys.
+// The start of a piece: the pages of its first tiles, then (with the columns' tables) the columns'
+// powers of two and the scales of the first keys.
+template <class S>
+__device__ __forceinline__ void quant_piece(Attend<S>& me, const Piece& p) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) me.scales.page[k] = key_page(me, p, k);
+}
 template <class S>
 __device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p) {
   auto& sh = me.sh;
-  const int page = key_page(me, p, 0);
-  me.scales.page = key_page(me, p, 1);
-  load_scales(me, p, 0, page);
+  load_scales(me, p, 0, 0, me.scales.page[0]);
+  load_scales(me, p, 1, 1, me.scales.page[1]);
+  me.scales.page[0] = me.scales.page[1];
+  me.scales.page[1] = me.scales.page[2];
+  me.scales.page[2] = key_page(me, p, 3);
   const int qs = p.turn % S::NQ;
   wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits);
 #pragma unroll 1
@@ -343,130 +375,164 @@ __device__ __noinline__ void apply_rule8(float* s, const ScoreRule& r, float awa
   apply_rule<S::CH>(*reinterpret_cast<float(*)[S::CH]>(s), r, away, slope, ahead);
 }
 
+// One pass: the piece's tiles from the i-th on, the y-th turn of the score buffer. Returns how many.
 template <class S>
-__device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>::Table& T,
-                                           const Piece& p, int t, int i, int x, int y,
-                                           Two (&l)[S::NC / 2]) {
+__device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>::Table& T,
+                                           const Piece& p, int i, int y, Two (&l)[S::NC / 2]) {
+  constexpr int kC = S::NC;
   const TileArgs& A = me.A;
   auto& sh = me.sh;
-  const int buf = y & 1, j = t * kTileKeys + me.key;
-  const bool edge = edge_tile(p, A.rule.window, t);
-  unsigned char* const pb = me.pbuf + y % S::NP * S::PBytes + me.key * 32;
+  const int t = tile_at<S>(p, i), j = t * kTileKeys + me.key;
+  const int both = tiles_at<S>(p, A.rule.window, i);
+  const bool edge = both == 1 && edge_tile(p, A.rule.window, t);
   const float* columns = sh.column_scale[p.turn & 1];
+  const int c0 = me.col0;
   // (every softmax thread has read the queries' scales by now: the barriers around set_columns)
   if (i == 0 && me.me == 0) mbar_arrive(&sh.q_empty[p.turn % S::NQ]);
-  float ks = me.scales.k, vs = me.scales.v;
-  load_scales(me, p, i + 1, me.scales.page);
-  me.scales.page = key_page(me, p, i + 2);
-  if (!(vs >= 0.0f && vs <= kMaxScale && fabsf(ks) < INFINITY)) {
-    ks = __uint_as_float(0x7fc00000u);
-    vs = 1.0f;
+  float ks[2], vs[2], lv[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    ks[q] = me.scales.k[q];
+    vs[q] = me.scales.v[q];
+    if (!(vs[q] >= 0.0f && vs[q] <= kMaxScale && fabsf(ks[q]) < INFINITY)) {
+      ks[q] = __uint_as_float(0x7fc00000u);
+      vs[q] = 1.0f;
+    }
+    lv[q] = vs[q] < 1.0f / kMaxScale ? -40.0f : __log2f(vs[q]);
   }
-  const float lv = vs < 1.0f / kMaxScale ? -40.0f : __log2f(vs);
-  wait_phase(&sh.s_full[0][buf], (uint32_t)(y >> 1) & 1u, &sh.waits);
+  load_scales(me, p, 0, i + both, both == 2 ? me.scales.page[1] : me.scales.page[0]);
+  load_scales(me, p, 1, i + both + 1, both == 2 ? me.scales.page[2] : me.scales.page[1]);
+  me.scales.page[0] = both == 2 ? me.scales.page[2] : me.scales.page[1];
+  me.scales.page[1] = key_page(me, p, i + both + 2);
+  me.scales.page[2] = key_page(me, p, i + both + 3);
+  wait_phase(&sh.s_full[0][0], (uint32_t)y & 1u, &sh.waits);
   tc_fence_after();
-  const int c0 = me.col0;
-  {
-    float s[S::CH];
-    Two e[S::CH / 2];
-    {
-      float low[S::CH];
-      tmem_ld16(me.lane_base + buf * 2 * S::N + c0, s);
-      tmem_ld16(me.lane_base + buf * 2 * S::N + S::N + c0, low);
-      tmem_wait_ld();
+  float s[2][kC];
 #pragma unroll
-      for (int c = 0; c < S::CH; c += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(&columns[c0 + c]);
-        const float2 a = split(two_mul(two_add(two(s[c], s[c + 1]), two(low[c], low[c + 1])), two(q.x, q.y)));
-        const float2 b = split(two_mul(two_add(two(s[c + 2], s[c + 3]), two(low[c + 2], low[c + 3])), two(q.z, q.w)));
-        s[c] = a.x, s[c + 1] = a.y, s[c + 2] = b.x, s[c + 3] = b.y;
+  for (int q = 0; q < 2; ++q) {
+    const uint32_t at = me.lane_base + q * S::SN;
+    float a[16], b[16];
+    tmem_ld16(at + c0, a);
+    if (kC == 16 || S::QWide == 4) tmem_ld16(kC == 16 ? at + S::N + c0 : at + 16, b);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < kC; c += 2) {
+      const float2 f = *reinterpret_cast<const float2*>(&columns[c0 + c]);
+      Two sum = kC == 16 ? two_add(two(a[c], a[c + 1]), two(b[c], b[c + 1]))
+                         : two_add(two(a[c], a[c + 1]), two(a[8 + c], a[9 + c]));
+      if (kC == 8 && S::QWide == 4) sum = two_add(sum, two(b[c], b[c + 1]));
+      const float2 v = split(two_mul(sum, two(f.x, f.y)));
+      s[q][c] = v.x;
+      s[q][c + 1] = v.y;
+    }
+  }
+  warp_arrive(&sh.s_empty[0][0], me.lane);
+  float scale[2] = {A.rule.scale * kLog2e * ks[0], A.rule.scale * kLog2e * ks[1]};
+  if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      if (q < both && (A.rule.softcap > 0.0f || A.rule.slopes)) {
+        float held[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) held[c] = s[q][c] * ks[q];
+        apply_rule8<S>(held, A.rule, (float)(p.pos0 - j + q * kTileKeys), &T.slope[c0], &T.ahead[c0]);
+#pragma unroll
+        for (int c = 0; c < kC; ++c) s[q][c] = held[c];
+        scale[q] = 1.0f;
       }
     }
-    warp_arrive(&sh.s_empty[0][buf], me.lane);
-    float scale = A.rule.scale * kLog2e * ks;  // to what the thread holds in s
-    if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
+    if (edge) {
 #pragma unroll
-      for (int c = 0; c < S::CH; ++c) s[c] *= ks;
-      if (A.rule.softcap > 0.0f || A.rule.slopes) {
-        float held[S::CH];
-#pragma unroll
-        for (int c = 0; c < S::CH; ++c) held[c] = s[c];
-        apply_rule8<S>(held, A.rule, (float)(p.pos0 - j), &T.slope[c0], &T.ahead[c0]);
-#pragma unroll
-        for (int c = 0; c < S::CH; ++c) s[c] = held[c];
-      } else {
-#pragma unroll
-        for (int c = 0; c < S::CH; ++c) s[c] *= A.rule.scale * kLog2e;
+      for (int c = 0; c < kC; ++c) {
+        s[0][c] *= scale[0];
+        if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[0][c] = -INFINITY;
       }
-      scale = 1.0f;
-      if (edge) {
-#pragma unroll
-        for (int c = 0; c < S::CH; ++c)
-          if (j > T.hi[c0 + c] || j <= T.lo[c0 + c]) s[c] = -INFINITY;
-      }
+      scale[0] = 1.0f;
     }
-    auto exponents = [&]() {
-      const Two sc = two(scale, scale);
+  }
+  float top = -INFINITY;
+  auto exponents = [&](int q, Two (&e)[kC / 2]) {
+    const Two sc = two(scale[q], scale[q]);
 #pragma unroll
-      for (int c = 0; c < S::CH; c += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(&T.m[c0 + c]);
-        e[c / 2] = two_fma(two(s[c], s[c + 1]), sc, two(m.x, m.y));
-        e[c / 2 + 1] = two_fma(two(s[c + 2], s[c + 3]), sc, two(m.z, m.w));
-      }
-    };
-    exponents();
-    float top = -INFINITY;
+    for (int c = 0; c < kC; c += 4) {
+      const float4 m = *reinterpret_cast<const float4*>(&T.m[c0 + c]);
+      e[c / 2] = two_fma(two(s[q][c], s[q][c + 1]), sc, two(m.x, m.y));
+      e[c / 2 + 1] = two_fma(two(s[q][c + 2], s[q][c + 3]), sc, two(m.z, m.w));
+    }
+  };
 #pragma unroll
-    for (int c = 0; c < S::CH / 2; ++c) {
+  for (int q = 0; q < 2; ++q) {
+    if (q == 1 && both == 1) break;
+    Two e[kC / 2];
+    exponents(q, e);
+    float most = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kC / 2; ++c) {
       const float2 v = split(e[c]);
-      top = fmaxf(top, fmaxf(v.x, v.y));
+      most = fmaxf(most, fmaxf(v.x, v.y));
     }
-    if (__builtin_expect(bar_or(1 + me.group, 128, top + lv > S::Top), 0)) {
-      if (i > 0) me.wait_values(y - 1);
+    top = fmaxf(top, most + lv[q]);
+  }
+  if (__builtin_expect(bar_or(1 + me.group, 128, top > S::Top), 0)) {
+    if (i > 0) me.wait_values(y - 1);
+    float most[kC];
 #pragma unroll
-      for (int c = 0; c < S::CH; ++c) s[c] = fmaf(s[c], scale, lv);
-      me.raise(T, s, l, 0, i == 0, me.output(p.turn));
-#pragma unroll
-      for (int c = 0; c < S::CH; ++c) s[c] -= lv;
-      scale = 1.0f;
-      exponents();
+    for (int c = 0; c < kC; ++c) {
+      most[c] = fmaf(s[0][c], scale[0], lv[0]);
+      if (both == 2) most[c] = fmaxf(most[c], fmaf(s[1][c], scale[1], lv[1]));
     }
-    uint32_t part[S::Parts][S::CH / 2];
-    // (what is below the last part's step of 2^-16 is rounded)
-    const Two unit2 = two(vs, vs), half2 = two(7.62939453125e-6f, 7.62939453125e-6f);
+    me.raise(T, most, l, 0, i == 0, me.output(p.turn));
+  }
+  // the product that last read the weights' buffer
+  if (y > 0) me.wait_values(y - 1);
+  // (what is below the last part's step of 2^-16 is rounded)
+  const Two half = two(7.62939453125e-6f, 7.62939453125e-6f);
 #pragma unroll
-    for (int c = 0; c < S::CH / 2; ++c) {
+  for (int q = 0; q < 2; ++q) {
+    if (q == 1 && both == 1) break;
+    Two e[kC / 2];
+    exponents(q, e);
+    uint32_t part[S::Parts][kC / 2];
+    const Two size = two(vs[q], vs[q]);
+#pragma unroll
+    for (int c = 0; c < kC / 2; ++c) {
       const float2 v = split(e[c]);
       const Two w = two(ex2(v.x), ex2(v.y));
       l[c] = two_add(l[c], w);
-      const float2 y2 = split(two_fma(w, unit2, half2));
+      const float2 y2 = split(two_fma(w, size, half));
       __half2 r = __floats2half2_rn(y2.x, y2.y);
 #pragma unroll
-      for (int q = 0; q < S::Parts; ++q) {
+      for (int k = 0; k < S::Parts; ++k) {
         // the upper byte of an fp16 number is an e5m2 number: what is left has three bits less
         const uint32_t bits = *reinterpret_cast<const uint32_t*>(&r), top3 = bits & 0xff00ff00u;
-        part[q][c] = bits;
-        if (q + 1 < S::Parts) r = __hsub2(r, *reinterpret_cast<const __half2*>(&top3));
+        part[k][c] = bits;
+        if (k + 1 < S::Parts) r = __hsub2(r, *reinterpret_cast<const __half2*>(&top3));
       }
     }
-    // the product that last read this buffer
-    if (y >= S::NP) me.wait_values(y - S::NP);
     // 32 columns of a key are 32 bytes, their 16-byte halves swapped in every other 4 keys
+    unsigned char* const pb = me.pbuf + q * S::PTile + me.key * 32;
+    auto bytes4 = [&](int k, int c) { return __byte_perm(part[k][c], part[k][c + 1], 0x7531); };
+    if (kC == 8) {
 #pragma unroll
-    for (int q = 0; q < S::Parts; ++q) {
-      const int n = q * S::N + c0;
-      const uint32_t* w = part[q];
-      *reinterpret_cast<uint4*>(pb + n / 32 * (kTileKeys * 32) + ((n / 16 ^ me.key >> 2) & 1) * 16) =
-          make_uint4(__byte_perm(w[0], w[1], 0x7531), __byte_perm(w[2], w[3], 0x7531),
-                     __byte_perm(w[4], w[5], 0x7531), __byte_perm(w[6], w[7], 0x7531));
+      for (int k = 0; k < S::Parts; k += 2)
+        *reinterpret_cast<uint4*>(pb + ((k / 2 ^ me.key >> 2) & 1) * 16) =
+            make_uint4(bytes4(k, 0), bytes4(k, 2), bytes4(k + 1, 0), bytes4(k + 1, 2));
+    } else {
+#pragma unroll
+      for (int k = 0; k < S::Parts; ++k) {
+        const int n = k * S::N + c0;
+        *reinterpret_cast<uint4*>(pb + n / 32 * (kTileKeys * 32) + ((n / 16 ^ me.key >> 2) & 1) * 16) =
+            make_uint4(bytes4(k, 0), bytes4(k, 2), bytes4(k, 4), bytes4(k, 6));
+      }
     }
   }
   if (__builtin_expect(edge, 0)) {
     wait_phase(&sh.v_ready[0], (uint32_t)(me.edges++) & 1u, &sh.waits);
-    if (me.group == 0) me.clean_values(T, p, x, j);
+    if (me.group == 0) me.clean_values(T, p, p.x0 + i, j);
   }
   fence_proxy_async();
-  warp_arrive(&sh.p_full[0][y % S::NP], me.lane);
+  warp_arrive(&sh.p_full[0][0], me.lane);
+  return both;
 }
 
 // The outputs that NaN codes among the values of partly visible keys make NaN (those codes went to

@@ -844,7 +844,7 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
-// Column-wise reduction over a warp's lanes of kC values per lane (16 or a multiple of 32):
+// Column-wise reduction over a warp's lanes of kC values per lane (8, 16 or a multiple of 32):
 // halves the columns a lane carries at every step, so 31 exchanges serve 32 columns. Lane l
 // ends with column 32 * g + l of each group g (16 columns: lanes l and l + 16 share column l).
 template <int kC, bool kMax>
@@ -865,7 +865,8 @@ __device__ __forceinline__ void column_reduce(const float (&v)[kC], float* out, 
         r[c] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
       }
     }
-    if (kW == 16) r[0] = op(r[0], __shfl_xor_sync(0xffffffffu, r[0], 16));
+    if (kW <= 16) r[0] = op(r[0], __shfl_xor_sync(0xffffffffu, r[0], 16));
+    if (kW <= 8) r[0] = op(r[0], __shfl_xor_sync(0xffffffffu, r[0], 8));
     if (lane < kW) out[g + lane] = r[0];
   }
 }
@@ -1031,9 +1032,10 @@ struct KeyScales {};
 template <class S>
 struct Attend;
 template <class S>
-__device__ __forceinline__ void quant_tile(Attend<S>& me, typename TileShared<S>::Table& T,
-                                           const Piece& p, int t, int i, int x, int y,
-                                           Two (&l)[S::NC / 2]);
+__device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>::Table& T,
+                                           const Piece& p, int i, int y, Two (&l)[S::NC / 2]);
+template <class S>
+__device__ __forceinline__ void quant_piece(Attend<S>& me, const Piece& p);
 template <class S>
 __device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p);
 template <class S>
@@ -1095,7 +1097,7 @@ struct Attend {
     }
     tc_fence_after();
 #pragma unroll 1
-    for (int m = 0; m < S::MBlocks * (S::Wide ? S::Parts : 1); ++m)  // (wide: a product per part)
+    for (int m = 0; m < S::MBlocks * (S::Wide ? S::Parts : 1); m += S::CH < 16 ? 2 : 1)  // (wide: a product per part)
 #pragma unroll 1
       for (int q = 0; q < S::CH; q += 16) {
         float o[16];
@@ -1103,7 +1105,7 @@ struct Attend {
         tmem_ld16(at, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] *= T.alpha[c0 + q + c];
+        for (int c = 0; c < 16; ++c) o[c] *= T.alpha[c0 + q + c % S::CH];
         tmem_st16(at, o);
       }
     tmem_wait_st();
@@ -1296,10 +1298,17 @@ struct Attend {
       for (int m = 0; m < S::MBlocks; ++m, d += 128)
 #pragma unroll 1
         for (int q = 0; q < S::NC && col0 + q < rows; q += 16) {
+          constexpr int kW = S::NC < 16 ? S::NC : 16;
           float o[16];
           tmem_ld16(output(p.turn) + m * S::ON + q, o);
           tmem_wait_ld();
-          if (S::Wide) {
+          if (kW == 8) {  // two parts side by side
+            float low[16];
+            tmem_ld16(output(p.turn) + m * S::ON + 16, low);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) o[c] = (o[c] + o[8 + c]) + (low[c] + low[8 + c]);
+          } else if (S::Wide) {
 #pragma unroll 1
             for (int part = 1; part < S::Parts; ++part) {
               float low[16];
@@ -1312,12 +1321,12 @@ struct Attend {
           const int n0 = col0 + q;
           float all = 0.0f;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) all = fmaf(o[c], T.red[0][n0 + c], all);
+          for (int c = 0; c < kW; ++c) all = fmaf(o[c], T.red[0][n0 + c], all);
           odd = fmaf(all, 0.0f, odd);  // (NaN from here on if one of them is not finite)
           if (whole) {
             uint16_t* out = static_cast<uint16_t*>(A.out) + row0 * S::D + d;
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) {
+            for (int c = 0; c < kW; c += 2) {
               const uint32_t w =
                   pack16<S::Bf16>(o[c] * T.alpha[n0 + c], o[c + 1] * T.alpha[n0 + c + 1]);
               if (n0 + c < rows) out[T.row[n0 + c] * S::D] = (uint16_t)w;
@@ -1325,7 +1334,7 @@ struct Attend {
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
+            for (int c = 0; c < kW; ++c)
               if (n0 + c < rows) part[(n0 + c) * S::D + d] = o[c];
           }
         }
@@ -1368,6 +1377,7 @@ struct Attend {
           }
           if (more) {
             Table& T = table(p.turn);
+            if constexpr (S::Quant) quant_piece<S>(*this, p);
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
             if (me == 0) T.piece = p, T.odd = 0;
@@ -1379,11 +1389,12 @@ struct Attend {
           for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
         }
         if (more) {
-          if constexpr (S::Quant)
-            quant_tile<S>(*this, table(p.turn), p, tile_at<S>(p, i), i, p.x0 + i, y, l);
-          else
+          if constexpr (S::Quant) {
+            i += quant_tiles<S>(*this, table(p.turn), p, i, y, l);
+          } else {
             tile(table(p.turn), p, tile_at<S>(p, i), i == 0, p.x0 + i, y, l);
-          ++i;
+            ++i;
+          }
           ++y;
         }
       }
