@@ -47,10 +47,10 @@ struct TileShape8 {
   static constexpr int Teams = 1, Groups = N == 8 ? 1 : N / 16, SoftWarps = 4 * Groups;
   static constexpr int CtasPerSm = N <= 16 ? 2 : 1;
   static constexpr int SoftThreads = 32 * SoftWarps;
-  // the softmax, then a warp each: key (and query) copies, scores, value copies, values
-  static constexpr int KeyWarp = SoftWarps, ScoreWarp = KeyWarp + 1, CopyVWarp = KeyWarp + 2,
-                       ValueWarp = KeyWarp + 3;
-  static constexpr int Threads = SoftThreads + 128;
+  // the softmax, then a warp each: copies, scores, values
+  static constexpr int KeyWarp = SoftWarps, ScoreWarp = KeyWarp + 1, ValueWarp = KeyWarp + 2,
+                       CopyVWarp = -1;
+  static constexpr int Threads = SoftThreads + 96;
   static constexpr int TeamThreads = SoftThreads;
   static constexpr int NC = N == 8 ? 8 : 16, CH = NC;  // columns per softmax thread
   // e4m3 numbers of a query element, and how many of them are columns of the score instruction (whose
@@ -58,10 +58,10 @@ struct TileShape8 {
   static constexpr int QParts = kBf16 ? 2 : 3, QWide = N == 8 && !kBf16 ? 4 : 2;
   static constexpr int QRows = QParts > QWide ? QParts : QWide;  // parts in the buffer
   static constexpr int QBytes = QRows * N * D;
-  static constexpr int NQ = 2;
+  static constexpr int NQ = 1;
   static constexpr int Parts = 4;  // of a weight
   static constexpr int PTile = Parts * kTileKeys * N, PBytes = 2 * PTile, NP = 1;
-  static constexpr int kTables = 112 * N + 1920;
+  static constexpr int kTables = 104 * N + 1920;
   static constexpr int kRoom = kSmemMax / CtasPerSm - (CtasPerSm == 2 ? 512 : 0) - kTables - 1024 -
                                NQ * QBytes - PBytes;
   static constexpr int NU = kRoom / UnitBytes > 16 ? 16 : kRoom / UnitBytes;
@@ -72,9 +72,7 @@ struct TileShape8 {
   static constexpr int ON = Parts * N;
   // a score buffer of two tiles, read into registers before the next ones need it
   static constexpr int SN = QWide * N, OBase = 2 * SN;
-  // one set of accumulators where tensor memory has no room for two: a piece's output is then
-  // written before the next one's first product
-  static constexpr int Outs = OBase + 2 * MBlocks * ON <= 512 / CtasPerSm ? 2 : 1;
+  static constexpr int Outs = 1;  // (a piece's output leaves while the next one's first scores are made)
   static constexpr int TmemNeed = OBase + Outs * MBlocks * ON;
   static constexpr int TmemCols = TmemNeed <= 128 ? 128 : TmemNeed <= 256 ? 256 : 512;
   // a tile's bytes take half the time of one in 16 bits, a piece's start as long
@@ -112,50 +110,144 @@ constexpr uint32_t kRowSwizzle = S::RowBytes == 128 ? kSwizzle128 : kSwizzle64;
 template <class S>
 constexpr uint32_t kRows8 = 8 * S::RowBytes;
 
-// ---- the queries ---------------------------------------------------------------------------------
-// The warp that copies the keys reads each piece's query rows and leaves them as e4m3 numbers, part
-// by part (per unit of the row's columns), in the layout of the instruction's operand: rows of
-// RowBytes, 16-byte pieces swapped by the row. False when a wait failed.
-template <class S>
-__device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& sh,
-                                              unsigned char* qbuf, const Piece& p) {
-  constexpr int kLanes = S::D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-  constexpr int kSteps = S::N / kPer;
-  constexpr int kBatch = kSteps % 8 == 0 ? 8 : kSteps % 4 == 0 ? 4 : 2;
-  static_assert(kSteps % kBatch == 0, "whole batches");
-  const int lane = threadIdx.x & 31, col = lane % kLanes * 8;
-  const int qs = p.turn % S::NQ, rows = p.live * A.G;
-  if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs],
-                                          ((uint32_t)(p.turn / S::NQ) & 1u) ^ 1u, &sh.waits)))
-    return false;
-  const uint16_t* q = static_cast<const uint16_t*>(A.q) + p.b * A.q_req + p.i0 * A.q_row +
-                      (int64_t)p.h * A.G * A.q_head + col;
-  unsigned char* buf = qbuf + qs * S::QBytes + col / S::UnitCols * (S::QRows * S::N * S::RowBytes);
+// ---- the copies ----------------------------------------------------------------------------------
+// The scales of a tile's blocks into L2, for the softmax threads' loads some tiles later: the lanes
+// share the blocks (page and slot are those of the lane's group of keys, -1 for a group not copied).
+__device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int slot, int head) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
-    uint4 x[kBatch];
-#pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      const int c = (s0 + s) * kPer + lane / kLanes, i = c / A.G;
-      x[s] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < rows)
-        x[s] = *reinterpret_cast<const uint4*>(q + i * A.q_row + (c - i * A.G) * A.q_head);
+  for (int j0 = 0; j0 < kTileKeys; j0 += 32 << A.log_block) {
+    const int j = j0 + (lane << A.log_block), from = (j / A.box) & 31;
+    const int of = __shfl_sync(0xffffffffu, page, from), at0 = __shfl_sync(0xffffffffu, slot, from);
+    if (j >= kTileKeys || of < 0) continue;
+    const int64_t at = scale_at(A, of, at0 + j % A.box, head);
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.k_scale + at));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.v_scale + at));
+  }
+}
+
+
+// One warp walks the work list, hands out the pieces and copies the keys and values of their tiles,
+// each lane those of its group of keys; the pages of the next tile are looked up a tile ahead.
+template <class S>
+__device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh, unsigned char* ring,
+                                           const CUtensorMap* mk, const CUtensorMap* mv) {
+  const int lane = threadIdx.x & 31;
+  Walk<S> walk(A, sh.start);
+  RingPos queue;
+  bool hollow = false;
+  // the next piece with tiles for the tensor cores; all lanes
+  auto take = [&](Piece& p) -> bool {
+    bool more;
+#pragma unroll 1
+    while ((more = walk.next(p)) && p.mb == p.ma) hollow |= (p.flags & kHollow) != 0;
+    if (!more) p.flags = kEndOfList;
+    if (!__all_sync(0xffffffffu, wait_phase(&sh.piece_empty[queue.slot], queue.phase ^ 1u, &sh.waits)))
+      return false;
+    if (lane == 0) {
+      sh.hollow = hollow;
+      sh.piece[queue.slot] = p;
+      mbar_arrive(&sh.piece_full[queue.slot]);
     }
+    queue.next(kPieceQueue);
+    return more;
+  };
+  // the units of a tile of keys or values into their ring; false when a wait failed
+  auto copy = [&](const CUtensorMap* map, RingPos& at, int base, int units, int& issued, bool mine,
+                  uint32_t bytes, int slot, int head, int page) -> bool {
+#pragma unroll 1
+    for (int c = 0; c < S::U; ++c) {
+      uint64_t* full = &sh.full[base + at.slot];
+      if (!__all_sync(0xffffffffu, wait_phase(&sh.empty[base + at.slot], at.phase ^ 1u, &sh.waits)))
+        return false;
+      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+      ++issued;
+      __syncwarp();
+      if (mine)
+        tile_g2s(ring + (base + at.slot) * S::UnitBytes + lane * A.box * S::RowBytes, map, full,
+                 c * S::UnitCols, slot, head, page);
+      at.next(units);
+    }
+    return true;
+  };
+  Piece p;
+  bool more = take(p);
+  int i = 0, keys = 0, values = 0;
+  bool seen = more && group_seen(A, p, tile_at<S>(p, 0), lane);
+  int page = seen ? group_page(A, p, tile_at<S>(p, 0), lane) : 0;
+  RingPos at_k, at_v;
+#pragma unroll 1
+  while (more) {
+    const int head = p.h, turn = p.turn;
+    const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
+    const bool mine = seen && page >= 0 && page < A.num_pages;
+    if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
+      *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
+    const int here = page;
+    const uint32_t bytes =
+        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
+    if (!copy(mk, at_k, 0, S::NK, keys, mine, bytes, slot, head, here)) break;
+    prefetch_scales(A, mine ? here : -1, slot, head);
+    if (__builtin_expect(++i == p.mb - p.ma, 0)) {
+      more = take(p);
+      i = 0;
+    }
+    seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
+    page = seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
+    if (!copy(mv, at_v, S::NK, S::NV, values, mine, bytes, slot, head, here)) break;
+  }
+  if (lane == 0) {
+    // no copy may outlive the CTA, should the others give up before they have seen it land
+#pragma unroll 1
+    for (int u = keys > S::NK ? keys - S::NK : 0; u < keys; ++u)
+      mbar_wait(&sh.full[u % S::NK], (uint32_t)(u / S::NK) & 1u, kTileWaitNs);
+#pragma unroll 1
+    for (int u = values > S::NV ? values - S::NV : 0; u < values; ++u)
+      mbar_wait(&sh.full[S::NK + u % S::NV], (uint32_t)(u / S::NV) & 1u, kTileWaitNs);
+  }
+  __syncwarp();
+}
+
+// ---- the queries ---------------------------------------------------------------------------------
+// The softmax threads read a piece's query rows, 8 elements at a time, and leave them as e4m3 numbers,
+// part by part (per unit of the row's columns), in the layout of the instruction's operand: rows of
+// RowBytes, 16-byte pieces swapped by the row. (One warp of its own took 5 us for 48 rows, which a
+// piece's first scores waited for.)
+template <class S>
+struct Queries8 {
+  static constexpr int kLanes = S::D / 8;  // threads of a row
+  static constexpr int kTurns = (S::N * kLanes + S::SoftThreads - 1) / S::SoftThreads;
+  uint4 x[kTurns];
+  __device__ __forceinline__ int row(int me, int s) const { return (s * S::SoftThreads + me) / kLanes; }
+  __device__ __forceinline__ void load(const TileArgs& A, const Piece& p, int me) {
+    const uint16_t* q = static_cast<const uint16_t*>(A.q) + p.b * A.q_req + p.i0 * A.q_row +
+                        (int64_t)p.h * A.G * A.q_head + me % kLanes * 8;
+    const int rows = p.live * A.G;
 #pragma unroll
-    for (int s = 0; s < kBatch; ++s) {
-      const int c = (s0 + s) * kPer + lane / kLanes;
+    for (int s = 0; s < kTurns; ++s) {
+      const int c = row(me, s), i = c / A.G;
+      x[s] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < rows) x[s] = *reinterpret_cast<const uint4*>(q + i * A.q_row + (c - i * A.G) * A.q_head);
+    }
+  }
+  __device__ __forceinline__ void give(int me, unsigned char* qbuf, float* column_scale) const {
+    const int col = me % kLanes * 8;
+    unsigned char* buf = qbuf + col / S::UnitCols * (S::QRows * S::N * S::RowBytes);
+#pragma unroll
+    for (int s = 0; s < kTurns; ++s) {
+      const int c = row(me, s);
+      if (c >= S::N) break;  // (whole warps)
       const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
       // the row's largest magnitude, by its bits (those of what is not finite are the largest)
       uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
+      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, w[e] >> 16 & 0x7fffu));
 #pragma unroll
-      for (int o = kLanes / 2; o >= 1; o >>= 1)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       const bool odd = top >= (S::Bf16 ? 0x7f80u : 0x7c00u);
       // 2^e <= top < 2^(e+1), e at least -100 (what is smaller counts as 0)
-      const int e = top == 0 ? 0 : max(-100, (int)(__float_as_uint(unpack16<S::Bf16>(top).x) >> 23) - 127);
+      const int e =
+          top == 0 ? 0 : max(-100, (int)(__float_as_uint(unpack16<S::Bf16>(top).x) >> 23) - 127);
       const float up = odd ? 1.0f : __uint_as_float((uint32_t)(127 + 7 - e) << 23);
       float f[8];
 #pragma unroll
@@ -164,35 +256,31 @@ __device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& 
         f[2 * k] = v.x * up;
         f[2 * k + 1] = v.y * up;
       }
-      const uint32_t row = c * S::RowBytes + col % S::UnitCols;
-      const uint32_t at = row ^ ((row >> 7 & (S::RowBytes == 128 ? 7u : 3u)) << 4);
+      const uint32_t at0 = c * S::RowBytes + col % S::UnitCols;
+      const uint32_t at = at0 ^ ((at0 >> 7 & (S::RowBytes == 128 ? 7u : 3u)) << 4);
 #pragma unroll
-      for (int part = 0; part < S::QParts; ++part) {
-        uint32_t out[2];
+      for (int part = 0; part < S::QRows; ++part) {
+        uint32_t out[2] = {0u, 0u};
+        if (part < S::QParts) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_fp8x2_storage_t b =
-              __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
-          const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
-          const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          f[2 * k] -= back.x;
-          f[2 * k + 1] -= back.y;
-          out[k / 2] = k & 1 ? out[k / 2] | (uint32_t)b << 16 : (uint32_t)b;
+          for (int k = 0; k < 4; ++k) {
+            const __nv_fp8x2_storage_t b =
+                __nv_cvt_float2_to_fp8x2(make_float2(f[2 * k], f[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(b, __NV_E4M3);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+            f[2 * k] -= back.x;
+            f[2 * k + 1] -= back.y;
+            out[k / 2] |= (uint32_t)b << 16 * (k & 1);
+          }
+          if (odd) out[0] = out[1] = 0x7f7f7f7fu;  // NaN
         }
-        if (odd) out[0] = out[1] = 0x7f7f7f7fu;  // NaN
         *reinterpret_cast<uint2*>(buf + part * (S::N * S::RowBytes) + at) = make_uint2(out[0], out[1]);
       }
-      if (S::QRows > S::QParts)
-        *reinterpret_cast<uint2*>(buf + S::QParts * (S::N * S::RowBytes) + at) = make_uint2(0u, 0u);
-      if (lane % kLanes == 0)
-        sh.q_scale[qs][c] = __uint_as_float((uint32_t)(127 - 7 + (odd ? 7 : e)) << 23);
+      if (me % kLanes == 0)
+        column_scale[c] = __uint_as_float((uint32_t)(127 - 7 + (odd ? 7 : e)) << 23);
     }
   }
-  fence_proxy_async();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(&sh.q_full[qs]);
-  return true;
-}
+};
 
 // ---- the threads that issue the matrix instructions -------------------------------------------
 // S^T = K Q^T of every tile, the queries' parts side by side as columns.
@@ -208,8 +296,8 @@ __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh
   Piece p;
 #pragma unroll 1
   while (reader.template next<false>(p)) {
-    const int qs = p.turn % S::NQ, tiles = p.mb - p.ma;
-    if (!wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits)) goto end;
+    const int tiles = p.mb - p.ma;
+    if (!wait_phase(&sh.q_full[0], (uint32_t)p.turn & 1u, &sh.waits)) goto end;
     int i = 0;
 #pragma unroll 1
     while (i < tiles) {
@@ -219,7 +307,7 @@ __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh
       uint32_t d = sh.tmem;
 #pragma unroll 1
       for (; i < last; ++i, d += S::SN) {
-        uint64_t b = b0 + qs * (S::QBytes >> 4);
+        uint64_t b = b0;
 #pragma unroll 1
         for (int c = 0; c < S::U; ++c, b += S::QRows * S::N * S::RowBytes >> 4) {
           if (!wait_phase(&sh.full[at.slot], at.phase, &sh.waits)) goto end;
@@ -241,7 +329,6 @@ __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh
       mma_commit(&sh.s_full[0][0]);
       ++y;
     }
-    mma_commit(&sh.q_empty[qs]);
   }
 end:
   drain<S>(sh, 0);
@@ -334,27 +421,6 @@ __device__ __forceinline__ void load_scales(Attend<S>& me, const Piece& p, int w
   }
 }
 
-// The start of a piece: the pages of its first tiles, then (with the columns' tables) the columns'
-// powers of two and the scales of the first keys.
-template <class S>
-__device__ __forceinline__ void quant_piece(Attend<S>& me, const Piece& p) {
-#pragma unroll
-  for (int k = 0; k < 3; ++k) me.scales.page[k] = key_page(me, p, k);
-}
-template <class S>
-__device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p) {
-  auto& sh = me.sh;
-  load_scales(me, p, 0, 0, me.scales.page[0]);
-  load_scales(me, p, 1, 1, me.scales.page[1]);
-  me.scales.page[0] = me.scales.page[1];
-  me.scales.page[1] = me.scales.page[2];
-  me.scales.page[2] = key_page(me, p, 3);
-  const int qs = p.turn % S::NQ;
-  wait_phase(&sh.q_full[qs], (uint32_t)(p.turn / S::NQ) & 1u, &sh.waits);
-#pragma unroll 1
-  for (int c = me.me; c < S::N; c += S::TeamThreads) sh.column_scale[table][c] = sh.q_scale[qs][c];
-}
-
 __device__ __forceinline__ Two two_mul(Two a, Two b) {
   Two v;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
@@ -387,8 +453,6 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
   const bool edge = both == 1 && edge_tile(p, A.rule.window, t);
   const float* columns = sh.column_scale[p.turn & 1];
   const int c0 = me.col0;
-  // (every softmax thread has read the queries' scales by now: the barriers around set_columns)
-  if (i == 0 && me.me == 0) mbar_arrive(&sh.q_empty[p.turn % S::NQ]);
   float ks[2], vs[2], lv[2];
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
@@ -533,6 +597,56 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
   fence_proxy_async();
   warp_arrive(&sh.p_full[0][0], me.lane);
   return both;
+}
+
+// The pieces in turn. A piece's queries are given before the output of the one before it leaves, so
+// that its first scores are made meanwhile. (The last scores of the piece before have been read, so
+// its queries are done with.)
+template <class S>
+__device__ __forceinline__ void run8(Attend<S>& me, unsigned char* qbuf) {
+  auto& sh = me.sh;
+  const TileArgs& A = me.A;
+  Reader<S> reader(sh);
+  int y = 0, ended = -1;
+#pragma unroll 1
+  for (;;) {
+    const Piece p = reader.wait();
+    bool more = !(p.flags & kEndOfList) && !*(volatile int*)&sh.waits.dead;
+    more = !bar_or(kAllBar<S>, S::SoftThreads, !more);
+    auto& T = sh.table[p.turn & 1];
+    if (more) {
+      reader.release(me.lane == 0);
+      Queries8<S> q;
+      q.load(A, p, me.me);
+      const int page = key_page(me, p, 0);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) me.scales.page[k] = key_page(me, p, k + 1);
+      set_columns<S>(A, T, p, me.me, S::TeamThreads);
+      if (me.me == 0) T.piece = p, T.odd = 0;
+      q.give(me.me, qbuf, sh.column_scale[p.turn & 1]);
+      fence_proxy_async();
+      warp_arrive(&sh.q_full[0], me.lane);
+      load_scales(me, p, 0, 0, page);
+      load_scales(me, p, 1, 1, me.scales.page[0]);
+    }
+    if (ended >= 0) me.finish(sh.table[ended & 1]);
+    if (!more) break;
+    bar_sync(kAllBar<S>, S::SoftThreads);
+    Two l[S::NC / 2];
+#pragma unroll
+    for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
+#pragma unroll 1
+    for (int i = 0; i < p.mb - p.ma; ++y) i += quant_tiles<S>(me, T, p, i, y, l);
+    float sums[S::NC];
+#pragma unroll
+    for (int c = 0; c < S::NC; c += 2) {
+      const float2 v = split(l[c / 2]);
+      sums[c] = v.x;
+      sums[c + 1] = v.y;
+    }
+    column_reduce<S::NC, false>(sums, &T.red[me.quarter][me.col0], me.lane);
+    ended = p.turn;
+  }
 }
 
 // The outputs that NaN codes among the values of partly visible keys make NaN (those codes went to

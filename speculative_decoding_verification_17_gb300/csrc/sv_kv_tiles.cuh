@@ -119,7 +119,7 @@ struct TileShape {
   static constexpr bool Quant = false;  // keys and values in 16 bits (in 8: sv_kv8_tiles.cuh)
   static constexpr float Lift = kBf16 ? 0.0f : 7.0f;  // (attention) of the weights' exponents
   static constexpr int U = D / 64;  // units of a key or value tile
-  static constexpr int UnitCols = 64, RowBytes = 128, UnitBytes = kUnitBytes;
+  static constexpr int RowBytes = 128, UnitBytes = kUnitBytes;
   // Softmax warps: two groups of four (one warp per quarter of the tile's keys). In the
   // attention of 16 columns the groups are two teams that take the pieces in turn, each
   // with its own score, weight and output buffers, so one team's end of a piece (its last
@@ -434,12 +434,12 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
 constexpr int kPieceQueue = 8;
 
 // ---- shared memory ------------------------------------------------------------------------------
-// Of an attention over 8 bits: the columns' powers of two, by query buffer and by table.
+// Of an attention over 8 bits: the columns' powers of two, by table.
 template <bool kQuant, int kN>
 struct QueryScales {};
 template <int kN>
 struct QueryScales<true, kN> {
-  alignas(16) float q_scale[2][kN], column_scale[2][kN];
+  alignas(16) float column_scale[2][kN];
 };
 
 template <class S>
@@ -540,26 +540,6 @@ struct Reader {
 __device__ __forceinline__ int64_t scale_at(const TileArgs& A, int page, int slot, int head) {
   return ((int64_t)page * (1 << (A.log_page - A.log_block)) + (slot >> A.log_block)) * A.Hkv + head;
 }
-// The scales of a tile's blocks into L2, for the softmax threads' loads some tiles later: the lanes
-// share the blocks (page and slot are those of the lane's group of keys, -1 for a group not copied).
-__device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int slot, int head) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll 1
-  for (int j0 = 0; j0 < kTileKeys; j0 += 32 << A.log_block) {
-    const int j = j0 + (lane << A.log_block), from = (j / A.box) & 31;
-    const int of = __shfl_sync(0xffffffffu, page, from), at0 = __shfl_sync(0xffffffffu, slot, from);
-    if (j >= kTileKeys || of < 0) continue;
-    const int64_t at = scale_at(A, of, at0 + j % A.box, head);
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.k_scale + at));
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.v_scale + at));
-  }
-}
-
-// (8 bits) A piece's query rows as the instruction takes them (sv_kv8_tiles.cuh).
-template <class S>
-__device__ __forceinline__ bool give_queries8(const TileArgs& A, TileShared<S>& sh,
-                                              unsigned char* qbuf, const Piece& p);
-
 // ---- the copying warps ------------------------------------------------------------------------
 // Whether some row sees a key of the lane's group of `box` keys in a tile, and that group's page
 // (not looked at here: the load is a tile ahead of its use).
@@ -582,7 +562,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
                                           const CUtensorMap* mq, const CUtensorMap* map) {
   constexpr int kBase = kValues ? S::NK : 0, kUnits = kValues ? S::NV + S::Weigh : S::NK;
   const int lane = threadIdx.x & 31;
-  unsigned char* dst = ring + kBase * S::UnitBytes + lane * A.box * S::RowBytes;
+  unsigned char* dst = ring + kBase * kUnitBytes + lane * A.box * 128;
   Walk<S> walk(A, sh.start);
   Reader<S> reader(sh);
   // the next piece with tiles for the tensor cores; all lanes
@@ -614,13 +594,8 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
 #pragma unroll 1
   while (more) {
     const int head = p.h, turn = p.turn;
-    const bool first = i == 0;
-    Piece at_hand;
-    if constexpr (S::Quant && !kValues) {
-      if (first) at_hand = p;
-    }
     const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
-    if (!S::Quant && !kValues && i == 0) {
+    if (!kValues && i == 0) {
       const int qs = turn % S::NQ;
       if (!__all_sync(0xffffffffu, wait_phase(&sh.q_empty[qs], ((uint32_t)(turn / S::NQ) & 1u) ^ 1u,
                                               &sh.waits)))
@@ -646,11 +621,8 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
       if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
         *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
     }
-    if constexpr (S::Quant) {
-      if (!kValues) prefetch_scales(A, mine ? page : -1, slot, head);
-    }
     const uint32_t bytes =
-        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
+        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
 #pragma unroll 1
     for (int c = 0; c < S::U; ++c) {
       uint64_t* full = &sh.full[kBase + at.slot];
@@ -659,13 +631,8 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
       if (lane == 0) mbar_arrive_expect_tx(full, bytes);
       ++issued;
       __syncwarp();
-      if (mine)
-        tile_g2s(dst + at.slot * S::UnitBytes, map, full, c * S::UnitCols, slot, head, page);
+      if (mine) tile_g2s(dst + at.slot * kUnitBytes, map, full, c * 64, slot, head, page);
       at.next(kUnits);
-    }
-    if constexpr (S::Quant && !kValues) {
-      // a piece's queries, once its first keys are on their way
-      if (first && !give_queries8<S>(A, sh, qbuf, at_hand)) goto end;
     }
     page = next_page;
     seen = next_seen;
@@ -676,11 +643,9 @@ end:
 #pragma unroll 1
     for (int u = issued > kUnits ? issued - kUnits : 0; u < issued; ++u)
       mbar_wait(&sh.full[kBase + u % kUnits], (uint32_t)(u / kUnits) & 1u, kTileWaitNs);
-    if constexpr (!S::Quant) {
 #pragma unroll 1
-      for (int u = q_issued > S::NQ ? q_issued - S::NQ : 0; u < q_issued; ++u)
-        mbar_wait(&sh.q_full[u % S::NQ], (uint32_t)(u / S::NQ) & 1u, kTileWaitNs);
-    }
+    for (int u = q_issued > S::NQ ? q_issued - S::NQ : 0; u < q_issued; ++u)
+      mbar_wait(&sh.q_full[u % S::NQ], (uint32_t)(u / S::NQ) & 1u, kTileWaitNs);
   }
   __syncwarp();
 }
@@ -871,6 +836,19 @@ __device__ __forceinline__ void column_reduce(const float (&v)[kC], float* out, 
   }
 }
 
+// The same maxima by the warp's own reduction (of the lanes 0 .. kC - 1 each keeps its column's).
+template <int kC>
+__device__ __forceinline__ void column_max(const float (&v)[kC], float* out, int lane) {
+  float mine = 0.0f;
+#pragma unroll
+  for (int c = 0; c < kC; ++c) {
+    float top;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(top) : "f"(v[c]));
+    if (lane == c) mine = top;
+  }
+  if (lane < kC) out[lane] = mine;
+}
+
 // Scores of a thread's key from the products q.k, in units of log2: scale, cap, distance.
 template <int kC>
 __device__ __forceinline__ void apply_rule(float (&s)[kC], const ScoreRule& r, float away,
@@ -1032,13 +1010,6 @@ struct KeyScales {};
 template <class S>
 struct Attend;
 template <class S>
-__device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>::Table& T,
-                                           const Piece& p, int i, int y, Two (&l)[S::NC / 2]);
-template <class S>
-__device__ __forceinline__ void quant_piece(Attend<S>& me, const Piece& p);
-template <class S>
-__device__ __forceinline__ void quant_columns(Attend<S>& me, int table, const Piece& p);
-template <class S>
 __device__ __noinline__ void special_values8(const TileArgs& A, const ValuePool& vpool,
                                              const typename TileShared<S>::Table& T,
                                              const Piece& p, int col0, int rows, int d0,
@@ -1078,7 +1049,10 @@ struct Attend {
   __device__ __forceinline__ void raise(Table& T, const float (&s)[S::CH], Two (&l)[S::NC / 2],
                                         int k, bool first, uint32_t o_base) {
     const int c0 = col0 + k;
-    column_reduce<S::CH, true>(s, &T.red[quarter][c0], lane);
+    if constexpr (S::Quant)
+      column_max<S::CH>(s, &T.red[quarter][c0], lane);
+    else
+      column_reduce<S::CH, true>(s, &T.red[quarter][c0], lane);
     group_sync();
     if (quarter == 0 && lane < S::CH) {
       const int c = c0 + lane;
@@ -1361,7 +1335,7 @@ struct Attend {
     auto table = [&](int turn) -> Table& { return sh.table[S::Teams == 2 ? team : turn & 1]; };
 #pragma unroll 1
     for (;;) {
-      const bool flush = (S::Teams == 2 || S::Outs == 1) && pending;  // the end first
+      const bool flush = S::Teams == 2 && pending;  // the end first
       bool more = true;
       if (!flush) {
         if (__builtin_expect(i == p.mb - p.ma, 0)) {
@@ -1377,11 +1351,9 @@ struct Attend {
           }
           if (more) {
             Table& T = table(p.turn);
-            if constexpr (S::Quant) quant_piece<S>(*this, p);
             team_sync();  // the last piece with this table is out of it
             set_columns<S>(A, T, p, me, S::TeamThreads);
             if (me == 0) T.piece = p, T.odd = 0;
-            if constexpr (S::Quant) quant_columns<S>(*this, S::Teams == 2 ? team : p.turn & 1, p);
             team_sync();
             i = 0;
           }
@@ -1389,12 +1361,8 @@ struct Attend {
           for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
         }
         if (more) {
-          if constexpr (S::Quant) {
-            i += quant_tiles<S>(*this, table(p.turn), p, i, y, l);
-          } else {
-            tile(table(p.turn), p, tile_at<S>(p, i), i == 0, p.x0 + i, y, l);
-            ++i;
-          }
+          tile(table(p.turn), p, tile_at<S>(p, i), i == 0, p.x0 + i, y, l);
+          ++i;
           ++y;
         }
       }
@@ -1578,6 +1546,11 @@ __device__ __noinline__ void write_rest(const TileArgs& A, const TileShared<S>& 
 // ---- the kernel ---------------------------------------------------------------------------------
 // The roles that differ over 8 bits (sv_kv8_tiles.cuh).
 template <class S>
+__device__ __forceinline__ void run8(Attend<S>& me, unsigned char* qbuf);
+template <class S>
+__device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh, unsigned char* ring,
+                                           const CUtensorMap* mk, const CUtensorMap* mv);
+template <class S>
 __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh,
                                             unsigned char* qbuf, unsigned char* ring);
 template <class S>
@@ -1605,8 +1578,8 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
       mbar_init(&sh.empty[s], 1);
     }
     for (int s = 0; s < S::NQ; ++s) {
-      mbar_init(&sh.q_full[s], 1);
-      mbar_init(&sh.q_empty[s], S::Quant ? 2 : 1);
+      mbar_init(&sh.q_full[s], S::Quant ? S::SoftWarps : 1);
+      mbar_init(&sh.q_empty[s], 1);
     }
     for (int t = 0; t < S::Teams; ++t) {
       for (int s = 0; s < 2; ++s) {
@@ -1623,8 +1596,8 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
     mbar_init(&sh.o_done[1], 1);
     for (int s = 0; s < kPieceQueue; ++s) {
       mbar_init(&sh.piece_full[s], 1);
-      // taken by the softmax warps, the issuing threads and the value copies
-      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : 3));
+      // taken by the softmax warps, the issuing threads and (not over 8 bits) the value copies
+      mbar_init(&sh.piece_empty[s], S::SoftWarps + (S::Weigh ? 1 : S::Quant ? 2 : 3));
     }
     mbar_init(&sh.drain[0], 1);
     mbar_init(&sh.drain[1], 1);
@@ -1665,7 +1638,10 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
   }
 
   if (warp == S::KeyWarp) {
-    copy_role<S, false>(A, sh, qbuf, ring, &mq, &mk);
+    if constexpr (S::Quant)
+      copy_role8<S>(A, sh, ring, &mk, &mv);
+    else
+      copy_role<S, false>(A, sh, qbuf, ring, &mq, &mk);
   } else if (warp == S::ScoreWarp) {
     if ((tid & 31) == 0) {
       if constexpr (S::Quant)
@@ -1674,7 +1650,7 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
         score_role<S>(A, sh, qbuf, ring);
     }
     __syncwarp();
-  } else if (!S::Weigh && warp == S::CopyVWarp) {
+  } else if (!S::Weigh && !S::Quant && warp == S::CopyVWarp) {
     copy_role<S, true>(A, sh, qbuf, ring, &mq, &mv);
   } else if (!S::Weigh && warp == S::ValueWarp) {
     if ((tid & 31) == 0) {
@@ -1692,7 +1668,10 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
     Attend<S> R{A, vpool, sh, pbuf, ring, lane, quarter, group, quarter * 32 + lane,
                 sh.tmem + ((uint32_t)(quarter * 32) << 16), team,
                 S::Teams == 2 ? tid & 127 : tid, S::Teams == 2 ? 0 : group * S::NC};
-    R.run();
+    if constexpr (S::Quant)
+      run8<S>(R, qbuf);
+    else
+      R.run();
   }
   tc_fence_before();
   __syncthreads();
