@@ -152,6 +152,7 @@ sv_status attend8(const sv_kv_shape* shape, const sv_score_rule* rule, const voi
   A.G = shape->Hq / shape->Hkv;
   A.log_page = log2_of(shape->page_size);
   A.log_block = log2_of(block);
+  A.scale_page = (uint32_t)(shape->page_size / block) * (uint32_t)shape->Hkv;
   A.num_pages = shape->num_pages;
   A.max_pages = shape->max_pages;
   A.box = shape->page_size < kTileKeys ? shape->page_size : kTileKeys;

@@ -38,7 +38,7 @@ template <int kD, int kN, bool kBf16>
 struct TileShape8 {
   static constexpr int D = kD, N = kN;
   static constexpr bool Bf16 = kBf16, Weigh = false, Quant = true;  // (the queries' and outputs' type)
-  static constexpr float Lift = 12.0f, Top = 15.875f;  // log2 of the largest weight when the maximum moves, and at most
+  static constexpr float Lift = kBf16 ? 10.0f : 11.0f, Top = 15.875f;  // log2 of the largest weight when the maximum moves, and at most
   static constexpr int UnitCols = D < 128 ? D : 128, RowBytes = UnitCols, UnitBytes = kTileKeys * RowBytes;
   static constexpr int U = D / UnitCols;
   // Softmax threads take a key and 16 columns (8 where there are no more) of two tiles at a time: a
@@ -75,20 +75,27 @@ struct TileShape8 {
   static constexpr int Outs = 1;  // (a piece's output leaves while the next one's first scores are made)
   static constexpr int TmemNeed = OBase + Outs * MBlocks * ON;
   static constexpr int TmemCols = TmemNeed <= 128 ? 128 : TmemNeed <= 256 ? 256 : 512;
-  // a tile's bytes take half the time of one in 16 bits, a piece's start as long
+  // the cost of a tile and of a piece's start and end, which only other CTAs of the SM can cover
+  // (one token of 64 requests, 8 columns: 62.9 us with 5, 57.3 with 12, 61.4 with 32; five drafts, 48
+  // columns: 129 with 5, 108 with 13, 97 with 24, 100 with 32)
   static constexpr int TileCost = 4;
-  static constexpr int PieceCost = 16 * 64 / D + 1;
+  static constexpr int PieceCost = CtasPerSm == 2 ? 12 * 128 / D : 26;
   static_assert(CtasPerSm * TmemCols <= 512 && NV >= U && NK >= U &&
                 CtasPerSm * (Smem + kTables) <= kSmemMax, "tile shape");
 };
 
-// The tiles of a piece that go together from its i-th on: two, but one alone where some row does not
-// see some key of either, and at the end of an odd number.
-template <class S>
-__device__ __forceinline__ int tiles_at(const Piece& p, int window, int i) {
-  return i + 1 < p.mb - p.ma && !edge_tile(p, window, tile_at<S>(p, i)) &&
-         !edge_tile(p, window, tile_at<S>(p, i + 1)) ? 2 : 1;
-}
+// The tiles [lo, hi) of a piece whose keys every row sees. Those go two at a time, others (and the
+// last of an odd number) alone.
+struct WholeTiles {
+  int lo, hi;
+  __device__ __forceinline__ WholeTiles(const Piece& p, int window)
+      : lo((first_full(p, window) + kTileKeys - 1) >> 7), hi((p.pos0 + 1) >> 7) {}
+  __device__ __forceinline__ bool edge(int t) const { return t < lo || t >= hi; }
+  // How many go together from tile t (of left tiles, newest first) on.
+  __device__ __forceinline__ int at(int t, int left) const {
+    return left > 1 && t < hi && t > lo ? 2 : 1;
+  }
+};
 
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        bool accumulate) {
@@ -298,10 +305,11 @@ __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh
   while (reader.template next<false>(p)) {
     const int tiles = p.mb - p.ma;
     if (!wait_phase(&sh.q_full[0], (uint32_t)p.turn & 1u, &sh.waits)) goto end;
+    const WholeTiles whole(p, A.rule.window);
     int i = 0;
 #pragma unroll 1
     while (i < tiles) {
-      const int last = i + tiles_at<S>(p, A.rule.window, i);
+      const int last = i + whole.at(tile_at<S>(p, i), tiles - i);
       if (!wait_phase(&sh.s_empty[0][0], (y & 1u) ^ 1u, &sh.waits)) goto end;
       tc_fence_after();
       uint32_t d = sh.tmem;
@@ -352,11 +360,12 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
   while (reader.template next<false>(p)) {
     const int tiles = p.mb - p.ma;
     const uint32_t o = sh.tmem + S::OBase + (p.turn & (S::Outs - 1)) * S::MBlocks * S::ON;
+    const WholeTiles whole(p, A.rule.window);
     int i = 0;
 #pragma unroll 1
     while (i < tiles) {
-      const int last = i + tiles_at<S>(p, A.rule.window, i);
-      if (__builtin_expect(edge_tile(p, A.rule.window, tile_at<S>(p, i)), 0)) {
+      const int last = i + whole.at(tile_at<S>(p, i), tiles - i);
+      if (__builtin_expect(whole.edge(tile_at<S>(p, i)), 0)) {
         RingPos look = at;
 #pragma unroll 1
         for (int c = 0; c < S::U; ++c) {
@@ -413,7 +422,7 @@ template <class S>
 __device__ __forceinline__ void load_scales(Attend<S>& me, const Piece& p, int which, int i, int page) {
   const TileArgs& A = me.A;
   me.scales.k[which] = me.scales.v[which] = 0.0f;
-  if (page >= 0 && page < A.num_pages) {
+  if ((unsigned)page < (unsigned)A.num_pages) {
     const int j = tile_at<S>(p, i) * kTileKeys + me.key;
     const int64_t at = scale_at(A, page, j & ((1 << A.log_page) - 1), p.h);
     me.scales.k[which] = __ldg(A.k_scale + at);
@@ -421,6 +430,11 @@ __device__ __forceinline__ void load_scales(Attend<S>& me, const Piece& p, int w
   }
 }
 
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ Two two_mul(Two a, Two b) {
   Two v;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
@@ -444,13 +458,14 @@ __device__ __noinline__ void apply_rule8(float* s, const ScoreRule& r, float awa
 // One pass: the piece's tiles from the i-th on, the y-th turn of the score buffer. Returns how many.
 template <class S>
 __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>::Table& T,
-                                           const Piece& p, int i, int y, Two (&l)[S::NC / 2]) {
+                                           const Piece& p, const WholeTiles& whole, int i, int y,
+                                           Two (&l)[S::NC / 2]) {
   constexpr int kC = S::NC;
   const TileArgs& A = me.A;
   auto& sh = me.sh;
   const int t = tile_at<S>(p, i), j = t * kTileKeys + me.key;
-  const int both = tiles_at<S>(p, A.rule.window, i);
-  const bool edge = both == 1 && edge_tile(p, A.rule.window, t);
+  const int both = whole.at(t, p.mb - p.ma - i);
+  const bool edge = both == 1 && whole.edge(t);
   const float* columns = sh.column_scale[p.turn & 1];
   const int c0 = me.col0;
   float ks[2], vs[2], lv[2];
@@ -462,7 +477,7 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
       ks[q] = __uint_as_float(0x7fc00000u);
       vs[q] = 1.0f;
     }
-    lv[q] = vs[q] < 1.0f / kMaxScale ? -40.0f : __log2f(vs[q]);
+    lv[q] = fmaxf(lg2(vs[q]), -40.0f);
   }
   load_scales(me, p, 0, i + both, both == 2 ? me.scales.page[1] : me.scales.page[0]);
   load_scales(me, p, 1, i + both + 1, both == 2 ? me.scales.page[2] : me.scales.page[1]);
@@ -480,14 +495,17 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
     if (kC == 16 || S::QWide == 4) tmem_ld16(kC == 16 ? at + S::N + c0 : at + 16, b);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < kC; c += 2) {
-      const float2 f = *reinterpret_cast<const float2*>(&columns[c0 + c]);
-      Two sum = kC == 16 ? two_add(two(a[c], a[c + 1]), two(b[c], b[c + 1]))
-                         : two_add(two(a[c], a[c + 1]), two(a[8 + c], a[9 + c]));
-      if (kC == 8 && S::QWide == 4) sum = two_add(sum, two(b[c], b[c + 1]));
-      const float2 v = split(two_mul(sum, two(f.x, f.y)));
-      s[q][c] = v.x;
-      s[q][c + 1] = v.y;
+    for (int c = 0; c < kC; c += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(&columns[c0 + c]);
+#pragma unroll
+      for (int k = c; k < c + 4; k += 2) {
+        Two sum = kC == 16 ? two_add(two(a[k], a[k + 1]), two(b[k], b[k + 1]))
+                           : two_add(two(a[k], a[k + 1]), two(a[8 + k], a[9 + k]));
+        if (kC == 8 && S::QWide == 4) sum = two_add(sum, two(b[k], b[k + 1]));
+        const float2 v = split(two_mul(sum, k == c ? two(f.x, f.y) : two(f.z, f.w)));
+        s[q][k] = v.x;
+        s[q][k + 1] = v.y;
+      }
     }
   }
   warp_arrive(&sh.s_empty[0][0], me.lane);
@@ -632,11 +650,12 @@ __device__ __forceinline__ void run8(Attend<S>& me, unsigned char* qbuf) {
     if (ended >= 0) me.finish(sh.table[ended & 1]);
     if (!more) break;
     bar_sync(kAllBar<S>, S::SoftThreads);
+    const WholeTiles whole(p, A.rule.window);
     Two l[S::NC / 2];
 #pragma unroll
     for (int c = 0; c < S::NC / 2; ++c) l[c] = 0ull;
 #pragma unroll 1
-    for (int i = 0; i < p.mb - p.ma; ++y) i += quant_tiles<S>(me, T, p, i, y, l);
+    for (int i = 0; i < p.mb - p.ma; ++y) i += quant_tiles<S>(me, T, p, whole, i, y, l);
     float sums[S::NC];
 #pragma unroll
     for (int c = 0; c < S::NC; c += 2) {

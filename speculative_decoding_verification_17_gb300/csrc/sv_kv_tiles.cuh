@@ -99,6 +99,7 @@ struct TileArgs {
   const void* q;
   int64_t q_req, q_row, q_head;  // of q, in elements
   int log_block;
+  uint32_t scale_page;  // scales of a page
   // key weights
   const float *lse, *prior;
   float* weights;
@@ -538,7 +539,7 @@ struct Reader {
 
 // Where the scales of a block of slots lie: of a page's slot and a kv head.
 __device__ __forceinline__ int64_t scale_at(const TileArgs& A, int page, int slot, int head) {
-  return ((int64_t)page * (1 << (A.log_page - A.log_block)) + (slot >> A.log_block)) * A.Hkv + head;
+  return (int64_t)((uint64_t)(uint32_t)page * A.scale_page + (uint32_t)((slot >> A.log_block) * A.Hkv + head));
 }
 // ---- the copying warps ------------------------------------------------------------------------
 // Whether some row sees a key of the lane's group of `box` keys in a tile, and that group's page
