@@ -121,18 +121,17 @@ constexpr uint32_t kRows8 = 8 * S::RowBytes;
 // The scales of a tile's blocks into L2, for the softmax threads' loads some tiles later: the lanes
 // share the blocks (page and slot are those of the lane's group of keys, -1 for a group not copied).
 __device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int slot, int head) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, log_box = A.log_page < 7 ? A.log_page : 7;
 #pragma unroll 1
-  for (int j0 = 0; j0 < kTileKeys; j0 += 32 << A.log_block) {
-    const int j = j0 + (lane << A.log_block), from = (j / A.box) & 31;
+  for (int j = lane << A.log_block; j - (lane << A.log_block) < kTileKeys; j += 32 << A.log_block) {
+    const int from = j >> log_box & 31;
     const int of = __shfl_sync(0xffffffffu, page, from), at0 = __shfl_sync(0xffffffffu, slot, from);
     if (j >= kTileKeys || of < 0) continue;
-    const int64_t at = scale_at(A, of, at0 + j % A.box, head);
+    const int64_t at = scale_at(A, of, at0 + (j & (A.box - 1)), head);
     asm volatile("prefetch.global.L2 [%0];" ::"l"(A.k_scale + at));
     asm volatile("prefetch.global.L2 [%0];" ::"l"(A.v_scale + at));
   }
 }
-
 
 // One warp walks the work list, hands out the pieces and copies the keys and values of their tiles,
 // each lane those of its group of keys; the pages of the next tile are looked up a tile ahead.
@@ -187,21 +186,22 @@ __device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh,
   while (more) {
     const int head = p.h, turn = p.turn;
     const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
-    const bool mine = seen && page >= 0 && page < A.num_pages;
-    if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
-      *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
-    const int here = page;
-    const uint32_t bytes =
-        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
-    if (!copy(mk, at_k, 0, S::NK, keys, mine, bytes, slot, head, here)) break;
-    prefetch_scales(A, mine ? here : -1, slot, head);
     if (__builtin_expect(++i == p.mb - p.ma, 0)) {
       more = take(p);
       i = 0;
     }
-    seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
-    page = seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
-    if (!copy(mv, at_v, S::NK, S::NV, values, mine, bytes, slot, head, here)) break;
+    const bool next_seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
+    const int next_page = next_seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
+    const bool mine = seen && (unsigned)page < (unsigned)A.num_pages;
+    if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
+      *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
+    const uint32_t bytes =
+        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
+    if (!copy(mk, at_k, 0, S::NK, keys, mine, bytes, slot, head, page)) break;
+    prefetch_scales(A, mine ? page : -1, slot, head);
+    if (!copy(mv, at_v, S::NK, S::NV, values, mine, bytes, slot, head, page)) break;
+    page = next_page;
+    seen = next_seen;
   }
   if (lane == 0) {
     // no copy may outlive the CTA, should the others give up before they have seen it land
