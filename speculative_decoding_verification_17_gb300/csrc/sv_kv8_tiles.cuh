@@ -134,7 +134,10 @@ __device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int
 }
 
 // One warp walks the work list, hands out the pieces and copies the keys and values of their tiles,
-// each lane those of its group of keys; the pages of the next tile are looked up a tile ahead.
+// each lane those of its group of keys; the pages of the next tile are looked up a tile ahead. The
+// values go kLag tiles behind the keys: a pass's scores need its keys alone, and keys that waited
+// behind values, whose ring is freed last, held up the next pass's scores (five drafts 96.9 -> 91.6 us,
+// long caches 127.5 -> 120.5, heads of 256 in a window 47.5 -> 40.9).
 template <class S>
 __device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh, unsigned char* ring,
                                            const CUtensorMap* mk, const CUtensorMap* mv) {
@@ -158,24 +161,34 @@ __device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh,
     queue.next(kPieceQueue);
     return more;
   };
+  // a tile as the lane copies it: its page (-1: not), the bytes of all lanes, where its keys lie
+  struct Group {
+    uint32_t bytes;
+    int slot, head, page;
+  };
   // the units of a tile of keys or values into their ring; false when a wait failed
-  auto copy = [&](const CUtensorMap* map, RingPos& at, int base, int units, int& issued, bool mine,
-                  uint32_t bytes, int slot, int head, int page) -> bool {
+  auto copy = [&](const CUtensorMap* map, RingPos& at, int base, int units, int& issued,
+                  const Group& g) -> bool {
 #pragma unroll 1
     for (int c = 0; c < S::U; ++c) {
       uint64_t* full = &sh.full[base + at.slot];
       if (!__all_sync(0xffffffffu, wait_phase(&sh.empty[base + at.slot], at.phase ^ 1u, &sh.waits)))
         return false;
-      if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+      if (lane == 0) mbar_arrive_expect_tx(full, g.bytes);
       ++issued;
       __syncwarp();
-      if (mine)
+      if (g.page >= 0)
         tile_g2s(ring + (base + at.slot) * S::UnitBytes + lane * A.box * S::RowBytes, map, full,
-                 c * S::UnitCols, slot, head, page);
+                 c * S::UnitCols, g.slot, g.head, g.page);
       at.next(units);
     }
     return true;
   };
+  // (a pass whose values have to be cleaned waits for them before its keys' successors are read: the
+  // key ring has to hold the tiles of the lag without any of them being freed)
+  constexpr int kLag = S::NK / S::U >= 2 ? 2 : 1;
+  Group behind[kLag];
+  int held = 0;  // tiles whose values are still to be copied, the oldest first
   Piece p;
   bool more = take(p);
   int i = 0, keys = 0, values = 0;
@@ -183,25 +196,39 @@ __device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh,
   int page = seen ? group_page(A, p, tile_at<S>(p, 0), lane) : 0;
   RingPos at_k, at_v;
 #pragma unroll 1
-  while (more) {
-    const int head = p.h, turn = p.turn;
-    const int slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
-    if (__builtin_expect(++i == p.mb - p.ma, 0)) {
-      more = take(p);
-      i = 0;
+  while (more || held > 0) {
+    Group g;
+    const bool key = more;
+    if (key) {
+      const int turn = p.turn;
+      const bool mine = seen && (unsigned)page < (unsigned)A.num_pages;
+      g.page = mine ? page : -1;
+      g.head = p.h;
+      g.slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
+      if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
+        *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
+      g.bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
+      if (__builtin_expect(++i == p.mb - p.ma, 0)) {
+        more = take(p);
+        i = 0;
+      }
+      seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
+      page = seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
+      if (!copy(mk, at_k, 0, S::NK, keys, g)) break;
+      prefetch_scales(A, g.page, g.slot, g.head);
     }
-    const bool next_seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
-    const int next_page = next_seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
-    const bool mine = seen && (unsigned)page < (unsigned)A.num_pages;
-    if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
-      *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
-    const uint32_t bytes =
-        (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
-    if (!copy(mk, at_k, 0, S::NK, keys, mine, bytes, slot, head, page)) break;
-    prefetch_scales(A, mine ? page : -1, slot, head);
-    if (!copy(mv, at_v, S::NK, S::NV, values, mine, bytes, slot, head, page)) break;
-    page = next_page;
-    seen = next_seen;
+    if (held == kLag || !key) {
+      if (!copy(mv, at_v, S::NK, S::NV, values, behind[0])) break;
+#pragma unroll
+      for (int k = 0; k + 1 < kLag; ++k) behind[k] = behind[k + 1];
+      --held;
+    }
+    if (key) {
+#pragma unroll
+      for (int k = 0; k < kLag; ++k)
+        if (k == held) behind[k] = g;
+      ++held;
+    }
   }
   if (lane == 0) {
     // no copy may outlive the CTA, should the others give up before they have seen it land
@@ -455,6 +482,45 @@ __device__ __noinline__ void apply_rule8(float* s, const ScoreRule& r, float awa
   apply_rule<S::CH>(*reinterpret_cast<float(*)[S::CH]>(s), r, away, slope, ahead);
 }
 
+// Raise the maxima of the thread's columns to those of these scores, and scale what the columns hold,
+// the product of the y-th turn among it.
+template <class S>
+__device__ __forceinline__ void raise8(Attend<S>& me, typename TileShared<S>::Table& T,
+                                       const float (&s)[S::NC], Two (&l)[S::NC / 2], bool first, int y,
+                                       uint32_t o_base) {
+  const int c0 = me.col0, lane = me.lane;
+  column_max<S::NC>(s, &T.red[me.quarter][c0], lane);
+  me.group_sync();
+  if (me.quarter == 0 && lane < S::NC) {
+    const int c = c0 + lane;
+    const float was = -T.m[c];
+    const float top = fmaxf(fmaxf(T.red[0][c], T.red[1][c]), fmaxf(T.red[2][c], T.red[3][c]));
+    const float m = fmaxf(top - S::Lift, was);
+    T.alpha[c] = ex2(was - m);
+    T.m[c] = -m;
+  }
+  me.group_sync();
+  if (first) return;
+#pragma unroll
+  for (int c = 0; c < S::NC; c += 2) {
+    const float2 v = split(l[c / 2]);
+    l[c / 2] = two(v.x * T.alpha[c0 + c], v.y * T.alpha[c0 + c + 1]);
+  }
+  me.wait_values(y);
+  tc_fence_after();
+#pragma unroll 1
+  for (int m = 0; m < S::MBlocks * S::Parts; m += S::NC < 16 ? 2 : 1) {
+    float o[16];
+    const uint32_t at = o_base + m * S::N;
+    tmem_ld16(at, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 16; ++c) o[c] *= T.alpha[c0 + c % S::NC];
+    tmem_st16(at, o);
+  }
+  tmem_wait_st();
+}
+
 // One pass: the piece's tiles from the i-th on, the y-th turn of the score buffer. Returns how many.
 template <class S>
 __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>::Table& T,
@@ -556,14 +622,13 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
     top = fmaxf(top, most + lv[q]);
   }
   if (__builtin_expect(bar_or(1 + me.group, 128, top > S::Top), 0)) {
-    if (i > 0) me.wait_values(y - 1);
     float most[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       most[c] = fmaf(s[0][c], scale[0], lv[0]);
       if (both == 2) most[c] = fmaxf(most[c], fmaf(s[1][c], scale[1], lv[1]));
     }
-    me.raise(T, most, l, 0, i == 0, me.output(p.turn));
+    raise8<S>(me, T, most, l, i == 0, y - 1, me.output(p.turn));
   }
   // the product that last read the weights' buffer
   if (y > 0) me.wait_values(y - 1);

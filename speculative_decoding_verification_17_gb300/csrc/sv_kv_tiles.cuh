@@ -1050,10 +1050,7 @@ struct Attend {
   __device__ __forceinline__ void raise(Table& T, const float (&s)[S::CH], Two (&l)[S::NC / 2],
                                         int k, bool first, uint32_t o_base) {
     const int c0 = col0 + k;
-    if constexpr (S::Quant)
-      column_max<S::CH>(s, &T.red[quarter][c0], lane);
-    else
-      column_reduce<S::CH, true>(s, &T.red[quarter][c0], lane);
+    column_reduce<S::CH, true>(s, &T.red[quarter][c0], lane);
     group_sync();
     if (quarter == 0 && lane < S::CH) {
       const int c = c0 + lane;
@@ -1072,7 +1069,7 @@ struct Attend {
     }
     tc_fence_after();
 #pragma unroll 1
-    for (int m = 0; m < S::MBlocks * (S::Wide ? S::Parts : 1); m += S::CH < 16 ? 2 : 1)  // (wide: a product per part)
+    for (int m = 0; m < S::MBlocks * (S::Wide ? S::Parts : 1); ++m)  // (wide: a product per part)
 #pragma unroll 1
       for (int q = 0; q < S::CH; q += 16) {
         float o[16];
@@ -1080,7 +1077,7 @@ struct Attend {
         tmem_ld16(at, o);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 16; ++c) o[c] *= T.alpha[c0 + q + c % S::CH];
+        for (int c = 0; c < 16; ++c) o[c] *= T.alpha[c0 + q + c];
         tmem_st16(at, o);
       }
     tmem_wait_st();
