@@ -118,21 +118,6 @@ template <class S>
 constexpr uint32_t kRows8 = 8 * S::RowBytes;
 
 // ---- the copies ----------------------------------------------------------------------------------
-// The scales of a tile's blocks into L2, for the softmax threads' loads some tiles later: the lanes
-// share the blocks (page and slot are those of the lane's group of keys, -1 for a group not copied).
-__device__ __forceinline__ void prefetch_scales(const TileArgs& A, int page, int slot, int head) {
-  const int lane = threadIdx.x & 31, log_box = A.log_page < 7 ? A.log_page : 7;
-#pragma unroll 1
-  for (int j = lane << A.log_block; j - (lane << A.log_block) < kTileKeys; j += 32 << A.log_block) {
-    const int from = j >> log_box & 31;
-    const int of = __shfl_sync(0xffffffffu, page, from), at0 = __shfl_sync(0xffffffffu, slot, from);
-    if (j >= kTileKeys || of < 0) continue;
-    const int64_t at = scale_at(A, of, at0 + (j & (A.box - 1)), head);
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.k_scale + at));
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(A.v_scale + at));
-  }
-}
-
 // One warp walks the work list, hands out the pieces and copies the keys and values of their tiles,
 // each lane those of its group of keys; the pages of the next tile are looked up a tile ahead. The
 // values go kLag tiles behind the keys: a pass's scores need its keys alone, and keys that waited
@@ -215,7 +200,6 @@ __device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh,
       seen = more && group_seen(A, p, tile_at<S>(p, i), lane);
       page = seen ? group_page(A, p, tile_at<S>(p, i), lane) : 0;
       if (!copy(mk, at_k, 0, S::NK, keys, g)) break;
-      prefetch_scales(A, g.page, g.slot, g.head);
     }
     if (held == kLag || !key) {
       if (!copy(mv, at_v, S::NK, S::NV, values, behind[0])) break;

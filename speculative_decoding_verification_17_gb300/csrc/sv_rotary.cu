@@ -23,6 +23,12 @@
 namespace sv {
 namespace {
 
+#ifndef ROT_CTAS
+#define ROT_CTAS 3
+#endif
+#ifndef ROT_AHEAD
+#define ROT_AHEAD 4
+#endif
 constexpr int kRotThreads = 256, kRotWarps = kRotThreads / 32;
 
 struct HeadRows {
@@ -52,15 +58,27 @@ __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
   }
 }
 
-// kSplit warps share a row (one token's heads); the CTA takes kRotWarps / kSplit rows at a time.
+// (Not through the read-only path: outputs may be the inputs.)
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+
+// kSplit warps share a row (one token's heads). Nothing is shared between warps but the frequencies
+// and the weights, so no warp waits for another one's rows: with a table of cosines per CTA and
+// barriers around it prompts of 24576 rows took 145 us.
 template <int D, bool kBf16, int kSplit>
-__global__ void __launch_bounds__(kRotThreads, 3) rotate_kernel(const __grid_constant__ RotArgs A) {
+__global__ void __launch_bounds__(kRotThreads, ROT_CTAS) rotate_kernel(const __grid_constant__ RotArgs A) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a head, heads at a time
-  constexpr int kRows = kRotWarps / kSplit;
-  constexpr int kAhead = kSplit == 8 ? 3 : 4;  // groups of heads in flight
-  __shared__ uint64_t turn[D / 2];             // frequencies in 2^-64 of a turn
-  __shared__ float odd[D / 2];                 // NaN where one is not finite, else 0
-  __shared__ float2 table[kRows][D / 2];       // cosines and sines of the rows at hand
+  constexpr int kAhead = ROT_AHEAD;                          // groups of heads in flight
+  __shared__ uint64_t turn[D / 2];                   // frequencies in 2^-64 of a turn
+  __shared__ float odd[D / 2];                       // NaN where one is not finite, else 0
+  __shared__ float weight[2][D];
+  __shared__ float2 table[kRotWarps][D / 2];  // cosines and sines of each warp's row
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int half = A.R / 2;
   for (int i = tid; i < half; i += kRotThreads) {
@@ -70,122 +88,116 @@ __global__ void __launch_bounds__(kRotThreads, 3) rotate_kernel(const __grid_con
     turn[i] = __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
     odd[i] = isfinite(f) ? 0.0f : __uint_as_float(0x7fc00000u);
   }
+  for (int e = tid; e < 2 * D; e += kRotThreads) {
+    const void* w = A.x[e / D].weight;
+    weight[e / D][e % D] = !w            ? 1.0f
+                           : A.weight_f32 ? static_cast<const float*>(w)[e % D]
+                                          : unpack16<kBf16>(static_cast<const uint16_t*>(w)[e % D]).x;
+  }
   __syncthreads();
-  const int mine = warp / kSplit, sub = warp % kSplit;
-  const int d0 = lane % kLanes * 8;
+  const int sub = warp % kSplit, d0 = lane % kLanes * 8;
+  const int mate = A.interleaved ? 0 : d0 < half ? half : -half;
+  const int from = A.interleaved || d0 >= A.R ? lane : lane + mate / 8;  // the partners' lane
+  const bool turned = d0 < A.R;
+  constexpr int64_t kRows = kRotWarps / kSplit;
 #pragma unroll 1
-  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < A.rows; row0 += (int64_t)gridDim.x * kRows) {
-    for (int e = tid; e < kRows * half; e += kRotThreads) {
-      const int r = e / half, i = e - r * half;
-      const int p = row0 + r < A.rows ? __ldg(A.positions + row0 + r) : 0;
+  for (int64_t row = blockIdx.x * kRows + warp / kSplit; row < A.rows; row += gridDim.x * kRows) {
+    const int p = __ldg(A.positions + row);
+    if (p < 0) continue;
+    const int64_t req = row / A.P, at = row - req * A.P;
+    __syncwarp();  // the last row's table has been read
+    for (int i = lane; i < half; i += 32) {
       // the signed fraction of a turn, in half turns
       const float t = (float)(int32_t)((turn[i] * (uint64_t)(int64_t)p) >> 32) * 4.656612873077393e-10f;
       float s, c;
       sincospif(t, &s, &c);
-      table[r][i] = make_float2(c + odd[i], s + odd[i]);
+      table[warp][i] = make_float2(c + odd[i], s + odd[i]);
     }
-    __syncthreads();
-    const int64_t row = row0 + mine;
-    if (row < A.rows && __ldg(A.positions + row) >= 0) {
-      const int64_t req = row / A.P, at = row - req * A.P;
+    __syncwarp();
 #pragma unroll 1
-      for (int which = 0; which < 2; ++which) {
-        const HeadRows& X = A.x[which];
-        // what multiplies the element and its partner
-        float c[8], s[8];
-        const int mate = A.interleaved ? 0 : d0 < half ? half : -half;
+    for (int which = 0; which < 2; ++which) {
+      const HeadRows& X = A.x[which];
+      // what multiplies the element and its partner
+      float c[8], s[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = d0 + e;
-          float2 cs = make_float2(1.0f, 0.0f);
-          int other = d;
-          if (d < A.R) {
-            cs = table[mine][A.interleaved ? d >> 1 : d < half ? d : d - half];
-            other = A.interleaved ? d ^ 1 : d + mate;
-            if (A.interleaved ? !(d & 1) : d < half) cs.y = -cs.y;
-          }
-          float w = 1.0f, v = 1.0f;
-          if (X.weight) {
-            if (A.weight_f32) {
-              w = __ldg(static_cast<const float*>(X.weight) + d);
-              v = __ldg(static_cast<const float*>(X.weight) + other);
-            } else {
-              w = unpack16<kBf16>(__ldg(static_cast<const unsigned short*>(X.weight) + d)).x;
-              v = unpack16<kBf16>(__ldg(static_cast<const unsigned short*>(X.weight) + other)).x;
-            }
-          }
-          c[e] = w * cs.x;
-          s[e] = v * cs.y;
+      for (int e = 0; e < 8; ++e) {
+        const int d = d0 + e;
+        float2 cs = make_float2(1.0f, 0.0f);
+        int other = d;
+        if (turned) {
+          cs = table[warp][A.interleaved ? d >> 1 : d < half ? d : d - half];
+          other = A.interleaved ? d ^ 1 : d + mate;
+          if (A.interleaved ? !(d & 1) : d < half) cs.y = -cs.y;
         }
-        const int from = A.interleaved || d0 >= A.R ? lane : lane + mate / 8;  // the partners' lane
-        const uint16_t* in = X.in + req * X.req + at * X.row + d0;
-        uint16_t* out = X.out + req * X.out_req + at * X.out_row + d0;
-        constexpr int kStep = kSplit * kPer;
+        c[e] = weight[which][d] * cs.x;
+        s[e] = weight[which][other] * cs.y;
+      }
+      const uint16_t* in = X.in + req * X.req + at * X.row + d0;
+      uint16_t* out = X.out + req * X.out_req + at * X.out_row + d0;
+      constexpr int kStep = kSplit * kPer;
+      const int first = sub * kPer + lane / kLanes;
 #pragma unroll 1
-        for (int h0 = sub * kPer + lane / kLanes; __any_sync(0xffffffffu, h0 < X.heads);
-             h0 += kAhead * kStep) {
-          uint4 raw[kAhead];
+      for (int h0 = 0; h0 < X.heads; h0 += kAhead * kStep) {
+        uint4 raw[kAhead];
 #pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            const int h = h0 + a * kStep;
-            raw[a] = make_uint4(0u, 0u, 0u, 0u);
-            if (h < X.heads) raw[a] = *reinterpret_cast<const uint4*>(in + h * X.head);
+        for (int a = 0; a < kAhead; ++a) {
+          const int h = h0 + first + a * kStep;
+          raw[a] = make_uint4(0u, 0u, 0u, 0u);
+          if (h < X.heads) raw[a] = load16(in + h * X.head);
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int h = h0 + first + a * kStep;
+          if (h0 + a * kStep >= X.heads) break;  // (whole warps)
+          float x[8], y[8];
+          unpack8<kBf16>(raw[a], x);
+          float r = 1.0f;
+          if (A.norm) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+#pragma unroll
+            for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            r = rsqrtf(sum * (1.0f / D) + A.eps);
           }
+          if (A.interleaved) {
 #pragma unroll
-          for (int a = 0; a < kAhead; ++a) {
-            const int h = h0 + a * kStep;
-            float x[8], y[8];
-            unpack8<kBf16>(raw[a], x);
-            float r = 1.0f;
-            if (A.norm) {
-              float sum = 0.0f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
-#pragma unroll
-              for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-              r = rsqrtf(sum * (1.0f / D) + A.eps);
-            }
-            if (A.interleaved) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-            } else {
-              uint4 v;
-              v.x = __shfl_sync(0xffffffffu, raw[a].x, from);
-              v.y = __shfl_sync(0xffffffffu, raw[a].y, from);
-              v.z = __shfl_sync(0xffffffffu, raw[a].z, from);
-              v.w = __shfl_sync(0xffffffffu, raw[a].w, from);
-              unpack8<kBf16>(v, y);
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = 2 * k;
-              // (components past R have no partner: what lies there may be infinite)
-              const float p0 = d0 < A.R ? fmaf(y[e], s[e], x[e] * c[e]) : x[e] * c[e];
-              const float p1 = d0 < A.R ? fmaf(y[e + 1], s[e + 1], x[e + 1] * c[e + 1]) : x[e + 1] * c[e + 1];
-              w[k] = pack16<kBf16>(r * p0, r * p1);
-            }
-            if (h < X.heads)
-              *reinterpret_cast<uint4*>(out + h * X.out_head) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+          } else {
+            uint4 v;
+            v.x = __shfl_sync(0xffffffffu, raw[a].x, from);
+            v.y = __shfl_sync(0xffffffffu, raw[a].y, from);
+            v.z = __shfl_sync(0xffffffffu, raw[a].z, from);
+            v.w = __shfl_sync(0xffffffffu, raw[a].w, from);
+            unpack8<kBf16>(v, y);
           }
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int e = 2 * k;
+            // (components past R have no partner: what lies there may be infinite)
+            const float p0 = turned ? fmaf(y[e], s[e], x[e] * c[e]) : x[e] * c[e];
+            const float p1 = turned ? fmaf(y[e + 1], s[e + 1], x[e + 1] * c[e + 1]) : x[e + 1] * c[e + 1];
+            w[k] = pack16<kBf16>(r * p0, r * p1);
+          }
+          if (h < X.heads)
+            *reinterpret_cast<uint4*>(out + h * X.out_head) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
     }
-    __syncthreads();
   }
 }
 
 template <int D, bool kBf16>
 sv_status launch_rotate(const RotArgs& A, cudaStream_t st) {
-  // a CTA per row while there are few, so that a row's heads are loaded at once; four rows per CTA
-  // once those fill the SMs
+  // a CTA per row while there are few, so that a row's heads are loaded at once; a warp per row once
+  // those fill the SMs
   const int64_t sms = device_sm_count();
   if (A.rows <= 8 * sms) {
-    const int64_t ctas = A.rows;
-    rotate_kernel<D, kBf16, 8><<<(unsigned)ctas, kRotThreads, 0, st>>>(A);
+    rotate_kernel<D, kBf16, 8><<<(unsigned)A.rows, kRotThreads, 0, st>>>(A);
   } else {
-    const int64_t want = (A.rows + 3) / 4, ctas = want < 3 * sms ? want : 3 * sms;
-    rotate_kernel<D, kBf16, 2><<<(unsigned)ctas, kRotThreads, 0, st>>>(A);
+    const int64_t want = (A.rows + kRotWarps - 1) / kRotWarps, ctas = want < ROT_CTAS * sms ? want : ROT_CTAS * sms;
+    rotate_kernel<D, kBf16, 1><<<(unsigned)ctas, kRotThreads, 0, st>>>(A);
   }
   return launch_status();
 }
