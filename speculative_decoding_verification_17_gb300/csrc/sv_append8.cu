@@ -9,7 +9,7 @@
 // Work: rows of one block stand side by side, so the first of them (its predecessor is in another
 // block) finds the others. A warp takes one such run for one head of keys or values: it reads the
 // run's rows once for the largest magnitude and codes them from registers, or again from L2 where
-// there are more than eight loads of them. No two warps share a block.
+// there are more than sixteen loads of them. No two warps share a block.
 //
 // Bound: 3 bytes an element (2 read, 1 written).
 #include <cstdint>
@@ -36,73 +36,91 @@ struct AppendArgs {
   int rows, Hkv, log_page, log_block;
 };
 
-// Eight numbers as e4m3 codes; what is not finite, or too large for any scale, becomes NaN.
-template <bool kBf16>
-__device__ __forceinline__ uint2 code8(const uint4& v, float scale, float inverse, bool exact,
-                                       uint32_t limit) {
+// Eight numbers as e4m3 codes. With a plain scale (a power of two, and no number of the run past the
+// limit) a product; else a quotient, and what is not finite, or too large for any scale, becomes NaN.
+template <bool kBf16, bool kPlain>
+__device__ __forceinline__ uint2 code8(const uint4& v, float scale, uint32_t limit) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t out[2] = {0u, 0u};
+  uint32_t b[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     float2 f = unpack16<kBf16>(w[k]);
-    if (exact) {
-      f.x *= inverse;
-      f.y *= inverse;
+    if (kPlain) {  // (scale is the reciprocal)
+      f = split(two_mul(two(f.x, f.y), two(scale, scale)));
     } else {
-      f.x = __fdiv_rn(f.x, scale);
-      f.y = __fdiv_rn(f.y, scale);
+      f.x = (w[k] & 0x7fffu) > limit ? __uint_as_float(0x7fc00000u) : __fdiv_rn(f.x, scale);
+      f.y = (w[k] >> 16 & 0x7fffu) > limit ? __uint_as_float(0x7fc00000u) : __fdiv_rn(f.y, scale);
     }
-    if ((w[k] & 0x7fffu) > limit) f.x = __uint_as_float(0x7fc00000u);
-    if ((w[k] >> 16 & 0x7fffu) > limit) f.y = __uint_as_float(0x7fc00000u);
-    out[k >> 1] |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << 16 * (k & 1);
+    b[k] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
   }
-  return make_uint2(out[0], out[1]);
+  return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
 }
 
+// The rows of a chunk of 32 and of those after it that its last run may reach: a bit each for rows
+// that go on with the block of the row ahead of them, and for those of them whose slot is higher.
+struct Rows {
+  static constexpr int kWindows = 5;  // of 32 rows: a run has at most 128, and one too many
+  uint32_t same[kWindows], higher[kWindows];
+};
+
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_constant__ AppendArgs A) {
+__global__ void __launch_bounds__(kAppThreads, 2) append_kernel(const __grid_constant__ AppendArgs A) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
-  constexpr int kKeep = 8;                           // loads of a run kept in registers
+  constexpr int kKeep = 16;                          // loads of a run kept in registers
   // the largest finite magnitude that a scale reaches (448 * 2^40 in bf16)
   constexpr uint32_t kLimit = kBf16 ? 0x57e0u : 0x7bffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int block = 1 << A.log_block;
+  const int block = 1 << A.log_block, windows = 2 + (block >> 5);
   const int t0 = blockIdx.x * 32;
-  // the block of a row's slot, -1 for a row that is left out
+  // a row's slot, -1 for a row that is left out
   auto slot_of = [&](int t) {
     const int64_t s = t >= 0 && t < A.rows ? __ldg(A.slots + t) : -1;
     return s < A.num_slots ? s : -1;
   };
-  const int64_t slot = slot_of(t0 + lane), before = slot_of(t0 + lane - 1);
-  uint32_t starts = __ballot_sync(0xffffffffu, slot >= 0 && (before < 0 || slot >> A.log_block != before >> A.log_block));
-  const int runs = __popc(starts), units = runs * A.Hkv * 2;
-  int taken = -1, cur = -1;  // the run at hand
-  int64_t first = 0;
-  int n = 0;
-  bool ordered = true;
+  Rows R;
+  uint32_t starts = 0;
+  int64_t slot = -1;  // of the lane's row of the chunk
+#pragma unroll
+  for (int w = 0; w < Rows::kWindows; ++w) {
+    R.same[w] = R.higher[w] = 0;
+    if (w < windows) {
+      const int64_t s = slot_of(t0 + 32 * w + lane), p = slot_of(t0 + 32 * w + lane - 1);
+      const bool same = s >= 0 && p >= 0 && s >> A.log_block == p >> A.log_block;
+      R.same[w] = __ballot_sync(0xffffffffu, same);
+      R.higher[w] = __ballot_sync(0xffffffffu, same && s > p);
+      if (w == 0) {
+        slot = s;
+        starts = __ballot_sync(0xffffffffu, s >= 0 && !same);
+      }
+    }
+  }
+  const int units = __popc(starts) * A.Hkv * 2;
+  int at_run = 0;  // the run that is the lowest bit of `starts`
 #pragma unroll 1
   for (int u = blockIdx.y * kAppWarps + warp; u < units; u += gridDim.y * kAppWarps) {
     const int run = u / (2 * A.Hkv), h = (u - run * 2 * A.Hkv) >> 1, which = u & 1;
-    if (run != taken) {
-      // the run's first row, its rows and whether their slots ascend
-      taken = run;
-      cur = __fns(starts, 0, run + 1);
-      first = __shfl_sync(0xffffffffu, slot, cur);
-      n = 0;
-      ordered = true;
-#pragma unroll 1
-      for (int i0 = 0; i0 <= block; i0 += 32) {
-        const int t = t0 + cur + i0 + lane;
-        const int64_t s = slot_of(t), p = slot_of(t - 1);
-        const bool in = s >= 0 && s >> A.log_block == first >> A.log_block;
-        const uint32_t all = __ballot_sync(0xffffffffu, in);
-        const int more = all == 0xffffffffu ? 32 : __ffs(~all) - 1;
-        ordered = ordered && !__any_sync(0xffffffffu, in && lane < more && (i0 + lane > 0) && s <= p);
+    for (; at_run < run; ++at_run) starts &= starts - 1;
+    const int cur = __ffs(starts) - 1;
+    const int64_t first = __shfl_sync(0xffffffffu, slot, cur);
+    const uint16_t* x =
+        A.x[which] + (int64_t)(t0 + cur) * A.row[which] + h * A.head[which] + lane % kLanes * 8;
+    const int mine = lane / kLanes;  // the lane's row of a load
+    // the run's rows, and whether their slots ascend
+    int n = 1;
+    bool ordered = true, open = true;
+#pragma unroll
+    for (int w = 0; w < Rows::kWindows; ++w) {
+      if (w < windows && open) {
+        const int from = w == 0 ? cur + 1 : 0;
+        const uint32_t rest = from < 32 ? R.same[w] >> from : 0u;
+        const int more = ~rest ? __ffs(~rest) - 1 : 32;  // rows that go on
+        const uint32_t mask = more == 32 ? 0xffffffffu : (1u << more) - 1;
+        ordered = ordered && !(mask & ~(from < 32 ? R.higher[w] >> from : 0u));
+        open = from + more == 32;
         n += more;
-        if (more < 32) break;
       }
-      ordered = ordered && n <= block;
     }
+    ordered = ordered && n <= block;
     const int64_t page = first >> A.log_page;
     const int at = (int)(first & ((1 << A.log_page) - 1));
     float* scale_at = A.scale[which] + (page * (1 << (A.log_page - A.log_block)) + (at >> A.log_block)) * A.Hkv + h;
@@ -111,36 +129,46 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
       continue;
     }
     const int earlier = at & (block - 1);  // slots of the block below the first new one
-    const float old = earlier ? *scale_at : 0.0f;
-    const uint16_t* x = A.x[which] + (int64_t)(t0 + cur) * A.row[which] + h * A.head[which] + lane % kLanes * 8;
-    const int mine = lane / kLanes;  // the lane's row of a load
     auto load = [&](int i) {
-      return i < n ? *reinterpret_cast<const uint4*>(x + i * A.row[which]) : make_uint4(0u, 0u, 0u, 0u);
+      return i < n ? ld_stream16(x + i * A.row[which]) : make_uint4(0u, 0u, 0u, 0u);
     };
     uint4 keep[kKeep];
-    uint32_t top = 0;
-    auto raise = [&](const uint4& v) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = w[k] & 0x7fffu, hi = w[k] >> 16 & 0x7fffu;
-        top = max(top, max(lo > kLimit ? 0u : lo, hi > kLimit ? 0u : hi));
-      }
-    };
 #pragma unroll
     for (int s = 0; s < kKeep; ++s) keep[s] = load(s * kPer + mine);
+    const float old = earlier ? *scale_at : 0.0f;
+    // the largest magnitude by its bits, two numbers in a word
+    uint32_t most = 0;
+    auto raise = [&](const uint4& v) {
+      most = __vmaxu2(most, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                     __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+    };
 #pragma unroll
-    for (int s = 0; s < kKeep; ++s) raise(keep[s]);
+    for (int s = 0; s < kKeep; ++s)
+      if (s * kPer < n) raise(keep[s]);
 #pragma unroll 1
-    for (int s0 = kKeep; s0 * kPer < n; s0 += kKeep) {
-      uint4 v[kKeep];
+    for (int s0 = kKeep; s0 * kPer < n; s0 += 4) {
+      uint4 v[4];
 #pragma unroll
-      for (int s = 0; s < kKeep; ++s) v[s] = load((s0 + s) * kPer + mine);
+      for (int s = 0; s < 4; ++s) v[s] = load((s0 + s) * kPer + mine);
 #pragma unroll
-      for (int s = 0; s < kKeep; ++s) raise(v[s]);
+      for (int s = 0; s < 4; ++s) raise(v[s]);
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    uint32_t top = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+    const bool odd = top > kLimit;
+    if (__builtin_expect(odd, 0)) {  // numbers past the limit do not count
+      most = 0;
+#pragma unroll 1
+      for (int s = 0; s * kPer < n; ++s) {
+        const uint4 v = load(s * kPer + mine);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = w[k] & 0x7fffu, hi = w[k] >> 16 & 0x7fffu;
+          most = max(most, max(lo > kLimit ? 0u : lo, hi > kLimit ? 0u : hi));
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, most);
+    }
     // 448 = 1.75 * 2^8
     const uint32_t bits = __float_as_uint(unpack16<kBf16>(top).x);
     const int e = max(-40, (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u));
@@ -156,7 +184,7 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
         // earlier codes, four at a time (those of a scale of 0 stand for 0, and become 0)
         const float ratio = old / scale;
         unsigned char* p = pool + (int64_t)(at - earlier) * token;
-#pragma unroll 4
+#pragma unroll 2
         for (int q = lane; q < earlier * (D / 4); q += 32) {
           uint32_t* w = reinterpret_cast<uint32_t*>(p + (int64_t)(q / (D / 4)) * token + q % (D / 4) * 4);
           const uint32_t v = *w;
@@ -173,24 +201,34 @@ __global__ void __launch_bounds__(kAppThreads) append_kernel(const __grid_consta
       }
     }
     if (lane == 0) *scale_at = scale;
-    const bool exact = (__float_as_uint(scale) & 0x7fffffu) == 0;
-    const float inverse = 1.0f / scale;
+    const bool plain = !odd && (__float_as_uint(scale) & 0x7fffffu) == 0;
+    unsigned char* const column = pool + lane % kLanes * 8;
     // slots ascend, but need not be neighbours
-    auto store = [&](int i, const uint4& v) {
-      if (i >= n) return;
-      const int64_t s = __ldg(A.slots + t0 + cur + i);
-      *reinterpret_cast<uint2*>(pool + (s & ((1 << A.log_page) - 1)) * token + lane % kLanes * 8) =
-          code8<kBf16>(v, scale, inverse, exact, kLimit);
-    };
+    const bool close = n == 1 || __ldg(A.slots + t0 + cur + n - 1) - first == n - 1;
+    if (__builtin_expect(plain && close, 1)) {
+      const float inverse = 1.0f / scale;
+      unsigned char* to = column + (at + mine) * token;
 #pragma unroll
-    for (int s = 0; s < kKeep; ++s) store(s * kPer + mine, keep[s]);
+      for (int s = 0; s < kKeep; ++s, to += kPer * token)
+        if (s * kPer < n && s * kPer + mine < n)
+          *reinterpret_cast<uint2*>(to) = code8<kBf16, true>(keep[s], inverse, kLimit);
 #pragma unroll 1
-    for (int s0 = kKeep; s0 * kPer < n; s0 += kKeep) {
-      uint4 v[kKeep];
+      for (int s0 = kKeep; s0 * kPer < n; s0 += 4, to += 4 * kPer * token) {
+        uint4 v[4];
 #pragma unroll
-      for (int s = 0; s < kKeep; ++s) v[s] = load((s0 + s) * kPer + mine);
+        for (int s = 0; s < 4; ++s) v[s] = load((s0 + s) * kPer + mine);
 #pragma unroll
-      for (int s = 0; s < kKeep; ++s) store((s0 + s) * kPer + mine, v[s]);
+        for (int s = 0; s < 4; ++s)
+          if ((s0 + s) * kPer + mine < n)
+            *reinterpret_cast<uint2*>(to + s * kPer * token) = code8<kBf16, true>(v[s], inverse, kLimit);
+      }
+    } else {
+      // (kept short, as rare as it is: beside the loop above it pushed that out of the instruction cache)
+#pragma unroll 1
+      for (int i = mine; i < n; i += kPer) {
+        const int s = (int)(__ldg(A.slots + t0 + cur + i) & ((1 << A.log_page) - 1));
+        *reinterpret_cast<uint2*>(column + s * token) = code8<kBf16, false>(load(i), scale, kLimit);
+      }
     }
   }
 }

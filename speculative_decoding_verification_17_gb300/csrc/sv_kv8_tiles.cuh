@@ -446,11 +446,6 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ Two two_mul(Two a, Two b) {
-  Two v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
 // One arrival per warp: those of single threads queue up (384 of them on two barriers per tile were a
 // third of the time of the long caches).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {

@@ -7,7 +7,8 @@
 // ring's end).
 //
 // Bound: latency for a step (three dependent loads and two scans); for packed prompts the 12 bytes of
-// a row. A thread takes four rows, which share a search and leave in 16-byte stores.
+// a row. There a thread takes eight rows, whose pages are looked up at once and which mostly share a
+// search.
 #include <cstdint>
 
 #include "specverify_step.h"
@@ -21,7 +22,6 @@ int device_sm_count();
 namespace {
 
 constexpr int kMapThreads = 512;
-constexpr int kRowsPer = 4;
 constexpr int kMaxRequests = 8192;
 
 struct MapArgs {
@@ -34,27 +34,42 @@ struct MapArgs {
   int32_t *positions, *out_len, *out_first, *out_state;
 };
 
-// Exclusive prefix of x over the block's threads, and the total (two CTA barriers).
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* scratch, int64_t* total) {
+// Exclusive prefixes of kCount numbers over the block's threads, and their totals (two CTA barriers).
+template <int kCount>
+__device__ __forceinline__ void block_scan(int64_t (&x)[kCount], int64_t (*scratch)[kMapThreads / 32],
+                                           int64_t (&total)[kCount]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = x;
+  int64_t incl[kCount];
+#pragma unroll
+  for (int k = 0; k < kCount; ++k) incl[k] = x[k];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kMapThreads / 32; ++w) {
-    const int64_t s = scratch[w];
-    if (w < warp) before += s;
-    all += s;
+    for (int k = 0; k < kCount; ++k) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl[k], o);
+      if (lane >= o) incl[k] += y;
+    }
+  }
+  constexpr int kWarps = kMapThreads / 32;
+  if (lane == 31) {
+#pragma unroll
+    for (int k = 0; k < kCount; ++k) scratch[k][warp] = incl[k];
   }
   __syncthreads();
-  *total = all;
-  return before + incl - x;
+  // every warp sums the warps' totals
+#pragma unroll
+  for (int k = 0; k < kCount; ++k) {
+    int64_t sum = lane < kWarps ? scratch[k][lane] : 0;
+#pragma unroll
+    for (int o = 1; o < kWarps; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const int64_t before = __shfl_sync(0xffffffffu, sum, (warp + 31) & 31);
+    total[k] = __shfl_sync(0xffffffffu, sum, kWarps - 1);
+    x[k] = (warp == 0 ? 0 : before) + incl[k] - x[k];
+  }
+  __syncthreads();
 }
 
 __device__ __forceinline__ int capped(int64_t x) { return x < INT32_MAX ? (int)x : INT32_MAX; }
@@ -90,58 +105,74 @@ __device__ __forceinline__ Request load_request(const MapArgs& A, int b) {
   return r;
 }
 
-__global__ void __launch_bounds__(kMapThreads) map_kernel(const MapArgs A) {
+// kRowsPer rows to a thread: one where rows are few, so that every load is on its way at once.
+template <int kRowsPer>
+__global__ void __launch_bounds__(kMapThreads, kRowsPer == 1 ? 2 : 3) map_kernel(const MapArgs A) {
   extern __shared__ int map_smem[];
-  __shared__ int64_t scratch[kMapThreads / 32];
-  int* first = map_smem;            // [B + 1] rows before each request (packed rows)
-  int* taken = first + A.B + 1;     // [B + 1] growth before each request
-  int* given = taken + A.B + 1;     // [B + 1] pages given back before each request
+  __shared__ int64_t scratch[2][kMapThreads / 32];
+  int* first = map_smem;         // [B + 1] rows before each request (packed rows)
+  int* taken = first + A.B + 1;  // [B + 1] growth before each request
+  int* given = taken + A.B + 1;  // [B + 1] pages given back before each request
+  int* have = given + A.B + 1;   // [B] pages held
+  int* rows_of = have + A.B;     // [B] new rows, 0 where the request gets none
+  int* begin = rows_of + A.B;    // [B] the first new row's position
+  int* length = begin + A.B;     // [B] the length it comes out with
   const int tid = threadIdx.x;
   const int head = __ldg(A.state), count = __ldg(A.state + 1);
   const int each = (A.B + kMapThreads - 1) / kMapThreads;
   const int b0 = min(tid * each, A.B), b1 = min(b0 + each, A.B);
 
-  int64_t rows = 0, total;
-  for (int b = b0; b < b1; ++b) rows += load_request(A, b).add;
-  int64_t at = block_scan(rows, scratch, &total);
-  if (tid == 0) first[A.B] = capped(total);
-  int64_t grow = 0, drop = 0;
+  int64_t total[1] = {0}, at[1] = {0};
+  if (A.P == 0) {
+    for (int b = b0; b < b1; ++b) at[0] += load_request(A, b).add;
+    block_scan<1>(at, scratch, total);
+  }
+  auto lost = [&](const Request& r, int64_t row) {  // a data error of the request, its first row given
+    return !r.valid || (A.P == 0 && row + r.add > A.rows);
+  };
+  int64_t moved[2] = {0, 0}, all[2], row = at[0];  // taken, given back
   for (int b = b0; b < b1; ++b) {
     const Request r = load_request(A, b);
-    first[b] = capped(at);
-    at += r.add;
-    if (A.P == 0 && at > A.rows) continue;  // its rows do not fit
-    grow += max(r.need - r.have, 0);
-    drop += max(r.have - r.need, 0);
+    if (!lost(r, row)) {
+      moved[0] += max(r.need - r.have, 0);
+      moved[1] += max(r.have - r.need, 0);
+    }
+    row += r.add;
   }
-  int64_t all_grow, all_drop;
-  int64_t g = block_scan(grow, scratch, &all_grow), d = block_scan(drop, scratch, &all_drop);
+  block_scan<2>(moved, scratch, all);
+  const bool ring_ok = head >= 0 && head < A.ring_size && count >= 0 && count <= A.ring_size &&
+                       all[1] <= (int64_t)A.ring_size - count;
+  // requests find pages as long as the sum of the growth up to them is at most count (a sum that was
+  // capped is more than any count)
+  auto enough = [&](int sum) { return sum <= count && sum != INT32_MAX; };
+  auto place = [&](unsigned x) { return x < (unsigned)A.ring_size ? x : x - A.ring_size; };
+  row = at[0];
+  for (int b = b0; b < b1; ++b) {
+    const Request r = load_request(A, b);
+    first[b] = A.P > 0 ? b * A.P : capped(row);
+    taken[b] = capped(moved[0]);
+    given[b] = capped(moved[1]);
+    const bool bad = lost(r, row);
+    if (!bad) {
+      moved[0] += max(r.need - r.have, 0);
+      moved[1] += max(r.have - r.need, 0);
+    }
+    row += r.add;
+    const bool fits = r.need <= r.have || enough(capped(moved[0]));
+    have[b] = r.have;
+    begin[b] = r.n - r.add;
+    rows_of[b] = ring_ok && !bad && fits ? r.add : 0;
+    length[b] = !ring_ok || bad ? -1 : fits ? r.n : r.old_len;
+  }
   if (tid == 0) {
-    taken[A.B] = capped(all_grow);
-    given[A.B] = capped(all_drop);
-  }
-  for (int b = b0; b < b1; ++b) {
-    const Request r = load_request(A, b);
-    taken[b] = capped(g);
-    given[b] = capped(d);
-    if (A.P == 0 && (int64_t)first[b] + r.add > A.rows) continue;
-    g += max(r.need - r.have, 0);
-    d += max(r.have - r.need, 0);
+    first[A.B] = A.P > 0 ? A.B * A.P : capped(total[0]);
+    taken[A.B] = capped(all[0]);
+    given[A.B] = capped(all[1]);
   }
   __syncthreads();
-
-  const bool ring_ok = head >= 0 && head < A.ring_size && count >= 0 && count <= A.ring_size &&
-                       all_drop <= (int64_t)A.ring_size - count;
-  // requests find pages as long as the sum of the growth up to them is at most count
-  // (a sum that was capped is more than any count)
-  auto enough = [&](int sum) { return sum <= count && sum != INT32_MAX; };
-  auto fits = [&](const Request& r, int b) { return r.need <= r.have || enough(taken[b + 1]); };
-  auto lost = [&](const Request& r, int b) {  // a data error of the request
-    return !r.valid || (A.P == 0 && (int64_t)first[b] + r.add > A.rows);
-  };
-  auto place = [&](unsigned x) { return x < (unsigned)A.ring_size ? x : x - A.ring_size; };
-  int most = 0;  // pages taken: the largest sum that fits
-  {
+  // pages taken: the largest sum that fits
+  int most = 0;
+  if (ring_ok) {
     int lo = 0, hi = A.B + 1;  // taken[lo] is enough, taken[hi] not
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -152,81 +183,73 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(const MapArgs A) {
     }
     most = taken[lo];
   }
-  const int stride = gridDim.x * kMapThreads, me = blockIdx.x * kMapThreads + tid;
+  const int drops = ring_ok ? (int)all[1] : 0;
 
-  // rows
-  for (int64_t row0 = (int64_t)me * kRowsPer; row0 < A.rows; row0 += (int64_t)stride * kRowsPer) {
-    int64_t slot[kRowsPer];
-    int pos[kRowsPer];
+  // one range of work: groups of rows, new table entries, pages that go back, requests
+  const int64_t groups = ((int64_t)A.rows + 32 * kRowsPer - 1) / (32 * kRowsPer) * 32;
+  const int64_t work = groups + most + drops + A.B + 1;
+#pragma unroll 1
+  for (int64_t x = (int64_t)blockIdx.x * kMapThreads + tid; x < work;
+       x += (int64_t)gridDim.x * kMapThreads) {
+    if (x >= groups) {
+      int y = (int)(x - groups);
+      if (y < most) {
+        const int b = find(taken, A.B, y);
+        A.table[(int64_t)b * A.max_pages + have[b] + (y - taken[b])] = __ldg(A.ring + place((unsigned)head + y));
+        continue;
+      }
+      y -= most;
+      if (y < drops) {
+        // (its entries from the new length's page on)
+        const int b = find(given, A.B, y), left = have[b] - (given[b + 1] - given[b]);
+        A.ring[place(place((unsigned)head + count) + (unsigned)y)] =
+            __ldg(A.table + (int64_t)b * A.max_pages + left + (y - given[b]));
+        continue;
+      }
+      y -= drops;
+      A.out_first[y] = first[y];
+      if (y < A.B) {
+        A.out_len[y] = length[y];
+      } else {
+        A.out_state[0] = ring_ok ? (int)place((unsigned)head + most) : -1;
+        A.out_state[1] = ring_ok ? count - most + drops : -1;
+      }
+      continue;
+    }
+    // (a warp's threads take its rows in turn: their stores lie side by side)
+    const uint32_t row0 = (uint32_t)x / 32 * (32 * kRowsPer) + (x & 31), rows = A.rows;
+    int pos[kRowsPer], page[kRowsPer];
     int b = -1, end = 0, start = 0;
-    Request r{};
-    bool live = false;
 #pragma unroll
     for (int k = 0; k < kRowsPer; ++k) {
-      const int64_t row = row0 + k;
-      slot[k] = pos[k] = -1;
-      if (row >= A.rows || !ring_ok) continue;
+      pos[k] = page[k] = -1;
+      if (row0 + 32 * k >= rows) continue;
+      const int row = (int)(row0 + 32 * k);
       if (b < 0 || row >= end) {
         if (A.P > 0) {
-          b = (int)(row / A.P);
-          start = b * A.P;
-          end = start + A.P;
+          b = row / A.P;
         } else {
           if (row >= first[A.B]) continue;
-          b = find(first, A.B, (int)row);
-          start = first[b];
-          end = first[b + 1];
+          b = find(first, A.B, row);
         }
-        r = load_request(A, b);
-        live = !lost(r, b) && fits(r, b);
+        start = first[b];
+        end = first[b + 1];
       }
-      const int i = (int)row - start;
-      if (!live || i >= r.add) continue;
-      const int p = r.n - r.add + i, t = p >> A.log_page;
-      const int page = t < r.have
-                           ? __ldg(A.table + (int64_t)b * A.max_pages + t)
-                           : __ldg(A.ring + place((unsigned)head + taken[b] + (t - r.have)));
-      pos[k] = p;
-      if (page >= 0 && page < A.num_pages)
-        slot[k] = ((int64_t)page << A.log_page) + (p & ((1 << A.log_page) - 1));
+      const int i = row - start;
+      if (i >= rows_of[b]) continue;
+      pos[k] = begin[b] + i;
+      const int t = pos[k] >> A.log_page, held = have[b];
+      page[k] = __ldg(t < held ? A.table + (int64_t)b * A.max_pages + t
+                               : A.ring + place((unsigned)head + taken[b] + (t - held)));
     }
-    if (row0 + kRowsPer <= A.rows && ((uintptr_t)A.slots & 15) == 0 &&
-        ((uintptr_t)A.positions & 15) == 0) {
-      longlong2* s = reinterpret_cast<longlong2*>(A.slots + row0);
-      s[0] = make_longlong2(slot[0], slot[1]);
-      s[1] = make_longlong2(slot[2], slot[3]);
-      *reinterpret_cast<int4*>(A.positions + row0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-    } else {
 #pragma unroll
-      for (int k = 0; k < kRowsPer; ++k)
-        if (row0 + k < A.rows) {
-          A.slots[row0 + k] = slot[k];
-          A.positions[row0 + k] = pos[k];
-        }
+    for (int k = 0; k < kRowsPer; ++k) {
+      const uint32_t row = row0 + 32 * k;
+      if (row >= rows) break;
+      const bool there = page[k] >= 0 && page[k] < A.num_pages;
+      A.slots[row] = there ? ((int64_t)page[k] << A.log_page) + (pos[k] & ((1 << A.log_page) - 1)) : -1;
+      A.positions[row] = pos[k];
     }
-  }
-  if (ring_ok) {
-    // table entries of new pages
-    for (int x = me; x < most; x += stride) {
-      const int b = find(taken, A.B, x);
-      A.table[(int64_t)b * A.max_pages + load_request(A, b).have + (x - taken[b])] =
-          __ldg(A.ring + place((unsigned)head + x));
-    }
-    // pages that go back
-    for (int x = me; x < (int)all_drop; x += stride) {
-      const int b = find(given, A.B, x);
-      A.ring[place(place((unsigned)head + count) + (unsigned)x)] =
-          __ldg(A.table + (int64_t)b * A.max_pages + load_request(A, b).need + (x - given[b]));
-    }
-  }
-  for (int b = me; b < A.B; b += stride) {
-    const Request r = load_request(A, b);
-    A.out_len[b] = !ring_ok || lost(r, b) ? -1 : fits(r, b) ? r.n : r.old_len;
-  }
-  for (int b = me; b <= A.B; b += stride) A.out_first[b] = A.P > 0 ? b * A.P : first[b];
-  if (me == 0) {
-    A.out_state[0] = ring_ok ? (int)place((unsigned)head + most) : -1;
-    A.out_state[1] = ring_ok ? count - most + (int)all_drop : -1;
   }
 }
 
@@ -272,17 +295,19 @@ extern "C" sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* p
   const MapArgs A{B,      log2_of(page_size), num_pages,  max_pages,     ring_size, P,         rows,
                   page_table, old_len,        seq_len,    num_new,       ring,      ring_state,
                   out_slots,  out_positions,  out_len,    out_first,     out_state};
-  const size_t smem = 3 * (size_t)(B + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 3 * (kMaxRequests + 1) * sizeof(int));
+  // a thread per row up to two CTAs per SM of them, then eight rows to a thread
+  const int64_t sms = device_sm_count(), few = 2 * sms * kMapThreads;
+  const int per = rows <= few ? 1 : 8;
+  auto kernel = per == 1 ? map_kernel<1> : map_kernel<8>;
+  const size_t smem = 7 * (size_t)(B + 1) * sizeof(int);
+  if (smem > 47 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               7 * (kMaxRequests + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return cuda_fail(e);
   }
-  // a CTA per 2048 rows and per 512 requests, at most two per SM
-  const int64_t wanted = (rows + kMapThreads * kRowsPer - 1ll) / (kMapThreads * kRowsPer);
-  const int64_t other = (B + kMapThreads - 1) / kMapThreads;
-  int64_t ctas = wanted > other ? wanted : other;
-  if (ctas > 2 * device_sm_count()) ctas = 2 * device_sm_count();
-  map_kernel<<<(unsigned)ctas, kMapThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(A);
+  int64_t ctas = (rows / per + 2ll * B + kMapThreads - 1) / kMapThreads;
+  const int64_t most = 2 * sms;
+  if (ctas > most) ctas = most;
+  kernel<<<(unsigned)ctas, kMapThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(A);
   return launch_status();
 }

@@ -11,8 +11,8 @@
 // product modulo one turn is an integer product modulo 2^64, off by 2^-65 of a turn per position; what
 // is left is rounded to fp32 once (2^-25 of a half turn).
 //
-// Bound: reading and writing every row once. A head of D = 128 is 16 lanes of 16 bytes, a warp takes
-// two at a time, and loads those it takes next before it works on the ones at hand.
+// Bound: reading and writing every row once. A head of D = 128 is 16 lanes of 16 bytes; a warp takes
+// two at a time and loads four such pairs at once.
 #include <cstdint>
 
 #include "specverify_step.h"
@@ -23,13 +23,7 @@
 namespace sv {
 namespace {
 
-#ifndef ROT_CTAS
-#define ROT_CTAS 3
-#endif
-#ifndef ROT_AHEAD
-#define ROT_AHEAD 4
-#endif
-constexpr int kRotThreads = 256, kRotWarps = kRotThreads / 32;
+constexpr int kRotThreads = 256, kRotWarps = kRotThreads / 32, kRotCtas = 4;
 
 struct HeadRows {
   const uint16_t* in;
@@ -47,22 +41,11 @@ struct RotArgs {
   float eps;
 };
 
-template <bool kBf16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 p = unpack16<kBf16>(w[k]);
-    f[2 * k] = p.x;
-    f[2 * k + 1] = p.y;
-  }
-}
-
 // (Not through the read-only path: outputs may be the inputs.)
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+__device__ __forceinline__ uint2 load8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
                : "l"(p)
                : "memory");
   return v;
@@ -71,10 +54,13 @@ __device__ __forceinline__ uint4 load16(const void* p) {
 // kSplit warps share a row (one token's heads). Nothing is shared between warps but the frequencies
 // and the weights, so no warp waits for another one's rows: with a table of cosines per CTA and
 // barriers around it prompts of 24576 rows took 145 us.
-template <int D, bool kBf16, int kSplit>
-__global__ void __launch_bounds__(kRotThreads, ROT_CTAS) rotate_kernel(const __grid_constant__ RotArgs A) {
+// A lane holds eight components of a head: four pairs (a, b). Of halves those are four of the first
+// and four of the second, in two loads of 8 bytes, so that no component has to come from another
+// lane (with 16 consecutive bytes per lane and shuffles, 157 instructions a step, 107 us).
+template <int D, bool kBf16, bool kInterleaved, int kSplit>
+__global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __grid_constant__ RotArgs A) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a head, heads at a time
-  constexpr int kAhead = ROT_AHEAD;                          // groups of heads in flight
+  constexpr int kAhead = 4;                          // groups of heads in flight
   __shared__ uint64_t turn[D / 2];                   // frequencies in 2^-64 of a turn
   __shared__ float odd[D / 2];                       // NaN where one is not finite, else 0
   __shared__ float weight[2][D];
@@ -95,10 +81,14 @@ __global__ void __launch_bounds__(kRotThreads, ROT_CTAS) rotate_kernel(const __g
                                           : unpack16<kBf16>(static_cast<const uint16_t*>(w)[e % D]).x;
   }
   __syncthreads();
-  const int sub = warp % kSplit, d0 = lane % kLanes * 8;
-  const int mate = A.interleaved ? 0 : d0 < half ? half : -half;
-  const int from = A.interleaved || d0 >= A.R ? lane : lane + mate / 8;  // the partners' lane
-  const bool turned = d0 < A.R;
+  const int place = lane % kLanes, sub = warp % kSplit;
+  // where the lane's two groups of four components start, and those of its k-th pair
+  const bool turned = place * 8 < A.R;
+  const int da = kInterleaved || !turned ? place * 8 : place * 4;
+  const int db = kInterleaved || !turned ? place * 8 + 4 : half + place * 4;
+  auto component = [&](int k, int which) {  // of the pair's first or second
+    return kInterleaved ? da + 2 * k + which : which ? db + k : da + k;
+  };
   constexpr int64_t kRows = kRotWarps / kSplit;
 #pragma unroll 1
   for (int64_t row = blockIdx.x * kRows + warp / kSplit; row < A.rows; row += gridDim.x * kRows) {
@@ -117,98 +107,121 @@ __global__ void __launch_bounds__(kRotThreads, ROT_CTAS) rotate_kernel(const __g
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
       const HeadRows& X = A.x[which];
-      // what multiplies the element and its partner
-      float c[8], s[8];
+      // out a = a * aa + b * ab, out b = a * ba + b * bb (times the head's own factor)
+      Two aa[2], ab[2], ba[2], bb[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = d0 + e;
-        float2 cs = make_float2(1.0f, 0.0f);
-        int other = d;
-        if (turned) {
-          cs = table[warp][A.interleaved ? d >> 1 : d < half ? d : d - half];
-          other = A.interleaved ? d ^ 1 : d + mate;
-          if (A.interleaved ? !(d & 1) : d < half) cs.y = -cs.y;
+      for (int k = 0; k < 4; k += 2) {
+        float f[2][4];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float wa = weight[which][component(k + q, 0)], wb = weight[which][component(k + q, 1)];
+          const float2 cs = turned ? table[warp][place * 4 + k + q] : make_float2(1.0f, 0.0f);
+          f[q][0] = wa * cs.x;
+          f[q][1] = -wb * cs.y;
+          f[q][2] = wa * cs.y;
+          f[q][3] = wb * cs.x;
         }
-        c[e] = weight[which][d] * cs.x;
-        s[e] = weight[which][other] * cs.y;
+        aa[k / 2] = two(f[0][0], f[1][0]);
+        ab[k / 2] = two(f[0][1], f[1][1]);
+        ba[k / 2] = two(f[0][2], f[1][2]);
+        bb[k / 2] = two(f[0][3], f[1][3]);
       }
-      const uint16_t* in = X.in + req * X.req + at * X.row + d0;
-      uint16_t* out = X.out + req * X.out_req + at * X.out_row + d0;
+      const uint16_t* in = X.in + req * X.req + at * X.row;
+      uint16_t* out = X.out + req * X.out_req + at * X.out_row;
       constexpr int kStep = kSplit * kPer;
       const int first = sub * kPer + lane / kLanes;
 #pragma unroll 1
       for (int h0 = 0; h0 < X.heads; h0 += kAhead * kStep) {
-        uint4 raw[kAhead];
+        const uint16_t* from = in + (h0 + first) * X.head;
+        uint16_t* to = out + (h0 + first) * X.out_head;
+        uint2 va[kAhead], vb[kAhead];
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          const int h = h0 + first + a * kStep;
-          raw[a] = make_uint4(0u, 0u, 0u, 0u);
-          if (h < X.heads) raw[a] = load16(in + h * X.head);
+        for (int g = 0; g < kAhead; ++g, from += kStep * X.head) {
+          va[g] = vb[g] = make_uint2(0u, 0u);
+          if (h0 + first + g * kStep < X.heads) {
+            va[g] = load8(from + da);
+            vb[g] = load8(from + db);
+          }
         }
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-          const int h = h0 + first + a * kStep;
-          if (h0 + a * kStep >= X.heads) break;  // (whole warps)
-          float x[8], y[8];
-          unpack8<kBf16>(raw[a], x);
+        for (int g = 0; g < kAhead; ++g, to += kStep * X.out_head) {
+          if (h0 + g * kStep >= X.heads) break;  // (whole warps)
+          const uint32_t w[4] = {va[g].x, va[g].y, vb[g].x, vb[g].y};
+          Two a[2], b[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 u = unpack16<kBf16>(w[kInterleaved ? 2 * k : k]);
+            const float2 v = unpack16<kBf16>(w[kInterleaved ? 2 * k + 1 : k + 2]);
+            a[k] = kInterleaved ? two(u.x, v.x) : two(u.x, u.y);
+            b[k] = kInterleaved ? two(u.y, v.y) : two(v.x, v.y);
+          }
           float r = 1.0f;
           if (A.norm) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], sum);
+            const float2 q = split(two_fma(a[0], a[0], two_fma(a[1], a[1], two_fma(b[0], b[0], two_mul(b[1], b[1])))));
+            float sum = q.x + q.y;
 #pragma unroll
             for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             r = rsqrtf(sum * (1.0f / D) + A.eps);
           }
-          if (A.interleaved) {
+          const Two rr = two(r, r);
+          float2 x[2], y[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
-          } else {
-            uint4 v;
-            v.x = __shfl_sync(0xffffffffu, raw[a].x, from);
-            v.y = __shfl_sync(0xffffffffu, raw[a].y, from);
-            v.z = __shfl_sync(0xffffffffu, raw[a].z, from);
-            v.w = __shfl_sync(0xffffffffu, raw[a].w, from);
-            unpack8<kBf16>(v, y);
-          }
-          uint32_t w[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = 2 * k;
+          for (int k = 0; k < 2; ++k) {
             // (components past R have no partner: what lies there may be infinite)
-            const float p0 = turned ? fmaf(y[e], s[e], x[e] * c[e]) : x[e] * c[e];
-            const float p1 = turned ? fmaf(y[e + 1], s[e + 1], x[e + 1] * c[e + 1]) : x[e + 1] * c[e + 1];
-            w[k] = pack16<kBf16>(r * p0, r * p1);
+            Two u = two_mul(a[k], aa[k]), v = two_mul(b[k], bb[k]);
+            if (turned) {
+              u = two_fma(b[k], ab[k], u);
+              v = two_fma(a[k], ba[k], v);
+            }
+            x[k] = split(two_mul(u, rr));
+            y[k] = split(two_mul(v, rr));
           }
-          if (h < X.heads)
-            *reinterpret_cast<uint4*>(out + h * X.out_head) = make_uint4(w[0], w[1], w[2], w[3]);
+          if (h0 + first + g * kStep < X.heads) {
+            if (kInterleaved) {
+              *reinterpret_cast<uint2*>(to + da) =
+                  make_uint2(pack16<kBf16>(x[0].x, y[0].x), pack16<kBf16>(x[0].y, y[0].y));
+              *reinterpret_cast<uint2*>(to + db) =
+                  make_uint2(pack16<kBf16>(x[1].x, y[1].x), pack16<kBf16>(x[1].y, y[1].y));
+            } else {
+              *reinterpret_cast<uint2*>(to + da) =
+                  make_uint2(pack16<kBf16>(x[0].x, x[0].y), pack16<kBf16>(x[1].x, x[1].y));
+              *reinterpret_cast<uint2*>(to + db) =
+                  make_uint2(pack16<kBf16>(y[0].x, y[0].y), pack16<kBf16>(y[1].x, y[1].y));
+            }
+          }
         }
       }
     }
   }
 }
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kInterleaved>
 sv_status launch_rotate(const RotArgs& A, cudaStream_t st) {
   // a CTA per row while there are few, so that a row's heads are loaded at once; a warp per row once
   // those fill the SMs
   const int64_t sms = device_sm_count();
   if (A.rows <= 8 * sms) {
-    rotate_kernel<D, kBf16, 8><<<(unsigned)A.rows, kRotThreads, 0, st>>>(A);
+    rotate_kernel<D, kBf16, kInterleaved, 8><<<(unsigned)A.rows, kRotThreads, 0, st>>>(A);
   } else {
-    const int64_t want = (A.rows + kRotWarps - 1) / kRotWarps, ctas = want < ROT_CTAS * sms ? want : ROT_CTAS * sms;
-    rotate_kernel<D, kBf16, 1><<<(unsigned)ctas, kRotThreads, 0, st>>>(A);
+    const int64_t want = (A.rows + kRotWarps - 1) / kRotWarps, most = kRotCtas * sms;
+    rotate_kernel<D, kBf16, kInterleaved, 1>
+        <<<(unsigned)(want < most ? want : most), kRotThreads, 0, st>>>(A);
   }
   return launch_status();
+}
+
+template <int D, bool kBf16>
+sv_status launch_rotate_kind(const RotArgs& A, cudaStream_t st) {
+  return A.interleaved ? launch_rotate<D, kBf16, true>(A, st) : launch_rotate<D, kBf16, false>(A, st);
 }
 
 template <bool kBf16>
 sv_status launch_rotate_width(int D, const RotArgs& A, cudaStream_t st) {
   switch (D) {
-    case 64: return launch_rotate<64, kBf16>(A, st);
-    case 128: return launch_rotate<128, kBf16>(A, st);
+    case 64: return launch_rotate_kind<64, kBf16>(A, st);
+    case 128: return launch_rotate_kind<128, kBf16>(A, st);
   }
-  return launch_rotate<256, kBf16>(A, st);
+  return launch_rotate_kind<256, kBf16>(A, st);
 }
 
 }  // namespace
