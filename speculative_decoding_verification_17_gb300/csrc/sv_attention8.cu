@@ -27,13 +27,14 @@ sv_status check_shape8(const sv_kv_shape* s) {
 }
 
 // Workspace: what each CTA leaves to join, then two pieces per CTA.
+constexpr int kMaxCtasPerSm = 2;  // of every shape
 struct Layout8 {
   size_t part, total;
 };
 Layout8 layout8(const sv_kv_shape* s) {
   int pos_block, blocks, columns;
   row_blocks8(s, &pos_block, &blocks, &columns);
-  const size_t ctas = 2 * (size_t)device_sm_count();  // (at most)
+  const size_t ctas = kMaxCtasPerSm * (size_t)device_sm_count();
   Layout8 L{};
   L.part = round_up(ctas * sizeof(JoinItem), 256);
   L.total = round_up(L.part + 2 * ctas * columns * (s->D + 2) * sizeof(float), 256);
@@ -55,6 +56,7 @@ template <int D, int N, bool kBf16>
 sv_status launch8(const TileArgs& A, const CUtensorMap& mk, const CUtensorMap& mv,
                   const ValuePool& v, cudaStream_t st) {
   using S = TileShape8<D, N, kBf16>;
+  static_assert(S::CtasPerSm <= kMaxCtasPerSm, "the workspace holds two slots for each CTA");
   auto kernel = tile_kernel<S>;
   static std::atomic<uint64_t> ready{0};  // devices whose shared-memory limit is raised
   int dev = 0;

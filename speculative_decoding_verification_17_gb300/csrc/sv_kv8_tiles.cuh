@@ -60,7 +60,11 @@ struct TileShape8 {
   static constexpr int QBytes = QRows * N * D;
   static constexpr int NQ = 1;
   static constexpr int Parts = 4;  // of a weight
-  static constexpr int PTile = Parts * kTileKeys * N, PBytes = 2 * PTile, NP = 1;
+  // Tiles of a pass. Two hide the chain of one CTA on an SM (24 rows of 64 requests: 83 us, one at a
+  // time 89; 48 rows: 102, 110). One leaves 64 columns, and two CTAs, enough registers (64 rows: 131
+  // us, two at a time 145; 12 rows: 62, 74; 4 rows of 128 dimensions 57 either way, 2 of 256: 54, 56).
+  static constexpr int Pair = N == 64 || CtasPerSm > 1 ? 1 : 2;
+  static constexpr int PTile = Parts * kTileKeys * N, PBytes = Pair * PTile, NP = 1;
   static constexpr int kTables = 104 * N + 1920;
   static constexpr int kRoom = kSmemMax / CtasPerSm - (CtasPerSm == 2 ? 512 : 0) - kTables - 1024 -
                                NQ * QBytes - PBytes;
@@ -70,8 +74,8 @@ struct TileShape8 {
   static constexpr int MBlocks = (D + 127) / 128;
   static constexpr bool Wide = true;
   static constexpr int ON = Parts * N;
-  // a score buffer of two tiles, read into registers before the next ones need it
-  static constexpr int SN = QWide * N, OBase = 2 * SN;
+  // a score buffer of two tiles, read into registers before the next ones need it (or two of one)
+  static constexpr int SN = QWide * N, OBase = 2 * SN, SBufs = 2 / Pair;
   static constexpr int Outs = 1;  // (a piece's output leaves while the next one's first scores are made)
   static constexpr int TmemNeed = OBase + Outs * MBlocks * ON;
   static constexpr int TmemCols = TmemNeed <= 128 ? 128 : TmemNeed <= 256 ? 256 : 512;
@@ -92,8 +96,9 @@ struct WholeTiles {
       : lo((first_full(p, window) + kTileKeys - 1) >> 7), hi((p.pos0 + 1) >> 7) {}
   __device__ __forceinline__ bool edge(int t) const { return t < lo || t >= hi; }
   // How many go together from tile t (of left tiles, newest first) on.
+  template <class S>
   __device__ __forceinline__ int at(int t, int left) const {
-    return left > 1 && t < hi && t > lo ? 2 : 1;
+    return S::Pair == 2 && left > 1 && t < hi && t > lo ? 2 : 1;
   }
 };
 
@@ -320,10 +325,11 @@ __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh
     int i = 0;
 #pragma unroll 1
     while (i < tiles) {
-      const int last = i + whole.at(tile_at<S>(p, i), tiles - i);
-      if (!wait_phase(&sh.s_empty[0][0], (y & 1u) ^ 1u, &sh.waits)) goto end;
+      const int last = i + whole.template at<S>(tile_at<S>(p, i), tiles - i);
+      const uint32_t buf = y % S::SBufs;
+      if (!wait_phase(&sh.s_empty[0][buf], (y / S::SBufs & 1u) ^ 1u, &sh.waits)) goto end;
       tc_fence_after();
-      uint32_t d = sh.tmem;
+      uint32_t d = sh.tmem + buf * S::SN;
 #pragma unroll 1
       for (; i < last; ++i, d += S::SN) {
         uint64_t b = b0;
@@ -345,7 +351,7 @@ __device__ __forceinline__ void score_role8(const TileArgs& A, TileShared<S>& sh
           at.next(S::NK);
         }
       }
-      mma_commit(&sh.s_full[0][0]);
+      mma_commit(&sh.s_full[0][buf]);
       ++y;
     }
   }
@@ -375,7 +381,7 @@ __device__ __forceinline__ void value_role8(const TileArgs& A, TileShared<S>& sh
     int i = 0;
 #pragma unroll 1
     while (i < tiles) {
-      const int last = i + whole.at(tile_at<S>(p, i), tiles - i);
+      const int last = i + whole.template at<S>(tile_at<S>(p, i), tiles - i);
       if (__builtin_expect(whole.edge(tile_at<S>(p, i)), 0)) {
         RingPos look = at;
 #pragma unroll 1
@@ -509,13 +515,13 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
   const TileArgs& A = me.A;
   auto& sh = me.sh;
   const int t = tile_at<S>(p, i), j = t * kTileKeys + me.key;
-  const int both = whole.at(t, p.mb - p.ma - i);
+  const int both = whole.template at<S>(t, p.mb - p.ma - i);
   const bool edge = both == 1 && whole.edge(t);
   const float* columns = sh.column_scale[p.turn & 1];
   const int c0 = me.col0;
-  float ks[2], vs[2], lv[2];
+  float ks[S::Pair], vs[S::Pair], lv[S::Pair];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < S::Pair; ++q) {
     ks[q] = me.scales.k[q];
     vs[q] = me.scales.v[q];
     if (!(vs[q] >= 0.0f && vs[q] <= kMaxScale && fabsf(ks[q]) < INFINITY)) {
@@ -529,12 +535,13 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
   me.scales.page[0] = both == 2 ? me.scales.page[2] : me.scales.page[1];
   me.scales.page[1] = key_page(me, p, i + both + 2);
   me.scales.page[2] = key_page(me, p, i + both + 3);
-  wait_phase(&sh.s_full[0][0], (uint32_t)y & 1u, &sh.waits);
+  const uint32_t buf = (uint32_t)y % S::SBufs;
+  wait_phase(&sh.s_full[0][buf], (uint32_t)y / S::SBufs & 1u, &sh.waits);
   tc_fence_after();
-  float s[2][kC];
+  float s[S::Pair][kC];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const uint32_t at = me.lane_base + q * S::SN;
+  for (int q = 0; q < S::Pair; ++q) {
+    const uint32_t at = me.lane_base + (buf + q) * S::SN;
     float a[16], b[16];
     tmem_ld16(at + c0, a);
     if (kC == 16 || S::QWide == 4) tmem_ld16(kC == 16 ? at + S::N + c0 : at + 16, b);
@@ -553,11 +560,13 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
       }
     }
   }
-  warp_arrive(&sh.s_empty[0][0], me.lane);
-  float scale[2] = {A.rule.scale * kLog2e * ks[0], A.rule.scale * kLog2e * ks[1]};
+  warp_arrive(&sh.s_empty[0][buf], me.lane);
+  float scale[S::Pair];
+#pragma unroll
+  for (int q = 0; q < S::Pair; ++q) scale[q] = A.rule.scale * kLog2e * ks[q];
   if (__builtin_expect(edge || A.rule.softcap > 0.0f || A.rule.slopes, 0)) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < S::Pair; ++q) {
       if (q < both && (A.rule.softcap > 0.0f || A.rule.slopes)) {
         float held[kC];
 #pragma unroll
@@ -588,7 +597,7 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
     }
   };
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < S::Pair; ++q) {
     if (q == 1 && both == 1) break;
     Two e[kC / 2];
     exponents(q, e);
@@ -605,7 +614,8 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       most[c] = fmaf(s[0][c], scale[0], lv[0]);
-      if (both == 2) most[c] = fmaxf(most[c], fmaf(s[1][c], scale[1], lv[1]));
+      if (S::Pair == 2 && both == 2)
+        most[c] = fmaxf(most[c], fmaf(s[S::Pair - 1][c], scale[S::Pair - 1], lv[S::Pair - 1]));
     }
     raise8<S>(me, T, most, l, i == 0, y - 1, me.output(p.turn));
   }
@@ -614,7 +624,7 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
   // (what is below the last part's step of 2^-16 is rounded)
   const Two half = two(7.62939453125e-6f, 7.62939453125e-6f);
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < S::Pair; ++q) {
     if (q == 1 && both == 1) break;
     Two e[kC / 2];
     exponents(q, e);
