@@ -48,10 +48,11 @@ extern "C" {
  *                range, or whose packed rows pass `rows`: nothing of it is changed.
  *   out_first    [B + 1] int32: the requests' first rows, and the number of rows used.
  *   out_state    [2] int32: the ring's state after the call.
- * out_len and out_state must not overlap old_len, seq_len, num_new or ring_state, else
+ * No output, nor page_table or ring, may overlap another of these or an input, else
  * SV_ERR_INVALID_ARG. A ring whose state is out of range, or that has no room for its pages and
- * those given back (a ring of as many places as there are pages always has), is a data error of the call: out_len and rows are all -1, out_state is {-1, -1}, and
- * nothing is changed. No workspace. Called again with the same inputs, a call does the same again.
+ * those given back (a ring of as many places as there are pages always has), is a data error of the
+ * call: out_len and rows are all -1, out_state is {-1, -1}, and nothing is changed. No workspace.
+ * Called again with the same inputs, a call does the same again.
  * ---------------------------------------------------------------------------------------- */
 sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* page_table, int max_pages,
                       const int32_t* old_len, const int32_t* seq_len, const int32_t* num_new,
@@ -61,7 +62,8 @@ sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* page_table, 
 
 /* Queries or keys of qk_norm_rotate: element d of head h of row (r, i) is at
  * data[r * req + i * row + h * head + d] (strides in elements, multiples of 8; data 16-byte
- * aligned). `out` likewise; it may be `data` with the same strides. HOST memory. */
+ * aligned). `out` likewise; it may be `data` with the same strides, and has no other element of the
+ * call's inputs or outputs in it. HOST memory. */
 typedef struct {
   const void* data;
   int64_t req, row, head;

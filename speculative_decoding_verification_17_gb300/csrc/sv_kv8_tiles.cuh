@@ -9,21 +9,39 @@
 // is ever widened: 32 KiB per 128 keys of D = 128 instead of 64.
 //
 // Rounding. Both operands of the instruction are 8 bits wide, so queries and weights are given to it
-// as sums of e4m3 numbers.
+// as sums of such numbers.
 // - A query row is scaled by a power of two to a largest magnitude in [128, 256) and split into two
-//   numbers (bf16) or three (fp16): its 8 or 11 bits exactly, or for an element below 2^-9 (bf16) or
-//   2^-6 (fp16) of the row's largest, to 2^-17 of that at worst.
-// - A weight, in units in which the largest possible is below 1, becomes an fp16 number y and what
-//   that leaves. y is three e4m3 numbers exactly, each 16 times finer than the one before (cut, not
-//   rounded: 4 + 4 + 3 bits), the rest a fourth: a weight is off by 2^-16 of it, or by 2^-30 of the
-//   largest possible (2^-27 of the largest there is, as the maximum below moves).
-// The four products are one instruction of four times the columns and are added, each by its unit,
-// at the end of a piece. The instruction adds up in fp32, cut: measured 2^-20.7 of sum |a b| over 128
-// products, and sums that fp32 holds exactly come out exact.
+//   e4m3 numbers (bf16) or three (fp16): its 8 or 11 bits exactly, or for an element below 2^-9 (bf16)
+//   or 2^-6 (fp16) of the row's largest, to 2^-17 of that at worst.
+// - A weight is rounded to fp16, to nearest: by 2^-11 of it at worst, as the output of fp16 itself and
+//   an eighth of bf16's. The upper byte of an fp16 number is an e5m2 number (cut, not rounded), what
+//   that leaves has three bits less, and four such cuts take all 11. Below 2^-16, the last step of
+//   e5m2, nothing is left to cut: half of that is added to the weight first, so that the last cut
+//   rounds, by 2^-17. The largest weight of a row is 2^Lift or more, so that is 2^-27 of it for bf16
+//   and 2^-28 for fp16.
+// The four products are one instruction of four times the columns and are added at the end of a piece.
+// The instruction adds up in fp32, cut: measured 2^-20.7 of sum |a b| over 128 products, and sums that
+// fp32 holds exactly come out exact.
+// Weights as four e4m3 numbers, each 16 times finer than the one before, keep 2^-16 of a weight; the
+// conversions took 9 % (one token of 64 requests 97 -> 94 us, five drafts 207 -> 196).
 //
-// Running maximum. Of s_j + log2 vs_j, as that is what bounds a weight: m is the maximum less 5 when
-// it moves, which it does when a weight passes 2^7.98 (8 times the largest so far). log2 vs_j counts
-// as -40 .. 40; a scale above 2^40, negative or not a number makes what sees the key NaN.
+// Running maximum. Of s_j + log2 vs_j, as that is what bounds a weight: m is the maximum less Lift when
+// it moves, which it does when a weight passes 2^15.875 (fp16 ends at 2^16). log2 vs_j counts as
+// -40 .. 40; a scale above 2^40, negative or not a number makes what sees the key NaN.
+//
+// Bound: reading the codes once, until the softmax takes longer. A tile of D = 128 is 1400 clocks of
+// one SM's share of the bandwidth; its softmax at 48 columns is a chain of about 2000 (loads from
+// tensor memory, two exponents, cuts, stores to shared memory, the hand-over), of which 12 warps hide
+// half, and four instructions of 128 x 4N x 32 take 400 up to 128 columns, 520 at 256. Measured, in
+// graph replays (the bytes read and written once at 6801 GB/s first):
+//   1 token of 64 requests, 200 .. 8192 keys, 32 / 8 heads   41.8 us   53.5 us   78 %
+//   6 positions of 32, 500 .. 16384 keys, 64 / 8 heads       42.4 us   87.6 us   48 %
+//   9 positions of 2, 100001 .. 131072 keys, 32 / 8 heads    77.4 us  119.0 us   65 %
+//   5 positions of 16, window 4096, 16 / 8 heads of 256      15.8 us   36.2 us   44 %
+//   1 token of 1 request of 777 keys                          0.2 us   10.4 us  (latency)
+// and by query rows per kv head (64 requests of 200 .. 8192 keys, 8 kv heads, D = 128, floor 42 to 44
+// us; over 16 bits in brackets): 4 57 (98), 12 62 (100), 24 83 (103), 32 84 (104), 48 102 (116), 64 131
+// (116), 72 169 (203). Above 48 rows the softmax bounds and half the bytes gain nothing.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -38,12 +56,13 @@ template <int kD, int kN, bool kBf16>
 struct TileShape8 {
   static constexpr int D = kD, N = kN;
   static constexpr bool Bf16 = kBf16, Weigh = false, Quant = true;  // (the queries' and outputs' type)
-  static constexpr float Lift = kBf16 ? 10.0f : 11.0f, Top = 15.875f;  // log2 of the largest weight when the maximum moves, and at most
+  // log2 of the largest weight when the maximum moves, and at most
+  static constexpr float Lift = kBf16 ? 10.0f : 11.0f, Top = 15.875f;
   static constexpr int UnitCols = D < 128 ? D : 128, RowBytes = UnitCols, UnitBytes = kTileKeys * RowBytes;
   static constexpr int U = D / UnitCols;
-  // Softmax threads take a key and 16 columns (8 where there are no more) of two tiles at a time: a
-  // group of four warps for each 16. Two CTAs share an SM up to 16 columns, so that one's chain of
-  // dependent steps passes under the other's.
+  // Softmax threads take a key and 16 columns (8 where there are no more): a group of four warps for
+  // each 16. Two CTAs share an SM up to 16 columns, so that one's chain of dependent steps passes under
+  // the other's (at 32 columns their 88 registers are too few: 24 rows 108 us, 82 with one).
   static constexpr int Teams = 1, Groups = N == 8 ? 1 : N / 16, SoftWarps = 4 * Groups;
   static constexpr int CtasPerSm = N <= 16 ? 2 : 1;
   static constexpr int SoftThreads = 32 * SoftWarps;
@@ -113,7 +132,8 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
 }
 // The instruction descriptor: fp32 accumulator, A of e4m3, B of e4m3 or e5m2.
 __device__ __forceinline__ uint32_t mma_desc8(bool mn, bool b_e5m2, int M, int N) {
-  return 1u << 4 | (b_e5m2 ? 1u << 10 : 0u) | (mn ? 3u << 15 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
+  return 1u << 4 | (b_e5m2 ? 1u << 10 : 0u) | (mn ? 3u << 15 : 0u) | (uint32_t)(N >> 3) << 17 |
+         (uint32_t)(M >> 4) << 24;
 }
 constexpr uint32_t kSwizzle64 = 4;
 // Operand rows of RowBytes bytes: their swizzle, and the bytes of eight of them.
@@ -452,8 +472,7 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// One arrival per warp: those of single threads queue up (384 of them on two barriers per tile were a
-// third of the time of the long caches).
+// One arrival per warp (of each thread made no difference that could be measured).
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   tc_fence_before();
   __syncwarp();
@@ -506,7 +525,7 @@ __device__ __forceinline__ void raise8(Attend<S>& me, typename TileShared<S>::Ta
   tmem_wait_st();
 }
 
-// One pass: the piece's tiles from the i-th on, the y-th turn of the score buffer. Returns how many.
+// One pass: one or two of the piece's tiles from the i-th on, the y-th turn of the score buffer. Returns how many.
 template <class S>
 __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>::Table& T,
                                            const Piece& p, const WholeTiles& whole, int i, int y,
@@ -621,7 +640,7 @@ __device__ __forceinline__ int quant_tiles(Attend<S>& me, typename TileShared<S>
   }
   // the product that last read the weights' buffer
   if (y > 0) me.wait_values(y - 1);
-  // (what is below the last part's step of 2^-16 is rounded)
+  // (half the last cut's step, 2^-17, so that it rounds)
   const Two half = two(7.62939453125e-6f, 7.62939453125e-6f);
 #pragma unroll
   for (int q = 0; q < S::Pair; ++q) {

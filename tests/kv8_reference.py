@@ -107,9 +107,11 @@ def attention8(cache, q, num_draft, *, scale, softcap=0.0, window=0, slopes=None
             # sums' and the rounding to fp16 (2^-11 of it at worst); the accumulator cuts each of its additions
             w = 2 * worst + 2.0 ** -21 + (n + 8) * 2.0 ** -23 + 2.0 ** -11 + (n / 32 + 8) * 2.0 ** -22
             t = w[..., None] * size + half * o.abs() + (2.0 ** -24 if q.dtype == torch.float16 else 1e-30)
-            if n:  # and by 2^-28 of the largest weight times its scale
+            if n:
+                # and by 2^-17, half the last step of what weights are cut into, in units in which the
+                # largest weight times its scale is 2^10 (bf16) or 2^11 (fp16) or more: 2^-27, 2^-28
                 big = (p * (v.abs().amax(-1) / 32).nan_to_num(0.0)).amax(-1)  # (a row of codes reaches 32)
-                t = t + 2.0 ** -28 * big[..., None] * 448 * n
+                t = t + (2.0 ** -28 if q.dtype == torch.float16 else 2.0 ** -27) * big[..., None] * 448 * n
             out[b, :rows, at], tol[b, :rows, at] = o, t
             lse[b, :rows, at] = l
             tol_lse[b, :rows, at] = worst + (n + 8) * 2.0 ** -23 + 2.0 ** -21 * (1 + l.abs().nan_to_num(0, 0, 0))

@@ -127,6 +127,18 @@ def test_page_map_refusals(kw, status):
     assert page_map(**kw) == status
 
 
+@pytest.mark.parametrize("kw", [
+    # table: 160 bytes, ring: 400, slots: 96, positions: 48, lengths: 16
+    dict(table=0x30000 - 156), dict(ring=0x10000 + 156), dict(table=0x20000), dict(ring=0x21000 - 396),
+    dict(slots=0x10000 - 88), dict(slots=0x30000 + 392), dict(slots=0x21008), dict(pos=0x22000 + 12),
+    dict(pos=0x10000 - 44), dict(pos=0x50000 + 92), dict(pos=0x40004), dict(out=0x50000 + 92),
+    dict(out=0x51000 - 12), dict(first=0x52000 - 16), dict(next=0x53000 + 16), dict(next=0x54000, first=0x54000 - 16),
+    dict(next=0x30000 + 396), dict(P=0, rows=3, pos=0x50000 + 20),
+])
+def test_page_map_arrays_that_share_bytes_are_refused(kw):
+    assert page_map(**kw) == INVALID
+
+
 def head_rows(data=FAKE, heads=4, req=1024, row=512, head=128, out=0x90000, oq=1024, orow=512, oh=128, w=None):
     return ctypes.byref(_native.HeadRows(data, req, row, head, out, oq, orow, oh, heads, w))
 
