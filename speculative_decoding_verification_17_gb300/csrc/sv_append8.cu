@@ -11,7 +11,9 @@
 // run's rows once for the largest magnitude and codes them from registers, or again from L2 where
 // there are more than sixteen loads of them. No two warps share a block.
 //
-// Bound: 3 bytes an element (2 read, 1 written).
+// Bound: 3 bytes an element (2 read, 1 written). Measured, in graph replays (bytes at 6801 GB/s first):
+// one token of 64 requests 0.06 us, 3.9 us; prompts of 64 requests, 48600 rows of 8 heads of 128 44.0 us,
+// 54.5 us, 81 % of a copy's bandwidth.
 #include <cstdint>
 
 #include <cuda_fp8.h>
@@ -23,7 +25,11 @@
 namespace sv {
 namespace {
 
-constexpr int kAppThreads = 256, kAppWarps = kAppThreads / 32;
+// Small CTAs, as many as registers for a run's loads leave room for: 640 threads of an SM hold 160 KB on
+// its way (prompts of 48600 rows of 8 heads of 128, in graph replays: 5 CTAs of 128 threads 54.5 us, 4 of
+// them 56.8, 2 of 256 60.7, 10 of 64 58.4; 6 of 128, whose loads spill, 61.2; half the loads kept and the
+// rest read again 70).
+constexpr int kAppThreads = 128, kAppCtas = 5, kAppWarps = kAppThreads / 32;
 
 struct AppendArgs {
   const uint16_t* x[2];  // keys, values
@@ -56,44 +62,46 @@ __device__ __forceinline__ uint2 code8(const uint4& v, float scale, uint32_t lim
   return make_uint2(__byte_perm(b[0], b[1], 0x5410), __byte_perm(b[2], b[3], 0x5410));
 }
 
-// The rows of a chunk of 32 and of those after it that its last run may reach: a bit each for rows
-// that go on with the block of the row ahead of them, and for those of them whose slot is higher.
+// The rows of a chunk of 32 and of those after it that its last run may reach (a run from the chunk's
+// last row on has at most 128, and one too many, so 31 + 1 + 128 rows): a bit each for rows that go on
+// with the block of the row ahead of them, and for those of them whose slot is higher.
 struct Rows {
-  static constexpr int kWindows = 5;  // of 32 rows: a run has at most 128, and one too many
+  static constexpr int kWindows = 1 + kMaxBlock / 32;
   uint32_t same[kWindows], higher[kWindows];
 };
 
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kAppThreads, 2) append_kernel(const __grid_constant__ AppendArgs A) {
+__global__ void __launch_bounds__(kAppThreads, kAppCtas) append_kernel(const __grid_constant__ AppendArgs A) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows at a time
   constexpr int kKeep = 16;                          // loads of a run kept in registers
   // the largest finite magnitude that a scale reaches (448 * 2^40 in bf16)
   constexpr uint32_t kLimit = kBf16 ? 0x57e0u : 0x7bffu;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int block = 1 << A.log_block, windows = 2 + (block >> 5);
+  const int block = 1 << A.log_block, windows = 1 + (block + 31) / 32;  // (of 32 rows)
   const int t0 = blockIdx.x * 32;
   // a row's slot, -1 for a row that is left out
   auto slot_of = [&](int t) {
     const int64_t s = t >= 0 && t < A.rows ? __ldg(A.slots + t) : -1;
     return s < A.num_slots ? s : -1;
   };
-  Rows R;
-  uint32_t starts = 0;
-  int64_t slot = -1;  // of the lane's row of the chunk
-#pragma unroll
-  for (int w = 0; w < Rows::kWindows; ++w) {
-    R.same[w] = R.higher[w] = 0;
-    if (w < windows) {
-      const int64_t s = slot_of(t0 + 32 * w + lane), p = slot_of(t0 + 32 * w + lane - 1);
-      const bool same = s >= 0 && p >= 0 && s >> A.log_block == p >> A.log_block;
-      R.same[w] = __ballot_sync(0xffffffffu, same);
-      R.higher[w] = __ballot_sync(0xffffffffu, same && s > p);
-      if (w == 0) {
-        slot = s;
-        starts = __ballot_sync(0xffffffffu, s >= 0 && !same);
-      }
+  __shared__ Rows R;
+  __shared__ int64_t slots[32];
+  __shared__ uint32_t first_rows;
+  for (int w = warp; w < windows; w += kAppWarps) {
+    const int64_t s = slot_of(t0 + 32 * w + lane), p = slot_of(t0 + 32 * w + lane - 1);
+    const bool same = s >= 0 && p >= 0 && s >> A.log_block == p >> A.log_block;
+    const uint32_t same_mask = __ballot_sync(0xffffffffu, same);
+    const uint32_t higher = __ballot_sync(0xffffffffu, same && s > p);
+    const uint32_t starting = __ballot_sync(0xffffffffu, s >= 0 && !same);
+    if (w == 0) slots[lane] = s;
+    if (lane == 0) {
+      R.same[w] = same_mask;
+      R.higher[w] = higher;
+      if (w == 0) first_rows = starting;
     }
   }
+  __syncthreads();
+  uint32_t starts = first_rows;
   const int units = __popc(starts) * A.Hkv * 2;
   int at_run = 0;  // the run that is the lowest bit of `starts`
 #pragma unroll 1
@@ -101,24 +109,22 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(const __grid_con
     const int run = u / (2 * A.Hkv), h = (u - run * 2 * A.Hkv) >> 1, which = u & 1;
     for (; at_run < run; ++at_run) starts &= starts - 1;
     const int cur = __ffs(starts) - 1;
-    const int64_t first = __shfl_sync(0xffffffffu, slot, cur);
+    const int64_t first = slots[cur];
     const uint16_t* x =
         A.x[which] + (int64_t)(t0 + cur) * A.row[which] + h * A.head[which] + lane % kLanes * 8;
     const int mine = lane / kLanes;  // the lane's row of a load
     // the run's rows, and whether their slots ascend
     int n = 1;
     bool ordered = true, open = true;
-#pragma unroll
-    for (int w = 0; w < Rows::kWindows; ++w) {
-      if (w < windows && open) {
-        const int from = w == 0 ? cur + 1 : 0;
-        const uint32_t rest = from < 32 ? R.same[w] >> from : 0u;
-        const int more = ~rest ? __ffs(~rest) - 1 : 32;  // rows that go on
-        const uint32_t mask = more == 32 ? 0xffffffffu : (1u << more) - 1;
-        ordered = ordered && !(mask & ~(from < 32 ? R.higher[w] >> from : 0u));
-        open = from + more == 32;
-        n += more;
-      }
+#pragma unroll 1
+    for (int w = 0; w < windows && open; ++w) {
+      const int from = w == 0 ? cur + 1 : 0;
+      const uint32_t rest = from < 32 ? R.same[w] >> from : 0u;
+      const int more = ~rest ? __ffs(~rest) - 1 : 32;  // rows that go on
+      const uint32_t mask = more == 32 ? 0xffffffffu : (1u << more) - 1;
+      ordered = ordered && !(mask & ~(from < 32 ? R.higher[w] >> from : 0u));
+      open = from + more == 32;
+      n += more;
     }
     ordered = ordered && n <= block;
     const int64_t page = first >> A.log_page;
@@ -236,8 +242,9 @@ __global__ void __launch_bounds__(kAppThreads, 2) append_kernel(const __grid_con
 template <int D, bool kBf16>
 sv_status launch_append(const AppendArgs& A, cudaStream_t st) {
   const int64_t chunks = (A.rows + 31) / 32;
-  // enough CTAs for the SMs; a chunk has at most 32 runs of 2 Hkv units, 8 warps to a CTA
-  int64_t split = (16 * (int64_t)device_sm_count() + chunks - 1) / chunks;
+  // enough CTAs for the SMs and a warp for each unit of one run, up to one for each unit of 32 runs (more
+  // CTAs than a chunk's units only look at its slots again)
+  int64_t split = (32 * (int64_t)device_sm_count() + chunks - 1) / chunks;
   const int64_t most = (64 * (int64_t)A.Hkv + kAppWarps - 1) / kAppWarps;
   const int64_t least = (2 * (int64_t)A.Hkv + kAppWarps - 1) / kAppWarps;
   split = split > most ? most : split < least ? least : split;

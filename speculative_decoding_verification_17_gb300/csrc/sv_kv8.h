@@ -6,6 +6,8 @@
 
 namespace sv {
 
+constexpr int kMaxBlock = 128;  // slots that share a scale
+
 inline sv_status check_pool8(const sv_kv_pool* p) {
   if (!p || !p->data || !aligned_to(p->data, 16)) return SV_ERR_INVALID_ARG;
   for (int64_t st : {p->page_stride, p->token_stride, p->head_stride})
@@ -16,7 +18,7 @@ inline sv_status check_pool8(const sv_kv_pool* p) {
 // Slots that share a scale: a power of two that divides a page, and a tile of 128 keys.
 inline sv_status check_block(const sv_kv_shape* s, int block) {
   if (block < 1 || (block & (block - 1)) != 0 || block > s->page_size) return SV_ERR_INVALID_ARG;
-  return block > 128 ? SV_ERR_UNSUPPORTED : SV_OK;
+  return block > kMaxBlock ? SV_ERR_UNSUPPORTED : SV_OK;
 }
 
 }  // namespace sv
