@@ -9,7 +9,8 @@
 // Bound: latency for a step (three dependent loads and two scans); for packed prompts the 12 bytes of
 // a row, written. There a thread takes eight rows, whose pages are looked up at once and which mostly
 // share a search. Measured, in graph replays (bytes at 6801 GB/s first): a step of 512 requests of 9
-// rows 0.02 us, 4.4 us; 1024 prompts of 16 .. 16384 tokens packed in 2.4 million rows 4.4 us, 16.4 us.
+// rows 0.02 us, 4.4 us; 1024 prompts of 16 .. 16384 tokens packed in 2.4 million rows 4.4 us, 15.5 us
+// (16.5 with a search wherever a request ends).
 #include <cstdint>
 
 #include "specverify_step.h"
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(kMapThreads, kRowsPer == 1 ? 2 : 3) map_kernel
           b = row / A.P;
         } else {
           if (row >= first[A.B]) continue;
-          b = find(first, A.B, row);
+          // (past a request's last row it is mostly the next one's)
+          b = b >= 0 && row < first[min(b + 2, A.B)] ? b + 1 : find(first, A.B, row);
         }
         start = first[b];
         end = first[b + 1];
