@@ -40,7 +40,7 @@
 //   5 positions of 16, window 4096, 16 / 8 heads of 256      15.8 us   34.6 us   46 %
 //   1 token of 1 request of 777 keys                          0.2 us   10.4 us  (latency)
 // and by query rows per kv head (64 requests of 200 .. 8192 keys, 8 kv heads, D = 128, floor 42 to 44
-// us; over 16 bits in brackets): 4 57 (98), 12 61 (100), 24 83 (103), 32 84 (104), 48 102 (116), 64 131
+// us; over 16 bits in brackets): 4 57 (98), 12 61 (100), 24 83 (103), 32 84 (104), 48 102 (116), 64 125
 // (116), 72 169 (203). Above 48 rows the softmax bounds and half the bytes gain nothing.
 #pragma once
 
@@ -98,13 +98,16 @@ struct TileShape8 {
   static constexpr int Outs = 1;  // (a piece's output leaves while the next one's first scores are made)
   static constexpr int TmemNeed = OBase + Outs * MBlocks * ON;
   static constexpr int TmemCols = TmemNeed <= 128 ? 128 : TmemNeed <= 256 ? 256 : 512;
-  // the cost of a tile and of a piece's start and end, which only other CTAs of the SM can cover
-  // (five drafts, 48 columns: 129 us with 5, 108 with 13, 97 with 24, 88 with 26, 91 with 40; 64 requests
-  // of 4 rows: 60 with 3, 58 with 8, 57.4 with 12, 57.9 with 16, 59.5 with 24; of 12 rows: 67 with 8,
-  // 62.5 with 12, 60.9 with 16, 63.4 with 24, and as much at D = 64; D = 256 in a window: 40 with 3, 36.2
-  // with 6, 34.6 with 9, 34.9 with 16, 35.5 with 24)
+  // The cost of a tile and of a piece's start and end, which only other CTAs of the SM can cover; with
+  // two tiles a pass a tile counts for less, so a piece for more. Measured, us, the figure that was taken
+  // third:  5 drafts, 48 columns      108 with 13    97 with 24    88 with 26   91 with 40
+  //         20 rows, D = 256          83 with 6      69 with 14    62 with 20   67 with 32
+  //         64 rows, 64 columns       159 with 6     137 with 10   125 with 16  132 with 26
+  //         12 rows, 16 columns       67 with 8      62 with 12    61 with 16   63 with 24
+  //         4 rows, 8 columns         60 with 3      58 with 8     57 with 12   59 with 24
+  //         window, D = 256           40 with 3      36 with 6     35 with 9    36 with 24
   static constexpr int TileCost = 4;
-  static constexpr int PieceCost = CtasPerSm == 1 ? 26 : D == 256 ? 9 : N == 8 ? 12 : 16;
+  static constexpr int PieceCost = Pair == 2 ? (D == 256 ? 20 : 26) : D == 256 ? 9 : N == 8 ? 12 : 16;
   static_assert(CtasPerSm * TmemCols <= 512 && NV >= U && NK >= U &&
                 CtasPerSm * (Smem + kTables) <= kSmemMax, "tile shape");
 };
