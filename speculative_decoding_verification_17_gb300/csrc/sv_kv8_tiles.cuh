@@ -221,7 +221,7 @@ __device__ __forceinline__ void copy_role8(const TileArgs& A, TileShared<S>& sh,
       g.head = p.h;
       g.slot = (tile_at<S>(p, i) * kTileKeys + lane * A.box) & ((1 << A.log_page) - 1);
       if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
-        *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
+        *(volatile int*)&sh.bad_piece[turn & (kMarks - 1)] = turn + 1;
       g.bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * (uint32_t)S::RowBytes;
       if (__builtin_expect(++i == p.mb - p.ma, 0)) {
         more = take(p);

@@ -433,6 +433,13 @@ __device__ __forceinline__ void find_start(const TileArgs& A, Start* s, int64_t*
 // ahead of X. (Any number of pieces without tiles may follow X: in the queue they would fill it while
 // the other roles wait for X's last tile.)
 constexpr int kPieceQueue = 8;
+// Marks of pieces with a bad page, by ordinal. A mark is read at the end of its piece X, when the roles
+// have given back no place past that of X + 1; so the copying warp has taken no piece past
+// X + 1 + kPieceQueue, and marked none: the marks from X to there need a place each. (With as many places
+// as the queue has, over 8 bits, whose copies wait for no query buffer, the marks of eight requests of one
+// tile each were lost to those of the next eight.)
+constexpr int kMarks = 2 * kPieceQueue;
+static_assert(kMarks >= kPieceQueue + 2 && (kMarks & (kMarks - 1)) == 0, "a place per mark");
 
 // ---- shared memory ------------------------------------------------------------------------------
 // Of an attention over 8 bits: the columns' powers of two, by table.
@@ -454,7 +461,7 @@ struct TileShared : QueryScales<S::Quant, S::N> {
   uint32_t tmem;
   Waits waits;
   int hollow;  // the range holds pieces without tiles for the tensor cores
-  int bad_piece[8];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % 8
+  int bad_piece[kMarks];  // 1 + the ordinal of a piece with a page outside the pool, by ordinal % kMarks
   uint64_t drain[2];
   // the pieces, from the warp that walks the work list to the other roles
   Piece piece[kPieceQueue];
@@ -620,7 +627,7 @@ __device__ __forceinline__ void copy_role(const TileArgs& A, TileShared<S>& sh,
     const bool mine = seen && page >= 0 && page < A.num_pages;
     if (!kValues) {
       if (__builtin_expect(__any_sync(0xffffffffu, seen && !mine), 0) && lane == 0)
-        *(volatile int*)&sh.bad_piece[turn & 7] = turn + 1;
+        *(volatile int*)&sh.bad_piece[turn & (kMarks - 1)] = turn + 1;
     }
     const uint32_t bytes =
         (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * A.box) * 128u;
@@ -1237,7 +1244,7 @@ struct Attend {
   __device__ __forceinline__ void finish(Table& T) {
     const Piece& p = T.piece;
     group_sync();
-    const bool poison = *(volatile int*)&sh.bad_piece[p.turn & 7] == p.turn + 1;
+    const bool poison = *(volatile int*)&sh.bad_piece[p.turn & (kMarks - 1)] == p.turn + 1;
     const bool starts = p.flags & kStarts, whole = starts && (p.flags & kEnds);
     const int rows = p.live * A.G;
     const int64_t row0 = first_row(p);
@@ -1607,7 +1614,7 @@ __global__ void __launch_bounds__(S::Threads, S::CtasPerSm)
     sh.waits.dead = sh.hollow = 0;
     sh.waits.limit_ns = A.wait_ns;
     sh.join.rows = 0;
-    for (int i = 0; i < 8; ++i) sh.bad_piece[i] = 0;
+    for (int i = 0; i < kMarks; ++i) sh.bad_piece[i] = 0;
     fence_barrier_init();
   }
   if (tid == 32) {
