@@ -33,7 +33,10 @@ extern "C" {
  * or -1 where that page is outside [0, num_pages).
  *
  * Arguments
- *   B            requests, 0 <= B <= 8192 (0 is a no-op), else SV_ERR_UNSUPPORTED.
+ *   B            requests, 0 <= B <= 8192, else SV_ERR_UNSUPPORTED. Of none, out_state is
+ *                ring_state (or {-1, -1}, as below), out_first[0] 0 and all rows -1, so that a step
+ *                without requests keeps the ring; their arrays may then be NULL. (Where out_state is
+ *                no memory of a CUDA device the call is a no-op.)
  *   page_size    a power of two from 8 to 1024. num_pages >= 0.
  *   page_table   [B, max_pages] int32, updated in place; max_pages * page_size < 2^30.
  *   old_len, seq_len   [B] int32 in [0, max_pages * page_size].

@@ -1019,7 +1019,7 @@ def kv_page_map(page_table, old_len, seq_len, num_new, ring, ring_state, page_si
     there are) or gives pages back to its end. Rows are [B, P], or packed in ``rows`` rows.
     Returns (slots [B, P] or [rows] int64, positions int32 likewise, both -1 in rows of no new
     token; out_len [B] int32: seq_len, old_len where no pages were left, -1 for a data error;
-    first rows [B + 1] int32; the ring's new state [2] int32)."""
+    first rows [B + 1] int32; the ring's new state [2] int32, also of a batch without requests)."""
     if out_slots is None:
         if (P is None) == (rows is None):
             raise ValueError("give P (rows per request) or rows (packed)")

@@ -256,6 +256,14 @@ __global__ void __launch_bounds__(kMapThreads, kRowsPer == 1 ? 2 : 3) map_kernel
   }
 }
 
+// Whether p is memory that CUDA knows. (Asked of an empty batch alone, whose caller may have no arrays.)
+bool on_device(const void* p) {
+  cudaPointerAttributes a{};
+  const bool known = p && cudaPointerGetAttributes(&a, p) == cudaSuccess;
+  if (!known) cudaGetLastError();
+  return known && a.type != cudaMemoryTypeUnregistered;
+}
+
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const char *p = static_cast<const char*>(a), *q = static_cast<const char*>(b);
   return na > 0 && nb > 0 && p < q + nb && q < p + na;
@@ -278,8 +286,9 @@ extern "C" sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* p
       (int64_t)max_pages * page_size >= (1ll << 30) || B > kMaxRequests)
     return SV_ERR_UNSUPPORTED;
   if (P > 0 && (int64_t)B * P != rows) return SV_ERR_INVALID_ARG;
-  if (B == 0) return SV_OK;
-  if (!page_table || !old_len || !seq_len || !num_new || !ring || !ring_state || !out_len ||
+  // an empty batch has a ring's state to hand on and rows to mark all the same
+  if (B == 0 && !on_device(out_state)) return SV_OK;
+  if ((B > 0 && (!page_table || !old_len || !seq_len || !num_new || !ring || !out_len)) || !ring_state ||
       !out_first || !out_state || (rows > 0 && (!out_slots || !out_positions)) ||
       !aligned_to(out_slots, 8))
     return SV_ERR_INVALID_ARG;
@@ -312,7 +321,7 @@ extern "C" sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* p
   }
   int64_t ctas = (rows / per + 2ll * B + kMapThreads - 1) / kMapThreads;
   const int64_t most = 2 * sms;
-  if (ctas > most) ctas = most;
+  ctas = ctas > most ? most : ctas < 1 ? 1 : ctas;
   kernel<<<(unsigned)ctas, kMapThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(A);
   return launch_status();
 }
