@@ -51,7 +51,9 @@ extern "C" {
  *              they do not stand side by side (a page shared by two requests that both append to
  *              it), what the block holds is one of the ways of writing them at once; nothing
  *              outside the block is touched.
- *   k_pool, v_pool, k_scale, v_scale, block   as above; written in place.
+ *   k_pool, v_pool, k_scale, v_scale, block   as above; written in place. The two pools share no
+ *              element and the two scales none; what starts at the same address, scales that share
+ *              bytes and strides below D (of a dimension of two or more) are SV_ERR_INVALID_ARG.
  * A row's element that is infinite, NaN or above 448 * 2^40 becomes the NaN code and does not count
  * for the scale. A block whose earlier slots have a scale that is negative, above 2^40 or NaN keeps
  * NaN. No workspace.

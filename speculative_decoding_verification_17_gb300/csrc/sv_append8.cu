@@ -284,6 +284,12 @@ extern "C" sv_status kv_cache_append_q8(const sv_kv_shape* shape, int rows, cons
     return SV_ERR_INVALID_ARG;
   for (int64_t st : {k_row, k_head, v_row, v_head})
     if (st < 0 || st % 8 != 0 || st >= (1ll << 39)) return SV_ERR_INVALID_ARG;
+  // no two warps may write one block's codes or scale
+  if (k_pool->data == v_pool->data || !heads_apart(shape, k_pool) || !heads_apart(shape, v_pool))
+    return SV_ERR_INVALID_ARG;
+  const uint64_t scales = (uint64_t)shape->num_pages * (shape->page_size / block) * shape->Hkv * sizeof(float);
+  const uintptr_t ka = reinterpret_cast<uintptr_t>(k_scale), va = reinterpret_cast<uintptr_t>(v_scale);
+  if ((ka < va ? va - ka : ka - va) < scales) return SV_ERR_INVALID_ARG;
   const AppendArgs A{{static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v)},
                      {k_row, v_row},
                      {k_head, v_head},

@@ -15,6 +15,12 @@ inline sv_status check_pool8(const sv_kv_pool* p) {
   return SV_OK;
 }
 
+// Whether heads of a pool that is written lie apart, as far as each stride by itself tells.
+inline bool heads_apart(const sv_kv_shape* s, const sv_kv_pool* p) {
+  return (s->num_pages < 2 || p->page_stride >= s->D) && p->token_stride >= s->D &&
+         (s->Hkv < 2 || p->head_stride >= s->D);
+}
+
 // Slots that share a scale: a power of two that divides a page, and a tile of 128 keys.
 inline sv_status check_block(const sv_kv_shape* s, int block) {
   if (block < 1 || (block & (block - 1)) != 0 || block > s->page_size) return SV_ERR_INVALID_ARG;
