@@ -66,7 +66,9 @@ sv_status kv_page_map(int B, int page_size, int num_pages, int32_t* page_table, 
 /* Queries or keys of qk_norm_rotate: element d of head h of row (r, i) is at
  * data[r * req + i * row + h * head + d] (strides in elements, multiples of 8; data 16-byte
  * aligned). `out` likewise; it may be `data` with the same strides, and has no other element of the
- * call's inputs or outputs in it. HOST memory. */
+ * call's inputs or outputs in it: data at other strides, an out that starts where the other rows' out
+ * or data does, and out strides below D (of a dimension of two or more) are SV_ERR_INVALID_ARG.
+ * HOST memory. */
 typedef struct {
   const void* data;
   int64_t req, row, head;

@@ -263,13 +263,21 @@ extern "C" sv_status qk_norm_rotate(sv_kv_dtype dtype, int B, int P, int D, int 
       return SV_ERR_INVALID_ARG;
     for (int64_t s : {x->req, x->row, x->head, x->out_req, x->out_row, x->out_head})
       if (x->heads > 0 && (s < 0 || s % 8 != 0 || s >= (1ll << 39))) return SV_ERR_INVALID_ARG;
-    // rows of the output lie apart
-    if (x->heads > 0 && ((B > 1 && x->out_req == 0) || (P > 1 && x->out_row == 0) ||
-                         (x->heads > 1 && x->out_head == 0)))
+    // heads of the output lie apart, as far as each stride by itself tells
+    if (x->heads > 0 && ((B > 1 && x->out_req < D) || (P > 1 && x->out_row < D) ||
+                         (x->heads > 1 && x->out_head < D)))
+      return SV_ERR_INVALID_ARG;
+    // in place, each head goes where it came from
+    if (x->heads > 0 && x->out == x->data &&
+        ((B > 1 && x->out_req != x->req) || (P > 1 && x->out_row != x->row) ||
+         (x->heads > 1 && x->out_head != x->head)))
       return SV_ERR_INVALID_ARG;
     A.x[i++] = {static_cast<const uint16_t*>(x->data), static_cast<uint16_t*>(x->out), x->req, x->row,
                 x->head, x->out_req, x->out_row, x->out_head, x->heads, x->weight};
   }
+  // no output starts where the other's rows do
+  if (q->heads > 0 && k->heads > 0 && (q->out == k->out || q->out == k->data || k->out == q->data))
+    return SV_ERR_INVALID_ARG;
   if (!positions || !aligned_to(positions, 4) ||
       (R > 0 && (!inv_freq || !aligned_to(inv_freq, freq_f64 ? 8 : 4))))
     return SV_ERR_INVALID_ARG;

@@ -31,3 +31,29 @@ def append(pages=40, Hkv=2, **kw):
 ])
 def test_pools_and_scales_that_share_memory_are_refused(kw):
     assert append(**kw) == INVALID
+
+
+def rows(data, out, heads=4, req=1024, row=512, head=128, oq=1024, orow=512, oh=128):
+    return ctypes.byref(_native.HeadRows(data, req, row, head, out, oq, orow, oh, heads, None))
+
+
+Q, K = (0x100000, 0x200000), (0x300000, 0x400000)  # data, out
+
+
+def rotate(q, k, B=3, P=2):
+    return sv.library().qk_norm_rotate(1, B, P, 128, 128, q, k, 1, 0x500000, 0x600000, 0, 1, 1e-6, 0, None)
+
+
+@pytest.mark.parametrize("q,k", [
+    (rows(Q[0], Q[1]), rows(K[0], Q[1], heads=1)),  # one place for both results
+    (rows(Q[0], K[0]), rows(K[0], K[1], heads=1)),  # the keys under the queries' result
+    (rows(Q[0], Q[1]), rows(K[0], Q[0], heads=1)),
+    (rows(Q[0], Q[0], oq=2048), rows(*K)),          # in place, but elsewhere
+    (rows(Q[0], Q[0], orow=256, oq=4096), rows(*K)),
+    (rows(*Q), rows(K[0], K[0], head=256, row=1024, req=2048)),
+    (rows(Q[0], Q[1], oh=64), rows(*K)),            # heads that overlap
+    (rows(*Q), rows(K[0], K[1], orow=120)),
+    (rows(*Q), rows(K[0], K[1], oq=8)),
+])
+def test_rows_that_share_memory_are_refused(q, k):
+    assert rotate(q, k) == INVALID
