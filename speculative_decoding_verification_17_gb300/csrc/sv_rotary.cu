@@ -55,6 +55,16 @@ __device__ __forceinline__ uint2 load8(const void* p) {
   return v;
 }
 
+// Squares of bf16 numbers pass the range of fp32 (fp16's do not): above where one is 2^60 or more, and
+// below they lose bits to subnormal numbers or vanish. Heads whose mean square with eps is outside
+// [2^-96, 2^128) are scaled by a power of two, which bf16 numbers take without loss: those with all
+// components below 2^-44 (2^-48 times the root of 256) by 2^100, and those with one of 2^60 or more by
+// 2^-70, which brings the largest below 2^58 and its square below 2^116 (and what lies below 2^-79, and
+// becomes subnormal, comes out below 2^-133, the smallest bf16 number). Zeros, infinities and NaN come out
+// as the formula has them.
+constexpr float kSmallMean = 1.262177448e-29f, kLargeMean = 3.402823466e38f;  // 2^-96, the largest number
+constexpr float kRaise = 1.267650600e30f, kLower = 8.470329473e-22f;          // 2^100, 2^-70
+
 // kSplit warps share a row (one token's heads). Nothing is shared between warps but the frequencies
 // and the weights, so no warp waits for another one's rows: with a table of cosines per CTA and
 // barriers around it prompts of 24576 rows took 145 us.
@@ -159,11 +169,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
           fetch(which, h0 + kAhead * kStep);
         else if (which == 0 && A.x[1].heads > 0)
           fetch(1, 0);
-#pragma unroll
-        for (int g = 0; g < kAhead; ++g, to += kStep * X.out_head) {
-          if (h0 + g * kStep >= X.heads) break;  // (whole warps)
-          const uint32_t w[4] = {va[g].x, va[g].y, vb[g].x, vb[g].y};
-          Two a[2], b[2];
+        // (the lane's share of a head, as pairs; the head's mean square with eps; and what it becomes)
+        auto pairs = [&](const uint2& va, const uint2& vb, Two (&a)[2], Two (&b)[2]) {
+          const uint32_t w[4] = {va.x, va.y, vb.x, vb.y};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 u = unpack16<kBf16>(w[kInterleaved ? 2 * k : k]);
@@ -171,14 +179,15 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
             a[k] = kInterleaved ? two(u.x, v.x) : two(u.x, u.y);
             b[k] = kInterleaved ? two(u.y, v.y) : two(v.x, v.y);
           }
-          float r = 1.0f;
-          if (A.norm) {
-            const float2 q = split(two_fma(a[0], a[0], two_fma(a[1], a[1], two_fma(b[0], b[0], two_mul(b[1], b[1])))));
-            float sum = q.x + q.y;
+        };
+        auto mean_of = [&](const Two (&a)[2], const Two (&b)[2], float eps, uint32_t lanes) {
+          const float2 q = split(two_fma(a[0], a[0], two_fma(a[1], a[1], two_fma(b[0], b[0], two_mul(b[1], b[1])))));
+          float sum = q.x + q.y;
 #pragma unroll
-            for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            r = rsqrtf(sum * (1.0f / D) + A.eps);
-          }
+          for (int o = kLanes / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+          return sum * (1.0f / D) + eps;
+        };
+        auto give = [&](const Two (&a)[2], const Two (&b)[2], float r, bool there, uint16_t* to) {
           const Two rr = two(r, r);
           float2 x[2], y[2];
 #pragma unroll
@@ -192,7 +201,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
             x[k] = split(two_mul(u, rr));
             y[k] = split(two_mul(v, rr));
           }
-          if (h0 + first + g * kStep < X.heads) {
+          if (there) {
             if (kInterleaved) {
               *reinterpret_cast<uint2*>(to + da) =
                   make_uint2(pack16<kBf16>(x[0].x, y[0].x), pack16<kBf16>(x[0].y, y[0].y));
@@ -204,6 +213,44 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas) rotate_kernel(const __g
               *reinterpret_cast<uint2*>(to + db) =
                   make_uint2(pack16<kBf16>(y[0].x, y[0].y), pack16<kBf16>(y[1].x, y[1].y));
             }
+          }
+        };
+        bool held[kAhead];  // in range
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) held[g] = true;
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g, to += kStep * X.out_head) {
+          if (h0 + g * kStep >= X.heads) break;  // (whole warps)
+          Two a[2], b[2];
+          pairs(va[g], vb[g], a, b);
+          float r = 1.0f;
+          if (A.norm) {
+            const float mean = mean_of(a, b, A.eps, 0xffffffffu);
+            r = rsqrtf(mean);
+            if (kBf16) held[g] = mean >= kSmallMean && mean <= kLargeMean;
+          }
+          give(a, b, r, h0 + first + g * kStep < X.heads && held[g], to);
+        }
+        // heads out of range once more, scaled (they have not been written, should that be in place)
+        if (kBf16 && __builtin_expect(!(held[0] && held[1] && held[2] && held[3]), 0)) {
+          static_assert(kAhead == 4, "heads at a time");
+          uint32_t again = 0;
+#pragma unroll
+          for (int g = 0; g < kAhead; ++g) again |= held[g] ? 0u : 1u << g;
+          const uint32_t lanes = kLanes == 32 ? 0xffffffffu : ((1u << kLanes % 32) - 1) << lane / kLanes * kLanes;
+#pragma unroll 1
+          for (int64_t h = h0 + first; again && h < X.heads; h += kStep, again >>= 1) {
+            if (!(again & 1u)) continue;
+            const uint16_t* x = X.in + req * X.req + at * X.row + h * X.head;
+            Two a[2], b[2];
+            pairs(load8(x + da), load8(x + db), a, b);
+            const float scale = mean_of(a, b, A.eps, lanes) < kSmallMean ? kRaise : kLower;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              a[k] = two_mul(a[k], two(scale, scale));
+              b[k] = two_mul(b[k], two(scale, scale));
+            }
+            give(a, b, rsqrtf(mean_of(a, b, A.eps * scale * scale, lanes)), true, out + h * X.out_head);
           }
         }
       }
