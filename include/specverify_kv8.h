@@ -76,7 +76,7 @@ sv_status kv_cache_append_q8(const sv_kv_shape* shape, int rows, const void* k, 
  *   queries      a row that is not finite gets NaN. An element below 2^-6 of its row's largest may
  *                be off by 2^-17 of that.
  * Scores, their softmax and the sums are fp32. The weights exp(s_j - max) * scale enter the product
- * with the codes rounded to fp16: off by 2^-11 of a weight, or 2^-27 of the row's largest weight.
+ * with the codes rounded to fp16, to nearest: off by 2^-11 of a weight and 2^-27 of the row's largest.
  * Equal calls give equal bits. More than 64 query rows per kv head (32 where D is 256) read the
  * cache once more for each 64 (32).
  * ---------------------------------------------------------------------------------------- */
