@@ -1016,7 +1016,8 @@ def kv_page_map(page_table, old_len, seq_len, num_new, ring, ring_state, page_si
     row of page_table [B, max_pages] int32 (updated in place) and is to have ``seq_len`` tokens, the
     last ``num_new`` of them new: it takes the pages it lacks from the front of ``ring`` (int32, the
     free pages, updated in place; ``ring_state`` [2] int32 holds the first one's place and how many
-    there are) or gives pages back to its end. Rows are [B, P], or packed in ``rows`` rows.
+    there are) or gives pages back to its end. Rows are [B, P], or packed in ``rows`` rows (of
+    ``out_slots``, where that is given).
     Returns (slots [B, P] or [rows] int64, positions int32 likewise, both -1 in rows of no new
     token; out_len [B] int32: seq_len, old_len where no pages were left, -1 for a data error;
     first rows [B + 1] int32; the ring's new state [2] int32, also of a batch without requests)."""
@@ -1025,6 +1026,9 @@ def kv_page_map(page_table, old_len, seq_len, num_new, ring, ring_state, page_si
             raise ValueError("give P (rows per request) or rows (packed)")
         size = (page_table.shape[0], P) if rows is None else (rows,)
         out_slots = _made(torch.empty, size, torch.int64, page_table.device, stream)
+    elif (P is not None and (out_slots.ndim != 2 or out_slots.shape[1] != P)
+          or rows is not None and (out_slots.ndim != 1 or out_slots.shape[0] != rows)):
+        raise ValueError(f"out_slots of shape {tuple(out_slots.shape)} is not of P={P}, rows={rows}")
     B = page_table.shape[0]
     made = [_made(torch.empty, size, torch.int32, page_table.device, stream) if t is None else t
             for t, size in ((out_positions, out_slots.shape), (out_len, (B,)),
