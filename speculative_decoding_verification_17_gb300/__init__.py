@@ -1058,6 +1058,10 @@ def kv_page_map(page_table, old_len, seq_len, num_new, ring, ring_state, page_si
         if t is None:
             raise TypeError(f"{name} must be a CUDA tensor")
         _check_cuda(name, t, dtype, shape, dev)
+    for name, x in (("page_size", page_size), ("num_pages", num_pages), ("rows", out_slots.numel()),
+                    ("the ring's size", ring.numel())):
+        if not -2 ** 31 <= x < 2 ** 31:  # (what ctypes would cut to 32 bits)
+            raise ValueError(f"{name} is {x}, past 32 bits")
     _ok(library().kv_page_map(
         B, page_size, num_pages, page_table.data_ptr(), page_table.shape[1], old_len.data_ptr(),
         seq_len.data_ptr(), num_new.data_ptr(), ring.data_ptr(), ring.numel(),
