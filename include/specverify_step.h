@@ -28,15 +28,17 @@ extern "C" {
  *   need < have   its entries need .. have-1 go to the ring's end, in the order of the requests
  *                 (they are free from the next call on; the table keeps the stale entries).
  * A request that is left without pages keeps what it holds: out_len = old_len, its slots -1.
+ * A page has one owner: one that stands in two rows (a common prefix) goes back with each of them, and is
+ * then given out twice. Rows that share pages are the caller's to keep apart.
  * Row i of request r is its token at position p = n - num_new + i, in slot
  *   page_table[r][p / page_size] * page_size + p % page_size
  * or -1 where that page is outside [0, num_pages).
  *
  * Arguments
- *   B            requests, 0 <= B <= 8192, else SV_ERR_UNSUPPORTED. Of none, out_state is
- *                ring_state (or {-1, -1}, as below), out_first[0] 0 and all rows -1, so that a step
- *                without requests keeps the ring; their arrays may then be NULL. (Where out_state is
- *                no memory of a CUDA device the call is a no-op.)
+ *   B            requests, 0 <= B <= 8192, else SV_ERR_UNSUPPORTED. With none the ring is kept:
+ *                out_state is ring_state (or {-1, -1}, as below), out_first[0] 0, all rows -1, and
+ *                the requests' arrays may be NULL. (With none and an out_state that is no memory of
+ *                CUDA's, as NULL, the call is a no-op.)
  *   page_size    a power of two from 8 to 1024. num_pages >= 0.
  *   page_table   [B, max_pages] int32, updated in place; max_pages * page_size < 2^30.
  *   old_len, seq_len   [B] int32 in [0, max_pages * page_size].
@@ -93,7 +95,8 @@ typedef struct {
  *   weight_f32   whether the weights are fp32, else of dtype.
  *   positions    [B, P] int32; rows at a negative position are left as they are.
  *   inv_freq     [R / 2], fp32, or fp64 where freq_f64.
- *   eps          >= 0.
+ *   eps          >= 0. A head's squares are summed in fp32; bf16 heads that pass its range there are
+ *                scaled by a power of two first.
  * No workspace.
  * ---------------------------------------------------------------------------------------- */
 sv_status qk_norm_rotate(sv_kv_dtype dtype, int B, int P, int D, int R, const sv_head_rows* q,

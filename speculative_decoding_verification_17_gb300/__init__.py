@@ -1076,7 +1076,8 @@ def qk_norm_rotate(q, k, positions, inv_freq=None, *, q_weight=None, k_weight=No
     """Divides every head of q [..., Hq, D] and k [..., Hkv, D] by its root mean square, multiplies
     by the weights [D] (fp32 or q's type), and rotates its first 2 * len(inv_freq) components by
     position * inv_freq (fp32 or fp64): component i with i + R/2, or 2i with 2i + 1 where
-    ``interleaved``. ``positions`` [...] int32; rows at a negative one are left as they are.
+    ``interleaved``. ``positions`` [...] int32; rows at a negative one are left as they are (in outputs that
+    the call makes, as the memory was).
     Returns (out_q, out_k), which may be q and k themselves."""
     if out_q is None:
         out_q = _made(torch.empty, q.shape, q.dtype, q.device, stream)

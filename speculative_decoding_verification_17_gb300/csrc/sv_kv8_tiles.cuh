@@ -36,14 +36,14 @@
 // tensor memory, two exponents, cuts, stores to shared memory, the hand-over), of which 12 warps hide
 // half, and four instructions of 128 x 4N x 32 take 400 up to 128 columns, 520 at 256. Measured, in
 // graph replays (the bytes read and written once at 6801 GB/s first):
-//   1 token of 64 requests, 200 .. 8192 keys, 32 / 8 heads   41.8 us   54.3 us   77 %
-//   6 positions of 32, 500 .. 16384 keys, 64 / 8 heads       42.4 us   87.5 us   48 %
-//   9 positions of 2, 100001 .. 131072 keys, 32 / 8 heads    77.4 us  119.0 us   65 %
-//   5 positions of 16, window 4096, 16 / 8 heads of 256      15.8 us   34.7 us   46 %
-//   1 token of 1 request of 777 keys                          0.2 us   10.4 us  (latency)
+//   1 token of 64 requests, 200 .. 8192 keys, 32 / 8 heads   41.8 us   54.8 us   76 %
+//   6 positions of 32, 500 .. 16384 keys, 64 / 8 heads       42.4 us   89.2 us   48 %
+//   9 positions of 2, 100001 .. 131072 keys, 32 / 8 heads    77.4 us  122.3 us   63 %
+//   5 positions of 16, window 4096, 16 / 8 heads of 256      15.8 us   35.0 us   45 %
+//   1 token of 1 request of 777 keys                          0.2 us   10.5 us  (latency)
 // and by query rows per kv head (64 requests of 200 .. 8192 keys, 8 kv heads, D = 128, floor 42 to 44
-// us; over 16 bits in brackets): 4 57 (98), 12 61 (100), 24 83 (103), 32 84 (104), 48 102 (116), 64 125
-// (116), 72 169 (203). Above 48 rows the softmax bounds and half the bytes gain nothing.
+// us; over 16 bits in brackets): 4 57 (98), 12 62 (100), 24 83 (103), 32 85 (104), 48 104 (116), 64 129
+// (116), 72 173 (200). Above 48 rows the softmax bounds and half the bytes gain nothing.
 #pragma once
 
 #include <cuda_fp8.h>
